@@ -346,8 +346,9 @@ def _stored_plain(x):
     b = _in_blocks(x)
     top = b.abs().amax(2, keepdim=True)
     kept = top >= TINY
-    inv = torch.where(kept, 127.0 / top, torch.zeros_like(top))
-    scale = torch.where(kept, top / 127.0, torch.zeros_like(top))
+    most = torch.full_like(top, 127.0)  # a tensor: division by a number may use its reciprocal
+    inv = torch.where(kept, most / top, torch.zeros_like(top))
+    scale = torch.where(kept, top / most, torch.zeros_like(top))
     return (torch.round(b * inv) * scale).reshape(x.shape[0], -1)[:, :x.shape[1]]
 
 

@@ -1,7 +1,8 @@
 """GB300 fused AdamW / AMSGrad step: thin Python binding of ``libfused_adamw.so``.
 
 Every function here marshals torch tensors into the C ABI of
-``include/fused_adamw.h`` under the same name; all arithmetic runs in the CUDA
+``include/fused_adamw.h`` (and, from ``model_ops``, of ``include/fa_model_ops.h``)
+under the same name; all arithmetic runs in the CUDA
 kernels of the library.  PyTorch supplies device memory and streams only.
 Layout checks that raw pointers cannot express (contiguity, strides, dtype,
 device) are made here, as the adapter's job ("実験的なデバイス上の融合 AdamW /
@@ -19,6 +20,8 @@ import torch
 from . import _lib
 from ._lib import (FA_BF16, FA_F16, FA_F32, FaOptions, FaStats, FaStepControl,  # noqa: F401
                    FaStepReport, FusedAdamWError, check)
+from . import model_ops
+from .model_ops import *  # noqa: F401,F403
 
 __all__ = [
     "fa_abi_version", "fa_device_error", "fa_bounds_check_report", "fa_pipeline_selftest",
@@ -31,6 +34,7 @@ __all__ = [
     "segment_rows", "fa_clip_decide", "fa_bucket_step_clipped", "fa_bucket_step_clipped_gated",
     "report_mailbox", "options", "control", "stats_buffer", "scratch_buffer",
     "FusedAdamWError", "FaStats", "FaStepReport", "bytes_per_param",
+    *model_ops.__all__,
 ]
 
 _TORCH_GRAD = {torch.float32: FA_F32, torch.float16: FA_F16, torch.bfloat16: FA_BF16}

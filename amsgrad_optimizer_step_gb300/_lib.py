@@ -1,4 +1,4 @@
-"""ctypes declarations of ``libfused_adamw.so`` (mirrors include/fused_adamw.h).
+"""ctypes declarations of ``libfused_adamw.so`` (mirrors the headers in include/).
 
 Loading fails loudly when the library has not been built: there is no
 fallback of any kind.
@@ -48,6 +48,26 @@ class FaBucketUpdate(ctypes.Structure):
 class FaStepReport(ctypes.Structure):
     _fields_ = [("updated", c_i32), ("skipped_nonfinite", c_i32), ("nonfinite", c_u64),
                 ("grad_norm", c_f64), ("clip_coef", c_f64)]
+
+
+class FaLogits(ctypes.Structure):
+    _fields_ = [("tokens", c_i64), ("vocab", c_i64), ("logits", c_vp), ("dtype", c_i32),
+                ("ld", c_i64), ("labels", c_vp), ("ltype", c_i32), ("logit_scale", c_f64)]
+
+
+class FaPreference(ctypes.Structure):
+    _fields_ = [("pairs", c_i64), ("seq_offsets", c_vp), ("ref_logp", c_vp), ("beta", c_f64),
+                ("label_smoothing", c_f64), ("average", c_i32), ("loss", c_vp),
+                ("pair_loss", c_vp), ("rewards", c_vp), ("logp", c_vp), ("lse", c_vp),
+                ("dlogp", c_vp)]
+
+
+class FaPolicy(ctypes.Structure):
+    _fields_ = [("old_logp", c_vp), ("advantages", c_vp), ("ref_logp", c_vp), ("weights", c_vp),
+                ("clip_low", c_f64), ("clip_high", c_f64), ("kl_coef", c_f64),
+                ("denominator", c_f64), ("grad_scale", c_f64), ("summary", c_vp),
+                ("logp", c_vp), ("token_loss", c_vp), ("token_kl", c_vp), ("dlogits", c_vp),
+                ("dlogits_ld", c_i64)]
 
 
 P = c_vp
@@ -104,6 +124,22 @@ SIGNATURES = {
     "fa_bucket_step_clipped": (c_i32, [PI64, c_i32, c_i64, P, P, c_i32, P, P, P, PU64,
                                        ctypes.POINTER(FaOptions), FaStepControl, c_f64, c_i32,
                                        P, c_i64, P, c_i64, P, ctypes.POINTER(FaStepReport), P]),
+    # fa_model_ops.h
+    "fa_embedding_lookup": (c_i32, [c_i64, P, c_i32, P, c_i32, c_i64, c_i64, c_i64, c_f64, P,
+                                    c_i32, c_i64, P]),
+    "fa_embedding_scratch": (c_i32, [c_i64, c_i64, c_i64, PI64]),
+    "fa_embedding_gradient": (c_i32, [c_i64, P, c_i32, P, c_i32, c_i64, c_f64, c_i64, c_i32, P,
+                                      c_i32, c_i64, c_i64, c_i64, P, c_i64, P]),
+    "fa_token_logprobs": (c_i32, [ctypes.POINTER(FaLogits), P, P, P]),
+    "fa_token_logprobs_gradient": (c_i32, [ctypes.POINTER(FaLogits), P, P, c_f64, P, P, c_i64,
+                                           P]),
+    "fa_preference_loss": (c_i32, [ctypes.POINTER(FaLogits), ctypes.POINTER(FaPreference), P]),
+    "fa_policy_loss": (c_i32, [ctypes.POINTER(FaLogits), ctypes.POINTER(FaPolicy), P]),
+    "fa_checkpoint_size": (c_i32, [c_i64, c_i64, PI64, PI64]),
+    "fa_gated_forward": (c_i32, [c_i64, c_i64, P, c_i64, P, c_i64, c_i32, c_i32, P, c_i64, P, P,
+                                 P]),
+    "fa_gated_backward": (c_i32, [c_i64, c_i64, P, P, c_i32, P, c_i64, c_i32, P, c_i64, P, c_i64,
+                                  P, c_i64, P]),
 }
 
 _LIB = None

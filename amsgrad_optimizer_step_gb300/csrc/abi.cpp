@@ -25,10 +25,11 @@
 #include <vector>
 
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include "fused_adamw.h"
+#include "abi_checks.h"
 #include "internal.h"
+#include "model_internal.h"
 
 namespace fa {
 
@@ -67,7 +68,15 @@ int resident_ctas(const void *kernel, int device, int threads) {
 
 namespace {
 
+using fa::any_overlap;
+using fa::check_device_ptr;
 using fa::Coef;
+using fa::dtype_bytes;
+using fa::overlap;
+using fa::Range;
+using fa::stream_device;
+using fa::TraceRange;
+using fa::valid_dtype;
 
 bool is_finite(double x) { return std::isfinite(x); }
 
@@ -98,77 +107,6 @@ fa_status check_control(const fa_step_control &c) {
     if (!is_finite(c.gradient_scale) || c.gradient_scale <= 0) return FA_ERR_OPTION;
     if (c.skip_update != 0 && c.skip_update != 1) return FA_ERR_OPTION;
     return FA_OK;
-}
-
-bool valid_dtype(fa_dtype d) { return d == FA_F32 || d == FA_F16 || d == FA_BF16; }
-size_t dtype_bytes(fa_dtype d) { return d == FA_F32 ? 4 : 2; }
-
-// Host-side trace ranges (NVTX): a profiler attached to the process shows each
-// entry point's span around the kernels it enqueues; without one they cost nothing.
-struct TraceRange {
-    explicit TraceRange(const char *name) { nvtxRangePushA(name); }
-    ~TraceRange() { nvtxRangePop(); }
-    TraceRange(const TraceRange &) = delete;
-    TraceRange &operator=(const TraceRange &) = delete;
-};
-
-// The current device, checked against the stream's device (the legacy default
-// stream belongs to the current device).
-fa_status stream_device(void *stream, int *dev) {
-    if (cudaGetDevice(dev) != cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_CUDA;
-    }
-    if (stream) {
-        // A stream that is being captured into a graph cannot report its device
-        // (the query fails and ends the capture); its work is recorded for the
-        // device the capture belongs to, so the check is left out then.
-        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-        if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cs) != cudaSuccess) {
-            cudaGetLastError();
-            return FA_ERR_POINTER;
-        }
-        if (cs == cudaStreamCaptureStatusActive) return FA_OK;
-        int sdev = -1;
-        if (cudaStreamGetDevice(static_cast<cudaStream_t>(stream), &sdev) != cudaSuccess) {
-            cudaGetLastError();
-            return FA_ERR_POINTER;
-        }
-        if (sdev != *dev) return FA_ERR_POINTER;
-    }
-    return FA_OK;
-}
-
-// Device (or managed) memory of device ``dev``, aligned to ``align`` bytes.
-fa_status check_device_ptr(const void *p, int dev, size_t align) {
-    if (!p) return FA_ERR_NULL;
-    cudaPointerAttributes at;
-    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_POINTER;
-    }
-    if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) return FA_ERR_POINTER;
-    if (at.device != dev) return FA_ERR_POINTER;
-    if (reinterpret_cast<uintptr_t>(p) % align) return FA_ERR_ALIGN;
-    return FA_OK;
-}
-
-struct Range {
-    const void *p;
-    size_t bytes;
-};
-
-bool overlap(Range a, Range b) {
-    if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-bool any_overlap(const Range *r, int count) {
-    for (int i = 0; i < count; ++i)
-        for (int j = i + 1; j < count; ++j)
-            if (overlap(r[i], r[j])) return true;
-    return false;
 }
 
 fa_status make_coef(const fa_options *o, uint64_t t, double scale, double grad_mult, Coef *c) {
@@ -428,14 +366,18 @@ fa_status fa_bounds_check_report(int32_t *enabled, uint64_t *violations, int32_t
     *enabled = FA_BOUNDS_CHECK;
     if (!violations) return FA_OK;
 #if FA_BOUNDS_CHECK
-    unsigned long long a = 0, b = 0, c = 0;
-    if (fa::update_bounds_violations(&a, clear != 0) != cudaSuccess ||
-        fa::stats_bounds_violations(&b, clear != 0) != cudaSuccess ||
-        fa::staged_bounds_violations(&c, clear != 0) != cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_CUDA;
+    unsigned long long total = 0;
+    for (auto *count : {fa::update_bounds_violations, fa::stats_bounds_violations,
+                        fa::staged_bounds_violations, fa::embedding_bounds_violations,
+                        fa::logprob_bounds_violations, fa::gated_bounds_violations}) {
+        unsigned long long n = 0;
+        if (count(&n, clear != 0) != cudaSuccess) {
+            cudaGetLastError();
+            return FA_ERR_CUDA;
+        }
+        total += n;
     }
-    *violations = a + b + c;
+    *violations = total;
 #else
     (void)clear;
     *violations = 0;

@@ -1,0 +1,140 @@
+// Internal interface between the C-ABI host layer of the model-side operators
+// (model_abi.cpp) and their kernels (embedding_kernels.cu, logprob_kernels.cu,
+// gated_kernels.cu).
+#pragma once
+
+#include <cstdint>
+#include <type_traits>
+
+#include <cuda_runtime.h>
+
+#include "fa_model_ops.h"
+
+namespace fa {
+
+constexpr int kCheckpointBlock = FA_CHECKPOINT_BLOCK;
+
+// ---- embedding ---------------------------------------------------------------
+struct LookupArgs {
+    const void *ids;
+    const void *table;
+    void *out;
+    int64_t tokens, vocab, dim, table_ld, out_ld;
+    float scale;
+};
+cudaError_t launch_embedding_lookup(const LookupArgs &a, fa_itype idt, fa_dtype tdt, fa_dtype odt,
+                                    cudaStream_t stream);
+
+// Scratch of the embedding gradient, in this order (each part 16-byte aligned).
+struct EmbeddingScratch {
+    int64_t chunks;  // runs of kSortChunk tokens that one CTA sorts
+    int64_t units;   // runs of kSumUnit sorted tokens that one CTA adds
+    int64_t sorted_words;  // 32-bit words of one sorted array (tokens, rounded up to 4)
+    int64_t bytes;
+};
+constexpr int kSortChunk = 8192;
+constexpr int kSumUnit = 32;
+EmbeddingScratch embedding_scratch_layout(int64_t tokens, int64_t dim);
+
+struct EmbeddingGradArgs {
+    const void *ids;
+    const void *dout;
+    void *dtable;
+    void *scratch;
+    int64_t tokens, vocab, dim, dout_ld, table_ld, padding_idx;
+    float scale;
+    bool accumulate;
+};
+cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &a, fa_itype idt, fa_dtype ddt,
+                                      fa_dtype tdt, cudaStream_t stream);
+
+// ---- losses from the logits -----------------------------------------------------
+struct LogitsArgs {
+    const void *logits;
+    const void *labels;
+    int64_t tokens, vocab, ld;
+    float scale;  // logit_scale
+    float k;      // logit_scale * log2(e): exp(scale * x) = 2^(k * x)
+};
+cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, fa_itype lt, float *logp,
+                                  float *lse, cudaStream_t stream);
+
+struct LogitGradArgs {
+    LogitsArgs x;
+    const float *lse;
+    const float *dlogp;
+    const float *grad_loss;
+    float factor;  // logit_scale * grad_scale
+    void *dlogits;
+    int64_t dlogits_ld;
+};
+cudaError_t launch_token_logprobs_gradient(const LogitGradArgs &a, fa_dtype dt, fa_itype lt,
+                                           cudaStream_t stream);
+
+struct PreferenceArgs {
+    const void *labels;
+    int64_t tokens, vocab, pairs;
+    const int64_t *seq_offsets;
+    const float *logp, *ref_logp;
+    float beta, smoothing;
+    bool average;
+    float *loss, *pair_loss, *rewards, *dlogp;
+};
+cudaError_t launch_preference(const PreferenceArgs &a, fa_itype lt, cudaStream_t stream);
+
+struct PolicyArgs {
+    LogitsArgs x;
+    const float *old_logp, *advantages, *ref_logp, *weights;
+    float clip_lo, clip_hi;  // 1 - clip_low, 1 + clip_high
+    float kl_coef;
+    float denominator;  // 0: the number of counted tokens, from summary[3]
+    float grad_factor;  // logit_scale * grad_scale
+    float *summary, *logp, *token_loss, *token_kl;
+    void *dlogits;
+    int64_t dlogits_ld;
+};
+cudaError_t launch_policy(const PolicyArgs &a, fa_dtype dt, fa_itype lt, cudaStream_t stream);
+
+// ---- gated activation -------------------------------------------------------------
+struct GatedForwardArgs {
+    const void *gate, *up;
+    void *h;
+    int8_t *codes;  // nullptr: no checkpoint
+    float *scales;
+    int64_t rows, cols, gate_ld, up_ld, h_ld, blocks;
+};
+cudaError_t launch_gated_forward(const GatedForwardArgs &a, fa_dtype dt, fa_activation act,
+                                 cudaStream_t stream);
+
+struct GatedBackwardArgs {
+    const int8_t *codes;
+    const float *scales;
+    const void *dh;
+    void *dgate, *dup, *h;  // h may be nullptr
+    int64_t rows, cols, dh_ld, dgate_ld, dup_ld, h_ld, blocks;
+};
+cudaError_t launch_gated_backward(const GatedBackwardArgs &a, fa_dtype dt, fa_activation act,
+                                  cudaStream_t stream);
+
+// Out-of-range accesses counted by each file's kernels in the bounds-checked build
+// (0 in the normal build).  Wait for the device.
+cudaError_t embedding_bounds_violations(unsigned long long *count, bool clear);
+cudaError_t logprob_bounds_violations(unsigned long long *count, bool clear);
+cudaError_t gated_bounds_violations(unsigned long long *count, bool clear);
+
+// Calls f with the validated type as a compile-time constant.
+template <typename F>
+inline cudaError_t for_dtype(fa_dtype dt, F f) {
+    switch (dt) {
+        case FA_F32: return f(std::integral_constant<int, FA_F32>{});
+        case FA_F16: return f(std::integral_constant<int, FA_F16>{});
+        default: return f(std::integral_constant<int, FA_BF16>{});
+    }
+}
+template <typename F>
+inline cudaError_t for_itype(fa_itype it, F f) {
+    return it == FA_I64 ? f(std::integral_constant<int, FA_I64>{})
+                        : f(std::integral_constant<int, FA_I32>{});
+}
+
+}  // namespace fa

@@ -25,6 +25,7 @@ namespace {
 FA_BOUNDS_COUNTER(g_embedding_oob)
 
 constexpr int kLookupThreads = 256;
+constexpr int kLookupGroups = 4;  // 16-byte groups a lane has in flight
 constexpr int kSortThreads = 1024;
 constexpr int kSortItems = kSortChunk / kSortThreads;
 constexpr int kDigits = 16;
@@ -39,27 +40,38 @@ constexpr int kGroup =
 
 // ---- lookup --------------------------------------------------------------------
 
+// 2^lanes_log2 lanes take a token's stretch (blockIdx.y) of kLookupGroups groups each: a row's
+// loads are in flight together once its id is there.
 template <int TT, int OT, int IT, bool VEC>
-__global__ void __launch_bounds__(kLookupThreads) lookup_kernel(LookupArgs a, int64_t groups) {
+__global__ void __launch_bounds__(kLookupThreads)
+lookup_kernel(LookupArgs a, int groups, int lanes_log2) {
     constexpr int N = kGroup<TT, OT, VEC>;
     using TE = typename Elem<TT>::T;
     using OE = typename Elem<OT>::T;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kLookupThreads + threadIdx.x;
-    if (i >= a.tokens * groups) return;
-    const int64_t t = i / groups, c = (i - t * groups) * N;
+    const int64_t thread = static_cast<int64_t>(blockIdx.x) * kLookupThreads + threadIdx.x;
+    const int64_t t = thread >> lanes_log2;
+    if (t >= a.tokens) return;
+    const int lanes = 1 << lanes_log2;
+    const int g0 = (blockIdx.y * kLookupGroups << lanes_log2) + (threadIdx.x & (lanes - 1));
     const int64_t id = load_id<IT>(a.ids, t);
-    float x[N];
-    if (id >= 0 && id < a.vocab) {
-        const TE *row = static_cast<const TE *>(a.table) + id * a.table_ld + c;
-        if (fa_in_bounds(c, N, a.dim)) load_n<TT, N>(row, x);
+    const bool known = id >= 0 && id < a.vocab;
+    const TE *row = static_cast<const TE *>(a.table) + (known ? id : 0) * a.table_ld;
+    OE *out = static_cast<OE *>(a.out) + t * a.out_ld;
+    float x[kLookupGroups][N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] *= a.scale;
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = 0.f;
+    for (int k = 0; k < kLookupGroups; ++k) {
+        const int g = g0 + k * lanes;
+        if (known && g < groups && fa_in_bounds(static_cast<int64_t>(g) * N, N, a.dim))
+            read_n<TT, N>(row + static_cast<int64_t>(g) * N, x[k]);
     }
-    if (fa_in_bounds(c, N, a.dim))
-        store_n<OT, N>(static_cast<OE *>(a.out) + t * a.out_ld + c, x);
+#pragma unroll
+    for (int k = 0; k < kLookupGroups; ++k) {
+        const int g = g0 + k * lanes;
+        if (g >= groups || !fa_in_bounds(static_cast<int64_t>(g) * N, N, a.dim)) break;
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[k][j] = known ? x[k][j] * a.scale : 0.f;
+        store_n<OT, N>(out + static_cast<int64_t>(g) * N, x[k]);
+    }
 }
 
 // ---- sort ----------------------------------------------------------------------
@@ -366,10 +378,17 @@ cudaError_t launch_embedding_lookup(const LookupArgs &a, fa_itype idt, fa_dtype 
                 const auto go = [&](auto v) {
                     constexpr bool VEC = decltype(v)::value;
                     const int64_t groups = a.dim / kGroup<td(), od(), VEC>;
-                    const int64_t ctas = (a.tokens * groups + kLookupThreads - 1) / kLookupThreads;
-                    if (ctas > kMaxGridX) return cudaErrorInvalidConfiguration;
+                    int lanes_log2 = 0;
+                    while (lanes_log2 < 5 && (int64_t(kLookupGroups) << lanes_log2) < groups)
+                        ++lanes_log2;
+                    const int64_t ctas = ((a.tokens << lanes_log2) + kLookupThreads - 1) /
+                                         kLookupThreads;
+                    const int64_t stretch = int64_t(kLookupGroups) << lanes_log2;
+                    const int64_t stretches = (groups + stretch - 1) / stretch;
+                    if (ctas > kMaxGridX || stretches > 65535) return cudaErrorInvalidConfiguration;
                     lookup_kernel<td(), od(), id(), VEC>
-                        <<<static_cast<unsigned>(ctas), kLookupThreads, 0, stream>>>(a, groups);
+                        <<<dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(stretches)),
+                           kLookupThreads, 0, stream>>>(a, static_cast<int>(groups), lanes_log2);
                     return cudaGetLastError();
                 };
                 return vec ? go(std::true_type{}) : go(std::false_type{});

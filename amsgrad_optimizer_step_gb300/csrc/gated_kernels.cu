@@ -1,9 +1,12 @@
 // The gated activation h = act(gate) * up with an 8-bit checkpoint of its two inputs,
 // and its backward pass from the checkpoint.
 //
-// Sixteen lanes take one block of kCheckpointBlock columns, eight consecutive columns
-// each: the block's largest magnitude is four shuffles away, and a lane's eight codes
-// are one 8-byte store.
+// Eight lanes take one block of kCheckpointBlock columns, two runs of eight consecutive
+// columns each, 64 apart: 16-byte accesses for 16-bit types, and a block's largest
+// magnitude is three shuffles away.  The four divisions of a block (127 / a and a / 127 of
+// gate and up) are one division in four of its lanes.  Codes are rounded and taken apart
+// without conversions: x * (127 / a) + 1.5 * 2^23 has the code in its low byte, and
+// a code's byte below the exponent of 2^23 is the code + 128 + 2^23.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -18,153 +21,222 @@ namespace {
 FA_BOUNDS_COUNTER(g_gated_oob)
 
 constexpr int kGatedThreads = 256;
-constexpr int kLanes = 16;                        // per block of columns
-constexpr int kCols = kCheckpointBlock / kLanes;  // per lane
+constexpr int kLanes = 8;                         // per block of columns
+constexpr int kRun = 8;                           // consecutive columns of a lane
+constexpr int kRunStride = kCheckpointBlock / 2;  // between its two runs
 constexpr float kTiny = 0x1p-100f;                // blocks below it are stored as zeros
+constexpr float kLog2E = 1.4426950408889634f;
 
-// sigmoid(z); 0 and 1 at the infinities.
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
 
+// sigmoid(-t / log2(e)) of a pair: 1 / (1 + 2^t).
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t t) {
+    float lo, hi;
+    unpair(t, lo, hi);
+    unpair(add2(both(1.f), pair(exp2_fast(lo), exp2_fast(hi))), lo, hi);
+    return pair(reciprocal(lo), reciprocal(hi));
+}
+
+// The activation of a pair and its derivative.
 template <int ACT>
 struct Activation;
 
 template <>
 struct Activation<FA_SILU> {
-    static __device__ __forceinline__ float value(float g) { return g * sigmoid(g); }
-    static __device__ __forceinline__ void both(float g, float &a, float &da) {
-        const float s = sigmoid(g);
-        a = g * s;
-        da = fmaf(a, 1.f - s, s);  // s (1 + g (1 - s))
+    static __device__ __forceinline__ uint64_t value(uint64_t g) {
+        return mul2(g, sigmoid2(mul2(g, both(-kLog2E))));
+    }
+    static __device__ __forceinline__ void with_slope(uint64_t g, uint64_t &a, uint64_t &da) {
+        const uint64_t s = sigmoid2(mul2(g, both(-kLog2E)));
+        a = mul2(g, s);
+        da = fma2(a, fma2(s, both(-1.f), both(1.f)), s);  // s (1 + g (1 - s))
     }
 };
 
 template <>
 struct Activation<FA_GELU_TANH> {
-    // 2 sqrt(2/pi) (g + 0.044715 g^3)
+    // 2 sqrt(2/pi) (g + 0.044715 g^3) = g (kA + kB g^2)
     static constexpr float kA = 1.5957691216057308f, kB = 0.071354816272600250f;
-    static __device__ __forceinline__ float value(float g) {
-        return g * sigmoid(g * fmaf(kB, g * g, kA));
+    static __device__ __forceinline__ uint64_t gate(uint64_t g, uint64_t q) {
+        return sigmoid2(mul2(g, fma2(q, both(-kB * kLog2E), both(-kA * kLog2E))));
     }
-    static __device__ __forceinline__ void both(float g, float &a, float &da) {
-        const float q = g * g, s = sigmoid(g * fmaf(kB, q, kA));
-        a = g * s;
-        da = fmaf(a * (1.f - s), fmaf(3.f * kB, q, kA), s);
+    static __device__ __forceinline__ uint64_t value(uint64_t g) {
+        return mul2(g, gate(g, mul2(g, g)));
+    }
+    static __device__ __forceinline__ void with_slope(uint64_t g, uint64_t &a, uint64_t &da) {
+        const uint64_t q = mul2(g, g), s = gate(g, q);
+        a = mul2(g, s);
+        const uint64_t rest = mul2(a, fma2(s, both(-1.f), both(1.f)));
+        da = fma2(rest, fma2(q, both(3.f * kB), both(kA)), s);
     }
 };
 
-// A lane's eight columns [c, c + 8) of a row: one 16-byte access (two for FP32) when the
-// rows are aligned and the columns all exist, element accesses otherwise; columns past
+// A lane's run of eight columns [c, c + 8) of a row: one 16-byte access (two for FP32) when
+// the rows are aligned and the columns all exist, element accesses otherwise; columns past
 // the end read as 0 and are not written.
 template <int DT, bool VEC>
-__device__ __forceinline__ void load_cols(const void *base, int64_t row, int64_t ld, int64_t c,
-                                          int64_t cols, float *x) {
+__device__ __forceinline__ void load_run(const void *base, int64_t row, int64_t ld, int64_t c,
+                                         int64_t cols, float *x) {
     using E = Elem<DT>;
     const typename E::T *p = static_cast<const typename E::T *>(base) + row * ld + c;
-    if (VEC && c + kCols <= cols) {
-        if (fa_in_bounds(c, kCols, cols)) load_n<DT, kCols>(p, x);
+    if (VEC && c + kRun <= cols) {
+        if (fa_in_bounds(c, kRun, cols)) load_n<DT, kRun>(p, x);
     } else {
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) x[j] = c + j < cols ? E::widen(p[j]) : 0.f;
+        for (int j = 0; j < kRun; ++j) x[j] = c + j < cols ? E::widen(p[j]) : 0.f;
     }
 }
 template <int DT, bool VEC>
-__device__ __forceinline__ void store_cols(void *base, int64_t row, int64_t ld, int64_t c,
-                                           int64_t cols, const float *x) {
+__device__ __forceinline__ void store_run(void *base, int64_t row, int64_t ld, int64_t c,
+                                          int64_t cols, const float *x) {
     using E = Elem<DT>;
     typename E::T *p = static_cast<typename E::T *>(base) + row * ld + c;
-    if (VEC && c + kCols <= cols) {
-        if (fa_in_bounds(c, kCols, cols)) store_n<DT, kCols>(p, x);
+    if (VEC && c + kRun <= cols) {
+        if (fa_in_bounds(c, kRun, cols)) store_n<DT, kRun>(p, x);
     } else {
 #pragma unroll
-        for (int j = 0; j < kCols; ++j)
+        for (int j = 0; j < kRun; ++j)
             if (c + j < cols) p[j] = E::round(x[j]);
     }
 }
 
-// Quantises a block held by the 16 lanes of the mask; the first stores the scale.
-__device__ __forceinline__ void store_codes(const float *x, int8_t *codes, float *scale,
-                                            bool first_lane, unsigned lanes) {
-    float top = 0.f;
-    bool bad = false;
+// The larger of two magnitudes; NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+// Largest magnitude of a lane's sixteen values.
+__device__ __forceinline__ float largest(const float (*x)[kRun]) {
+    float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-        top = fmaxf(top, fabsf(x[j]));
-        bad |= !isfinite(x[j]);
-    }
-    if (bad) top = INFINITY;
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(lanes, top, o, kLanes));
-    const bool kept = top >= kTiny && top < INFINITY;
-    const float inv = kept ? __fdiv_rn(127.f, top) : 0.f;
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-        const int q = kept ? __float2int_rn(__fmul_rn(x[j], inv)) : 0;
-        w[j / 4] |= (static_cast<uint32_t>(q) & 0xffu) << (8 * (j % 4));
-    }
-    __stcs(reinterpret_cast<uint2 *>(codes), make_uint2(w[0], w[1]));
-    if (first_lane) *scale = kept ? __fdiv_rn(top, 127.f) : top == INFINITY ? NAN : 0.f;
+        for (int j = 0; j < kRun; ++j) m = max_nan(m, fabsf(x[r][j]));
+    return m;
 }
 
-__device__ __forceinline__ void load_codes(const int8_t *codes, float scale, float *x) {
-    const uint2 r = __ldcs(reinterpret_cast<const uint2 *>(codes));
-    const uint32_t w[2] = {r.x, r.y};
+// Eight codes of a run, packed.
+__device__ __forceinline__ uint2 encode(const float *x, float inv) {
+    uint32_t y[kRun];
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-        const int q = static_cast<int8_t>(w[j / 4] >> (8 * (j % 4)));
-        x[j] = static_cast<float>(q) * scale;
+    for (int j = 0; j < kRun; ++j)  // two roundings, as the rule says: the packed pair of
+        // instructions was measured to round once
+        y[j] = __float_as_uint(__fadd_rn(__fmul_rn(x[j], inv), 0x1.8p23f));
+    const auto four = [](const uint32_t *q) {
+        return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040),
+                           0x5410);
+    };
+    return make_uint2(four(y), four(y + 4));
+}
+
+// What eight codes stand for, in pairs.
+__device__ __forceinline__ void decode(uint2 codes, float scale, uint64_t *x) {
+    const uint32_t w[2] = {codes.x ^ 0x80808080u, codes.y ^ 0x80808080u};
+#pragma unroll
+    for (int j = 0; j < kRun; j += 2) {
+        const uint32_t b = w[j / 4];
+        const uint32_t lo = __byte_perm(b, 0x4b000000u, j % 4 == 0 ? 0x7440 : 0x7442);
+        const uint32_t hi = __byte_perm(b, 0x4b000000u, j % 4 == 0 ? 0x7441 : 0x7443);
+        const uint64_t q = add2(pair(__uint_as_float(lo), __uint_as_float(hi)),
+                                both(-(0x1p23f + 128.f)));  // exact
+        x[j / 2] = mul2(q, both(scale));
     }
 }
 
 template <int DT, int ACT, bool VEC, bool KEEP>
 __global__ void __launch_bounds__(kGatedThreads) gated_forward_kernel(GatedForwardArgs a) {
-    const int64_t b = (static_cast<int64_t>(blockIdx.x) * kGatedThreads + threadIdx.x) / kLanes;
+    const uint32_t b = (blockIdx.x * kGatedThreads + threadIdx.x) / kLanes;
     const int lane = threadIdx.x % kLanes;
     const int64_t n = a.rows * a.blocks;
-    if (b >= n || !fa_in_bounds(b, 1, n)) return;  // all sixteen lanes of a block
-    const int64_t row = b / a.blocks;
-    const int64_t c = (b - row * a.blocks) * kCheckpointBlock + lane * kCols;
-    float g[kCols], u[kCols];
-    load_cols<DT, VEC>(a.gate, row, a.gate_ld, c, a.cols, g);
-    load_cols<DT, VEC>(a.up, row, a.up_ld, c, a.cols, u);
-    float h[kCols];
+    if (b >= n || !fa_in_bounds(b, 1, n)) return;  // all eight lanes of a block
+    const uint32_t row = a.by_blocks.quotient(b);
+    const int64_t c = static_cast<int64_t>(b - row * static_cast<uint32_t>(a.blocks)) *
+                          kCheckpointBlock + lane * kRun;
+    float g[2][kRun], u[2][kRun];
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) h[j] = Activation<ACT>::value(g[j]) * u[j];
-    store_cols<DT, VEC>(a.h, row, a.h_ld, c, a.cols, h);
+    for (int r = 0; r < 2; ++r) load_run<DT, VEC>(a.gate, row, a.gate_ld, c + r * kRunStride, a.cols, g[r]);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) load_run<DT, VEC>(a.up, row, a.up_ld, c + r * kRunStride, a.cols, u[r]);
     if (KEEP) {
-        const unsigned lanes = 0xffffu << (threadIdx.x & kLanes);
-        int8_t *code = a.codes + b * kCheckpointBlock + lane * kCols;
-        store_codes(g, code, a.scales + b, lane == 0, lanes);
-        store_codes(u, code + n * kCheckpointBlock, a.scales + n + b, lane == 0, lanes);
+        const unsigned lanes = 0xffu << (threadIdx.x & 24);
+        float tg = largest(g), tu = largest(u);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) {
+            tg = max_nan(tg, __shfl_xor_sync(lanes, tg, o));
+            tu = max_nan(tu, __shfl_xor_sync(lanes, tu, o));
+        }
+        // lane 0: 127 / tg, 1: tg / 127, 2 and 3: the same of tu (the others repeat them)
+        const float top = lane & 2 ? tu : tg;
+        const bool kept = top >= kTiny && top < INFINITY, scale = lane & 1;
+        float q = __fdiv_rn(scale ? top : 127.f, scale ? 127.f : top);
+        if (!kept) q = scale && !(top < INFINITY) ? NAN : 0.f;
+        const float inv_g = __shfl_sync(lanes, q, 0, kLanes), inv_u = __shfl_sync(lanes, q, 2, kLanes);
+        if (lane == 1) a.scales[b] = q;
+        if (lane == 3) a.scales[n + b] = q;
+        int8_t *code = a.codes + static_cast<int64_t>(b) * kCheckpointBlock + lane * kRun;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            __stcs(reinterpret_cast<uint2 *>(code + r * kRunStride), encode(g[r], inv_g));
+            __stcs(reinterpret_cast<uint2 *>(code + n * kCheckpointBlock + r * kRunStride),
+                   encode(u[r], inv_u));
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float h[kRun];
+#pragma unroll
+        for (int j = 0; j < kRun; j += 2)
+            unpair(mul2(Activation<ACT>::value(pair(g[r][j], g[r][j + 1])),
+                        pair(u[r][j], u[r][j + 1])), h[j], h[j + 1]);
+        store_run<DT, VEC>(a.h, row, a.h_ld, c + r * kRunStride, a.cols, h);
     }
 }
 
 template <int DT, int ACT, bool VEC>
 __global__ void __launch_bounds__(kGatedThreads) gated_backward_kernel(GatedBackwardArgs a) {
-    const int64_t b = (static_cast<int64_t>(blockIdx.x) * kGatedThreads + threadIdx.x) / kLanes;
+    const uint32_t b = (blockIdx.x * kGatedThreads + threadIdx.x) / kLanes;
     const int lane = threadIdx.x % kLanes;
     const int64_t n = a.rows * a.blocks;
     if (b >= n || !fa_in_bounds(b, 1, n)) return;
-    const int64_t row = b / a.blocks;
-    const int64_t c = (b - row * a.blocks) * kCheckpointBlock + lane * kCols;
-    const int8_t *code = a.codes + b * kCheckpointBlock + lane * kCols;
-    float g[kCols], u[kCols], d[kCols];
-    load_codes(code, a.scales[b], g);
-    load_codes(code + n * kCheckpointBlock, a.scales[n + b], u);
-    load_cols<DT, VEC>(a.dh, row, a.dh_ld, c, a.cols, d);
-    float dg[kCols], du[kCols], h[kCols];
+    const uint32_t row = a.by_blocks.quotient(b);
+    const int64_t c = static_cast<int64_t>(b - row * static_cast<uint32_t>(a.blocks)) *
+                          kCheckpointBlock + lane * kRun;
+    const int8_t *code = a.codes + static_cast<int64_t>(b) * kCheckpointBlock + lane * kRun;
+    uint2 qg[2], qu[2];
+    float d[2][kRun];
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-        float act, dact;
-        Activation<ACT>::both(g[j], act, dact);
-        dg[j] = d[j] * dact * u[j];  // |act'| < 1.13: overflows only where the gradient does
-        du[j] = d[j] * act;
-        h[j] = act * u[j];
+    for (int r = 0; r < 2; ++r) {
+        qg[r] = __ldcs(reinterpret_cast<const uint2 *>(code + r * kRunStride));
+        qu[r] = __ldcs(reinterpret_cast<const uint2 *>(code + n * kCheckpointBlock + r * kRunStride));
+        load_run<DT, VEC>(a.dh, row, a.dh_ld, c + r * kRunStride, a.cols, d[r]);
     }
-    store_cols<DT, VEC>(a.dgate, row, a.dgate_ld, c, a.cols, dg);
-    store_cols<DT, VEC>(a.dup, row, a.dup_ld, c, a.cols, du);
-    if (a.h) store_cols<DT, VEC>(a.h, row, a.h_ld, c, a.cols, h);
+    const float sg = a.scales[b], su = a.scales[n + b];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        uint64_t g[kRun / 2], u[kRun / 2];
+        decode(qg[r], sg, g);
+        decode(qu[r], su, u);
+        float dg[kRun], du[kRun], h[kRun];
+#pragma unroll
+        for (int j = 0; j < kRun; j += 2) {
+            uint64_t act, slope;
+            Activation<ACT>::with_slope(g[j / 2], act, slope);
+            const uint64_t dh = pair(d[r][j], d[r][j + 1]);
+            // |act'| < 1.13: overflows only where the gradient does
+            unpair(mul2(mul2(dh, slope), u[j / 2]), dg[j], dg[j + 1]);
+            unpair(mul2(dh, act), du[j], du[j + 1]);
+            unpair(mul2(act, u[j / 2]), h[j], h[j + 1]);
+        }
+        store_run<DT, VEC>(a.dgate, row, a.dgate_ld, c + r * kRunStride, a.cols, dg);
+        store_run<DT, VEC>(a.dup, row, a.dup_ld, c + r * kRunStride, a.cols, du);
+        if (a.h) store_run<DT, VEC>(a.h, row, a.h_ld, c + r * kRunStride, a.cols, h);
+    }
 }
 
 // Whether 16-byte accesses at multiples of eight columns are aligned in every row.
@@ -197,7 +269,6 @@ cudaError_t gated_bounds_violations(unsigned long long *count, bool clear) {
 cudaError_t launch_gated_forward(const GatedForwardArgs &a, fa_dtype dt, fa_activation act,
                                  cudaStream_t stream) {
     const int64_t ctas = (a.rows * a.blocks * kLanes + kGatedThreads - 1) / kGatedThreads;
-    if (ctas > kMaxGridX) return cudaErrorInvalidConfiguration;
     const bool vec = vector_rows(a.gate, a.gate_ld, dt) && vector_rows(a.up, a.up_ld, dt) &&
                      vector_rows(a.h, a.h_ld, dt);
     return for_dtype(dt, [&](auto d) {
@@ -215,7 +286,6 @@ cudaError_t launch_gated_forward(const GatedForwardArgs &a, fa_dtype dt, fa_acti
 cudaError_t launch_gated_backward(const GatedBackwardArgs &a, fa_dtype dt, fa_activation act,
                                   cudaStream_t stream) {
     const int64_t ctas = (a.rows * a.blocks * kLanes + kGatedThreads - 1) / kGatedThreads;
-    if (ctas > kMaxGridX) return cudaErrorInvalidConfiguration;
     const bool vec = vector_rows(a.dh, a.dh_ld, dt) && vector_rows(a.dgate, a.dgate_ld, dt) &&
                      vector_rows(a.dup, a.dup_ld, dt) && vector_rows(a.h, a.h_ld, dt);
     return for_dtype(dt, [&](auto d) {

@@ -5,10 +5,14 @@
 //   top = max_v x_v,  s = sum_v exp(scale (x_v - top)),
 //   logp = scale (x_label - top) - ln s,
 //   dlogits_v = c (1[v = label] - exp(scale (x_v - top)) / s).
-// exp(scale (x - top)) is 2^(k x - k top) with k = scale log2(e): one fused
-// multiply-add whose product is exact, so that every term of a row, and its label's,
-// carries the same rounding of k top; rows whose k top leaves FP32's range (masks of
-// the type's lowest value) take the difference first.
+// exp(scale (x - top)) is 2^(k x - k top), k = scale log2(e) in two FP32 parts: two fused
+// multiply-adds, the first of which cancels exactly.  k top is rounded once for the row,
+// so that every term, and the label's, carries the same rounding; with k in one part the
+// log-probabilities were off by 1.3e-8 of a row's spread, all the same way.  Rows whose
+// k top leaves FP32's range (masks of the type's lowest value) take the difference first.
+#include <algorithm>
+
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -20,127 +24,182 @@
 namespace fa {
 namespace {
 
+namespace cg = cooperative_groups;
+
 FA_BOUNDS_COUNTER(g_logprob_oob)
 
 constexpr int kRowThreads = 256;
-constexpr int kBatch = 4;  // 16-byte vectors a thread has in flight
+constexpr int kBatch = 4;  // 16-byte vectors a thread takes at a time
 
 // A row cut for 16-byte accesses: head scalars up to the first boundary, then nvec
 // vectors, then the scalars left over.
 struct RowSpan {
-    int64_t head, nvec, n;
+    int head;
+    int64_t nvec, tail;  // tail: the first scalar after the vectors
 };
 template <int DT>
-__device__ __forceinline__ RowSpan row_span(const void *row, int64_t n) {
+__host__ __device__ __forceinline__ RowSpan row_span(const void *row, int64_t n) {
     constexpr int V = Elem<DT>::kVec;
-    const int64_t past = (reinterpret_cast<uintptr_t>(row) & 15) / sizeof(typename Elem<DT>::T);
+    const int past =
+        static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(typename Elem<DT>::T));
     RowSpan r;
-    r.n = n;
     r.head = past ? V - past : 0;
-    if (r.head > n) r.head = n;
+    if (r.head > n) r.head = static_cast<int>(n);
     r.nvec = (n - r.head) / V;
+    r.tail = r.head + r.nvec * V;
     return r;
 }
 
-// The running maximum and the sum of 2^(k (x - top)) over some of a row's elements.
-struct Softmax {
-    float top = -INFINITY, s = 0.f;
+// 2^(k (x - top)) for the elements of a row.
+struct Exponent {
+    float k, k_lo, top, c;  // c = k top, rounded once
+    bool fine;              // c is finite
 
-    // 2^(k x - k top), by one FMA where k top is finite.
-    static __device__ __forceinline__ float term(float x, float top, float k, float ktop) {
-        return isfinite(ktop) ? exp2_fast(fmaf(x, k, -ktop)) : exp2_fast((x - top) * k);
+    __device__ __forceinline__ Exponent(const LogitsArgs &a, float top_) : k(a.k), k_lo(a.k_lo) {
+        set(top_);
     }
-
-    template <int N>
-    __device__ __forceinline__ void add(const float *x, float k) {
-        float best = x[0];
-#pragma unroll
-        for (int j = 1; j < N; ++j) best = fmaxf(best, x[j]);
-        if (best > top) {
-            s = s == 0.f ? 0.f : s * exp2_fast((top - best) * k);
-            top = best;
-        }
-        if (top == -INFINITY) {  // nothing but -inf (and NaN) so far
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (isnan(x[j])) s = x[j];
-            return;
-        }
-        const float ktop = k * top;
-#pragma unroll
-        for (int j = 0; j < N; ++j) s += term(x[j], top, k, ktop);
+    __device__ __forceinline__ void set(float top_) {
+        top = top_;
+        c = fmaf(top, k_lo, top * k);
+        fine = isfinite(c);
     }
-    __device__ __forceinline__ void merge(const Softmax &o, float k) {
-        const float best = fmaxf(top, o.top);
-        // a part without any finite value keeps its sum (0, or NaN)
-        const float a = top == best || top == -INFINITY ? s : s * exp2_fast((top - best) * k);
-        const float b = o.top == best || o.top == -INFINITY ? o.s
-                                                            : o.s * exp2_fast((o.top - best) * k);
-        top = best;
-        s = a + b;
+    __device__ __forceinline__ float log2_of(float x) const {
+        return fine ? fmaf(x, k_lo, fmaf(x, k, -c)) : (x - top) * k;
+    }
+    __device__ __forceinline__ float operator()(float x) const { return exp2_fast(log2_of(x)); }
+    // Of a pair, where fine.
+    __device__ __forceinline__ uint64_t log2_of(uint64_t x) const {
+        return fma2(x, pair(k_lo, k_lo), fma2(x, pair(k, k), pair(-c, -c)));
+    }
+    // What sums taken relative to ``from`` are multiplied by to be relative to this.
+    __device__ __forceinline__ float rebase(const Exponent &from) const {
+        return exp2_exact(fine && from.fine ? from.c - c : (from.top - top) * k);
     }
 };
 
-// The softmax statistics of one row, by the whole CTA; every thread returns them.
-template <int DT>
-__device__ __forceinline__ Softmax row_softmax(const void *row, int64_t n, float k) {
-    using E = Elem<DT>;
-    using T = typename E::T;
-    const T *x = static_cast<const T *>(row);
-    const RowSpan sp = row_span<DT>(row, n);
-    Softmax acc;
-    const int t = threadIdx.x, nt = blockDim.x;
-    if (t < sp.head && fa_in_bounds(t, 1, n)) {
-        const float v = E::widen(x[t]);
-        acc.add<1>(&v, k);
-    }
-    const uint4 *q = reinterpret_cast<const uint4 *>(x + sp.head);
-    int64_t i = t;
-    for (; i + (kBatch - 1) * nt < sp.nvec; i += kBatch * nt) {
-        uint4 r[kBatch];
+// The running maximum and the sum of 2^(k (x - top)) over the elements a warp has seen: the
+// maximum is the warp's, so that it rises for all lanes at once (and seldom: after the
+// first vectors, once in n times for n times the elements); each lane has its own sum, in
+// two interleaved parts.  Every lane of the warp calls add.
+struct Softmax {
+    Exponent e;
+    uint64_t sum;
+
+    __device__ __forceinline__ explicit Softmax(const LogitsArgs &a)
+        : e(a, -INFINITY), sum(pair(0.f, 0.f)) {}
+
+    __device__ __forceinline__ void raise(float best) {
+        if (!__any_sync(0xffffffffu, best > e.top)) return;
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) r[j] = __ldg(q + i + j * nt);
-        float v[kBatch * E::kVec];
+        for (int o = 16; o > 0; o >>= 1)
+            best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+        const Exponent from = e;
+        e.set(best);
+        // a sum of nothing but -inf so far is 0, or NaN, and stays
+        const float f = from.top == -INFINITY ? 1.f : e.rebase(from);
+        sum = mul2(sum, pair(f, f));
+    }
+    // One element, where no FMA can take it: k top is not finite, or nothing but -inf and NaN
+    // has been seen.
+    __device__ __forceinline__ float slow(float x) const {
+        return e.top == -INFINITY ? (isnan(x) ? x : 0.f) : e(x);
+    }
+    // A scalar per lane (-inf: none).
+    __device__ __forceinline__ void add1(float x) {
+        raise(x);
+        sum = add2(sum, pair(slow(x), 0.f));
+    }
+    template <int DT>
+    static __device__ __noinline__ float add_slow(Softmax s, uint4 r) {
+        float x[Elem<DT>::kVec], y = 0.f;
+        Elem<DT>::unpack(r, x);
+#pragma unroll 1
+        for (int j = 0; j < Elem<DT>::kVec; ++j) y += s.slow(x[j]);
+        return y;
+    }
+    template <int DT, int N>
+    __device__ __forceinline__ void add(const uint4 *r) {
+        constexpr int V = Elem<DT>::kVec;
+        raise(Elem<DT>::template largest<N>(r));
+        if (e.fine) {
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) E::unpack(r[j], v + j * E::kVec);
-        acc.add<kBatch * E::kVec>(v, k);
-    }
-    for (; i < sp.nvec; i += nt) {
-        float v[E::kVec];
-        E::unpack(__ldg(q + i), v);
-        acc.add<E::kVec>(v, k);
-    }
-    const int64_t tail = sp.head + sp.nvec * E::kVec + t;
-    if (tail < n && fa_in_bounds(tail, 1, n)) {
-        const float v = E::widen(x[tail]);
-        acc.add<1>(&v, k);
-    }
-    // lanes, then warps
+            for (int i = 0; i < N; ++i) {
+                float x[V];
+                Elem<DT>::unpack(r[i], x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Softmax other;
-        other.top = __shfl_xor_sync(0xffffffffu, acc.top, o);
-        other.s = __shfl_xor_sync(0xffffffffu, acc.s, o);
-        acc.merge(other, k);
+                for (int j = 0; j < V; j += 2) {
+                    float lo, hi;
+                    unpair(e.log2_of(pair(x[j], x[j + 1])), lo, hi);
+                    sum = add2(sum, pair(exp2_fast(lo), exp2_fast(hi)));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) sum = add2(sum, pair(add_slow<DT>(*this, r[i]), 0.f));
+        }
     }
-    __shared__ Softmax part[32];
-    const int warps = nt / 32;
-    __syncthreads();  // part may still be read for the row before
-    if ((t & 31) == 0) part[t / 32] = acc;
+};
+
+// What a row comes to: the largest logit and the sum of 2^(k (x - top)).
+struct RowSum {
+    float top, s;
+
+    // The sum relative to a larger maximum.
+    __device__ __forceinline__ float at(const Exponent &e) const {
+        if (top == e.top || top == -INFINITY) return s;  // (0 or NaN of nothing)
+        Exponent from = e;
+        from.set(top);
+        return s * e.rebase(from);
+    }
+};
+
+// Merges what the warps of the CTAs of a cluster hold of a row; every thread returns the
+// row's.  The maximum first, so that a part is rebased once.  ``part``: shared, [warps];
+// ``whole``: shared, one per CTA.
+__device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, RowSum *whole,
+                                            unsigned split) {
+    const int warps = blockDim.x / 32, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const auto warp_total = [](float s) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
+    };
+    float lo, hi;
+    unpair(acc.sum, lo, hi);
+    const float s = warp_total(lo + hi);
+    if (lane == 0) part[warp] = RowSum{acc.e.top, s};
     __syncthreads();
-    acc = part[0];
-    for (int w = 1; w < warps; ++w) acc.merge(part[w], k);
-    if (acc.top == -INFINITY) acc.s = NAN;  // no finite logit
-    return acc;
+    // every warp adds the warps' parts alike
+    RowSum w = lane < warps ? part[lane] : RowSum{-INFINITY, 0.f};
+    Exponent e = acc.e;
+    float top = w.top;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    e.set(top);
+    RowSum row{top, warp_total(w.at(e))};
+    if (split > 1) {
+        cg::cluster_group cluster = cg::this_cluster();
+        if (threadIdx.x == 0) *whole = row;
+        cluster.sync();
+        w = lane < static_cast<int>(split) ? *cluster.map_shared_rank(whole, lane)
+                                           : RowSum{-INFINITY, 0.f};
+        cluster.sync();  // no CTA leaves while another reads its part
+        top = w.top;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        e.set(top);
+        row = RowSum{top, warp_total(w.at(e))};
+    }
+    if (row.top == -INFINITY) row.s = NAN;  // no finite logit
+    return row;
 }
 
 // logp of the label from its logit and the row's statistics: the exponent is the one the
-// sum's terms have, so that the rounding of k top cancels.
-__device__ __forceinline__ float label_logp(float x, const Softmax &r, const LogitsArgs &a) {
+// sum's terms have.
+__device__ __forceinline__ float label_logp(float x, const RowSum &r, const LogitsArgs &a) {
     constexpr float kLn2 = 0.693147180559945309f;
-    const float ktop = a.k * r.top;
-    const float d = isfinite(ktop) ? fmaf(x, a.k, -ktop) * kLn2 : (x - r.top) * a.scale;
-    return d - logf(r.s);
+    const Exponent e(a, r.top);
+    return (e.fine ? e.log2_of(x) * kLn2 : (x - r.top) * a.scale) - logf(r.s);
 }
 
 template <int IT>
@@ -149,97 +208,203 @@ __device__ __forceinline__ bool load_label(const LogitsArgs &x, int64_t t, int64
     return *label >= 0 && *label < x.vocab;
 }
 
-// dlogits of one row: c (1[v = label] - 2^(k (x - top)) / s), by the whole CTA.  The
-// output may be the row itself: every element is read before it is written, by the
-// thread that writes it.
+// The part of a row's vectors that CTA ``rank`` of ``split`` takes.
+struct RowPart {
+    int64_t begin, nvec;
+    int count;
+
+    __device__ __forceinline__ RowPart(const RowSpan &sp, unsigned rank, unsigned split)
+        : nvec(sp.nvec) {
+        const int64_t each = (nvec + split - 1) / split;
+        begin = min(nvec, each * rank);
+        count = static_cast<int>(min(each, nvec - begin));
+    }
+    __device__ __forceinline__ bool in_bounds(int i) const {
+        return fa_in_bounds(begin + i, 1, nvec);
+    }
+};
+
+// The scalars of a row outside its vectors: the head by the first CTA, the tail by the last.
+template <typename F>
+__device__ __forceinline__ void row_ends(const RowSpan &sp, int64_t n, unsigned rank,
+                                         unsigned split, F f) {
+    const int t = threadIdx.x;
+    if (rank == 0 && t < sp.head && fa_in_bounds(t, 1, n)) f(static_cast<int64_t>(t));
+    if (rank == split - 1 && t < n - sp.tail && fa_in_bounds(sp.tail + t, 1, n)) f(sp.tail + t);
+}
+
+// One vector of the gradient: c (1[v = label] - 2^(k (x - top)) / s); at = the label's place in
+// the vector (outside [0, kVec): none).
 template <int DT>
-__device__ __forceinline__ void row_gradient(const void *row, void *out, int64_t n, float k,
-                                             Softmax r, float c, int64_t label, int t, int nt) {
+__device__ __forceinline__ uint4 gradient_vector(const uint4 &r, const Exponent &e, float w,
+                                                 float c, int at) {
+    constexpr int V = Elem<DT>::kVec;
+    float x[V];
+    Elem<DT>::unpack(r, x);
+    if (e.fine) {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            float lo, hi;
+            unpair(e.log2_of(pair(x[j], x[j + 1])), lo, hi);
+            unpair(mul2(pair(exp2_fast(lo), exp2_fast(hi)), pair(w, w)), x[j], x[j + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = e(x[j]) * w;
+    }
+    if (static_cast<unsigned>(at) < V) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (at == j) x[j] += c;
+    }
+    return Elem<DT>::pack(x);
+}
+
+// dlogits of (a part of) one row from global memory.  The output may be the row itself:
+// every element is read before it is written, by the thread that writes it.
+template <int DT>
+__device__ __forceinline__ void row_gradient(const void *row, void *out, int64_t n,
+                                             const LogitsArgs &a, RowSum r, float c,
+                                             int64_t label, unsigned rank, unsigned split) {
     using E = Elem<DT>;
     using T = typename E::T;
     const T *x = static_cast<const T *>(row);
     T *y = static_cast<T *>(out);
-    const float ktop = k * r.top, w = -c / r.s;
+    const Exponent e(a, r.top);
+    const float w = -c / r.s;
     const auto one = [&](int64_t i) {
-        if (!fa_in_bounds(i, 1, n)) return;
-        const float p = Softmax::term(E::widen(x[i]), r.top, k, ktop) * w;
+        const float p = e(E::widen(x[i])) * w;
         y[i] = E::round(i == label ? p + c : p);
     };
-    RowSpan sp = row_span<DT>(row, n);
     if ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) {
-        for (int64_t i = t; i < n; i += nt) one(i);  // the two are not co-aligned
+        // not co-aligned: element by element
+        for (int64_t i = rank * blockDim.x + threadIdx.x; i < n; i += split * blockDim.x)
+            if (fa_in_bounds(i, 1, n)) one(i);
         return;
     }
-    if (t < sp.head) one(t);
-    const uint4 *q = reinterpret_cast<const uint4 *>(x + sp.head);
-    uint4 *o = reinterpret_cast<uint4 *>(y + sp.head);
-    for (int64_t i = t; i < sp.nvec; i += nt) {
-        float v[E::kVec];
-        E::unpack(q[i], v);
+    const RowSpan sp = row_span<DT>(row, n);
+    row_ends(sp, n, rank, split, one);
+    const RowPart part(sp, rank, split);
+    const uint4 *q = reinterpret_cast<const uint4 *>(x + sp.head) + part.begin;
+    uint4 *o = reinterpret_cast<uint4 *>(y + sp.head) + part.begin;
+    const int at = static_cast<int>(label - sp.head - part.begin * E::kVec), nt = blockDim.x;
+    for (int i = threadIdx.x; i < part.count; i += kBatch * nt) {
+        uint4 v[kBatch];
 #pragma unroll
-        for (int j = 0; j < E::kVec; ++j) v[j] = Softmax::term(v[j], r.top, k, ktop) * w;
-        const int64_t at = label - sp.head - i * E::kVec;
+        for (int j = 0; j < kBatch; ++j)
+            if (i + j * nt < part.count && part.in_bounds(i + j * nt)) v[j] = __ldcs(q + i + j * nt);
 #pragma unroll
-        for (int j = 0; j < E::kVec; ++j)
-            if (at == j) v[j] += c;
-        __stcs(o + i, E::pack(v));
+        for (int j = 0; j < kBatch; ++j)
+            if (i + j * nt < part.count && part.in_bounds(i + j * nt))
+                __stcs(o + i + j * nt,
+                       gradient_vector<DT>(v[j], e, w, c, at - (i + j * nt) * E::kVec));
     }
-    const int64_t tail = sp.head + sp.nvec * E::kVec + t;
-    if (tail < n) one(tail);
 }
 
-// Zeros for the row of a token that is not counted.
+// Zeros for (a part of) the row of a token that is not counted.
 template <int DT>
-__device__ __forceinline__ void row_zeros(void *out, int64_t n, int t, int nt) {
+__device__ __forceinline__ void row_zeros(void *out, int64_t n, unsigned rank, unsigned split) {
     using E = Elem<DT>;
     using T = typename E::T;
     T *y = static_cast<T *>(out);
     const RowSpan sp = row_span<DT>(out, n);
-    if (t < sp.head && fa_in_bounds(t, 1, n)) y[t] = E::round(0.f);
-    uint4 *o = reinterpret_cast<uint4 *>(y + sp.head);
-    for (int64_t i = t; i < sp.nvec; i += nt) __stcs(o + i, make_uint4(0u, 0u, 0u, 0u));
-    const int64_t tail = sp.head + sp.nvec * E::kVec + t;
-    if (tail < n && fa_in_bounds(tail, 1, n)) y[tail] = E::round(0.f);
+    row_ends(sp, n, rank, split, [&](int64_t i) { y[i] = E::round(0.f); });
+    const RowPart part(sp, rank, split);
+    uint4 *o = reinterpret_cast<uint4 *>(y + sp.head) + part.begin;
+    for (int i = threadIdx.x; i < part.count; i += blockDim.x)
+        if (part.in_bounds(i)) __stcs(o + i, make_uint4(0u, 0u, 0u, 0u));
+}
+
+// The scalars of a row into its sum: warp 0 of the first CTA has the head, of the last the
+// tail (both are shorter than a warp).
+template <int DT>
+__device__ __forceinline__ void add_ends(Softmax &acc, const void *row, const RowSpan &sp,
+                                         int64_t n, unsigned rank, unsigned split) {
+    if (threadIdx.x >= 32 || sp.nvec * Elem<DT>::kVec == n) return;
+    const typename Elem<DT>::T *x = static_cast<const typename Elem<DT>::T *>(row);
+    float head = -INFINITY, tail = -INFINITY;
+    row_ends(sp, n, rank, split, [&](int64_t i) {
+        (i < sp.head ? head : tail) = Elem<DT>::widen(x[i]);
+    });
+    acc.add1(head);
+    acc.add1(tail);
+}
+
+// -inf in every element of a vector: what a lane without one adds.
+template <int DT>
+__device__ __forceinline__ uint4 no_vector() {
+    constexpr uint32_t w = DT == FA_F32 ? 0xff800000u : DT == FA_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+    return make_uint4(w, w, w, w);
+}
+
+// The softmax statistics of a row by the CTAs of a cluster, read from global memory.
+template <int DT>
+__device__ __forceinline__ RowSum row_softmax(const void *row, const LogitsArgs &a, unsigned rank,
+                                              unsigned split) {
+    using T = typename Elem<DT>::T;
+    __shared__ RowSum parts[kRowThreads / 32], whole;
+    const RowSpan sp = row_span<DT>(row, a.vocab);
+    Softmax acc(a);
+    add_ends<DT>(acc, row, sp, a.vocab, rank, split);
+    const RowPart part(sp, rank, split);
+    const uint4 *q =
+        reinterpret_cast<const uint4 *>(static_cast<const T *>(row) + sp.head) + part.begin;
+    const int nt = blockDim.x;
+    // whole warps: a lane past the end adds -inf
+    for (int i0 = threadIdx.x & ~31; i0 < part.count; i0 += kBatch * nt) {
+        const int i = i0 + (threadIdx.x & 31);
+        uint4 r[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            r[j] = i + j * nt < part.count && part.in_bounds(i + j * nt) ? __ldg(q + i + j * nt)
+                                                                         : no_vector<DT>();
+        acc.add<DT, kBatch>(r);
+    }
+    return merge_row(acc, parts, &whole, split);
 }
 
 template <int DT, int IT>
 __global__ void __launch_bounds__(kRowThreads)
-token_logprobs_kernel(LogitsArgs x, float *logp, float *lse) {
+token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split) {
     using T = typename Elem<DT>::T;
-    const int64_t t = blockIdx.x;
+    fa_allow_dependents();
+    const unsigned rank = blockIdx.x % split;
+    const int64_t t = blockIdx.x / split;
     int64_t label;
     if (!load_label<IT>(x, t, &label)) {
-        if (threadIdx.x == 0) {
+        if (rank == 0 && threadIdx.x == 0) {
             logp[t] = 0.f;
             if (lse) reinterpret_cast<float2 *>(lse)[t] = make_float2(0.f, 1.f);
         }
         return;
     }
     const T *row = static_cast<const T *>(x.logits) + t * x.ld;
-    const Softmax r = row_softmax<DT>(row, x.vocab, x.k);
-    if (threadIdx.x == 0) {
+    const RowSum r = row_softmax<DT>(row, x, rank, split);
+    if (rank == 0 && threadIdx.x == 0) {
         logp[t] = label_logp(Elem<DT>::widen(row[label]), r, x);
         if (lse) reinterpret_cast<float2 *>(lse)[t] = make_float2(r.top, r.s);
     }
 }
 
+// Rows are taken from the last to the first: the pass that made the statistics left the
+// last rows in L2.
 template <int DT, int IT>
-__global__ void __launch_bounds__(kRowThreads) logprob_gradient_kernel(LogitGradArgs a) {
+__global__ void __launch_bounds__(kRowThreads)
+logprob_gradient_kernel(LogitGradArgs a, unsigned split) {
     using T = typename Elem<DT>::T;
-    const int64_t t = blockIdx.x;
+    const unsigned rank = blockIdx.x % split;
+    const int64_t t = a.x.tokens - 1 - blockIdx.x / split;
     T *out = static_cast<T *>(a.dlogits) + t * a.dlogits_ld;
     int64_t label;
     if (!load_label<IT>(a.x, t, &label)) {
-        row_zeros<DT>(out, a.x.vocab, threadIdx.x, kRowThreads);
+        row_zeros<DT>(out, a.x.vocab, rank, split);
         return;
     }
     const T *row = static_cast<const T *>(a.x.logits) + t * a.x.ld;
     const float2 l = reinterpret_cast<const float2 *>(a.lse)[t];
-    Softmax r;
-    r.top = l.x;
-    r.s = l.y;
+    const RowSum r{l.x, l.y};
     const float c = a.dlogp[t] * a.factor * (a.grad_loss ? *a.grad_loss : 1.f);
-    row_gradient<DT>(row, out, a.x.vocab, a.x.k, r, c, label, threadIdx.x, kRowThreads);
+    row_gradient<DT>(row, out, a.x.vocab, a.x, r, c, label, rank, split);
 }
 
 // ---- preference loss ------------------------------------------------------------
@@ -267,6 +432,7 @@ __device__ __forceinline__ float softplus(float z) {
 // its tokens.  Tokens of no sequence are zeroed by the first and the last pair's CTA.
 template <int IT>
 __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(PreferenceArgs a) {
+    fa_grid_dependency_wait();
     fa_allow_dependents();
     const int64_t pair = blockIdx.x;
     const auto clamped = [&](int64_t j) {
@@ -347,22 +513,29 @@ __device__ __forceinline__ float kl_term(float d) {
     return expm1f(d) - d;
 }
 
+// A token's inputs, and what its log-probability makes of them.
 struct PolicyToken {
+    float old_logp, adv, ref_logp, weight;
+
+    __device__ __forceinline__ PolicyToken(const PolicyArgs &a, int64_t t)
+        : old_logp(a.old_logp[t]), adv(a.advantages[t]), ref_logp(a.ref_logp ? a.ref_logp[t] : 0.f),
+          weight(a.weights ? a.weights[t] : 1.f) {}
+};
+struct PolicyTerms {
     float loss, kl, dlogp;  // dlogp: d loss / d logp
     bool clipped;
 };
-__device__ __forceinline__ PolicyToken policy_token(const PolicyArgs &a, int64_t t, float logp) {
-    const float r = expf(logp - a.old_logp[t]), adv = a.advantages[t];
-    const float free = r * adv, held = fminf(fmaxf(r, a.clip_lo), a.clip_hi) * adv;
-    PolicyToken o;
+__device__ __forceinline__ PolicyTerms policy_terms(const PolicyArgs &a, const PolicyToken &in,
+                                                    float logp) {
+    const float r = expf(logp - in.old_logp);
+    const float free = r * in.adv, held = fminf(fmaxf(r, a.clip_lo), a.clip_hi) * in.adv;
+    PolicyTerms o;
     o.clipped = free > held;
+    o.loss = o.clipped ? -held : -free;  // a NaN ratio is not clipped, and stays
+    o.dlogp = o.clipped ? 0.f : -free;
     o.kl = 0.f;
-    o.dlogp = free <= held ? -free : 0.f;
-    // a NaN ratio stays one (fminf would drop it)
-    o.loss = isnan(free) ? free : o.clipped ? -held : -free;
-    if (isnan(free)) o.dlogp = free;
     if (a.ref_logp) {
-        const float d = a.ref_logp[t] - logp;
+        const float d = in.ref_logp - logp;
         o.kl = kl_term(d);
         if (a.kl_coef != 0.f) {
             o.loss = fmaf(a.kl_coef, o.kl, o.loss);
@@ -372,82 +545,193 @@ __device__ __forceinline__ PolicyToken policy_token(const PolicyArgs &a, int64_t
     return o;
 }
 
-// summary[3] = the number of counted tokens.
+// Counted tokens among the labels, by the whole CTA; every thread returns their number.
 template <int IT>
-__global__ void __launch_bounds__(kSummaryThreads) policy_count_kernel(PolicyArgs a) {
-    fa_allow_dependents();
+__device__ __forceinline__ int count_labels(const LogitsArgs &x) {
+    __shared__ int total[32];
     int n = 0;
-    for (int64_t t = threadIdx.x; t < a.x.tokens; t += kSummaryThreads) {
+    for (int64_t t = threadIdx.x; t < x.tokens; t += blockDim.x) {
         int64_t label;
-        n += load_label<IT>(a.x, t, &label);
+        n += load_label<IT>(x, t, &label);
     }
-    __shared__ int total[kSummaryThreads / 32];
     n = __reduce_add_sync(0xffffffffu, n);
     if ((threadIdx.x & 31) == 0) total[threadIdx.x / 32] = n;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kSummaryThreads / 32; ++w) n += total[w];
-        a.summary[3] = static_cast<float>(n);
-    }
+    n = 0;
+    for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) n += total[w];
+    return n;
 }
 
-template <int DT, int IT>
-__global__ void __launch_bounds__(kRowThreads) policy_row_kernel(PolicyArgs a) {
-    using T = typename Elem<DT>::T;
-    const int64_t t = blockIdx.x;
+// summary[3] = the number of counted tokens, for the rows' kernel.
+template <int IT>
+__global__ void __launch_bounds__(kSummaryThreads) policy_count_kernel(PolicyArgs a) {
+    fa_allow_dependents();
+    const int n = count_labels<IT>(a.x);
+    if (threadIdx.x == 0) a.summary[3] = static_cast<float>(n);
+}
+
+// Where the rows' kernel has the divisor of a loss without a denominator from.
+enum Divisor { kGiven, kFromKernel, kCountHere };
+
+// One row by a cluster of ``split`` CTAs.  HELD > 0: each CTA's part of the row, at most
+// 4 * HELD vectors a thread, is copied to shared memory once, in four groups so that the
+// sum begins when the first has come, and the gradient is made from there: one read and
+// one write of the logits.  HELD == 0 (rows wider than a cluster holds): the gradient
+// reads the row again.
+template <int DT, int IT, int HELD>
+__global__ void __launch_bounds__(kRowThreads)
+policy_row_kernel(PolicyArgs a, unsigned split, Divisor divisor) {
+    using E = Elem<DT>;
+    using T = typename E::T;
+    extern __shared__ uint4 slot[];  // [4 * HELD][kRowThreads]
+    __shared__ RowSum parts[kRowThreads / 32], whole;
+    __shared__ float coef;
+    const unsigned rank = blockIdx.x % split;
+    const int64_t t = blockIdx.x / split, n = a.x.vocab;
+    const int tid = threadIdx.x;
     T *out = a.dlogits ? static_cast<T *>(a.dlogits) + t * a.dlogits_ld : nullptr;
-    fa_grid_dependency_wait();
+    // Nothing here but summary[3] comes from the counting kernel, which began after all
+    // earlier work of the stream had ended: only its reader waits for it.
     fa_allow_dependents();
     int64_t label;
     if (!load_label<IT>(a.x, t, &label)) {
-        if (threadIdx.x == 0) {
+        if (rank == 0 && tid == 0) {
             a.logp[t] = 0.f;
             a.token_loss[t] = 0.f;
             a.token_kl[t] = 0.f;
         }
-        if (out) row_zeros<DT>(out, a.x.vocab, threadIdx.x, kRowThreads);
+        if (out) row_zeros<DT>(out, n, rank, split);
+        if (divisor == kFromKernel) fa_grid_dependency_wait();
         return;
     }
     const T *row = static_cast<const T *>(a.x.logits) + t * a.x.ld;
-    const Softmax r = row_softmax<DT>(row, a.x.vocab, a.x.k);
-    __shared__ float coef;
-    if (threadIdx.x == 0) {
-        const float logp = label_logp(Elem<DT>::widen(row[label]), r, a.x);
-        const PolicyToken o = policy_token(a, t, logp);
-        a.logp[t] = logp;
-        a.token_loss[t] = o.loss;
-        a.token_kl[t] = o.kl;
-        const float denom = a.denominator != 0.f ? a.denominator : a.summary[3];
-        const float w = (a.weights ? a.weights[t] : 1.f) / denom;
-        coef = o.dlogp * w * a.grad_factor;
+    const RowSpan sp = row_span<DT>(row, n);
+    const RowPart part(sp, rank, split);  // HELD: at most 4 * HELD * kRowThreads vectors
+    const uint4 *q = reinterpret_cast<const uint4 *>(row + sp.head) + part.begin;
+    if (HELD > 0) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+#pragma unroll
+            for (int j = 0; j < HELD; ++j) {
+                const int i = (g * HELD + j) * kRowThreads + tid;
+                if (i < part.count && part.in_bounds(i)) copy_async16(slot + i, q + i);
+            }
+            copy_async_commit();
+        }
+    }
+    // what one thread needs of the token, asked for before the sum
+    const bool first = tid == 0;
+    const PolicyToken in(a, first ? t : 0);
+    const float label_logit = first ? E::widen(row[label]) : 0.f;
+    float denom = a.denominator;
+    if (divisor == kCountHere) denom = static_cast<float>(count_labels<IT>(a.x));
+
+    RowSum r;
+    if constexpr (HELD > 0) {
+        Softmax acc(a.x);
+        add_ends<DT>(acc, row, sp, n, rank, split);
+        const auto group = [&](int g) {
+            const int i0 = g * HELD * kRowThreads + tid;
+            if ((i0 & ~31) >= part.count) return;
+            uint4 v[HELD];
+#pragma unroll
+            for (int j = 0; j < HELD; ++j)
+                v[j] = i0 + j * kRowThreads < part.count ? slot[i0 + j * kRowThreads]
+                                                         : no_vector<DT>();
+            acc.add<DT, HELD>(v);
+        };
+        copy_async_wait<3>();
+        group(0);
+        copy_async_wait<2>();
+        group(1);
+        copy_async_wait<1>();
+        group(2);
+        copy_async_wait<0>();
+        group(3);
+        r = merge_row(acc, parts, &whole, split);
+    } else {
+        r = row_softmax<DT>(row, a.x, rank, split);
+    }
+    if (first) {
+        const float logp = label_logp(label_logit, r, a.x);
+        const PolicyTerms o = policy_terms(a, in, logp);
+        if (rank == 0) {
+            a.logp[t] = logp;
+            a.token_loss[t] = o.loss;
+            a.token_kl[t] = o.kl;
+        }
+        if (divisor == kFromKernel) {
+            fa_grid_dependency_wait();
+            denom = a.summary[3];
+        }
+        coef = o.dlogp * (in.weight / denom) * a.grad_factor;
     }
     if (!out) return;
     __syncthreads();
-    row_gradient<DT>(row, out, a.x.vocab, a.x.k, r, coef, label, threadIdx.x, kRowThreads);
+    if constexpr (HELD > 0) {
+        if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
+            const Exponent e(a.x, r.top);
+            const float c = coef, w = -c / r.s;
+            row_ends(sp, n, rank, split, [&](int64_t i) {
+                const float p = e(E::widen(row[i])) * w;
+                out[i] = E::round(i == label ? p + c : p);
+            });
+            uint4 *o = reinterpret_cast<uint4 *>(out + sp.head) + part.begin;
+            const int at = static_cast<int>(label - sp.head - part.begin * E::kVec);
+#pragma unroll 4
+            for (int i = tid; i < part.count; i += kRowThreads)
+                if (part.in_bounds(i))
+                    __stcs(o + i, gradient_vector<DT>(slot[i], e, w, c, at - i * E::kVec));
+            return;
+        }
+    }
+    row_gradient<DT>(row, out, n, a.x, r, coef, label, rank, split);
 }
 
 // The sums over the tokens, by one CTA.
 template <int IT>
 __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyArgs a) {
     fa_grid_dependency_wait();
-    Sum2 loss, kl, clipped;
+    Sum2 loss, kl;
+    int n = 0, clipped = 0;
     for (int64_t t = threadIdx.x; t < a.x.tokens; t += kSummaryThreads) {
         int64_t label;
         if (!load_label<IT>(a.x, t, &label)) continue;
-        loss.add(a.weights ? a.weights[t] * a.token_loss[t] : a.token_loss[t]);
+        const PolicyToken in(a, t);
+        loss.add(in.weight * a.token_loss[t]);
         kl.add(a.token_kl[t]);
-        const float r = expf(a.logp[t] - a.old_logp[t]), adv = a.advantages[t];
-        if (r * adv > fminf(fmaxf(r, a.clip_lo), a.clip_hi) * adv) clipped.add(1.f);
+        // the ratio and the clip as the rows' kernel took them
+        const float r = expf(a.logp[t] - in.old_logp);
+        clipped += r * in.adv > fminf(fmaxf(r, a.clip_lo), a.clip_hi) * in.adv;
+        ++n;
     }
     loss = cta_sum2(loss);
     kl = cta_sum2(kl);
-    clipped = cta_sum2(clipped);
+    __shared__ int counts[2];
+    if (threadIdx.x < 2) counts[threadIdx.x] = 0;
+    __syncthreads();
+    n = __reduce_add_sync(0xffffffffu, n);
+    clipped = __reduce_add_sync(0xffffffffu, clipped);
+    if ((threadIdx.x & 31) == 0) {  // whole numbers: any order
+        atomicAdd(&counts[0], n);
+        atomicAdd(&counts[1], clipped);
+    }
+    __syncthreads();
     if (threadIdx.x == 0) {
-        const float n = a.summary[3], by = fmaxf(n, 1.f);
+        const float all = static_cast<float>(counts[0]), by = fmaxf(all, 1.f);
         a.summary[0] = loss.value() / (a.denominator != 0.f ? a.denominator : by);
         a.summary[1] = kl.value() / by;
-        a.summary[2] = clipped.value() / by;
+        a.summary[2] = static_cast<float>(counts[1]) / by;
+        a.summary[3] = all;
     }
+}
+
+// CTAs a row is split over so that a call of few tokens covers the GPU: doubled while the
+// grid is under two CTAs an SM and each still has ``least`` vectors.
+unsigned split_for(int64_t tokens, int64_t nvec, int64_t least, unsigned at_least) {
+    unsigned s = at_least;
+    while (s < 8 && tokens * s < 2 * 152 && nvec / (2 * s) >= least) s *= 2;
+    return s;
 }
 
 }  // namespace
@@ -469,9 +753,13 @@ cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, fa_itype lt,
                                   float *lse, cudaStream_t stream) {
     return for_dtype(dt, [&](auto d) {
         return for_itype(lt, [&](auto i) {
-            token_logprobs_kernel<d(), i()>
-                <<<static_cast<unsigned>(x.tokens), kRowThreads, 0, stream>>>(x, logp, lse);
-            return cudaGetLastError();
+            const unsigned split =
+                split_for(x.tokens, x.vocab / Elem<d()>::kVec, kBatch * kRowThreads, 1);
+            if (x.tokens * split > kMaxGridX) return cudaErrorInvalidConfiguration;
+            return launch_clusters(token_logprobs_kernel<d(), i()>,
+                                   dim3(static_cast<unsigned>(x.tokens * split)),
+                                   dim3(kRowThreads), 0, split, false, stream, x, logp, lse,
+                                   split);
         });
     });
 }
@@ -480,8 +768,11 @@ cudaError_t launch_token_logprobs_gradient(const LogitGradArgs &a, fa_dtype dt, 
                                            cudaStream_t stream) {
     return for_dtype(dt, [&](auto d) {
         return for_itype(lt, [&](auto i) {
+            const unsigned split = split_for(a.x.tokens, a.x.vocab / Elem<d()>::kVec,
+                                             kBatch * kRowThreads, 1);
+            if (a.x.tokens * split > kMaxGridX) return cudaErrorInvalidConfiguration;
             logprob_gradient_kernel<d(), i()>
-                <<<static_cast<unsigned>(a.x.tokens), kRowThreads, 0, stream>>>(a);
+                <<<static_cast<unsigned>(a.x.tokens * split), kRowThreads, 0, stream>>>(a, split);
             return cudaGetLastError();
         });
     });
@@ -490,25 +781,64 @@ cudaError_t launch_token_logprobs_gradient(const LogitGradArgs &a, fa_dtype dt, 
 cudaError_t launch_preference(const PreferenceArgs &a, fa_itype lt, cudaStream_t stream) {
     return for_itype(lt, [&](auto i) {
         if (a.pairs > 0) {
-            preference_pair_kernel<i()>
-                <<<static_cast<unsigned>(a.pairs), kPairThreads, 0, stream>>>(a);
-            cudaError_t err = cudaGetLastError();
+            cudaError_t err = launch_dependent(preference_pair_kernel<i()>,
+                                               dim3(static_cast<unsigned>(a.pairs)),
+                                               dim3(kPairThreads), 0, stream, a);
             if (err != cudaSuccess) return err;
         }
         return launch_dependent(preference_mean_kernel, dim3(1), dim3(kPairThreads), 0, stream, a);
     });
 }
 
+namespace {
+
+template <int DT, int IT, int HELD>
+cudaError_t launch_policy_rows(const PolicyArgs &a, unsigned split, Divisor divisor,
+                               cudaStream_t stream) {
+    constexpr int kSmem = 4 * HELD * kRowThreads * 16;
+    auto kernel = policy_row_kernel<DT, IT, HELD>;
+    if (kSmem > 48 * 1024) {
+        cudaError_t err =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (err != cudaSuccess) return err;
+    }
+    return launch_clusters(kernel, dim3(static_cast<unsigned>(a.x.tokens * split)),
+                           dim3(kRowThreads), kSmem, split, divisor == kFromKernel, stream, a,
+                           split, divisor);
+}
+
+}  // namespace
+
 cudaError_t launch_policy(const PolicyArgs &a, fa_dtype dt, fa_itype lt, cudaStream_t stream) {
     return for_itype(lt, [&](auto i) {
-        policy_count_kernel<i()><<<1, kSummaryThreads, 0, stream>>>(a);
-        cudaError_t err = cudaGetLastError();
-        if (err != cudaSuccess) return err;
         if (a.x.tokens > 0) {
-            err = for_dtype(dt, [&](auto d) {
-                return launch_dependent(policy_row_kernel<d(), i()>,
-                                        dim3(static_cast<unsigned>(a.x.tokens)),
-                                        dim3(kRowThreads), 0, stream, a);
+            // Every CTA counts the labels itself when they are few (a launch less); else one
+            // kernel does before the rows'.
+            constexpr int64_t kFewLabels = 2048;
+            const bool counts = a.dlogits && a.denominator == 0.f;
+            const Divisor divisor = !counts                     ? kGiven
+                                    : a.x.tokens <= kFewLabels ? kCountHere
+                                                               : kFromKernel;
+            if (divisor == kFromKernel) {
+                policy_count_kernel<i()><<<1, kSummaryThreads, 0, stream>>>(a);
+                cudaError_t err = cudaGetLastError();
+                if (err != cudaSuccess) return err;
+            }
+            cudaError_t err = for_dtype(dt, [&](auto d) {
+                constexpr int64_t kMost = 4 * 4 * kRowThreads;  // vectors a CTA holds
+                const int64_t nvec = a.x.vocab / Elem<d()>::kVec;
+                unsigned split = 1;
+                while (split < 8 && nvec > split * kMost) split *= 2;
+                const bool held = a.dlogits && nvec <= split * kMost;
+                split = split_for(a.x.tokens, nvec, kRowThreads, held || !a.dlogits ? split : 1);
+                if (a.x.tokens * split > kMaxGridX) return cudaErrorInvalidConfiguration;
+                const int64_t each = (nvec + split - 1) / split;
+                if (!held) return launch_policy_rows<d(), i(), 0>(a, split, divisor, stream);
+                if (each <= kMost / 4)
+                    return launch_policy_rows<d(), i(), 1>(a, split, divisor, stream);
+                if (each <= kMost / 2)
+                    return launch_policy_rows<d(), i(), 2>(a, split, divisor, stream);
+                return launch_policy_rows<d(), i(), 4>(a, split, divisor, stream);
             });
             if (err != cudaSuccess) return err;
         }

@@ -20,7 +20,9 @@ using fa::TraceRange;
 using fa::valid_dtype;
 
 constexpr int64_t kMaxCount = 0x7fffffff;        // tokens, ids, rows: the grid's limit
+constexpr int64_t kMaxDim = int64_t(1) << 22;       // of an embedding: the grid's other limit
 constexpr int64_t kMaxElements = int64_t(1) << 56;  // of one matrix: byte offsets stay in 64 bits
+constexpr int64_t kMaxBlocks = int64_t(1) << 28;    // of a checkpoint: 8 lanes each, in one grid
 constexpr double kLog2E = 1.4426950408889634;
 
 bool valid_itype(fa_itype t) { return t == FA_I32 || t == FA_I64; }
@@ -122,6 +124,7 @@ fa::LogitsArgs logits_args(const fa_logits *x) {
     a.ld = x->ld;
     a.scale = static_cast<float>(x->logit_scale);
     a.k = static_cast<float>(x->logit_scale * kLog2E);
+    a.k_lo = static_cast<float>(x->logit_scale * kLog2E - static_cast<double>(a.k));
     return a;
 }
 // dlogits: the logits' type; the logits themselves, or no overlap with them.
@@ -146,6 +149,7 @@ fa_status fa_embedding_lookup(int64_t tokens, const void *ids, fa_itype idt, con
     if (!valid_dtype(tdt) || !valid_dtype(odt) || !valid_itype(idt)) return FA_ERR_DTYPE;
     FA_TRY(check_matrix(vocab, dim, table_ld));
     FA_TRY(check_matrix(tokens, dim, out_ld));
+    if (tokens > kMaxCount || dim > kMaxDim) return FA_ERR_SIZE;
     if (!float_ok(scale)) return FA_ERR_OPTION;
     if (tokens == 0 || dim == 0) return FA_OK;
     int dev;
@@ -175,7 +179,7 @@ fa_status fa_embedding_lookup(int64_t tokens, const void *ids, fa_itype idt, con
 fa_status fa_embedding_scratch(int64_t tokens, int64_t vocab, int64_t dim, int64_t *bytes) {
     if (!bytes) return FA_ERR_NULL;
     if (tokens < 0 || vocab < 0 || dim < 0 || tokens > kMaxCount || vocab >= kMaxCount ||
-        dim > kMaxCount)
+        dim > kMaxDim)
         return FA_ERR_SIZE;
     *bytes = fa::embedding_scratch_layout(tokens, dim).bytes;
     return FA_OK;
@@ -390,7 +394,7 @@ fa_status fa_checkpoint_size(int64_t rows, int64_t cols, int64_t *code_bytes,
     if (!code_bytes || !scale_elements) return FA_ERR_NULL;
     if (rows < 0 || cols < 0 || cols > kMaxElements) return FA_ERR_SIZE;
     const int64_t blocks = (cols + fa::kCheckpointBlock - 1) / fa::kCheckpointBlock;
-    if (rows && blocks * fa::kCheckpointBlock > kMaxElements / rows) return FA_ERR_SIZE;
+    if (rows && blocks > kMaxBlocks / rows) return FA_ERR_SIZE;
     *code_bytes = 2 * rows * blocks * fa::kCheckpointBlock;
     *scale_elements = 2 * rows * blocks;
     return FA_OK;
@@ -436,6 +440,7 @@ fa_status fa_gated_forward(int64_t rows, int64_t cols, const void *gate, int64_t
     a.up_ld = up_ld;
     a.h_ld = h_ld;
     a.blocks = (cols + fa::kCheckpointBlock - 1) / fa::kCheckpointBlock;
+    a.by_blocks = fa::Divider(static_cast<uint32_t>(a.blocks));
     return cuda_status(
         fa::launch_gated_forward(a, dtype, activation, static_cast<cudaStream_t>(stream)));
 }
@@ -482,6 +487,7 @@ fa_status fa_gated_backward(int64_t rows, int64_t cols, const int8_t *codes, con
     a.dup_ld = dup_ld;
     a.h_ld = h_ld;
     a.blocks = (cols + fa::kCheckpointBlock - 1) / fa::kCheckpointBlock;
+    a.by_blocks = fa::Divider(static_cast<uint32_t>(a.blocks));
     return cuda_status(
         fa::launch_gated_backward(a, dtype, activation, static_cast<cudaStream_t>(stream)));
 }

@@ -28,6 +28,17 @@ struct Elem<FA_F32> {
         x[2] = __uint_as_float(r.z);
         x[3] = __uint_as_float(r.w);
     }
+    // Largest element of n vectors, NaN ignored where there is another.
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 *r) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            m = fmaxf(fmaxf(m, __uint_as_float(r[i].x)), __uint_as_float(r[i].y));
+            m = fmaxf(fmaxf(m, __uint_as_float(r[i].z)), __uint_as_float(r[i].w));
+        }
+        return m;
+    }
     static __device__ __forceinline__ uint4 pack(const float *x) {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
                           __float_as_uint(x[3]));
@@ -39,6 +50,14 @@ struct Elem<FA_F16> {
     using T = __half;
     static constexpr int kVec = 8;
     static __device__ __forceinline__ float widen(T x) { return __half2float(x); }
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 *r) {
+        const __half2 *p = reinterpret_cast<const __half2 *>(r);
+        __half2 m = p[0];
+#pragma unroll
+        for (int i = 1; i < 4 * N; ++i) m = __hmax2(m, p[i]);
+        return __half2float(__hmax(__low2half(m), __high2half(m)));
+    }
     static __device__ __forceinline__ T round(float x) { return __float2half_rn(x); }
     static __device__ __forceinline__ void unpack(const uint4 &r, float *x) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -65,6 +84,14 @@ struct Elem<FA_BF16> {
     using T = __nv_bfloat16;
     static constexpr int kVec = 8;
     static __device__ __forceinline__ float widen(T x) { return __bfloat162float(x); }
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 *r) {
+        const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(r);
+        __nv_bfloat162 m = p[0];
+#pragma unroll
+        for (int i = 1; i < 4 * N; ++i) m = __hmax2(m, p[i]);
+        return __bfloat162float(__hmax(__low2bfloat16(m), __high2bfloat16(m)));
+    }
     static __device__ __forceinline__ T round(float x) { return __float2bfloat16_rn(x); }
     static __device__ __forceinline__ void unpack(const uint4 &r, float *x) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -113,10 +140,40 @@ __device__ __forceinline__ void load_n(const typename Elem<DT>::T *p, float *x) 
     }
 }
 
+// The same for rows that others read too (kept in L2).
+template <int DT, int N>
+__device__ __forceinline__ void read_n(const typename Elem<DT>::T *p, float *x) {
+    constexpr int V = Elem<DT>::kVec;
+    if constexpr (N % V == 0) {
+#pragma unroll
+        for (int j = 0; j < N; j += V)
+            Elem<DT>::unpack(__ldg(reinterpret_cast<const uint4 *>(p + j)), x + j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = Elem<DT>::widen(p[j]);
+    }
+}
+
 template <int IT>
 __device__ __forceinline__ int64_t load_id(const void *ids, int64_t i) {
     return IT == FA_I64 ? __ldg(static_cast<const long long *>(ids) + i)
                         : static_cast<int64_t>(__ldg(static_cast<const int *>(ids) + i));
+}
+
+// Asynchronous 16-byte copies from global to shared memory, by the thread that uses them.
+__device__ __forceinline__ void copy_async16(void *shared, const void *global) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(shared))),
+                 "l"(global)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits until at most N of the thread's groups are in flight.
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // 2^x, within 2 ulp; 0 for -inf, inf above the range, NaN for NaN.
@@ -124,6 +181,48 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 2^t for t <= 0 within 1.5 ulp: 2^i times the series of 2^f, |f| <= 1/2 (the term left out
+// is below 6e-9).  For the factors that whole sums are multiplied by, whose error does not
+// average out: six exp2_fast in a row left the log-probabilities 2e-7 off, all the same way.
+__device__ __forceinline__ float exp2_exact(float t) {
+    if (!(t > -126.f)) return t <= -126.f ? 0.f : t;  // NaN stays
+    const float i = rintf(t), f = t - i;
+    float p = 1.5252733804059841e-05f;  // ln(2)^n / n!, n = 7 down to 0
+    p = fmaf(p, f, 1.5403530393381609e-04f);
+    p = fmaf(p, f, 1.3333558146428443e-03f);
+    p = fmaf(p, f, 9.6181291076284772e-03f);
+    p = fmaf(p, f, 5.5504108664821580e-02f);
+    p = fmaf(p, f, 2.4022650695910072e-01f);
+    p = fmaf(p, f, 6.9314718055994531e-01f);
+    p = fmaf(p, f, 1.f);
+    return p * __int_as_float((static_cast<int>(i) + 127) << 23);
+}
+
+// Pairs of FP32 values for the packed instructions (two lanes an instruction).
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 // A sum held as an FP32 value and its FP32 residual; each addition is error-free but

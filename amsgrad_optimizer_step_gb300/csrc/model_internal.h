@@ -14,6 +14,26 @@ namespace fa {
 
 constexpr int kCheckpointBlock = FA_CHECKPOINT_BLOCK;
 
+// Division of a number below 2^31 by a constant: the high word of a product with the
+// divisor's inverse, rounded up, at 31 + ceil(log2 d) fractional bits.
+struct Divider {
+    uint32_t mul = 0, shift = 0;  // mul 0: the divisor is 1
+
+    Divider() = default;
+    explicit Divider(uint32_t d) {
+        if (d < 2) return;
+        uint32_t bits = 1;
+        while (bits < 31 && (uint64_t(1) << bits) < d) ++bits;
+        mul = static_cast<uint32_t>(((uint64_t(1) << (31 + bits)) + d - 1) / d);
+        shift = bits - 1;
+    }
+#if defined(__CUDACC__)
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const {
+        return mul ? __umulhi(n, mul) >> shift : n;
+    }
+#endif
+};
+
 // ---- embedding ---------------------------------------------------------------
 struct LookupArgs {
     const void *ids;
@@ -54,7 +74,7 @@ struct LogitsArgs {
     const void *labels;
     int64_t tokens, vocab, ld;
     float scale;  // logit_scale
-    float k;      // logit_scale * log2(e): exp(scale * x) = 2^(k * x)
+    float k, k_lo;  // logit_scale * log2(e) as an FP32 value and its residual
 };
 cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, fa_itype lt, float *logp,
                                   float *lse, cudaStream_t stream);
@@ -102,6 +122,7 @@ struct GatedForwardArgs {
     int8_t *codes;  // nullptr: no checkpoint
     float *scales;
     int64_t rows, cols, gate_ld, up_ld, h_ld, blocks;
+    Divider by_blocks;
 };
 cudaError_t launch_gated_forward(const GatedForwardArgs &a, fa_dtype dt, fa_activation act,
                                  cudaStream_t stream);
@@ -112,6 +133,7 @@ struct GatedBackwardArgs {
     const void *dh;
     void *dgate, *dup, *h;  // h may be nullptr
     int64_t rows, cols, dh_ld, dgate_ld, dup_ld, h_ld, blocks;
+    Divider by_blocks;
 };
 cudaError_t launch_gated_backward(const GatedBackwardArgs &a, fa_dtype dt, fa_activation act,
                                   cudaStream_t stream);
@@ -121,6 +143,36 @@ cudaError_t launch_gated_backward(const GatedBackwardArgs &a, fa_dtype dt, fa_ac
 cudaError_t embedding_bounds_violations(unsigned long long *count, bool clear);
 cudaError_t logprob_bounds_violations(unsigned long long *count, bool clear);
 cudaError_t gated_bounds_violations(unsigned long long *count, bool clear);
+
+#if defined(__CUDACC__)
+// Launches ``kernel`` in clusters of ``cluster`` CTAs (1: none), as a programmatic
+// dependent of the kernel before it or not.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_clusters(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                                   unsigned cluster, bool dependent, cudaStream_t stream,
+                                   const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    if (dependent) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
 
 // Calls f with the validated type as a compile-time constant.
 template <typename F>

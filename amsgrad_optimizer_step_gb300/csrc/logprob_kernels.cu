@@ -5,11 +5,9 @@
 //   top = max_v x_v,  s = sum_v exp(scale (x_v - top)),
 //   logp = scale (x_label - top) - ln s,
 //   dlogits_v = c (1[v = label] - exp(scale (x_v - top)) / s).
-// exp(scale (x - top)) is 2^(k x - k top), k = scale log2(e) in two FP32 parts: two fused
-// multiply-adds, the first of which cancels exactly.  k top is rounded once for the row,
-// so that every term, and the label's, carries the same rounding; with k in one part the
-// log-probabilities were off by 1.3e-8 of a row's spread, all the same way.  Rows whose
-// k top leaves FP32's range (masks of the type's lowest value) take the difference first.
+// exp(scale (x - top)) is 2^(k d) with d = x - top (exact for 16-bit logits) and k = scale
+// log2(e) in two FP32 parts: k d is rounded once.  With k in one part the log-probabilities
+// were 2e-8 of a row's spread off, all the same way.
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -50,30 +48,25 @@ __host__ __device__ __forceinline__ RowSpan row_span(const void *row, int64_t n)
     return r;
 }
 
-// 2^(k (x - top)) for the elements of a row.
+// 2^(k (x - top)) for the elements of a row.  k_lo > 0, so that -inf stays -inf.
 struct Exponent {
-    float k, k_lo, top, c;  // c = k top, rounded once
-    bool fine;              // c is finite
+    float k, k_lo;
+    float top;  // 0 while nothing but -inf has been seen
 
     __device__ __forceinline__ Exponent(const LogitsArgs &a, float top_) : k(a.k), k_lo(a.k_lo) {
         set(top_);
     }
-    __device__ __forceinline__ void set(float top_) {
-        top = top_;
-        c = fmaf(top, k_lo, top * k);
-        fine = isfinite(c);
-    }
+    __device__ __forceinline__ void set(float top_) { top = top_ == -INFINITY ? 0.f : top_; }
     __device__ __forceinline__ float log2_of(float x) const {
-        return fine ? fmaf(x, k_lo, fmaf(x, k, -c)) : (x - top) * k;
+        const float d = x - top;
+        return fmaf(d, k, d * k_lo);
     }
     __device__ __forceinline__ float operator()(float x) const { return exp2_fast(log2_of(x)); }
-    // Of a pair, where fine.
-    __device__ __forceinline__ uint64_t log2_of(uint64_t x) const {
-        return fma2(x, pair(k_lo, k_lo), fma2(x, pair(k, k), pair(-c, -c)));
-    }
-    // What sums taken relative to ``from`` are multiplied by to be relative to this.
-    __device__ __forceinline__ float rebase(const Exponent &from) const {
-        return exp2_exact(fine && from.fine ? from.c - c : (from.top - top) * k);
+    __device__ __forceinline__ uint64_t of_pair(float x0, float x1) const {
+        const uint64_t d = add2(pair(x0, x1), pair(-top, -top));
+        float lo, hi;
+        unpair(fma2(d, pair(k, k), mul2(d, pair(k_lo, k_lo))), lo, hi);
+        return pair(exp2_fast(lo), exp2_fast(hi));
     }
 };
 
@@ -82,6 +75,7 @@ struct Exponent {
 // first vectors, once in n times for n times the elements); each lane has its own sum, in
 // two interleaved parts.  Every lane of the warp calls add.
 struct Softmax {
+    float top = -INFINITY;
     Exponent e;
     uint64_t sum;
 
@@ -89,54 +83,36 @@ struct Softmax {
         : e(a, -INFINITY), sum(pair(0.f, 0.f)) {}
 
     __device__ __forceinline__ void raise(float best) {
-        if (!__any_sync(0xffffffffu, best > e.top)) return;
+        if (!__any_sync(0xffffffffu, best > top)) return;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-        const Exponent from = e;
         e.set(best);
         // a sum of nothing but -inf so far is 0, or NaN, and stays
-        const float f = from.top == -INFINITY ? 1.f : e.rebase(from);
+        const float f = top == -INFINITY ? 1.f : exp2_exact(e.log2_of(top));
         sum = mul2(sum, pair(f, f));
-    }
-    // One element, where no FMA can take it: k top is not finite, or nothing but -inf and NaN
-    // has been seen.
-    __device__ __forceinline__ float slow(float x) const {
-        return e.top == -INFINITY ? (isnan(x) ? x : 0.f) : e(x);
+        top = best;
     }
     // A scalar per lane (-inf: none).
     __device__ __forceinline__ void add1(float x) {
         raise(x);
-        sum = add2(sum, pair(slow(x), 0.f));
-    }
-    template <int DT>
-    static __device__ __noinline__ float add_slow(Softmax s, uint4 r) {
-        float x[Elem<DT>::kVec], y = 0.f;
-        Elem<DT>::unpack(r, x);
-#pragma unroll 1
-        for (int j = 0; j < Elem<DT>::kVec; ++j) y += s.slow(x[j]);
-        return y;
+        sum = add2(sum, pair(e(x), 0.f));
     }
     template <int DT, int N>
     __device__ __forceinline__ void add(const uint4 *r) {
         constexpr int V = Elem<DT>::kVec;
         raise(Elem<DT>::template largest<N>(r));
-        if (e.fine) {
+        // these vectors' sum first: small terms beside a large one in the running sum would
+        // be rounded off one by one, all the same way
+        uint64_t some = pair(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                float x[V];
-                Elem<DT>::unpack(r[i], x);
+        for (int i = 0; i < N; ++i) {
+            float x[V];
+            Elem<DT>::unpack(r[i], x);
 #pragma unroll
-                for (int j = 0; j < V; j += 2) {
-                    float lo, hi;
-                    unpair(e.log2_of(pair(x[j], x[j + 1])), lo, hi);
-                    sum = add2(sum, pair(exp2_fast(lo), exp2_fast(hi)));
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) sum = add2(sum, pair(add_slow<DT>(*this, r[i]), 0.f));
+            for (int j = 0; j < V; j += 2) some = add2(some, e.of_pair(x[j], x[j + 1]));
         }
+        sum = add2(sum, some);
     }
 };
 
@@ -144,12 +120,9 @@ struct Softmax {
 struct RowSum {
     float top, s;
 
-    // The sum relative to a larger maximum.
+    // The sum relative to a larger maximum, that of e.
     __device__ __forceinline__ float at(const Exponent &e) const {
-        if (top == e.top || top == -INFINITY) return s;  // (0 or NaN of nothing)
-        Exponent from = e;
-        from.set(top);
-        return s * e.rebase(from);
+        return top == -INFINITY || top == e.top ? s : s * exp2_exact(e.log2_of(top));
     }
 };
 
@@ -167,7 +140,7 @@ __device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, Ro
     float lo, hi;
     unpair(acc.sum, lo, hi);
     const float s = warp_total(lo + hi);
-    if (lane == 0) part[warp] = RowSum{acc.e.top, s};
+    if (lane == 0) part[warp] = RowSum{acc.top, s};
     __syncthreads();
     // every warp adds the warps' parts alike
     RowSum w = lane < warps ? part[lane] : RowSum{-INFINITY, 0.f};
@@ -194,12 +167,14 @@ __device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, Ro
     return row;
 }
 
-// logp of the label from its logit and the row's statistics: the exponent is the one the
-// sum's terms have.
-__device__ __forceinline__ float label_logp(float x, const RowSum &r, const LogitsArgs &a) {
-    constexpr float kLn2 = 0.693147180559945309f;
-    const Exponent e(a, r.top);
-    return (e.fine ? e.log2_of(x) * kLn2 : (x - r.top) * a.scale) - logf(r.s);
+// logp of the label from its logit and the row's statistics, rounded once: the product and
+// the difference in two parts each.
+__device__ __forceinline__ float label_logp(float x, const RowSum &r, float scale) {
+    const float d = x - r.top, log_s = logf(r.s);
+    if (!(d > -1e30f)) return d * scale - log_s;  // the parts would not be finite
+    const float p = d * scale, p_lo = fmaf(d, scale, -p);
+    const float y = p - log_s, b = y - p;
+    return y + ((p - (y - b)) - (log_s + b) + p_lo);
 }
 
 template <int IT>
@@ -241,17 +216,9 @@ __device__ __forceinline__ uint4 gradient_vector(const uint4 &r, const Exponent 
     constexpr int V = Elem<DT>::kVec;
     float x[V];
     Elem<DT>::unpack(r, x);
-    if (e.fine) {
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-            float lo, hi;
-            unpair(e.log2_of(pair(x[j], x[j + 1])), lo, hi);
-            unpair(mul2(pair(exp2_fast(lo), exp2_fast(hi)), pair(w, w)), x[j], x[j + 1]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = e(x[j]) * w;
-    }
+    for (int j = 0; j < V; j += 2)
+        unpair(mul2(e.of_pair(x[j], x[j + 1]), pair(w, w)), x[j], x[j + 1]);
     if (static_cast<unsigned>(at) < V) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -381,7 +348,7 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split) {
     const T *row = static_cast<const T *>(x.logits) + t * x.ld;
     const RowSum r = row_softmax<DT>(row, x, rank, split);
     if (rank == 0 && threadIdx.x == 0) {
-        logp[t] = label_logp(Elem<DT>::widen(row[label]), r, x);
+        logp[t] = label_logp(Elem<DT>::widen(row[label]), r, x.scale);
         if (lse) reinterpret_cast<float2 *>(lse)[t] = make_float2(r.top, r.s);
     }
 }
@@ -409,18 +376,20 @@ logprob_gradient_kernel(LogitGradArgs a, unsigned split) {
 
 // ---- preference loss ------------------------------------------------------------
 
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 512;
 
-// Sum of one value a thread over the CTA, as FP32 pairs; every thread returns it.
-__device__ __forceinline__ Sum2 cta_sum2(Sum2 s) {
-    __shared__ Sum2 part[32];
+// Sum of one value a thread over the CTA, as FP32 pairs; every thread returns it.  ``part``:
+// shared, [warps].
+__device__ __forceinline__ Sum2 cta_sum2(Sum2 s, Sum2 *part) {
     s = warp_sum2(s);
-    __syncthreads();
     if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = s;
     __syncthreads();
-    Sum2 total = part[0];
-    for (int w = 1; w < static_cast<int>(blockDim.x) / 32; ++w) total.add(part[w]);
-    return total;
+    s = Sum2();
+    if ((threadIdx.x & 31) < blockDim.x / 32) s = part[threadIdx.x & 31];
+    s = warp_sum2(s);
+    s.hi = __shfl_sync(0xffffffffu, s.hi, 0);
+    s.lo = __shfl_sync(0xffffffffu, s.lo, 0);
+    return s;
 }
 
 // ln(1 + e^z) without overflow.
@@ -428,13 +397,16 @@ __device__ __forceinline__ float softplus(float z) {
     return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z)));
 }
 
-// One CTA per pair: both sequences' sums, the pair's loss and the coefficient of each of
-// its tokens.  Tokens of no sequence are zeroed by the first and the last pair's CTA.
+// One CTA per pair: a half of it for each sequence's sum, the pair's loss and the
+// coefficient of each of its tokens.  Tokens of no sequence are zeroed by the first and the
+// last pair's CTA.
 template <int IT>
 __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(PreferenceArgs a) {
-    fa_grid_dependency_wait();
-    fa_allow_dependents();
+    constexpr int kHalf = kPairThreads / 2, kWarps = kHalf / 32;
+    __shared__ Sum2 part[2][kWarps];
+    __shared__ int counts[2][kWarps];
     const int64_t pair = blockIdx.x;
+    const int q = threadIdx.x / kHalf, tid = threadIdx.x % kHalf, lane = tid & 31;
     const auto clamped = [&](int64_t j) {
         const int64_t o = a.seq_offsets[j];
         return o < 0 ? 0 : o > a.tokens ? a.tokens : o;
@@ -443,21 +415,36 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(Preferenc
         const int64_t label = load_id<IT>(a.labels, t);
         return label >= 0 && label < a.vocab;
     };
-    int64_t lo[2], hi[2];
+    fa_grid_dependency_wait();
+    fa_allow_dependents();
+    const int64_t lo = clamped(2 * pair + q), hi = clamped(2 * pair + q + 1);
+    Sum2 s;
+    int n = 0;
+#pragma unroll 4
+    for (int64_t t = lo + tid; t < hi; t += kHalf)
+        if (counted(t) && fa_in_bounds(t, 1, a.tokens)) {
+            s.add(a.logp[t] - a.ref_logp[t]);
+            ++n;
+        }
+    s = warp_sum2(s);
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) {
+        part[q][tid / 32] = s;
+        counts[q][tid / 32] = n;
+    }
+    __syncthreads();
     float mean[2], per[2];
-    for (int q = 0; q < 2; ++q) {
-        lo[q] = clamped(2 * pair + q);
-        hi[q] = clamped(2 * pair + q + 1);
-        Sum2 s, n;
-        for (int64_t t = lo[q] + threadIdx.x; t < hi[q]; t += kPairThreads)
-            if (counted(t) && fa_in_bounds(t, 1, a.tokens)) {
-                s.add(a.logp[t] - a.ref_logp[t]);
-                n.add(1.f);
-            }
-        s = cta_sum2(s);
-        n = cta_sum2(n);
-        per[q] = a.average ? 1.f / fmaxf(n.value(), 1.f) : 1.f;
-        mean[q] = a.average ? s.value() / fmaxf(n.value(), 1.f) : s.value();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        s = part[h][0];
+        n = counts[h][0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            s.add(part[h][w]);
+            n += counts[h][w];
+        }
+        per[h] = a.average ? 1.f / static_cast<float>(max(n, 1)) : 1.f;
+        mean[h] = a.average ? s.value() / static_cast<float>(max(n, 1)) : s.value();
     }
     const float z = a.beta * (mean[0] - mean[1]);
     const float e = a.smoothing;
@@ -470,23 +457,23 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(Preferenc
         a.rewards[2 * pair] = a.beta * mean[0];
         a.rewards[2 * pair + 1] = a.beta * mean[1];
     }
-    for (int q = 0; q < 2; ++q) {
-        const float c = (q ? -d : d) * per[q];
-        for (int64_t t = lo[q] + threadIdx.x; t < hi[q]; t += kPairThreads)
-            if (fa_in_bounds(t, 1, a.tokens)) a.dlogp[t] = counted(t) ? c : 0.f;
-    }
-    if (pair == 0)
-        for (int64_t t = threadIdx.x; t < lo[0]; t += kPairThreads) a.dlogp[t] = 0.f;
-    if (pair == a.pairs - 1)
-        for (int64_t t = hi[1] + threadIdx.x; t < a.tokens; t += kPairThreads) a.dlogp[t] = 0.f;
+    const float c = q ? -d * per[1] : d * per[0];
+#pragma unroll 4
+    for (int64_t t = lo + tid; t < hi; t += kHalf)
+        if (fa_in_bounds(t, 1, a.tokens)) a.dlogp[t] = counted(t) ? c : 0.f;
+    if (pair == 0 && q == 0)
+        for (int64_t t = tid; t < lo; t += kHalf) a.dlogp[t] = 0.f;
+    if (pair == a.pairs - 1 && q == 1)
+        for (int64_t t = hi + tid; t < a.tokens; t += kHalf) a.dlogp[t] = 0.f;
 }
 
 // The mean over the pairs, by one CTA (no pairs: 0, and no token has a coefficient).
 __global__ void __launch_bounds__(kPairThreads) preference_mean_kernel(PreferenceArgs a) {
+    __shared__ Sum2 part[kPairThreads / 32];
     fa_grid_dependency_wait();
     Sum2 s;
     for (int64_t k = threadIdx.x; k < a.pairs; k += kPairThreads) s.add(a.pair_loss[k]);
-    s = cta_sum2(s);
+    s = cta_sum2(s, part);
     if (threadIdx.x == 0) *a.loss = a.pairs ? s.value() / static_cast<float>(a.pairs) : 0.f;
     if (a.pairs == 0)
         for (int64_t t = threadIdx.x; t < a.tokens; t += kPairThreads) a.dlogp[t] = 0.f;
@@ -653,7 +640,7 @@ policy_row_kernel(PolicyArgs a, unsigned split, Divisor divisor) {
         r = row_softmax<DT>(row, a.x, rank, split);
     }
     if (first) {
-        const float logp = label_logp(label_logit, r, a.x);
+        const float logp = label_logp(label_logit, r, a.x.scale);
         const PolicyTerms o = policy_terms(a, in, logp);
         if (rank == 0) {
             a.logp[t] = logp;
@@ -694,6 +681,7 @@ __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyA
     fa_grid_dependency_wait();
     Sum2 loss, kl;
     int n = 0, clipped = 0;
+#pragma unroll 4
     for (int64_t t = threadIdx.x; t < a.x.tokens; t += kSummaryThreads) {
         int64_t label;
         if (!load_label<IT>(a.x, t, &label)) continue;
@@ -705,11 +693,11 @@ __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyA
         clipped += r * in.adv > fminf(fmaxf(r, a.clip_lo), a.clip_hi) * in.adv;
         ++n;
     }
-    loss = cta_sum2(loss);
-    kl = cta_sum2(kl);
+    __shared__ Sum2 parts[2][kSummaryThreads / 32];
     __shared__ int counts[2];
     if (threadIdx.x < 2) counts[threadIdx.x] = 0;
-    __syncthreads();
+    loss = cta_sum2(loss, parts[0]);
+    kl = cta_sum2(kl, parts[1]);
     n = __reduce_add_sync(0xffffffffu, n);
     clipped = __reduce_add_sync(0xffffffffu, clipped);
     if ((threadIdx.x & 31) == 0) {  // whole numbers: any order

@@ -101,7 +101,8 @@ fa_status check_logits(const fa_logits *x) {
     FA_TRY(check_matrix(x->tokens, x->vocab, x->ld));
     if (x->tokens > kMaxCount || x->vocab > kMaxCount) return FA_ERR_SIZE;
     if (x->tokens > 0 && x->vocab < 1) return FA_ERR_SIZE;
-    if (!(x->logit_scale > 0) || !float_ok(x->logit_scale * kLog2E)) return FA_ERR_OPTION;
+    // (k and its residual are normal FP32 numbers)
+    if (!(x->logit_scale >= 1e-4) || !(x->logit_scale <= 1e4)) return FA_ERR_OPTION;
     return FA_OK;
 }
 // Its device pointers.
@@ -123,8 +124,11 @@ fa::LogitsArgs logits_args(const fa_logits *x) {
     a.vocab = x->vocab;
     a.ld = x->ld;
     a.scale = static_cast<float>(x->logit_scale);
-    a.k = static_cast<float>(x->logit_scale * kLog2E);
-    a.k_lo = static_cast<float>(x->logit_scale * kLog2E - static_cast<double>(a.k));
+    // k rounded down, so that its residual is positive: -inf times either part is -inf
+    const double k = x->logit_scale * kLog2E;
+    a.k = static_cast<float>(k);
+    if (a.k > k) a.k = std::nextafter(a.k, 0.0f);
+    a.k_lo = std::fmax(static_cast<float>(k - a.k), 1e-30f * a.k);
     return a;
 }
 // dlogits: the logits' type; the logits themselves, or no overlap with them.

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -140,7 +141,35 @@ __device__ __forceinline__ void load_n(const typename Elem<DT>::T *p, float *x) 
     }
 }
 
-// The same for rows that others read too (kept in L2).
+// N elements as they lie in memory, to be widened later: half the registers for 16-bit types.
+template <int DT, int N>
+struct Raw {
+    using E = Elem<DT>;
+    static constexpr bool kWhole = N % E::kVec == 0;
+    static constexpr int kWords = kWhole ? N / E::kVec : N;
+    std::conditional_t<kWhole, uint4, typename E::T> r[kWords];
+
+    __device__ __forceinline__ void load(const typename E::T *p) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            if constexpr (kWhole)
+                r[k] = __ldcs(reinterpret_cast<const uint4 *>(p) + k);
+            else
+                r[k] = p[k];
+        }
+    }
+    __device__ __forceinline__ void widen(float *x) const {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            if constexpr (kWhole)
+                E::unpack(r[k], x + k * E::kVec);
+            else
+                x[k] = E::widen(r[k]);
+        }
+    }
+};
+
+// load_n for rows that others read too (kept in L2).
 template <int DT, int N>
 __device__ __forceinline__ void read_n(const typename Elem<DT>::T *p, float *x) {
     constexpr int V = Elem<DT>::kVec;

@@ -47,13 +47,14 @@ cudaError_t launch_embedding_lookup(const LookupArgs &a, fa_itype idt, fa_dtype 
 
 // Scratch of the embedding gradient, in this order (each part 16-byte aligned).
 struct EmbeddingScratch {
-    int64_t chunks;  // runs of kSortChunk tokens that one CTA sorts
+    int64_t chunks;  // runs of kSortChunk tokens that one cluster sorts
     int64_t units;   // runs of kSumUnit sorted tokens that one CTA adds
     int64_t sorted_words;  // 32-bit words of one sorted array (tokens, rounded up to 4)
     int64_t bytes;
 };
-constexpr int kSortChunk = 8192;
-constexpr int kSumUnit = 32;
+constexpr int kSortSlots = 8192;            // tokens in one CTA's shared memory
+constexpr int kSortChunk = 8 * kSortSlots;  // in a cluster's
+constexpr int kSumUnit = 32;                // (a warp's ballot holds one)
 EmbeddingScratch embedding_scratch_layout(int64_t tokens, int64_t dim);
 
 struct EmbeddingGradArgs {

@@ -85,8 +85,8 @@ fa_status fa_embedding_gradient(int64_t tokens, const void *ids, fa_itype idt, c
 /* ---- losses from the logits ---------------------------------------------------- */
 
 /* Logits of a batch of tokens with their labels: row t is a distribution over
- * vocab ids after multiplication by logit_scale (an inverse temperature; finite,
- * > 0).  A label outside [0, vocab) marks a token that is not counted (a prompt,
+ * vocab ids after multiplication by logit_scale (an inverse temperature, from 1e-4
+ * to 1e4).  A label outside [0, vocab) marks a token that is not counted (a prompt,
  * padding): its row is never read, so it may hold anything.  -Inf logits have
  * probability zero; a row with no finite logit, or with a NaN or +Inf, gives NaN. */
 typedef struct fa_logits {
@@ -104,8 +104,7 @@ typedef struct fa_logits {
  * logp[t] = log softmax(logit_scale * logits[t])[labels[t]], FP32 (the pages have
  * no counterpart); 0 for a token that is not counted.  lse (FP32 [tokens][2], may
  * be NULL; 8-byte aligned) receives the row's log-sum-exp in two parts (m, s), as the
- * gradient takes it: logit_scale * m + ln(s), with m the row's largest logit (the
- * product rounded as the library's kernels round it); (0, 1)
+ * gradient takes it: logit_scale * m + ln(s), with m the row's largest logit; (0, 1)
  * for a token that is not counted.  tokens == 0: nothing is launched
  * or checked.  vocab >= 1 else.
  */

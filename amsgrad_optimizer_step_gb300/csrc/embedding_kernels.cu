@@ -7,13 +7,17 @@
 // are distributed.  A run inside one unit is finished there; a run that several units
 // share leaves FP32 partial sums, which the join adds in unit order.
 //
-// Sort: a cluster of up to eight CTAs sorts up to kSortChunk tokens in its shared memory,
+// Sort: a cluster of up to sixteen CTAs sorts up to kSortChunk tokens in its shared memory,
 // least significant digit first: each warp ranks its tokens by digit, the CTAs exchange
-// their digit counts, and every token goes to its place in the cluster, in whichever
-// CTA's memory that is.  A chunk's ids are sorted in two or three such passes with no
-// global memory between them.  With several chunks, a token's place in the whole order is
+// their digit counts, each CTA orders its own by digit, and the runs so made go to their
+// places in the cluster, in whichever CTA's memory that is (sent token by token, each to
+// a place of its own, a pass took 18 us).  A chunk's ids are sorted in two or three such passes with no
+// global memory between them; the rest of the GPU zeroes the table meanwhile, so that only
+// ids that occur are written after.  With several chunks, a token's place in the whole order is
 // its place in its chunk plus, for every other chunk, the number of its ids that come
 // before (ties: earlier chunks come before), found by binary search.
+#include <algorithm>
+
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -84,59 +88,101 @@ lookup_kernel(LookupArgs a, int groups, int lanes_log2) {
 
 // ---- sort ----------------------------------------------------------------------
 
+// Rows of the table that are zeroed while its gradient's tokens are sorted: bytes from p,
+// ld bytes apart.
+struct ZeroArgs {
+    char *p;
+    int64_t rows, bytes, ld;
+};
+
+// The share of CTA ``rank`` of ``ctas``: rows in turn, or stretches of a single row.
+__device__ __forceinline__ void zero_rows(const ZeroArgs &z, int64_t rank, int64_t ctas) {
+    const int64_t parts = z.rows == 1 ? ctas : 1;
+    for (int64_t row = z.rows == 1 ? 0 : rank; row < z.rows; row += z.rows == 1 ? 1 : ctas) {
+        char *p = z.p + row * z.ld;
+        const int64_t past = reinterpret_cast<uintptr_t>(p) & 15;
+        const int64_t head = past ? min(int64_t(16) - past, z.bytes) : 0;
+        const int64_t vecs = (z.bytes - head) / 16, tail = head + vecs * 16;
+        if (parts == 1 || rank == 0) {  // elements are two bytes at least
+            for (int64_t i = 2 * threadIdx.x; i < head; i += 2 * blockDim.x)
+                *reinterpret_cast<uint16_t *>(p + i) = 0;
+            for (int64_t i = tail + 2 * threadIdx.x; i < z.bytes; i += 2 * blockDim.x)
+                *reinterpret_cast<uint16_t *>(p + i) = 0;
+        }
+        uint4 *q = reinterpret_cast<uint4 *>(p + head);
+        const int64_t each = (vecs + parts - 1) / parts;
+        const int64_t begin = parts == 1 ? 0 : rank * each, end = min(vecs, begin + each);
+        for (int64_t i = begin + threadIdx.x; i < end; i += blockDim.x)
+            if (fa_in_bounds(i, 1, vecs)) q[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
 struct SortArgs {
     const void *ids;
     int64_t tokens, vocab, padding_idx;
     uint32_t *keys, *pos;     // the chunks' sorted ids and token indices
     int passes, digit_bits;   // passes * digit_bits bits hold vocab, the key of a token without an id
+    unsigned chunks, ctas;    // clusters that sort, and the CTAs of a cluster
+    ZeroArgs zero;
 };
 
-// Shared memory of a sorting CTA.
+// A token on its way: its id above its index in the chunk.
+template <typename Item>
 struct SortSmem {
-    uint32_t key[kSortSlots];
-    uint16_t place[kSortSlots];                // the token's index in the chunk
-    uint16_t count[kSortWarps][kMostDigits];   // each warp's tokens by digit, then those before it
+    Item item[kSortSlots];
+    Item own[kSortSlots];                      // the CTA's, by digit
+    uint16_t count[kSortWarps][kMostDigits];   // each warp's tokens by digit, then their places
     uint32_t total[kMostDigits];               // the CTA's tokens by digit
-    uint32_t base[kMostDigits];                // where the CTA's first of a digit goes
-    uint32_t warp_total[kSortWarps];
+    int base[kMostDigits];                     // from a place among its own to one in the chunk
+    uint32_t warp_total[2][kSortWarps];
 };
 
-template <int IT>
-__global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a, unsigned ctas) {
+// The first chunks' clusters sort; the CTAs after them zero the table meanwhile.
+template <int IT, typename Item>
+__global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a) {
     fa_allow_dependents();
+    if (blockIdx.x >= a.chunks * a.ctas) {
+        zero_rows(a.zero, blockIdx.x - a.chunks * a.ctas, gridDim.x - a.chunks * a.ctas);
+        return;
+    }
     extern __shared__ uint4 raw[];
-    SortSmem &s = *reinterpret_cast<SortSmem *>(raw);
+    SortSmem<Item> &s = *reinterpret_cast<SortSmem<Item> *>(raw);
     cg::cluster_group cluster = cg::this_cluster();
     const int t = threadIdx.x, lane = t & 31, warp = t / 32;
-    const unsigned rank = blockIdx.x % ctas;
-    const int64_t chunk = static_cast<int64_t>(blockIdx.x / ctas) * kSortChunk;
+    const unsigned rank = blockIdx.x % a.ctas;
+    const int64_t chunk = static_cast<int64_t>(blockIdx.x / a.ctas) * kSortChunk;
     const int64_t left = a.tokens - chunk;
     const int n = left < kSortChunk ? static_cast<int>(left) : kSortChunk;
     const int digits = 1 << a.digit_bits;
     // a thread's items are 32 apart: a warp's are consecutive, taken in rounds
     const int first = warp * 32 * kSortItems + lane;
+    const auto finish = [&](int i, Item x) {  // the i-th of the sorted chunk
+        if (i >= n || !fa_in_bounds(chunk + i, 1, a.tokens)) return;
+        a.keys[chunk + i] = static_cast<uint32_t>(x >> 16);
+        a.pos[chunk + i] = static_cast<uint32_t>(chunk + static_cast<uint16_t>(x));
+    };
 
-    uint32_t key[kSortItems];
-    uint16_t place[kSortItems];
+    Item item[kSortItems];
 #pragma unroll
     for (int j = 0; j < kSortItems; ++j) {
         const int i = static_cast<int>(rank) * kSortSlots + first + 32 * j;
-        key[j] = 0xffffffffu;  // past the end: came last, and stays last
-        place[j] = static_cast<uint16_t>(i);
+        item[j] = ~Item(0);  // past the end: came last, and stays last
         if (i < n && fa_in_bounds(chunk + i, 1, a.tokens)) {
             const int64_t id = load_id<IT>(a.ids, chunk + i);
-            key[j] = id >= 0 && id < a.vocab && id != a.padding_idx ? static_cast<uint32_t>(id)
-                                                                    : static_cast<uint32_t>(a.vocab);
+            const bool known = id >= 0 && id < a.vocab && id != a.padding_idx;
+            item[j] = static_cast<Item>(known ? id : a.vocab) << 16 | static_cast<Item>(i);
         }
     }
     for (int pass = 0; pass < a.passes; ++pass) {
-        const int shift = pass * a.digit_bits;
-        for (int d = lane; d < digits; d += 32) s.count[warp][d] = 0;
+        const int shift = 16 + pass * a.digit_bits;
+        const auto digit = [&](Item x) { return static_cast<int>(x >> shift) & (digits - 1); };
+        for (int d = 2 * lane; d < digits; d += 64)
+            *reinterpret_cast<uint32_t *>(&s.count[warp][d]) = 0u;
         __syncwarp();
         uint16_t before[kSortItems];  // tokens of the digit before this one in the warp
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
-            const uint32_t d = (key[j] >> shift) & (digits - 1);
+            const int d = digit(item[j]);
             const unsigned same = __match_any_sync(0xffffffffu, d);
             const int ahead = __popc(same & ((1u << lane) - 1));
             const uint16_t c = s.count[warp][d];
@@ -146,62 +192,75 @@ __global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a, un
             before[j] = static_cast<uint16_t>(c + ahead);
         }
         __syncthreads();
-        uint32_t mine = 0;
-        if (t < digits) {  // thread d: the warps' counts of digit d
-            uint16_t c[kSortWarps];
+        uint32_t mine = 0;  // thread d: the CTA's tokens of digit d
+        uint16_t c[kSortWarps];
+        if (t < digits) {
 #pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) c[w] = s.count[w][t];
-#pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) {
-                s.count[w][t] = static_cast<uint16_t>(mine);
-                mine += c[w];
-            }
+            for (int w = 0; w < kSortWarps; ++w) mine += c[w] = s.count[w][t];
             s.total[t] = mine;
         }
         cluster.sync();
         uint32_t all = 0, earlier = 0;  // tokens of digit d in the cluster, and in earlier CTAs
         if (t < digits)
-            for (unsigned r = 0; r < ctas; ++r) {
-                const uint32_t c = *cluster.map_shared_rank(&s.total[t], r);
-                all += c;
-                if (r < rank) earlier += c;
+            for (unsigned r = 0; r < a.ctas; ++r) {
+                const uint32_t x = *cluster.map_shared_rank(&s.total[t], r);
+                all += x;
+                if (r < rank) earlier += x;
             }
-        // tokens of smaller digits: a prefix sum over the threads
-        uint32_t upto = all;
+        // tokens of smaller digits, in the cluster and of its own: prefix sums over the threads
+        uint32_t upto = all, own_upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
+            const uint32_t y = __shfl_up_sync(0xffffffffu, own_upto, o);
+            if (lane >= o) {
+                upto += x;
+                own_upto += y;
+            }
         }
-        if (lane == 31) s.warp_total[warp] = upto;
+        if (lane == 31) {
+            s.warp_total[0][warp] = upto;
+            s.warp_total[1][warp] = own_upto;
+        }
         __syncthreads();
         if (t < digits) {
-            for (int w = 0; w < warp; ++w) upto += s.warp_total[w];
-            s.base[t] = upto - all + earlier;
+            for (int w = 0; w < warp; ++w) {
+                upto += s.warp_total[0][w];
+                own_upto += s.warp_total[1][w];
+            }
+            uint32_t own = own_upto - mine;
+            s.base[t] = static_cast<int>(upto - all + earlier) - static_cast<int>(own);
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) {
+                s.count[w][t] = static_cast<uint16_t>(own);
+                own += c[w];
+            }
         }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
-            const uint32_t d = (key[j] >> shift) & (digits - 1);
-            const uint32_t at = s.base[d] + s.count[warp][d] + before[j];  // < ctas * kSortSlots
-            if (!fa_in_bounds(at, 1, static_cast<int64_t>(ctas) * kSortSlots)) continue;
-            const unsigned r = at / kSortSlots, slot = at % kSortSlots;
-            *cluster.map_shared_rank(&s.key[slot], r) = key[j];
-            *cluster.map_shared_rank(&s.place[slot], r) = place[j];
+            const int at = s.count[warp][digit(item[j])] + before[j];
+            if (fa_in_bounds(at, 1, kSortSlots)) s.own[at] = item[j];
         }
-        cluster.sync();
+        __syncthreads();
+        const bool last = pass == a.passes - 1;
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
-            key[j] = s.key[first + 32 * j];
-            place[j] = s.place[first + 32 * j];
+            const int i = t + j * kSortThreads;
+            const Item x = s.own[i];
+            const int at = s.base[digit(x)] + i;  // < ctas * kSortSlots
+            if (!fa_in_bounds(at, 1, static_cast<int64_t>(a.ctas) * kSortSlots)) continue;
+            if (last)
+                finish(at, x);
+            else
+                *cluster.map_shared_rank(&s.item[at % kSortSlots],
+                                         static_cast<unsigned>(at) / kSortSlots) = x;
         }
-    }
+        // the next pass's items have come; after the last, no CTA still reads another's counts
+        cluster.sync();
+        if (last) break;
 #pragma unroll
-    for (int j = 0; j < kSortItems; ++j) {
-        const int i = static_cast<int>(rank) * kSortSlots + first + 32 * j;
-        if (i >= n || !fa_in_bounds(chunk + i, 1, a.tokens)) continue;
-        a.keys[chunk + i] = key[j];
-        a.pos[chunk + i] = static_cast<uint32_t>(chunk + place[j]);
+        for (int j = 0; j < kSortItems; ++j) item[j] = s.item[first + 32 * j];
     }
 }
 
@@ -246,11 +305,13 @@ merge_chunks_kernel(const uint32_t *keys, const uint32_t *pos, uint32_t *out_key
 struct SumArgs {
     EmbeddingGradArgs g;
     const uint32_t *keys, *pos;  // sorted
+    uint32_t *shared;            // [units]: how the unit's runs reach into its neighbours
     float *partial;              // [units][2][dim]
-    int64_t units;               // CTAs that add
-    int64_t zero_ctas;           // CTAs that zero the rows of absent ids, kZeroRows each
+    int64_t units;
 };
-constexpr int kZeroRows = 32;
+// shared[u]: the unit is one run that began before it and goes on after it; it begins a run
+// that goes on.
+constexpr uint32_t kThrough = 1, kBegins = 2;
 
 // Writes ``sum * scale`` to (or adds it to) elements [c, c + N) of table row v.
 template <int TT, int N>
@@ -301,35 +362,9 @@ __device__ __forceinline__ void load_partial(const float *p, float *x) {
     }
 }
 
-// The rows [v0, v0 + kZeroRows) of ids that no token has.
-template <int TT, int N>
-__device__ __forceinline__ void zero_absent(const SumArgs &a, int64_t v0, int64_t c) {
-    const EmbeddingGradArgs &g = a.g;
-    __shared__ bool absent[kZeroRows];
-    if (threadIdx.x < kZeroRows) {
-        const int64_t v = v0 + threadIdx.x;
-        bool none = false;
-        if (v < g.vocab) {
-            const int64_t at = bound(a.keys, g.tokens, static_cast<uint32_t>(v), false);
-            none = at >= g.tokens || a.keys[at] != v;
-        }
-        absent[threadIdx.x] = none;
-    }
-    __syncthreads();
-    if (c >= g.dim || !fa_in_bounds(c, N, g.dim)) return;
-    float zero[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) zero[j] = 0.f;
-    for (int r = 0; r < kZeroRows; ++r)
-        if (absent[r] && fa_in_bounds(v0 + r, 1, g.vocab))
-            store_n<TT, N>(
-                static_cast<typename Elem<TT>::T *>(g.dtable) + (v0 + r) * g.table_ld + c, zero);
-}
-
 // CTA (u, slab): unit u's tokens, columns of slab.  A run that began before the unit
 // leaves its sum in partial[u][0], one that goes on after it in partial[u][1] (a run
-// that does both, in [0]).  The zeroing CTAs lie between the adding ones, so that their
-// searches wait beside loads.
+// that does both, in [0]).
 template <int DT, int TT, bool VEC>
 __global__ void __launch_bounds__(kSumThreads, 4) sum_units_kernel(SumArgs a) {
     constexpr int N = kGroup<DT, TT, VEC>;
@@ -339,16 +374,11 @@ __global__ void __launch_bounds__(kSumThreads, 4) sum_units_kernel(SumArgs a) {
     fa_grid_dependency_wait();
     fa_allow_dependents();
     const int64_t c = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * N;
-    const int64_t both = 2 * min(a.units, a.zero_ctas);
-    int64_t u = blockIdx.x;
-    if (u < both ? (u & 1) : a.zero_ctas > a.units) {
-        zero_absent<TT, N>(a, (u < both ? u / 2 : u - a.units) * kZeroRows, c);
-        return;
-    }
-    u = u < both ? u / 2 : u - a.zero_ctas;
+    const int64_t u = blockIdx.x;
     __shared__ uint32_t key[kSumUnit];
     __shared__ uint32_t pos[kSumUnit];
-    __shared__ uint32_t ends, bounds;  // bit i: token i is its run's last here; began before, goes on
+    __shared__ uint32_t ends;    // bit i: token i is its run's last here
+    __shared__ bool began, goes;  // the first run began before the unit; the last goes on
     const int64_t first = u * kSumUnit;
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
@@ -360,19 +390,24 @@ __global__ void __launch_bounds__(kSumThreads, 4) sum_units_kernel(SumArgs a) {
         uint32_t next = __shfl_down_sync(0xffffffffu, k, 1);
         if (lane == 31) next = at + 1 < g.tokens ? a.keys[at + 1] : none;
         const uint32_t e = __ballot_sync(0xffffffffu, next != k || lane == 31);
+        const uint32_t before = lane == 0 && first > 0 ? a.keys[first - 1] : none;
+        const bool in = __shfl_sync(0xffffffffu, before == k && k < g.vocab, 0);
+        const bool on = __shfl_sync(0xffffffffu, next == k && k < g.vocab, 31);
         if (lane == 0) {
             ends = e;
-            bounds = first > 0 && a.keys[first - 1] == k ? 1u : 0u;
+            began = in;
+            goes = on;
+            // one run: only the last token ends one
+            const bool one = e == 0x80000000u;
+            if (blockIdx.y == 0) a.shared[u] = !on ? 0u : in && one ? kThrough : kBegins;
         }
-        __syncwarp();
-        if (lane == 31 && next == k) bounds |= 2u;
     }
     __syncthreads();
     if (c >= g.dim) return;
     const DE *dout = static_cast<const DE *>(g.dout) + c;
     const uint32_t last = ends;
-    bool began_before = bounds & 1u;
-    const bool goes_on = bounds & 2u;
+    bool began_before = began;
+    const bool goes_on = goes;
     float sum[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) sum[j] = 0.f;
@@ -406,11 +441,12 @@ __global__ void __launch_bounds__(kSumThreads, 4) sum_units_kernel(SumArgs a) {
     }
 }
 
-// Runs that several units share.  A warp looks after one unit, for the columns of slab: if
-// the unit began a run that goes on, it adds the run's partial sums in unit order.  Runs of
-// more than kLong units are taken by the CTA's warps together, each a stretch of them, and
-// the stretches' sums are added in order.
+// Runs that several units share.  A warp looks after one unit, for the slabs of 32 * N columns
+// that its CTA takes in turn: if the unit began a run that goes on, it adds the run's partial
+// sums in unit order.  Runs of more than kLong units are taken by the CTA's warps together,
+// each a stretch of them, and the stretches' sums are added in order.
 constexpr int kLong = 16;
+constexpr int kJoinSlabs = 4;  // CTAs side by side over the columns
 template <int DT, int TT, bool VEC>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_units_kernel(SumArgs a) {
     constexpr int N = kGroup<DT, TT, VEC>;
@@ -418,34 +454,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_units_kernel(SumArgs a) 
     __shared__ int64_t last_unit[kJoinWarps];  // of the run that the warp's unit began (0: none)
     __shared__ float stretch[kJoinWarps][32 * N];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kJoinWarps;
-    const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * N;
+    const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kJoinWarps, mine = u0 + warp;
+    const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * N;
+    const int64_t stride = static_cast<int64_t>(gridDim.y) * 32 * N;
     fa_grid_dependency_wait();
     fa_allow_dependents();
-    int64_t end = 0;
+    int64_t end = 0;  // the last unit of the run that this warp's unit began
     {
-        const int64_t u = u0 + warp, first = u * kSumUnit, last = first + kSumUnit - 1;
-        if (last + 1 < g.tokens) {
-            const uint32_t key = a.keys[last];
-            if (key < g.vocab && a.keys[last + 1] == key &&
-                !(first > 0 && a.keys[first] == key && a.keys[first - 1] == key)) {
-                // the run's end: steps of growing length, then a search within the last
-                int64_t lo = last + 1, step = kSumUnit;
-                while (lo + step < g.tokens && a.keys[lo + step] == key) {
-                    lo += step;
-                    step *= 2;
-                }
-                const int64_t room = min(step, g.tokens - lo);
-                end = (lo + bound(a.keys + lo, room, key, true) - 1) / kSumUnit;
+        const auto through = [&](int64_t w) { return w < a.units && a.shared[w] == kThrough; };
+        const bool next = through(mine + 1 + lane);  // asked for together with the unit's own
+        if (mine < a.units - 1 && a.shared[mine] == kBegins) {
+            end = mine + 1;
+            unsigned on = __ballot_sync(0xffffffffu, next);
+            while (on == 0xffffffffu) {
+                end += 32;
+                on = __ballot_sync(0xffffffffu, through(end + lane));
             }
+            end += __ffs(~on) - 1;
         }
-        if (lane == 0) last_unit[warp] = end;
     }
-    __syncthreads();
-    const bool here = c < g.dim;
-    // partials of units [w0, w1], added onto sum in order
-    const auto add = [&](float *sum, int64_t w0, int64_t w1) {
-#pragma unroll 8
+    if (lane == 0) last_unit[warp] = end;
+    // partials of units [w0, w1] in columns [c, c + N), added onto sum in order
+    const auto add = [&](float *sum, int64_t c, int64_t w0, int64_t w1) {
+#pragma unroll 4
         for (int64_t w = w0; w <= w1; ++w) {
             float x[N];
             if (!fa_in_bounds(w, 1, a.units)) break;
@@ -454,34 +485,40 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_units_kernel(SumArgs a) 
             for (int j = 0; j < N; ++j) sum[j] += x[j];
         }
     };
-    const int64_t mine = u0 + warp;
-    if (end && end - mine <= kLong && here) {
-        float sum[N];
-        load_partial<N>(a.partial + (2 * mine + 1) * g.dim + c, sum);
-        add(sum, mine + 1, end);
-        finish_row<TT, N>(g, a.keys[(mine + 1) * kSumUnit], c, sum);
+    if (end && end - mine <= kLong) {
+        const uint32_t key = a.keys[(mine + 1) * kSumUnit];
+        for (int64_t c = c0; c < g.dim; c += stride) {
+            float sum[N];
+            load_partial<N>(a.partial + (2 * mine + 1) * g.dim + c, sum);
+            add(sum, c, mine + 1, end);
+            finish_row<TT, N>(g, key, c, sum);
+        }
     }
+    __syncthreads();
     for (int k = 0; k < kJoinWarps; ++k) {
         const int64_t u = u0 + k, units = last_unit[k] - u;
         if (!last_unit[k] || units <= kLong) continue;  // the same for the whole CTA
         const int64_t each = (units + kJoinWarps - 1) / kJoinWarps;
-        float sum[N];
+        for (int64_t c = c0; c - lane * N < g.dim; c += stride) {
+            const bool here = c < g.dim;
+            float sum[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) sum[j] = 0.f;
-        if (here) {
-            if (warp == 0) load_partial<N>(a.partial + (2 * u + 1) * g.dim + c, sum);
-            add(sum, u + 1 + warp * each, min(u + (warp + 1) * each, last_unit[k]));
+            for (int j = 0; j < N; ++j) sum[j] = 0.f;
+            if (here) {
+                if (warp == 0) load_partial<N>(a.partial + (2 * u + 1) * g.dim + c, sum);
+                add(sum, c, u + 1 + warp * each, min(u + (warp + 1) * each, last_unit[k]));
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) stretch[warp][j * 32 + lane] = sum[j];
+            __syncthreads();
+            if (warp == 0 && here) {
+                for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) sum[j] += stretch[w][j * 32 + lane];
+                finish_row<TT, N>(g, a.keys[(u + 1) * kSumUnit], c, sum);
+            }
+            __syncthreads();
         }
-#pragma unroll
-        for (int j = 0; j < N; ++j) stretch[warp][j * 32 + lane] = sum[j];
-        __syncthreads();
-        if (warp == 0 && here) {
-            for (int w = 1; w < kJoinWarps; ++w)
-#pragma unroll
-                for (int j = 0; j < N; ++j) sum[j] += stretch[w][j * 32 + lane];
-            finish_row<TT, N>(g, a.keys[(u + 1) * kSumUnit], c, sum);
-        }
-        __syncthreads();
     }
 }
 
@@ -544,7 +581,8 @@ EmbeddingScratch embedding_scratch_layout(int64_t tokens, int64_t dim) {
     s.chunks = (tokens + kSortChunk - 1) / kSortChunk;
     s.units = (tokens + kSumUnit - 1) / kSumUnit;
     s.sorted_words = round_up(tokens, 4);
-    s.bytes = 4 * (s.sorted_words * (s.chunks > 1 ? 4 : 2) + s.units * 2 * round_up(dim, 4));
+    s.bytes = 4 * (s.sorted_words * (s.chunks > 1 ? 4 : 2) + round_up(s.units, 4) +
+                   s.units * 2 * round_up(dim, 4));
     return s;
 }
 
@@ -559,7 +597,7 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
         chunk_pos = chunk_keys + s.sorted_words;
         end = chunk_pos + s.sorted_words;
     }
-    if (g.tokens > 0) {
+    {
         SortArgs sa;
         sa.ids = g.ids;
         sa.tokens = g.tokens;
@@ -571,19 +609,36 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
         while (g.vocab >> bits) ++bits;  // vocab itself is a key
         sa.passes = (bits + 8) / 9;
         sa.digit_bits = (bits + sa.passes - 1) / sa.passes;
-        const unsigned ctas =
-            s.chunks > 1 ? kSortChunk / kSortSlots
-                         : static_cast<unsigned>((g.tokens + kSortSlots - 1) / kSortSlots);
-        cudaError_t err = for_itype(idt, [&](auto it) {
-            auto kernel = sort_chunk_kernel<it()>;
-            constexpr int kSmem = sizeof(SortSmem);
+        sa.chunks = static_cast<unsigned>(s.chunks);
+        sa.ctas = s.chunks > 1 ? kSortChunk / kSortSlots
+                               : static_cast<unsigned>(
+                                     std::max<int64_t>(1, (g.tokens + kSortSlots - 1) / kSortSlots));
+        const int64_t elem = tdt == FA_F32 ? 4 : 2;
+        const bool flat = g.table_ld == g.dim;
+        sa.zero.p = static_cast<char *>(g.dtable);
+        sa.zero.rows = flat ? 1 : g.vocab;
+        sa.zero.bytes = (flat ? g.vocab * g.dim : g.dim) * elem;
+        sa.zero.ld = g.table_ld * elem;
+        // enough CTAs to zero the table at the memory's rate, 64 KB each at least
+        const int64_t zeroing =
+            g.accumulate ? 0 : std::min<int64_t>(2 * 152, g.vocab * g.dim * elem / 65536 + 1);
+        const int64_t zero_clusters = (zeroing + sa.ctas - 1) / sa.ctas;
+        const auto go = [&](auto it, auto item) {
+            auto kernel = sort_chunk_kernel<it(), decltype(item)>;
+            constexpr int kSmem = sizeof(SortSmem<decltype(item)>);
             cudaError_t e = cudaFuncSetAttribute(
                 kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            if (e == cudaSuccess && sa.ctas > 8)
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e != cudaSuccess) return e;
-            return launch_clusters(kernel, dim3(static_cast<unsigned>(s.chunks) * ctas),
-                                   dim3(kSortThreads), kSmem, ctas, false, stream, sa, ctas);
+            return launch_clusters(
+                kernel, dim3(static_cast<unsigned>((sa.chunks + zero_clusters) * sa.ctas)),
+                dim3(kSortThreads), kSmem, sa.ctas, false, stream, sa);
+        };
+        cudaError_t err = for_itype(idt, [&](auto it) {
+            return g.vocab < 65536 ? go(it, uint32_t{}) : go(it, uint64_t{});
         });
-        if (err != cudaSuccess) return err;
+        if (err != cudaSuccess || g.tokens == 0) return err;
         if (s.chunks > 1) {
             err = launch_dependent(merge_chunks_kernel,
                                    dim3(static_cast<unsigned>((g.tokens + kMergeThreads - 1) /
@@ -599,9 +654,9 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
     a.g = g;
     a.keys = keys;
     a.pos = pos;
-    a.partial = reinterpret_cast<float *>(end);
+    a.shared = end;
+    a.partial = reinterpret_cast<float *>(end + round_up(s.units, 4));
     a.units = s.units;
-    a.zero_ctas = g.accumulate ? 0 : (g.vocab + kZeroRows - 1) / kZeroRows;
     const bool vec = vector_rows(g.dout, g.dout_ld, ddt, g.dtable, g.table_ld, tdt, g.dim);
     return for_dtype(ddt, [&](auto dd) {
         return for_dtype(tdt, [&](auto td) {
@@ -614,14 +669,14 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
                 const int64_t slabs = (groups + threads - 1) / threads;
                 cudaError_t e = launch_dependent(
                     sum_units_kernel<dd(), td(), VEC>,
-                    dim3(static_cast<unsigned>(a.units + a.zero_ctas),
-                         static_cast<unsigned>(slabs)),
+                    dim3(static_cast<unsigned>(a.units), static_cast<unsigned>(slabs)),
                     dim3(threads), 0, stream, a);
                 if (e != cudaSuccess || a.units < 2) return e;
                 return launch_dependent(
                     join_units_kernel<dd(), td(), VEC>,
                     dim3(static_cast<unsigned>((a.units - 1 + kJoinWarps - 1) / kJoinWarps),
-                         static_cast<unsigned>((groups + 31) / 32)),
+                         static_cast<unsigned>(
+                             std::min<int64_t>(kJoinSlabs, (groups + 31) / 32))),
                     dim3(kJoinWarps * 32), 0, stream, a);
             };
             return vec ? go(std::true_type{}) : go(std::false_type{});

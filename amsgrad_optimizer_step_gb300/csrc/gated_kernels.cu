@@ -80,16 +80,20 @@ struct Activation<FA_GELU_TANH> {
 // the rows are aligned and the columns all exist, element accesses otherwise; columns past
 // the end read as 0 and are not written.
 template <int DT, bool VEC>
-__device__ __forceinline__ void load_run(const void *base, int64_t row, int64_t ld, int64_t c,
-                                         int64_t cols, float *x) {
+__device__ __forceinline__ Raw<DT, kRun> load_run(const void *base, int64_t row, int64_t ld,
+                                                  int64_t c, int64_t cols) {
     using E = Elem<DT>;
     const typename E::T *p = static_cast<const typename E::T *>(base) + row * ld + c;
+    Raw<DT, kRun> x;
     if (VEC && c + kRun <= cols) {
-        if (fa_in_bounds(c, kRun, cols)) load_n<DT, kRun>(p, x);
+        if (fa_in_bounds(c, kRun, cols)) x.load(p);
     } else {
+        float y[kRun];
 #pragma unroll
-        for (int j = 0; j < kRun; ++j) x[j] = c + j < cols ? E::widen(p[j]) : 0.f;
+        for (int j = 0; j < kRun; ++j) y[j] = c + j < cols ? E::widen(p[j]) : 0.f;
+        x.from(y);  // exact: they came from this type
     }
+    return x;
 }
 template <int DT, bool VEC>
 __device__ __forceinline__ void store_run(void *base, int64_t row, int64_t ld, int64_t c,
@@ -110,15 +114,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
-}
-// Largest magnitude of a lane's sixteen values.
-__device__ __forceinline__ float largest(const float (*x)[kRun]) {
-    float m = 0.f;
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int j = 0; j < kRun; ++j) m = max_nan(m, fabsf(x[r][j]));
-    return m;
 }
 
 // Eight codes of a run, packed.
@@ -150,7 +145,8 @@ __device__ __forceinline__ void decode(uint2 codes, float scale, uint64_t *x) {
 }
 
 template <int DT, int ACT, bool VEC, bool KEEP>
-__global__ void __launch_bounds__(kGatedThreads) gated_forward_kernel(GatedForwardArgs a) {
+__global__ void __launch_bounds__(kGatedThreads, VEC && DT != FA_F32 ? 5 : 2)
+gated_forward_kernel(GatedForwardArgs a) {
     const uint32_t b = (blockIdx.x * kGatedThreads + threadIdx.x) / kLanes;
     const int lane = threadIdx.x % kLanes;
     const int64_t n = a.rows * a.blocks;
@@ -158,14 +154,16 @@ __global__ void __launch_bounds__(kGatedThreads) gated_forward_kernel(GatedForwa
     const uint32_t row = a.by_blocks.quotient(b);
     const int64_t c = static_cast<int64_t>(b - row * static_cast<uint32_t>(a.blocks)) *
                           kCheckpointBlock + lane * kRun;
-    float g[2][kRun], u[2][kRun];
+    Raw<DT, kRun> g[2], u[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) load_run<DT, VEC>(a.gate, row, a.gate_ld, c + r * kRunStride, a.cols, g[r]);
+    for (int r = 0; r < 2; ++r) g[r] = load_run<DT, VEC>(a.gate, row, a.gate_ld, c + r * kRunStride, a.cols);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) load_run<DT, VEC>(a.up, row, a.up_ld, c + r * kRunStride, a.cols, u[r]);
+    for (int r = 0; r < 2; ++r) u[r] = load_run<DT, VEC>(a.up, row, a.up_ld, c + r * kRunStride, a.cols);
+    float inv_g = 0.f, inv_u = 0.f;
     if (KEEP) {
         const unsigned lanes = 0xffu << (threadIdx.x & 24);
-        float tg = largest(g), tu = largest(u);
+        float tg = max_nan(g[0].magnitude(), g[1].magnitude());
+        float tu = max_nan(u[0].magnitude(), u[1].magnitude());
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) {
             tg = max_nan(tg, __shfl_xor_sync(lanes, tg, o));
@@ -176,25 +174,27 @@ __global__ void __launch_bounds__(kGatedThreads) gated_forward_kernel(GatedForwa
         const bool kept = top >= kTiny && top < INFINITY, scale = lane & 1;
         float q = __fdiv_rn(scale ? top : 127.f, scale ? 127.f : top);
         if (!kept) q = scale && !(top < INFINITY) ? NAN : 0.f;
-        const float inv_g = __shfl_sync(lanes, q, 0, kLanes), inv_u = __shfl_sync(lanes, q, 2, kLanes);
+        inv_g = __shfl_sync(lanes, q, 0, kLanes);
+        inv_u = __shfl_sync(lanes, q, 2, kLanes);
         if (lane == 1) a.scales[b] = q;
         if (lane == 3) a.scales[n + b] = q;
-        int8_t *code = a.codes + static_cast<int64_t>(b) * kCheckpointBlock + lane * kRun;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            __stcs(reinterpret_cast<uint2 *>(code + r * kRunStride), encode(g[r], inv_g));
-            __stcs(reinterpret_cast<uint2 *>(code + n * kCheckpointBlock + r * kRunStride),
-                   encode(u[r], inv_u));
-        }
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        float h[kRun];
+        float x[kRun], y[kRun];
+        g[r].widen(x);
+        u[r].widen(y);
+        if (KEEP) {
+            int8_t *code = a.codes + static_cast<int64_t>(b) * kCheckpointBlock + lane * kRun +
+                           r * kRunStride;
+            __stcs(reinterpret_cast<uint2 *>(code), encode(x, inv_g));
+            __stcs(reinterpret_cast<uint2 *>(code + n * kCheckpointBlock), encode(y, inv_u));
+        }
 #pragma unroll
         for (int j = 0; j < kRun; j += 2)
-            unpair(mul2(Activation<ACT>::value(pair(g[r][j], g[r][j + 1])),
-                        pair(u[r][j], u[r][j + 1])), h[j], h[j + 1]);
-        store_run<DT, VEC>(a.h, row, a.h_ld, c + r * kRunStride, a.cols, h);
+            unpair(mul2(Activation<ACT>::value(pair(x[j], x[j + 1])), pair(y[j], y[j + 1])), x[j],
+                   x[j + 1]);
+        store_run<DT, VEC>(a.h, row, a.h_ld, c + r * kRunStride, a.cols, x);
     }
 }
 
@@ -209,12 +209,12 @@ __global__ void __launch_bounds__(kGatedThreads) gated_backward_kernel(GatedBack
                           kCheckpointBlock + lane * kRun;
     const int8_t *code = a.codes + static_cast<int64_t>(b) * kCheckpointBlock + lane * kRun;
     uint2 qg[2], qu[2];
-    float d[2][kRun];
+    Raw<DT, kRun> d[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         qg[r] = __ldcs(reinterpret_cast<const uint2 *>(code + r * kRunStride));
         qu[r] = __ldcs(reinterpret_cast<const uint2 *>(code + n * kCheckpointBlock + r * kRunStride));
-        load_run<DT, VEC>(a.dh, row, a.dh_ld, c + r * kRunStride, a.cols, d[r]);
+        d[r] = load_run<DT, VEC>(a.dh, row, a.dh_ld, c + r * kRunStride, a.cols);
     }
     const float sg = a.scales[b], su = a.scales[n + b];
 #pragma unroll
@@ -222,12 +222,13 @@ __global__ void __launch_bounds__(kGatedThreads) gated_backward_kernel(GatedBack
         uint64_t g[kRun / 2], u[kRun / 2];
         decode(qg[r], sg, g);
         decode(qu[r], su, u);
-        float dg[kRun], du[kRun], h[kRun];
+        float x[kRun], dg[kRun], du[kRun], h[kRun];
+        d[r].widen(x);
 #pragma unroll
         for (int j = 0; j < kRun; j += 2) {
             uint64_t act, slope;
             Activation<ACT>::with_slope(g[j / 2], act, slope);
-            const uint64_t dh = pair(d[r][j], d[r][j + 1]);
+            const uint64_t dh = pair(x[j], x[j + 1]);
             // |act'| < 1.13: overflows only where the gradient does
             unpair(mul2(mul2(dh, slope), u[j / 2]), dg[j], dg[j + 1]);
             unpair(mul2(dh, act), du[j], du[j + 1]);

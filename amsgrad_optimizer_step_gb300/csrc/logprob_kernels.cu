@@ -9,6 +9,7 @@
 // log2(e) in two FP32 parts: k d is rounded once.  With k in one part the log-probabilities
 // were 2e-8 of a row's spread off, all the same way.
 #include <algorithm>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -208,23 +209,36 @@ __device__ __forceinline__ void row_ends(const RowSpan &sp, int64_t n, unsigned 
     if (rank == split - 1 && t < n - sp.tail && fa_in_bounds(sp.tail + t, 1, n)) f(sp.tail + t);
 }
 
-// One vector of the gradient: c (1[v = label] - 2^(k (x - top)) / s); at = the label's place in
-// the vector (outside [0, kVec): none).
+// One vector of the gradient but for the label's element: -c 2^(k (x - top)) / s.
 template <int DT>
-__device__ __forceinline__ uint4 gradient_vector(const uint4 &r, const Exponent &e, float w,
-                                                 float c, int at) {
+__device__ __forceinline__ uint4 gradient_vector(const uint4 &r, const Exponent &e, float w) {
     constexpr int V = Elem<DT>::kVec;
     float x[V];
     Elem<DT>::unpack(r, x);
 #pragma unroll
     for (int j = 0; j < V; j += 2)
         unpair(mul2(e.of_pair(x[j], x[j + 1]), pair(w, w)), x[j], x[j + 1]);
-    if (static_cast<unsigned>(at) < V) {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (at == j) x[j] += c;
-    }
     return Elem<DT>::pack(x);
+}
+
+// Whether this thread writes the label's element of the row: it then reads the logit before
+// it writes anything, and the element, c (1 - p), last.
+template <int DT>
+__device__ __forceinline__ bool label_is_mine(int64_t label, const RowSpan &sp,
+                                              const RowPart &part, unsigned rank, unsigned split) {
+    if (label < sp.head) return rank == 0 && threadIdx.x == label;
+    if (label >= sp.tail) return rank == split - 1 && threadIdx.x == label - sp.tail;
+    const int64_t i = (label - sp.head) / Elem<DT>::kVec - part.begin;
+    return i >= 0 && i < part.count && i % kRowThreads == threadIdx.x;
+}
+
+// f(i, whole batch) for the vectors i, i + kRowThreads, ... of a thread in batches of N: whole
+// ones first, without a check of each vector, then one that may be cut short.
+template <int N, typename F>
+__device__ __forceinline__ void for_batches(int count, F f) {
+    int i0 = 0;
+    for (; i0 + N * kRowThreads <= count; i0 += N * kRowThreads) f(i0, std::true_type{});
+    if (i0 < count) f(i0, std::false_type{});
 }
 
 // dlogits of (a part of) one row from global memory.  The output may be the row itself:
@@ -239,33 +253,36 @@ __device__ __forceinline__ void row_gradient(const void *row, void *out, int64_t
     T *y = static_cast<T *>(out);
     const Exponent e(a, r.top);
     const float w = -c / r.s;
-    const auto one = [&](int64_t i) {
-        const float p = e(E::widen(x[i])) * w;
-        y[i] = E::round(i == label ? p + c : p);
-    };
+    const int tid = threadIdx.x;
     if ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) {
         // not co-aligned: element by element
-        for (int64_t i = rank * blockDim.x + threadIdx.x; i < n; i += split * blockDim.x)
-            if (fa_in_bounds(i, 1, n)) one(i);
+        for (int64_t i = rank * kRowThreads + tid; i < n; i += split * kRowThreads)
+            if (fa_in_bounds(i, 1, n))
+                y[i] = E::round(fmaf(e(E::widen(x[i])), w, i == label ? c : 0.f));
         return;
     }
     const RowSpan sp = row_span<DT>(row, n);
-    row_ends(sp, n, rank, split, one);
     const RowPart part(sp, rank, split);
-    const uint4 *q = reinterpret_cast<const uint4 *>(x + sp.head) + part.begin;
-    uint4 *o = reinterpret_cast<uint4 *>(y + sp.head) + part.begin;
-    const int at = static_cast<int>(label - sp.head - part.begin * E::kVec), nt = blockDim.x;
-    for (int i = threadIdx.x; i < part.count; i += kBatch * nt) {
+    const bool mine = label_is_mine<DT>(label, sp, part, rank, split);
+    const float label_logit = mine ? E::widen(x[label]) : 0.f;
+    row_ends(sp, n, rank, split, [&](int64_t i) { y[i] = E::round(e(E::widen(x[i])) * w); });
+    const uint4 *q = reinterpret_cast<const uint4 *>(x + sp.head) + part.begin + tid;
+    uint4 *o = reinterpret_cast<uint4 *>(y + sp.head) + part.begin + tid;
+    for_batches<kBatch>(part.count, [&](int i0, auto whole) {
         uint4 v[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            if (i + j * nt < part.count && part.in_bounds(i + j * nt)) v[j] = __ldcs(q + i + j * nt);
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * kRowThreads;
+            if ((decltype(whole)::value || i + tid < part.count) && part.in_bounds(i + tid)) v[j] = __ldcs(q + i);
+        }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            if (i + j * nt < part.count && part.in_bounds(i + j * nt))
-                __stcs(o + i + j * nt,
-                       gradient_vector<DT>(v[j], e, w, c, at - (i + j * nt) * E::kVec));
-    }
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * kRowThreads;
+            if ((decltype(whole)::value || i + tid < part.count) && part.in_bounds(i + tid))
+                __stcs(o + i, gradient_vector<DT>(v[j], e, w));
+        }
+    });
+    if (mine) y[label] = E::round(fmaf(e(label_logit), w, c));
 }
 
 // Zeros for (a part of) the row of a token that is not counted.
@@ -314,19 +331,21 @@ __device__ __forceinline__ RowSum row_softmax(const void *row, const LogitsArgs 
     Softmax acc(a);
     add_ends<DT>(acc, row, sp, a.vocab, rank, split);
     const RowPart part(sp, rank, split);
+    const int tid = threadIdx.x;
     const uint4 *q =
-        reinterpret_cast<const uint4 *>(static_cast<const T *>(row) + sp.head) + part.begin;
-    const int nt = blockDim.x;
-    // whole warps: a lane past the end adds -inf
-    for (int i0 = threadIdx.x & ~31; i0 < part.count; i0 += kBatch * nt) {
-        const int i = i0 + (threadIdx.x & 31);
+        reinterpret_cast<const uint4 *>(static_cast<const T *>(row) + sp.head) + part.begin + tid;
+    for_batches<kBatch>(part.count, [&](int i0, auto full) {
+        if (!decltype(full)::value && i0 + (tid & ~31) >= part.count) return;  // whole warps
         uint4 r[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            r[j] = i + j * nt < part.count && part.in_bounds(i + j * nt) ? __ldg(q + i + j * nt)
-                                                                         : no_vector<DT>();
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * kRowThreads;
+            r[j] = (decltype(full)::value || i + tid < part.count) && part.in_bounds(i + tid)
+                       ? __ldg(q + i)
+                       : no_vector<DT>();
+        }
         acc.add<DT, kBatch>(r);
-    }
+    });
     return merge_row(acc, parts, &whole, split);
 }
 
@@ -609,7 +628,7 @@ policy_row_kernel(PolicyArgs a, unsigned split, Divisor divisor) {
     // what one thread needs of the token, asked for before the sum
     const bool first = tid == 0;
     const PolicyToken in(a, first ? t : 0);
-    const float label_logit = first ? E::widen(row[label]) : 0.f;
+    const float label_logit = E::widen(row[label]);
     float denom = a.denominator;
     if (divisor == kCountHere) denom = static_cast<float>(count_labels<IT>(a.x));
 
@@ -618,13 +637,15 @@ policy_row_kernel(PolicyArgs a, unsigned split, Divisor divisor) {
         Softmax acc(a.x);
         add_ends<DT>(acc, row, sp, n, rank, split);
         const auto group = [&](int g) {
-            const int i0 = g * HELD * kRowThreads + tid;
-            if ((i0 & ~31) >= part.count) return;
+            const int i0 = g * HELD * kRowThreads;
+            const bool full = i0 + HELD * kRowThreads <= part.count;
+            if (i0 + (tid & ~31) >= part.count) return;
             uint4 v[HELD];
 #pragma unroll
-            for (int j = 0; j < HELD; ++j)
-                v[j] = i0 + j * kRowThreads < part.count ? slot[i0 + j * kRowThreads]
-                                                         : no_vector<DT>();
+            for (int j = 0; j < HELD; ++j) {
+                const int i = i0 + j * kRowThreads + tid;
+                v[j] = full || i < part.count ? slot[i] : no_vector<DT>();
+            }
             acc.add<DT, HELD>(v);
         };
         copy_async_wait<3>();
@@ -659,16 +680,19 @@ policy_row_kernel(PolicyArgs a, unsigned split, Divisor divisor) {
         if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
             const Exponent e(a.x, r.top);
             const float c = coef, w = -c / r.s;
-            row_ends(sp, n, rank, split, [&](int64_t i) {
-                const float p = e(E::widen(row[i])) * w;
-                out[i] = E::round(i == label ? p + c : p);
+            row_ends(sp, n, rank, split,
+                     [&](int64_t i) { out[i] = E::round(e(E::widen(row[i])) * w); });
+            uint4 *o = reinterpret_cast<uint4 *>(out + sp.head) + part.begin + tid;
+            for_batches<HELD>(part.count, [&](int i0, auto whole) {
+#pragma unroll
+                for (int j = 0; j < HELD; ++j) {
+                    const int i = i0 + j * kRowThreads;
+                    if ((decltype(whole)::value || i + tid < part.count) && part.in_bounds(i + tid))
+                        __stcs(o + i, gradient_vector<DT>(slot[i + tid], e, w));
+                }
             });
-            uint4 *o = reinterpret_cast<uint4 *>(out + sp.head) + part.begin;
-            const int at = static_cast<int>(label - sp.head - part.begin * E::kVec);
-#pragma unroll 4
-            for (int i = tid; i < part.count; i += kRowThreads)
-                if (part.in_bounds(i))
-                    __stcs(o + i, gradient_vector<DT>(slot[i], e, w, c, at - i * E::kVec));
+            if (label_is_mine<DT>(label, sp, part, rank, split))
+                out[label] = E::round(fmaf(e(label_logit), w, c));
             return;
         }
     }

@@ -29,7 +29,21 @@ struct Elem<FA_F32> {
         x[2] = __uint_as_float(r.z);
         x[3] = __uint_as_float(r.w);
     }
-    // Largest element of n vectors, NaN ignored where there is another.
+    // Largest magnitude in N vectors, NaN where any element is.
+    template <int N>
+    static __device__ __forceinline__ float magnitude(const uint4 *r) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float x[4];
+            unpack(r[i], x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(x[j])));
+        }
+        return m;
+    }
+    // Largest element of N vectors, NaN ignored where there is another.
     template <int N>
     static __device__ __forceinline__ float largest(const uint4 *r) {
         float m = -INFINITY;
@@ -51,6 +65,14 @@ struct Elem<FA_F16> {
     using T = __half;
     static constexpr int kVec = 8;
     static __device__ __forceinline__ float widen(T x) { return __half2float(x); }
+    template <int N>
+    static __device__ __forceinline__ float magnitude(const uint4 *r) {
+        const __half2 *p = reinterpret_cast<const __half2 *>(r);
+        __half2 m = __habs2(p[0]);
+#pragma unroll
+        for (int i = 1; i < 4 * N; ++i) m = __hmax2_nan(m, __habs2(p[i]));
+        return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+    }
     template <int N>
     static __device__ __forceinline__ float largest(const uint4 *r) {
         const __half2 *p = reinterpret_cast<const __half2 *>(r);
@@ -85,6 +107,14 @@ struct Elem<FA_BF16> {
     using T = __nv_bfloat16;
     static constexpr int kVec = 8;
     static __device__ __forceinline__ float widen(T x) { return __bfloat162float(x); }
+    template <int N>
+    static __device__ __forceinline__ float magnitude(const uint4 *r) {
+        const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(r);
+        __nv_bfloat162 m = __habs2(p[0]);
+#pragma unroll
+        for (int i = 1; i < 4 * N; ++i) m = __hmax2_nan(m, __habs2(p[i]));
+        return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+    }
     template <int N>
     static __device__ __forceinline__ float largest(const uint4 *r) {
         const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(r);
@@ -166,6 +196,17 @@ struct Raw {
             else
                 x[k] = E::widen(r[k]);
         }
+    }
+    // From values of this type.
+    __device__ __forceinline__ void from(const float *x) {
+        static_assert(kWhole, "whole vectors");
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) r[k] = E::pack(x + k * E::kVec);
+    }
+    // The largest magnitude; NaN where any element is.
+    __device__ __forceinline__ float magnitude() const {
+        static_assert(kWhole, "whole vectors");
+        return E::template magnitude<kWords>(r);
     }
 };
 

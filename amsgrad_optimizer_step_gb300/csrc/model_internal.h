@@ -52,8 +52,8 @@ struct EmbeddingScratch {
     int64_t sorted_words;  // 32-bit words of one sorted array (tokens, rounded up to 4)
     int64_t bytes;
 };
-constexpr int kSortSlots = 8192;            // tokens in one CTA's shared memory
-constexpr int kSortChunk = 8 * kSortSlots;  // in a cluster's
+constexpr int kSortSlots = 4096;             // tokens in one CTA's shared memory
+constexpr int kSortChunk = 16 * kSortSlots;  // in a cluster's
 constexpr int kSumUnit = 32;                // (a warp's ballot holds one)
 EmbeddingScratch embedding_scratch_layout(int64_t tokens, int64_t dim);
 

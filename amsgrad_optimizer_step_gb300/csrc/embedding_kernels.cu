@@ -4,8 +4,10 @@
 // are sorted by id (stable: ascending t within an id), so that each id's rows are one
 // run of the sorted order, and the sorted order is cut into units of kSumUnit tokens,
 // each added by one CTA in order: the work of a unit does not depend on how the ids
-// are distributed.  A run inside one unit is finished there; a run that several units
-// share leaves FP32 partial sums, which the join adds in unit order.
+// are distributed.  A run inside one unit is finished there.  Units that share a run leave
+// FP32 partial sums: of two, the one that comes second adds both; more are added in unit
+// order by the join.  (Two numbers have one sum, whoever adds them: the result does not
+// depend on the order in which CTAs run.)
 //
 // Sort: a cluster of up to sixteen CTAs sorts up to kSortChunk tokens in its shared memory,
 // least significant digit first: each warp ranks its tokens by digit, the CTAs exchange
@@ -124,6 +126,8 @@ struct SortArgs {
     int passes, digit_bits;   // passes * digit_bits bits hold vocab, the key of a token without an id
     unsigned chunks, ctas;    // clusters that sort, and the CTAs of a cluster
     ZeroArgs zero;
+    uint32_t *arrived;        // counters of the sums' kernel, zeroed here
+    int64_t counters;
 };
 
 // A token on its way: its id above its index in the chunk.
@@ -145,6 +149,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a) {
         zero_rows(a.zero, blockIdx.x - a.chunks * a.ctas, gridDim.x - a.chunks * a.ctas);
         return;
     }
+    for (int64_t i = blockIdx.x * kSortThreads + threadIdx.x; i < a.counters;
+         i += static_cast<int64_t>(a.chunks * a.ctas) * kSortThreads)
+        a.arrived[i] = 0;
     extern __shared__ uint4 raw[];
     SortSmem<Item> &s = *reinterpret_cast<SortSmem<Item> *>(raw);
     cg::cluster_group cluster = cg::this_cluster();
@@ -305,12 +312,13 @@ merge_chunks_kernel(const uint32_t *keys, const uint32_t *pos, uint32_t *out_key
 struct SumArgs {
     EmbeddingGradArgs g;
     const uint32_t *keys, *pos;  // sorted
-    uint32_t *shared;            // [units]: how the unit's runs reach into its neighbours
+    uint32_t *shared;            // [units]: runs that the join adds up
+    uint32_t *arrived;           // [slabs][units]: sums of the run across the unit's end so far
     float *partial;              // [units][2][dim]
     int64_t units;
 };
 // shared[u]: the unit is one run that began before it and goes on after it; it begins a run
-// that goes on.
+// that goes on past the next unit.
 constexpr uint32_t kThrough = 1, kBegins = 2;
 
 // Writes ``sum * scale`` to (or adds it to) elements [c, c + N) of table row v.
@@ -345,12 +353,13 @@ __device__ __forceinline__ void store_partial(float *p, const float *x) {
         for (int j = 0; j < N; ++j) p[j] = x[j];
     }
 }
+// (another CTA's: from L2)
 template <int N>
 __device__ __forceinline__ void load_partial(const float *p, float *x) {
     if constexpr (N % 4 == 0) {
 #pragma unroll
         for (int j = 0; j < N; j += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(p + j);
+            const float4 f = __ldcg(reinterpret_cast<const float4 *>(p + j));
             x[j] = f.x;
             x[j + 1] = f.y;
             x[j + 2] = f.z;
@@ -358,7 +367,7 @@ __device__ __forceinline__ void load_partial(const float *p, float *x) {
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = p[j];
+        for (int j = 0; j < N; ++j) x[j] = __ldcg(p + j);
     }
 }
 
@@ -369,84 +378,118 @@ template <int DT, int TT, bool VEC>
 __global__ void __launch_bounds__(kSumThreads, 4) sum_units_kernel(SumArgs a) {
     constexpr int N = kGroup<DT, TT, VEC>;
     constexpr int kAhead = 8;  // rows in flight
+    constexpr uint32_t kNone = 0xffffffffu;  // no id: ids are below 2^31
     using DE = typename Elem<DT>::T;
     const EmbeddingGradArgs &g = a.g;
     fa_grid_dependency_wait();
     fa_allow_dependents();
     const int64_t c = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * N;
-    const int64_t u = blockIdx.x;
+    const int64_t u = blockIdx.x, first = u * kSumUnit;
     __shared__ uint32_t key[kSumUnit];
     __shared__ uint32_t pos[kSumUnit];
-    __shared__ uint32_t ends;    // bit i: token i is its run's last here
-    __shared__ bool began, goes;  // the first run began before the unit; the last goes on
-    const int64_t first = u * kSumUnit;
+    __shared__ uint32_t ends;       // bit i: token i is its run's last here
+    __shared__ bool began, goes;    // the first run began before the unit; the last goes on
+    __shared__ bool with_last, with_next;  // and is shared with that one unit only
+    __shared__ bool add_last, add_next;    // whose sum came first: this CTA adds both
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        const int64_t at = first + lane;
-        const uint32_t none = 0xffffffffu;  // no id has it: ids are below 2^31
-        const uint32_t k = at < g.tokens ? a.keys[at] : none;
-        pos[lane] = at < g.tokens ? a.pos[at] : 0u;
-        key[lane] = k < g.vocab ? k : none;
+        const auto key_at = [&](int64_t i) { return i >= 0 && i < g.tokens ? a.keys[i] : kNone; };
+        const uint32_t k = key_at(first + lane);
+        // lanes 0 to 3: the tokens on both sides of the units before and after this one
+        const uint32_t around =
+            key_at(lane == 0   ? first - 1
+                   : lane == 1 ? first - kSumUnit - 1
+                   : lane == 2 ? first + kSumUnit
+                   : lane == 3 ? first + 2 * kSumUnit
+                               : -1);
+        pos[lane] = first + lane < g.tokens ? a.pos[first + lane] : 0u;
+        key[lane] = k < g.vocab ? k : kNone;
+        const uint32_t head = __shfl_sync(0xffffffffu, k, 0), tail = __shfl_sync(0xffffffffu, k, 31);
+        const uint32_t after = __shfl_sync(0xffffffffu, around, 2);
         uint32_t next = __shfl_down_sync(0xffffffffu, k, 1);
-        if (lane == 31) next = at + 1 < g.tokens ? a.keys[at + 1] : none;
+        if (lane == 31) next = after;
         const uint32_t e = __ballot_sync(0xffffffffu, next != k || lane == 31);
-        const uint32_t before = lane == 0 && first > 0 ? a.keys[first - 1] : none;
-        const bool in = __shfl_sync(0xffffffffu, before == k && k < g.vocab, 0);
-        const bool on = __shfl_sync(0xffffffffu, next == k && k < g.vocab, 31);
+        const bool in = __shfl_sync(0xffffffffu, around, 0) == head && head < g.vocab;
+        const bool on = after == tail && tail < g.vocab;
+        const bool one = e == 0x80000000u;  // one run: only the last token ends one
+        const bool before_last = __shfl_sync(0xffffffffu, around, 1) == head;
+        const bool after_next = __shfl_sync(0xffffffffu, around, 3) == tail;
         if (lane == 0) {
             ends = e;
             began = in;
             goes = on;
-            // one run: only the last token ends one
-            const bool one = e == 0x80000000u;
-            if (blockIdx.y == 0) a.shared[u] = !on ? 0u : in && one ? kThrough : kBegins;
+            with_last = in && !(one && on) && !before_last;
+            with_next = on && !(one && in) && !after_next;
+            if (blockIdx.y == 0)
+                a.shared[u] = in && on && one ? kThrough : on && after_next ? kBegins : 0u;
         }
     }
     __syncthreads();
-    if (c >= g.dim) return;
-    const DE *dout = static_cast<const DE *>(g.dout) + c;
+    const bool here = c < g.dim;
     const uint32_t last = ends;
     bool began_before = began;
     const bool goes_on = goes;
-    float sum[N];
+    if (here) {
+        const DE *dout = static_cast<const DE *>(g.dout) + c;
+        float sum[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) sum[j] = 0.f;
+        for (int j = 0; j < N; ++j) sum[j] = 0.f;
 #pragma unroll 1
-    for (int i0 = 0; i0 < kSumUnit; i0 += kAhead) {
-        Raw<DT, N> rows[kAhead];
+        for (int i0 = 0; i0 < kSumUnit && key[i0] != kNone; i0 += kAhead) {
+            Raw<DT, N> rows[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (key[i0 + k] != 0xffffffffu && fa_in_bounds(c, N, g.dim) &&
-                fa_in_bounds(pos[i0 + k], 1, g.tokens))
-                rows[k].load(dout + static_cast<int64_t>(pos[i0 + k]) * g.dout_ld);
+            for (int k = 0; k < kAhead; ++k)
+                if (key[i0 + k] != kNone && fa_in_bounds(c, N, g.dim) &&
+                    fa_in_bounds(pos[i0 + k], 1, g.tokens))
+                    rows[k].load(dout + static_cast<int64_t>(pos[i0 + k]) * g.dout_ld);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int i = i0 + k;
-            const uint32_t v = key[i];
-            if (v == 0xffffffffu) return;  // tokens without an id come last
-            float x[N];
-            rows[k].widen(x);
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k;
+                const uint32_t v = key[i];
+                if (v == kNone) break;  // tokens without an id come last
+                float x[N];
+                rows[k].widen(x);
 #pragma unroll
-            for (int j = 0; j < N; ++j) sum[j] += x[j];
-            if (!(last >> i & 1u)) continue;
-            const bool on = i == kSumUnit - 1 && goes_on;
-            if (began_before || on)
-                store_partial<N>(a.partial + (2 * u + (began_before ? 0 : 1)) * g.dim + c, sum);
-            else
-                finish_row<TT, N>(g, v, c, sum);
-            began_before = false;
+                for (int j = 0; j < N; ++j) sum[j] += x[j];
+                if (!(last >> i & 1u)) continue;
+                const bool on = i == kSumUnit - 1 && goes_on;
+                if (began_before || on)
+                    store_partial<N>(a.partial + (2 * u + (began_before ? 0 : 1)) * g.dim + c, sum);
+                else
+                    finish_row<TT, N>(g, v, c, sum);
+                began_before = false;
 #pragma unroll
-            for (int j = 0; j < N; ++j) sum[j] = 0.f;
+                for (int j = 0; j < N; ++j) sum[j] = 0.f;
+            }
         }
     }
+    if (!with_last && !with_next) return;  // the same for the whole CTA
+    // partial sums are in memory before they are counted, and the other's read after
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint32_t *arrived = a.arrived + blockIdx.y * a.units;
+        add_last = with_last && atomicAdd(&arrived[u - 1], 1u) == 1u;
+        add_next = with_next && atomicAdd(&arrived[u], 1u) == 1u;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!here) return;
+    const auto add_pair = [&](int64_t w, uint32_t v) {  // the run across the end of unit w
+        float x[N], y[N];
+        load_partial<N>(a.partial + (2 * w + 1) * g.dim + c, x);
+        load_partial<N>(a.partial + 2 * (w + 1) * g.dim + c, y);
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] += y[j];
+        finish_row<TT, N>(g, v, c, x);
+    };
+    if (add_last) add_pair(u - 1, key[0]);
+    if (add_next) add_pair(u, key[kSumUnit - 1]);
 }
 
-// Runs that several units share.  A warp looks after one unit, for the slabs of 32 * N columns
-// that its CTA takes in turn: if the unit began a run that goes on, it adds the run's partial
-// sums in unit order.  Runs of more than kLong units are taken by the CTA's warps together,
-// each a stretch of them, and the stretches' sums are added in order.
-constexpr int kLong = 16;
-constexpr int kJoinSlabs = 4;  // CTAs side by side over the columns
+// Runs of three units and more, in columns [32 N blockIdx.y, + 32 N).  Each warp of a CTA looks
+// whether one unit began such a run; the CTA's warps then add each of these runs together,
+// each a stretch of its partial sums in unit order, and the stretches' sums in order.
 template <int DT, int TT, bool VEC>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_units_kernel(SumArgs a) {
     constexpr int N = kGroup<DT, TT, VEC>;
@@ -455,15 +498,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_units_kernel(SumArgs a) 
     __shared__ float stretch[kJoinWarps][32 * N];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kJoinWarps, mine = u0 + warp;
-    const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * N;
-    const int64_t stride = static_cast<int64_t>(gridDim.y) * 32 * N;
+    const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * N;
     fa_grid_dependency_wait();
     fa_allow_dependents();
-    int64_t end = 0;  // the last unit of the run that this warp's unit began
+    int64_t end = 0;
     {
         const auto through = [&](int64_t w) { return w < a.units && a.shared[w] == kThrough; };
         const bool next = through(mine + 1 + lane);  // asked for together with the unit's own
-        if (mine < a.units - 1 && a.shared[mine] == kBegins) {
+        if (mine < a.units && a.shared[mine] == kBegins) {
             end = mine + 1;
             unsigned on = __ballot_sync(0xffffffffu, next);
             while (on == 0xffffffffu) {
@@ -474,51 +516,36 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_units_kernel(SumArgs a) 
         }
     }
     if (lane == 0) last_unit[warp] = end;
-    // partials of units [w0, w1] in columns [c, c + N), added onto sum in order
-    const auto add = [&](float *sum, int64_t c, int64_t w0, int64_t w1) {
-#pragma unroll 4
-        for (int64_t w = w0; w <= w1; ++w) {
-            float x[N];
-            if (!fa_in_bounds(w, 1, a.units)) break;
-            load_partial<N>(a.partial + 2 * w * g.dim + c, x);
-#pragma unroll
-            for (int j = 0; j < N; ++j) sum[j] += x[j];
-        }
-    };
-    if (end && end - mine <= kLong) {
-        const uint32_t key = a.keys[(mine + 1) * kSumUnit];
-        for (int64_t c = c0; c < g.dim; c += stride) {
-            float sum[N];
-            load_partial<N>(a.partial + (2 * mine + 1) * g.dim + c, sum);
-            add(sum, c, mine + 1, end);
-            finish_row<TT, N>(g, key, c, sum);
-        }
-    }
     __syncthreads();
+    const bool here = c < g.dim;
     for (int k = 0; k < kJoinWarps; ++k) {
-        const int64_t u = u0 + k, units = last_unit[k] - u;
-        if (!last_unit[k] || units <= kLong) continue;  // the same for the whole CTA
-        const int64_t each = (units + kJoinWarps - 1) / kJoinWarps;
-        for (int64_t c = c0; c - lane * N < g.dim; c += stride) {
-            const bool here = c < g.dim;
-            float sum[N];
+        if (!last_unit[k]) continue;  // the same for the whole CTA
+        const int64_t u = u0 + k, each = (last_unit[k] - u + kJoinWarps - 1) / kJoinWarps;
+        const int64_t w1 = min(u + (warp + 1) * each, last_unit[k]);
+        float sum[N];
 #pragma unroll
-            for (int j = 0; j < N; ++j) sum[j] = 0.f;
-            if (here) {
-                if (warp == 0) load_partial<N>(a.partial + (2 * u + 1) * g.dim + c, sum);
-                add(sum, c, u + 1 + warp * each, min(u + (warp + 1) * each, last_unit[k]));
+        for (int j = 0; j < N; ++j) sum[j] = 0.f;
+        if (here) {
+            if (warp == 0) load_partial<N>(a.partial + (2 * u + 1) * g.dim + c, sum);
+#pragma unroll 4
+            for (int64_t w = u + 1 + warp * each; w <= w1; ++w) {
+                float x[N];
+                if (!fa_in_bounds(w, 1, a.units)) break;
+                load_partial<N>(a.partial + 2 * w * g.dim + c, x);
+#pragma unroll
+                for (int j = 0; j < N; ++j) sum[j] += x[j];
             }
-#pragma unroll
-            for (int j = 0; j < N; ++j) stretch[warp][j * 32 + lane] = sum[j];
-            __syncthreads();
-            if (warp == 0 && here) {
-                for (int w = 1; w < kJoinWarps; ++w)
-#pragma unroll
-                    for (int j = 0; j < N; ++j) sum[j] += stretch[w][j * 32 + lane];
-                finish_row<TT, N>(g, a.keys[(u + 1) * kSumUnit], c, sum);
-            }
-            __syncthreads();
         }
+#pragma unroll
+        for (int j = 0; j < N; ++j) stretch[warp][j * 32 + lane] = sum[j];
+        __syncthreads();
+        if (warp == 0 && here) {
+            for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+                for (int j = 0; j < N; ++j) sum[j] += stretch[w][j * 32 + lane];
+            finish_row<TT, N>(g, a.keys[(u + 1) * kSumUnit], c, sum);
+        }
+        __syncthreads();
     }
 }
 
@@ -581,8 +608,10 @@ EmbeddingScratch embedding_scratch_layout(int64_t tokens, int64_t dim) {
     s.chunks = (tokens + kSortChunk - 1) / kSortChunk;
     s.units = (tokens + kSumUnit - 1) / kSumUnit;
     s.sorted_words = round_up(tokens, 4);
+    // slabs of the sums' kernel: a column a thread at most
+    s.counters = s.units * ((dim + kSumThreads - 1) / kSumThreads);
     s.bytes = 4 * (s.sorted_words * (s.chunks > 1 ? 4 : 2) + round_up(s.units, 4) +
-                   s.units * 2 * round_up(dim, 4));
+                   round_up(s.counters, 4) + s.units * 2 * round_up(dim, 4));
     return s;
 }
 
@@ -619,6 +648,8 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
         sa.zero.rows = flat ? 1 : g.vocab;
         sa.zero.bytes = (flat ? g.vocab * g.dim : g.dim) * elem;
         sa.zero.ld = g.table_ld * elem;
+        sa.arrived = end + round_up(s.units, 4);
+        sa.counters = s.counters;
         // enough CTAs to zero the table at the memory's rate, 64 KB each at least
         const int64_t zeroing =
             g.accumulate ? 0 : std::min<int64_t>(2 * 152, g.vocab * g.dim * elem / 65536 + 1);
@@ -655,7 +686,8 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
     a.keys = keys;
     a.pos = pos;
     a.shared = end;
-    a.partial = reinterpret_cast<float *>(end + round_up(s.units, 4));
+    a.arrived = end + round_up(s.units, 4);
+    a.partial = reinterpret_cast<float *>(a.arrived + round_up(s.counters, 4));
     a.units = s.units;
     const bool vec = vector_rows(g.dout, g.dout_ld, ddt, g.dtable, g.table_ld, tdt, g.dim);
     return for_dtype(ddt, [&](auto dd) {
@@ -671,12 +703,11 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
                     sum_units_kernel<dd(), td(), VEC>,
                     dim3(static_cast<unsigned>(a.units), static_cast<unsigned>(slabs)),
                     dim3(threads), 0, stream, a);
-                if (e != cudaSuccess || a.units < 2) return e;
+                if (e != cudaSuccess || a.units < 3) return e;
                 return launch_dependent(
                     join_units_kernel<dd(), td(), VEC>,
-                    dim3(static_cast<unsigned>((a.units - 1 + kJoinWarps - 1) / kJoinWarps),
-                         static_cast<unsigned>(
-                             std::min<int64_t>(kJoinSlabs, (groups + 31) / 32))),
+                    dim3(static_cast<unsigned>((a.units - 2 + kJoinWarps - 1) / kJoinWarps),
+                         static_cast<unsigned>((groups + 31) / 32)),
                     dim3(kJoinWarps * 32), 0, stream, a);
             };
             return vec ? go(std::true_type{}) : go(std::false_type{});

@@ -33,8 +33,7 @@ constexpr int kBatch = 4;  // 16-byte vectors a thread takes at a time
 // A row cut for 16-byte accesses: head scalars up to the first boundary, then nvec
 // vectors, then the scalars left over.
 struct RowSpan {
-    int head;
-    int64_t nvec, tail;  // tail: the first scalar after the vectors
+    int head, nvec, tail;  // tail: the first scalar after the vectors
 };
 template <int DT>
 __host__ __device__ __forceinline__ RowSpan row_span(const void *row, int64_t n) {
@@ -44,10 +43,23 @@ __host__ __device__ __forceinline__ RowSpan row_span(const void *row, int64_t n)
     RowSpan r;
     r.head = past ? V - past : 0;
     if (r.head > n) r.head = static_cast<int>(n);
-    r.nvec = (n - r.head) / V;
+    r.nvec = (static_cast<int>(n) - r.head) / V;
     r.tail = r.head + r.nvec * V;
     return r;
 }
+
+// One of the 2^log2 CTAs that take a row together, and the row.  (Powers of two: divisions
+// by a number known at run time were a fifth of a CTA's instructions.)
+struct Share {
+    unsigned rank, log2;
+    int64_t row;
+
+    __device__ __forceinline__ explicit Share(unsigned log2_)
+        : rank(blockIdx.x & ((1u << log2_) - 1)), log2(log2_), row(blockIdx.x >> log2_) {}
+    __device__ __forceinline__ unsigned split() const { return 1u << log2; }
+    __device__ __forceinline__ bool first() const { return rank == 0; }
+    __device__ __forceinline__ bool last() const { return rank == split() - 1; }
+};
 
 // 2^(k (x - top)) for the elements of a row.  k_lo > 0, so that -inf stays -inf.
 struct Exponent {
@@ -131,8 +143,9 @@ struct RowSum {
 // row's.  The maximum first, so that a part is rebased once.  ``part``: shared, [warps];
 // ``whole``: shared, one per CTA.
 __device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, RowSum *whole,
-                                            unsigned split) {
-    const int warps = blockDim.x / 32, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+                                            const Share &sh) {
+    constexpr int warps = kRowThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const auto warp_total = [](float s) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -151,11 +164,11 @@ __device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, Ro
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     e.set(top);
     RowSum row{top, warp_total(w.at(e))};
-    if (split > 1) {
+    if (sh.log2 > 0) {
         cg::cluster_group cluster = cg::this_cluster();
         if (threadIdx.x == 0) *whole = row;
         cluster.sync();
-        w = lane < static_cast<int>(split) ? *cluster.map_shared_rank(whole, lane)
+        w = lane < static_cast<int>(sh.split()) ? *cluster.map_shared_rank(whole, lane)
                                            : RowSum{-INFINITY, 0.f};
         cluster.sync();  // no CTA leaves while another reads its part
         top = w.top;
@@ -184,16 +197,14 @@ __device__ __forceinline__ bool load_label(const LogitsArgs &x, int64_t t, int64
     return *label >= 0 && *label < x.vocab;
 }
 
-// The part of a row's vectors that CTA ``rank`` of ``split`` takes.
+// The part of a row's vectors that a CTA takes.
 struct RowPart {
-    int64_t begin, nvec;
-    int count;
+    int begin, nvec, count;
 
-    __device__ __forceinline__ RowPart(const RowSpan &sp, unsigned rank, unsigned split)
-        : nvec(sp.nvec) {
-        const int64_t each = (nvec + split - 1) / split;
-        begin = min(nvec, each * rank);
-        count = static_cast<int>(min(each, nvec - begin));
+    __device__ __forceinline__ RowPart(const RowSpan &sp, const Share &sh) : nvec(sp.nvec) {
+        const int each = (nvec + static_cast<int>(sh.split()) - 1) >> sh.log2;
+        begin = min(nvec, each * static_cast<int>(sh.rank));
+        count = min(each, nvec - begin);
     }
     __device__ __forceinline__ bool in_bounds(int i) const {
         return fa_in_bounds(begin + i, 1, nvec);
@@ -202,11 +213,10 @@ struct RowPart {
 
 // The scalars of a row outside its vectors: the head by the first CTA, the tail by the last.
 template <typename F>
-__device__ __forceinline__ void row_ends(const RowSpan &sp, int64_t n, unsigned rank,
-                                         unsigned split, F f) {
+__device__ __forceinline__ void row_ends(const RowSpan &sp, int64_t n, const Share &sh, F f) {
     const int t = threadIdx.x;
-    if (rank == 0 && t < sp.head && fa_in_bounds(t, 1, n)) f(static_cast<int64_t>(t));
-    if (rank == split - 1 && t < n - sp.tail && fa_in_bounds(sp.tail + t, 1, n)) f(sp.tail + t);
+    if (sh.first() && t < sp.head && fa_in_bounds(t, 1, n)) f(t);
+    if (sh.last() && t < n - sp.tail && fa_in_bounds(sp.tail + t, 1, n)) f(sp.tail + t);
 }
 
 // One vector of the gradient but for the label's element: -c 2^(k (x - top)) / s.
@@ -225,11 +235,12 @@ __device__ __forceinline__ uint4 gradient_vector(const uint4 &r, const Exponent 
 // it writes anything, and the element, c (1 - p), last.
 template <int DT>
 __device__ __forceinline__ bool label_is_mine(int64_t label, const RowSpan &sp,
-                                              const RowPart &part, unsigned rank, unsigned split) {
-    if (label < sp.head) return rank == 0 && threadIdx.x == label;
-    if (label >= sp.tail) return rank == split - 1 && threadIdx.x == label - sp.tail;
-    const int64_t i = (label - sp.head) / Elem<DT>::kVec - part.begin;
-    return i >= 0 && i < part.count && i % kRowThreads == threadIdx.x;
+                                              const RowPart &part, const Share &sh) {
+    const int at = static_cast<int>(label), t = threadIdx.x;
+    if (at < sp.head) return sh.first() && t == at;
+    if (at >= sp.tail) return sh.last() && t == at - sp.tail;
+    const int i = (at - sp.head) / Elem<DT>::kVec - part.begin;
+    return i >= 0 && i < part.count && i % kRowThreads == t;
 }
 
 // f(i, whole batch) for the vectors i, i + kRowThreads, ... of a thread in batches of N: whole
@@ -246,7 +257,7 @@ __device__ __forceinline__ void for_batches(int count, F f) {
 template <int DT>
 __device__ __forceinline__ void row_gradient(const void *row, void *out, int64_t n,
                                              const LogitsArgs &a, RowSum r, float c,
-                                             int64_t label, unsigned rank, unsigned split) {
+                                             int64_t label, const Share &sh) {
     using E = Elem<DT>;
     using T = typename E::T;
     const T *x = static_cast<const T *>(row);
@@ -256,16 +267,16 @@ __device__ __forceinline__ void row_gradient(const void *row, void *out, int64_t
     const int tid = threadIdx.x;
     if ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) {
         // not co-aligned: element by element
-        for (int64_t i = rank * kRowThreads + tid; i < n; i += split * kRowThreads)
+        for (int64_t i = sh.rank * kRowThreads + tid; i < n; i += sh.split() * kRowThreads)
             if (fa_in_bounds(i, 1, n))
                 y[i] = E::round(fmaf(e(E::widen(x[i])), w, i == label ? c : 0.f));
         return;
     }
     const RowSpan sp = row_span<DT>(row, n);
-    const RowPart part(sp, rank, split);
-    const bool mine = label_is_mine<DT>(label, sp, part, rank, split);
+    const RowPart part(sp, sh);
+    const bool mine = label_is_mine<DT>(label, sp, part, sh);
     const float label_logit = mine ? E::widen(x[label]) : 0.f;
-    row_ends(sp, n, rank, split, [&](int64_t i) { y[i] = E::round(e(E::widen(x[i])) * w); });
+    row_ends(sp, n, sh, [&](int i) { y[i] = E::round(e(E::widen(x[i])) * w); });
     const uint4 *q = reinterpret_cast<const uint4 *>(x + sp.head) + part.begin + tid;
     uint4 *o = reinterpret_cast<uint4 *>(y + sp.head) + part.begin + tid;
     for_batches<kBatch>(part.count, [&](int i0, auto whole) {
@@ -287,13 +298,13 @@ __device__ __forceinline__ void row_gradient(const void *row, void *out, int64_t
 
 // Zeros for (a part of) the row of a token that is not counted.
 template <int DT>
-__device__ __forceinline__ void row_zeros(void *out, int64_t n, unsigned rank, unsigned split) {
+__device__ __forceinline__ void row_zeros(void *out, int64_t n, const Share &sh) {
     using E = Elem<DT>;
     using T = typename E::T;
     T *y = static_cast<T *>(out);
     const RowSpan sp = row_span<DT>(out, n);
-    row_ends(sp, n, rank, split, [&](int64_t i) { y[i] = E::round(0.f); });
-    const RowPart part(sp, rank, split);
+    row_ends(sp, n, sh, [&](int i) { y[i] = E::round(0.f); });
+    const RowPart part(sp, sh);
     uint4 *o = reinterpret_cast<uint4 *>(y + sp.head) + part.begin;
     for (int i = threadIdx.x; i < part.count; i += blockDim.x)
         if (part.in_bounds(i)) __stcs(o + i, make_uint4(0u, 0u, 0u, 0u));
@@ -303,11 +314,11 @@ __device__ __forceinline__ void row_zeros(void *out, int64_t n, unsigned rank, u
 // tail (both are shorter than a warp).
 template <int DT>
 __device__ __forceinline__ void add_ends(Softmax &acc, const void *row, const RowSpan &sp,
-                                         int64_t n, unsigned rank, unsigned split) {
+                                         int64_t n, const Share &sh) {
     if (threadIdx.x >= 32 || sp.nvec * Elem<DT>::kVec == n) return;
     const typename Elem<DT>::T *x = static_cast<const typename Elem<DT>::T *>(row);
     float head = -INFINITY, tail = -INFINITY;
-    row_ends(sp, n, rank, split, [&](int64_t i) {
+    row_ends(sp, n, sh, [&](int i) {
         (i < sp.head ? head : tail) = Elem<DT>::widen(x[i]);
     });
     acc.add1(head);
@@ -323,14 +334,14 @@ __device__ __forceinline__ uint4 no_vector() {
 
 // The softmax statistics of a row by the CTAs of a cluster, read from global memory.
 template <int DT>
-__device__ __forceinline__ RowSum row_softmax(const void *row, const LogitsArgs &a, unsigned rank,
-                                              unsigned split) {
+__device__ __forceinline__ RowSum row_softmax(const void *row, const LogitsArgs &a,
+                                              const Share &sh) {
     using T = typename Elem<DT>::T;
     __shared__ RowSum parts[kRowThreads / 32], whole;
     const RowSpan sp = row_span<DT>(row, a.vocab);
     Softmax acc(a);
-    add_ends<DT>(acc, row, sp, a.vocab, rank, split);
-    const RowPart part(sp, rank, split);
+    add_ends<DT>(acc, row, sp, a.vocab, sh);
+    const RowPart part(sp, sh);
     const int tid = threadIdx.x;
     const uint4 *q =
         reinterpret_cast<const uint4 *>(static_cast<const T *>(row) + sp.head) + part.begin + tid;
@@ -346,27 +357,27 @@ __device__ __forceinline__ RowSum row_softmax(const void *row, const LogitsArgs 
         }
         acc.add<DT, kBatch>(r);
     });
-    return merge_row(acc, parts, &whole, split);
+    return merge_row(acc, parts, &whole, sh);
 }
 
 template <int DT, int IT>
 __global__ void __launch_bounds__(kRowThreads)
-token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split) {
+token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2) {
     using T = typename Elem<DT>::T;
     fa_allow_dependents();
-    const unsigned rank = blockIdx.x % split;
-    const int64_t t = blockIdx.x / split;
+    const Share sh(split_log2);
+    const int64_t t = sh.row;
     int64_t label;
     if (!load_label<IT>(x, t, &label)) {
-        if (rank == 0 && threadIdx.x == 0) {
+        if (sh.first() && threadIdx.x == 0) {
             logp[t] = 0.f;
             if (lse) reinterpret_cast<float2 *>(lse)[t] = make_float2(0.f, 1.f);
         }
         return;
     }
     const T *row = static_cast<const T *>(x.logits) + t * x.ld;
-    const RowSum r = row_softmax<DT>(row, x, rank, split);
-    if (rank == 0 && threadIdx.x == 0) {
+    const RowSum r = row_softmax<DT>(row, x, sh);
+    if (sh.first() && threadIdx.x == 0) {
         logp[t] = label_logp(Elem<DT>::widen(row[label]), r, x.scale);
         if (lse) reinterpret_cast<float2 *>(lse)[t] = make_float2(r.top, r.s);
     }
@@ -376,21 +387,21 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split) {
 // last rows in L2.
 template <int DT, int IT>
 __global__ void __launch_bounds__(kRowThreads)
-logprob_gradient_kernel(LogitGradArgs a, unsigned split) {
+logprob_gradient_kernel(LogitGradArgs a, unsigned split_log2) {
     using T = typename Elem<DT>::T;
-    const unsigned rank = blockIdx.x % split;
-    const int64_t t = a.x.tokens - 1 - blockIdx.x / split;
+    const Share sh(split_log2);
+    const int64_t t = a.x.tokens - 1 - sh.row;
     T *out = static_cast<T *>(a.dlogits) + t * a.dlogits_ld;
     int64_t label;
     if (!load_label<IT>(a.x, t, &label)) {
-        row_zeros<DT>(out, a.x.vocab, rank, split);
+        row_zeros<DT>(out, a.x.vocab, sh);
         return;
     }
     const T *row = static_cast<const T *>(a.x.logits) + t * a.x.ld;
     const float2 l = reinterpret_cast<const float2 *>(a.lse)[t];
     const RowSum r{l.x, l.y};
     const float c = a.dlogp[t] * a.factor * (a.grad_loss ? *a.grad_loss : 1.f);
-    row_gradient<DT>(row, out, a.x.vocab, a.x, r, c, label, rank, split);
+    row_gradient<DT>(row, out, a.x.vocab, a.x, r, c, label, sh);
 }
 
 // ---- preference loss ------------------------------------------------------------
@@ -579,21 +590,22 @@ __global__ void __launch_bounds__(kSummaryThreads) policy_count_kernel(PolicyArg
 // Where the rows' kernel has the divisor of a loss without a denominator from.
 enum Divisor { kGiven, kFromKernel, kCountHere };
 
-// One row by a cluster of ``split`` CTAs.  HELD > 0: each CTA's part of the row, at most
-// 4 * HELD vectors a thread, is copied to shared memory once, in four groups so that the
-// sum begins when the first has come, and the gradient is made from there: one read and
-// one write of the logits.  HELD == 0 (rows wider than a cluster holds): the gradient
-// reads the row again.
+// One row by a cluster of 2^split_log2 CTAs.  HELD > 0: each CTA's part of the row, at most
+// 4 * HELD vectors a thread, is read once and held on chip: three groups of HELD vectors
+// come to shared memory asynchronously, so that the sum begins when the first has come, the
+// fourth to registers (four CTAs of 64 KB rows then fit an SM instead of three).  The
+// gradient is made from there: one read and one write of the logits.  HELD == 0 (rows wider
+// than a cluster holds, or no gradient): the row is read again.
 template <int DT, int IT, int HELD>
-__global__ void __launch_bounds__(kRowThreads)
-policy_row_kernel(PolicyArgs a, unsigned split, Divisor divisor) {
+__global__ void __launch_bounds__(kRowThreads, 4)
+policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
     using E = Elem<DT>;
     using T = typename E::T;
-    extern __shared__ uint4 slot[];  // [4 * HELD][kRowThreads]
+    extern __shared__ uint4 slot[];  // [3 * HELD][kRowThreads]
     __shared__ RowSum parts[kRowThreads / 32], whole;
     __shared__ float coef;
-    const unsigned rank = blockIdx.x % split;
-    const int64_t t = blockIdx.x / split, n = a.x.vocab;
+    const Share sh(split_log2);
+    const int64_t t = sh.row, n = a.x.vocab;
     const int tid = threadIdx.x;
     T *out = a.dlogits ? static_cast<T *>(a.dlogits) + t * a.dlogits_ld : nullptr;
     // Nothing here but summary[3] comes from the counting kernel, which began after all
@@ -601,28 +613,38 @@ policy_row_kernel(PolicyArgs a, unsigned split, Divisor divisor) {
     fa_allow_dependents();
     int64_t label;
     if (!load_label<IT>(a.x, t, &label)) {
-        if (rank == 0 && tid == 0) {
+        if (sh.first() && tid == 0) {
             a.logp[t] = 0.f;
             a.token_loss[t] = 0.f;
             a.token_kl[t] = 0.f;
         }
-        if (out) row_zeros<DT>(out, n, rank, split);
+        if (out) row_zeros<DT>(out, n, sh);
         if (divisor == kFromKernel) fa_grid_dependency_wait();
         return;
     }
     const T *row = static_cast<const T *>(a.x.logits) + t * a.x.ld;
     const RowSpan sp = row_span<DT>(row, n);
-    const RowPart part(sp, rank, split);  // HELD: at most 4 * HELD * kRowThreads vectors
-    const uint4 *q = reinterpret_cast<const uint4 *>(row + sp.head) + part.begin;
-    if (HELD > 0) {
+    const RowPart part(sp, sh);  // HELD: at most 4 * HELD * kRowThreads vectors
+    const uint4 *q = reinterpret_cast<const uint4 *>(row + sp.head) + part.begin + tid;
+    constexpr int kGroup = HELD * kRowThreads;
+    constexpr int kRegs = HELD > 0 ? HELD : 1;
+    uint4 held[kRegs];
+    if constexpr (HELD > 0) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 3; ++g) {
 #pragma unroll
             for (int j = 0; j < HELD; ++j) {
-                const int i = (g * HELD + j) * kRowThreads + tid;
-                if (i < part.count && part.in_bounds(i)) copy_async16(slot + i, q + i);
+                const int i = g * kGroup + j * kRowThreads;
+                if (i + tid < part.count && part.in_bounds(i + tid))
+                    copy_async16(slot + i + tid, q + i);
             }
             copy_async_commit();
+        }
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) {
+            const int i = 3 * kGroup + j * kRowThreads;
+            held[j] = i + tid < part.count && part.in_bounds(i + tid) ? __ldcs(q + i)
+                                                                     : no_vector<DT>();
         }
     }
     // what one thread needs of the token, asked for before the sum
@@ -635,12 +657,12 @@ policy_row_kernel(PolicyArgs a, unsigned split, Divisor divisor) {
     RowSum r;
     if constexpr (HELD > 0) {
         Softmax acc(a.x);
-        add_ends<DT>(acc, row, sp, n, rank, split);
+        add_ends<DT>(acc, row, sp, n, sh);
         const auto group = [&](int g) {
-            const int i0 = g * HELD * kRowThreads;
-            const bool full = i0 + HELD * kRowThreads <= part.count;
+            const int i0 = g * kGroup;
             if (i0 + (tid & ~31) >= part.count) return;
-            uint4 v[HELD];
+            const bool full = i0 + kGroup <= part.count;
+            uint4 v[kRegs];
 #pragma unroll
             for (int j = 0; j < HELD; ++j) {
                 const int i = i0 + j * kRowThreads + tid;
@@ -648,22 +670,21 @@ policy_row_kernel(PolicyArgs a, unsigned split, Divisor divisor) {
             }
             acc.add<DT, HELD>(v);
         };
-        copy_async_wait<3>();
-        group(0);
         copy_async_wait<2>();
-        group(1);
+        group(0);
         copy_async_wait<1>();
-        group(2);
+        group(1);
         copy_async_wait<0>();
-        group(3);
-        r = merge_row(acc, parts, &whole, split);
+        group(2);
+        if (3 * kGroup + (tid & ~31) < part.count) acc.add<DT, HELD>(held);
+        r = merge_row(acc, parts, &whole, sh);
     } else {
-        r = row_softmax<DT>(row, a.x, rank, split);
+        r = row_softmax<DT>(row, a.x, sh);
     }
     if (first) {
         const float logp = label_logp(label_logit, r, a.x.scale);
         const PolicyTerms o = policy_terms(a, in, logp);
-        if (rank == 0) {
+        if (sh.first()) {
             a.logp[t] = logp;
             a.token_loss[t] = o.loss;
             a.token_kl[t] = o.kl;
@@ -680,46 +701,69 @@ policy_row_kernel(PolicyArgs a, unsigned split, Divisor divisor) {
         if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
             const Exponent e(a.x, r.top);
             const float c = coef, w = -c / r.s;
-            row_ends(sp, n, rank, split,
-                     [&](int64_t i) { out[i] = E::round(e(E::widen(row[i])) * w); });
+            row_ends(sp, n, sh, [&](int i) { out[i] = E::round(e(E::widen(row[i])) * w); });
             uint4 *o = reinterpret_cast<uint4 *>(out + sp.head) + part.begin + tid;
-            for_batches<HELD>(part.count, [&](int i0, auto whole) {
+            const auto write = [&](int i, const uint4 &v) {
+                if (part.in_bounds(i + tid)) __stcs(o + i, gradient_vector<DT>(v, e, w));
+            };
+            if (3 * kGroup + (HELD - 1) * kRowThreads + tid < part.count) {  // all of its vectors
+#pragma unroll 1
+                for (int g = 0; g < 3; ++g)
 #pragma unroll
-                for (int j = 0; j < HELD; ++j) {
-                    const int i = i0 + j * kRowThreads;
-                    if ((decltype(whole)::value || i + tid < part.count) && part.in_bounds(i + tid))
-                        __stcs(o + i, gradient_vector<DT>(slot[i + tid], e, w));
-                }
-            });
-            if (label_is_mine<DT>(label, sp, part, rank, split))
+                    for (int j = 0; j < HELD; ++j)
+                        write(g * kGroup + j * kRowThreads, slot[g * kGroup + j * kRowThreads + tid]);
+#pragma unroll
+                for (int j = 0; j < HELD; ++j) write(3 * kGroup + j * kRowThreads, held[j]);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < 3 * kGroup && i + tid < part.count; i += kRowThreads)
+                    write(i, slot[i + tid]);
+#pragma unroll
+                for (int j = 0; j < HELD; ++j)
+                    if (3 * kGroup + j * kRowThreads + tid < part.count)
+                        write(3 * kGroup + j * kRowThreads, held[j]);
+            }
+            if (label_is_mine<DT>(label, sp, part, sh))
                 out[label] = E::round(fmaf(e(label_logit), w, c));
             return;
         }
     }
-    row_gradient<DT>(row, out, n, a.x, r, coef, label, rank, split);
+    row_gradient<DT>(row, out, n, a.x, r, coef, label, sh);
 }
 
-// The sums over the tokens, by one CTA.
+// The sums over the tokens, by a cluster of CTAs: each adds its tokens, the first adds the
+// CTAs' sums in order.
+constexpr unsigned kSummaryCtas = 8;
+struct PolicySums {
+    Sum2 loss, kl;
+    int n, clipped;
+};
 template <int IT>
 __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyArgs a) {
+    __shared__ Sum2 parts[2][kSummaryThreads / 32];
+    __shared__ int counts[2];
+    __shared__ PolicySums sums;
+    cg::cluster_group cluster = cg::this_cluster();
+    const unsigned ctas = gridDim.x;
+    if (threadIdx.x < 2) counts[threadIdx.x] = 0;
     fa_grid_dependency_wait();
     Sum2 loss, kl;
     int n = 0, clipped = 0;
-#pragma unroll 4
-    for (int64_t t = threadIdx.x; t < a.x.tokens; t += kSummaryThreads) {
+#pragma unroll 2
+    for (int64_t t = blockIdx.x * kSummaryThreads + threadIdx.x; t < a.x.tokens;
+         t += ctas * kSummaryThreads) {
         int64_t label;
-        if (!load_label<IT>(a.x, t, &label)) continue;
-        const PolicyToken in(a, t);
-        loss.add(in.weight * a.token_loss[t]);
-        kl.add(a.token_kl[t]);
+        const bool counted = load_label<IT>(a.x, t, &label);
+        const PolicyToken in(a, t);  // loaded beside the label
+        const float token_loss = a.token_loss[t], token_kl = a.token_kl[t], logp = a.logp[t];
+        if (!counted) continue;
+        loss.add(in.weight * token_loss);
+        kl.add(token_kl);
         // the ratio and the clip as the rows' kernel took them
-        const float r = expf(a.logp[t] - in.old_logp);
+        const float r = expf(logp - in.old_logp);
         clipped += r * in.adv > fminf(fmaxf(r, a.clip_lo), a.clip_hi) * in.adv;
         ++n;
     }
-    __shared__ Sum2 parts[2][kSummaryThreads / 32];
-    __shared__ int counts[2];
-    if (threadIdx.x < 2) counts[threadIdx.x] = 0;
     loss = cta_sum2(loss, parts[0]);
     kl = cta_sum2(kl, parts[1]);
     n = __reduce_add_sync(0xffffffffu, n);
@@ -729,21 +773,31 @@ __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyA
         atomicAdd(&counts[1], clipped);
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        const float all = static_cast<float>(counts[0]), by = fmaxf(all, 1.f);
-        a.summary[0] = loss.value() / (a.denominator != 0.f ? a.denominator : by);
-        a.summary[1] = kl.value() / by;
-        a.summary[2] = static_cast<float>(counts[1]) / by;
-        a.summary[3] = all;
+    if (threadIdx.x == 0) sums = PolicySums{loss, kl, counts[0], counts[1]};
+    cluster.sync();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        PolicySums all = sums;
+        for (unsigned r = 1; r < ctas; ++r) {
+            const PolicySums *o = cluster.map_shared_rank(&sums, r);
+            all.loss.add(o->loss);
+            all.kl.add(o->kl);
+            all.n += o->n;
+            all.clipped += o->clipped;
+        }
+        const float count = static_cast<float>(all.n), by = fmaxf(count, 1.f);
+        a.summary[0] = all.loss.value() / (a.denominator != 0.f ? a.denominator : by);
+        a.summary[1] = all.kl.value() / by;
+        a.summary[2] = static_cast<float>(all.clipped) / by;
+        a.summary[3] = count;
     }
+    cluster.sync();  // no CTA leaves while the first reads its sums
 }
 
-// CTAs a row is split over so that a call of few tokens covers the GPU: doubled while the
-// grid is under two CTAs an SM and each still has ``least`` vectors.
-unsigned split_for(int64_t tokens, int64_t nvec, int64_t least, unsigned at_least) {
-    unsigned s = at_least;
-    while (s < 8 && tokens * s < 2 * 152 && nvec / (2 * s) >= least) s *= 2;
-    return s;
+// CTAs a row is split over (their logarithm) so that a call of few tokens covers the GPU:
+// doubled while the grid is under two CTAs an SM and each still has ``least`` vectors.
+unsigned split_for(int64_t tokens, int64_t nvec, int64_t least, unsigned log2) {
+    while (log2 < 3 && (tokens << log2) < 2 * 152 && nvec >> (log2 + 1) >= least) ++log2;
+    return log2;
 }
 
 }  // namespace
@@ -765,13 +819,13 @@ cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, fa_itype lt,
                                   float *lse, cudaStream_t stream) {
     return for_dtype(dt, [&](auto d) {
         return for_itype(lt, [&](auto i) {
-            const unsigned split =
-                split_for(x.tokens, x.vocab / Elem<d()>::kVec, kBatch * kRowThreads, 1);
-            if (x.tokens * split > kMaxGridX) return cudaErrorInvalidConfiguration;
+            const unsigned log2 =
+                split_for(x.tokens, x.vocab / Elem<d()>::kVec, kBatch * kRowThreads, 0);
+            if (x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;
             return launch_clusters(token_logprobs_kernel<d(), i()>,
-                                   dim3(static_cast<unsigned>(x.tokens * split)),
-                                   dim3(kRowThreads), 0, split, false, stream, x, logp, lse,
-                                   split);
+                                   dim3(static_cast<unsigned>(x.tokens << log2)),
+                                   dim3(kRowThreads), 0, 1u << log2, false, stream, x, logp, lse,
+                                   log2);
         });
     });
 }
@@ -780,11 +834,11 @@ cudaError_t launch_token_logprobs_gradient(const LogitGradArgs &a, fa_dtype dt, 
                                            cudaStream_t stream) {
     return for_dtype(dt, [&](auto d) {
         return for_itype(lt, [&](auto i) {
-            const unsigned split = split_for(a.x.tokens, a.x.vocab / Elem<d()>::kVec,
-                                             kBatch * kRowThreads, 1);
-            if (a.x.tokens * split > kMaxGridX) return cudaErrorInvalidConfiguration;
+            const unsigned log2 =
+                split_for(a.x.tokens, a.x.vocab / Elem<d()>::kVec, kBatch * kRowThreads, 0);
+            if (a.x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;
             logprob_gradient_kernel<d(), i()>
-                <<<static_cast<unsigned>(a.x.tokens * split), kRowThreads, 0, stream>>>(a, split);
+                <<<static_cast<unsigned>(a.x.tokens << log2), kRowThreads, 0, stream>>>(a, log2);
             return cudaGetLastError();
         });
     });
@@ -805,18 +859,18 @@ cudaError_t launch_preference(const PreferenceArgs &a, fa_itype lt, cudaStream_t
 namespace {
 
 template <int DT, int IT, int HELD>
-cudaError_t launch_policy_rows(const PolicyArgs &a, unsigned split, Divisor divisor,
+cudaError_t launch_policy_rows(const PolicyArgs &a, unsigned log2, Divisor divisor,
                                cudaStream_t stream) {
-    constexpr int kSmem = 4 * HELD * kRowThreads * 16;
+    constexpr int kSmem = 3 * HELD * kRowThreads * 16;
     auto kernel = policy_row_kernel<DT, IT, HELD>;
-    if (kSmem > 48 * 1024) {
+    if (kSmem >= 48 * 1024) {  // with the static part, past what needs no asking
         cudaError_t err =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (err != cudaSuccess) return err;
     }
-    return launch_clusters(kernel, dim3(static_cast<unsigned>(a.x.tokens * split)),
-                           dim3(kRowThreads), kSmem, split, divisor == kFromKernel, stream, a,
-                           split, divisor);
+    return launch_clusters(kernel,
+                           dim3(static_cast<unsigned>(a.x.tokens << log2)), dim3(kRowThreads),
+                           kSmem, 1u << log2, divisor == kFromKernel, stream, a, log2, divisor);
 }
 
 }  // namespace
@@ -839,23 +893,24 @@ cudaError_t launch_policy(const PolicyArgs &a, fa_dtype dt, fa_itype lt, cudaStr
             cudaError_t err = for_dtype(dt, [&](auto d) {
                 constexpr int64_t kMost = 4 * 4 * kRowThreads;  // vectors a CTA holds
                 const int64_t nvec = a.x.vocab / Elem<d()>::kVec;
-                unsigned split = 1;
-                while (split < 8 && nvec > split * kMost) split *= 2;
-                const bool held = a.dlogits && nvec <= split * kMost;
-                split = split_for(a.x.tokens, nvec, kRowThreads, held || !a.dlogits ? split : 1);
-                if (a.x.tokens * split > kMaxGridX) return cudaErrorInvalidConfiguration;
-                const int64_t each = (nvec + split - 1) / split;
-                if (!held) return launch_policy_rows<d(), i(), 0>(a, split, divisor, stream);
+                unsigned log2 = 0;
+                while (log2 < 3 && nvec > kMost << log2) ++log2;
+                const bool held = a.dlogits && nvec <= kMost << log2;
+                log2 = split_for(a.x.tokens, nvec, kRowThreads, held ? log2 : 0);
+                if (a.x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;
+                const int64_t each = (nvec + (int64_t(1) << log2) - 1) >> log2;
+                if (!held) return launch_policy_rows<d(), i(), 0>(a, log2, divisor, stream);
                 if (each <= kMost / 4)
-                    return launch_policy_rows<d(), i(), 1>(a, split, divisor, stream);
+                    return launch_policy_rows<d(), i(), 1>(a, log2, divisor, stream);
                 if (each <= kMost / 2)
-                    return launch_policy_rows<d(), i(), 2>(a, split, divisor, stream);
-                return launch_policy_rows<d(), i(), 4>(a, split, divisor, stream);
+                    return launch_policy_rows<d(), i(), 2>(a, log2, divisor, stream);
+                return launch_policy_rows<d(), i(), 4>(a, log2, divisor, stream);
             });
             if (err != cudaSuccess) return err;
         }
-        return launch_dependent(policy_summary_kernel<i()>, dim3(1), dim3(kSummaryThreads), 0,
-                                stream, a);
+        const unsigned ctas = a.x.tokens > 2 * kSummaryThreads ? kSummaryCtas : 1;
+        return launch_clusters(policy_summary_kernel<i()>, dim3(ctas), dim3(kSummaryThreads), 0,
+                               ctas, true, stream, a);
     });
 }
 

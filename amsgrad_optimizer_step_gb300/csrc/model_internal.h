@@ -49,6 +49,7 @@ cudaError_t launch_embedding_lookup(const LookupArgs &a, fa_itype idt, fa_dtype 
 struct EmbeddingScratch {
     int64_t chunks;  // runs of kSortChunk tokens that one cluster sorts
     int64_t units;   // runs of kSumUnit sorted tokens that one CTA adds
+    int64_t counters;      // of the sums' kernel
     int64_t sorted_words;  // 32-bit words of one sorted array (tokens, rounded up to 4)
     int64_t bytes;
 };

@@ -3,19 +3,18 @@
 // Gradient of row v: scale * sum over the tokens t with id v of dout[t].  The tokens
 // are sorted by id (stable: ascending t within an id), so that each id's rows are one
 // run of the sorted order, and the sorted order is cut into units of kSumUnit tokens,
-// each added by one CTA in order: the work of a unit does not depend on how the ids
-// are distributed.  A run inside one unit is finished there.  Units that share a run leave
-// FP32 partial sums: of two, the one that comes second adds both; more are added in unit
-// order by the join.  (Two numbers have one sum, whoever adds them: the result does not
-// depend on the order in which CTAs run.)
+// one CTA each.  A run of at most kSumUnit tokens is added by the unit it begins in, past
+// that unit's end if need be; a longer one is cut where the units are, and their FP32
+// partial sums are added in unit order by the join.  So the work of a unit is at most twice
+// another's however the ids are distributed, and only long runs pay for partial sums.
 //
 // Sort: a cluster of up to sixteen CTAs sorts up to kSortChunk tokens in its shared memory,
 // least significant digit first: each warp ranks its tokens by digit, the CTAs exchange
 // their digit counts, each CTA orders its own by digit, and the runs so made go to their
 // places in the cluster, in whichever CTA's memory that is (sent token by token, each to
 // a place of its own, a pass took 18 us).  A chunk's ids are sorted in two or three such passes with no
-// global memory between them; the rest of the GPU zeroes the table meanwhile, so that only
-// ids that occur are written after.  With several chunks, a token's place in the whole order is
+// global memory between them; the rest of the GPU zeroes the table meanwhile.  With several
+// chunks, a token's place in the whole order is
 // its place in its chunk plus, for every other chunk, the number of its ids that come
 // before (ties: earlier chunks come before), found by binary search.
 #include <algorithm>
@@ -41,7 +40,8 @@ namespace cg = cooperative_groups;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortItems = kSortSlots / kSortThreads;
-constexpr int kMostDigits = 512;  // values of a digit: up to nine bits
+constexpr int kMostDigitBits = 9;
+constexpr int kMostDigits = 1 << kMostDigitBits;
 constexpr int kSumThreads = 256;
 constexpr int kMergeThreads = 256;
 constexpr int kJoinWarps = 8;
@@ -90,32 +90,75 @@ lookup_kernel(LookupArgs a, int groups, int lanes_log2) {
 
 // ---- sort ----------------------------------------------------------------------
 
-// Rows of the table that are zeroed while its gradient's tokens are sorted: bytes from p,
-// ld bytes apart.
+// What is zeroed of the table while its gradient's tokens are sorted: rows of ``bytes`` bytes
+// from p, ld bytes apart; with claims, only the rows of ids that no token has.
 struct ZeroArgs {
     char *p;
     int64_t rows, bytes, ld;
+    const uint32_t *claims;  // [rows], or nullptr
 };
 
-// The share of CTA ``rank`` of ``ctas``: rows in turn, or stretches of a single row.
-__device__ __forceinline__ void zero_rows(const ZeroArgs &z, int64_t rank, int64_t ctas) {
-    const int64_t parts = z.rows == 1 ? ctas : 1;
-    for (int64_t row = z.rows == 1 ? 0 : rank; row < z.rows; row += z.rows == 1 ? 1 : ctas) {
-        char *p = z.p + row * z.ld;
-        const int64_t past = reinterpret_cast<uintptr_t>(p) & 15;
-        const int64_t head = past ? min(int64_t(16) - past, z.bytes) : 0;
-        const int64_t vecs = (z.bytes - head) / 16, tail = head + vecs * 16;
-        if (parts == 1 || rank == 0) {  // elements are two bytes at least
-            for (int64_t i = 2 * threadIdx.x; i < head; i += 2 * blockDim.x)
-                *reinterpret_cast<uint16_t *>(p + i) = 0;
-            for (int64_t i = tail + 2 * threadIdx.x; i < z.bytes; i += 2 * blockDim.x)
-                *reinterpret_cast<uint16_t *>(p + i) = 0;
+// claims[id] = a token that has the id, whichever comes last.  Entries of other ids hold
+// anything: a token that does not have the id shows that the entry is none.
+template <int IT>
+__global__ void __launch_bounds__(256)
+claim_kernel(const void *ids, uint32_t *claims, int64_t tokens, int64_t vocab, int64_t padding_idx) {
+    fa_allow_dependents();
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (t >= tokens) return;
+    const int64_t id = load_id<IT>(ids, t);
+    if (id >= 0 && id < vocab && id != padding_idx && fa_in_bounds(id, 1, vocab))
+        claims[id] = static_cast<uint32_t>(t);
+}
+
+// ``bytes`` zeros from p (two-byte aligned) by ``count`` threads, of which this is ``rank``.
+__device__ __forceinline__ void zero_bytes(char *p, int64_t bytes, int64_t rank, int64_t count) {
+    const int64_t past = reinterpret_cast<uintptr_t>(p) & 15;
+    const int64_t head = past ? min(int64_t(16) - past, bytes) : 0;
+    const int64_t vecs = (bytes - head) / 16, tail = head + vecs * 16;
+    if (2 * rank < head) *reinterpret_cast<uint16_t *>(p + 2 * rank) = 0;
+    if (tail + 2 * rank < bytes) *reinterpret_cast<uint16_t *>(p + tail + 2 * rank) = 0;
+    uint4 *q = reinterpret_cast<uint4 *>(p + head);
+    for (int64_t i = rank; i < vecs; i += count)
+        if (fa_in_bounds(i, 1, vecs)) __stcs(q + i, make_uint4(0u, 0u, 0u, 0u));
+}
+
+// The share of CTA ``cta`` of ``ctas``.
+template <int IT>
+__device__ __forceinline__ void zero_rows(const ZeroArgs &z, const void *ids, int64_t tokens,
+                                          int64_t padding_idx, int64_t cta, int64_t ctas) {
+    if (z.rows == 1) {
+        zero_bytes(z.p, z.bytes, cta * kSortThreads + threadIdx.x, ctas * kSortThreads);
+        return;
+    }
+    // a warp takes kRows rows at a time; lane r asks whether row r has a token
+    constexpr int kRows = 4;
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = ctas * kSortWarps, warp = cta * kSortWarps + threadIdx.x / 32;
+    for (int64_t v0 = warp * kRows; v0 < z.rows; v0 += warps * kRows) {
+        bool absent = lane < kRows && v0 + lane < z.rows;
+        if (z.claims && absent) {
+            const uint32_t t = z.claims[v0 + lane];
+            absent = t >= tokens || load_id<IT>(ids, t) != v0 + lane || v0 + lane == padding_idx;
         }
-        uint4 *q = reinterpret_cast<uint4 *>(p + head);
-        const int64_t each = (vecs + parts - 1) / parts;
-        const int64_t begin = parts == 1 ? 0 : rank * each, end = min(vecs, begin + each);
-        for (int64_t i = begin + threadIdx.x; i < end; i += blockDim.x)
-            if (fa_in_bounds(i, 1, vecs)) q[i] = make_uint4(0u, 0u, 0u, 0u);
+        const unsigned rows = __ballot_sync(0xffffffffu, absent);
+        for (int r = 0; r < kRows; ++r)
+            if (rows >> r & 1u) zero_bytes(z.p + (v0 + r) * z.ld, z.bytes, lane, 32);
+    }
+}
+
+// Rows that are asked into L2 while the tokens are sorted: the sums read them next.
+struct PrefetchArgs {
+    const char *p;
+    int64_t rows, bytes, ld;
+};
+__device__ __forceinline__ void prefetch_rows(const PrefetchArgs &f, int64_t cta, int64_t ctas) {
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = ctas * kSortWarps, warp = cta * kSortWarps + threadIdx.x / 32;
+    for (int64_t r = warp; r < f.rows; r += warps) {
+        const char *row = f.p + r * f.ld;
+        for (int64_t i = lane * 128; i < f.bytes; i += 32 * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row + i));
     }
 }
 
@@ -126,8 +169,8 @@ struct SortArgs {
     int passes, digit_bits;   // passes * digit_bits bits hold vocab, the key of a token without an id
     unsigned chunks, ctas;    // clusters that sort, and the CTAs of a cluster
     ZeroArgs zero;
-    uint32_t *arrived;        // counters of the sums' kernel, zeroed here
-    int64_t counters;
+    PrefetchArgs prefetch;
+    uint32_t *long_runs;      // their number, zeroed here
 };
 
 // A token on its way: its id above its index in the chunk.
@@ -146,12 +189,15 @@ template <int IT, typename Item>
 __global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a) {
     fa_allow_dependents();
     if (blockIdx.x >= a.chunks * a.ctas) {
-        zero_rows(a.zero, blockIdx.x - a.chunks * a.ctas, gridDim.x - a.chunks * a.ctas);
+        const int64_t cta = blockIdx.x - a.chunks * a.ctas, ctas = gridDim.x - a.chunks * a.ctas;
+        if (a.zero.rows) {
+            fa_grid_dependency_wait();  // the claims
+            zero_rows<IT>(a.zero, a.ids, a.tokens, a.padding_idx, cta, ctas);
+        }
+        prefetch_rows(a.prefetch, cta, ctas);
         return;
     }
-    for (int64_t i = blockIdx.x * kSortThreads + threadIdx.x; i < a.counters;
-         i += static_cast<int64_t>(a.chunks * a.ctas) * kSortThreads)
-        a.arrived[i] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.long_runs = 0;
     extern __shared__ uint4 raw[];
     SortSmem<Item> &s = *reinterpret_cast<SortSmem<Item> *>(raw);
     cg::cluster_group cluster = cg::this_cluster();
@@ -190,7 +236,15 @@ __global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a) {
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
             const int d = digit(item[j]);
-            const unsigned same = __match_any_sync(0xffffffffu, d);
+            // the lanes with this digit, from a ballot of each of its bits (with match.any a
+            // sort of 4096 tokens took 2 us more)
+            unsigned same = 0xffffffffu;
+#pragma unroll
+            for (int b = 0; b < kMostDigitBits; ++b) {
+                const bool bit = d >> b & 1;
+                const unsigned set = __ballot_sync(0xffffffffu, bit);
+                same &= bit ? set : ~set;
+            }
             const int ahead = __popc(same & ((1u << lane) - 1));
             const uint16_t c = s.count[warp][d];
             __syncwarp();
@@ -309,28 +363,37 @@ merge_chunks_kernel(const uint32_t *keys, const uint32_t *pos, uint32_t *out_key
 
 // ---- sums ----------------------------------------------------------------------
 
+// A run of more than kSumUnit tokens that several units share: its first and last unit.
+struct LongRun {
+    uint32_t first, last, key;
+};
+
 struct SumArgs {
     EmbeddingGradArgs g;
     const uint32_t *keys, *pos;  // sorted
-    uint32_t *shared;            // [units]: runs that the join adds up
-    uint32_t *arrived;           // [slabs][units]: sums of the run across the unit's end so far
+    uint32_t *long_runs;         // how many there are,
+    LongRun *runs;               // and which, in any order
     float *partial;              // [units][2][dim]
     int64_t units;
 };
-// shared[u]: the unit is one run that began before it and goes on after it; it begins a run
-// that goes on past the next unit.
-constexpr uint32_t kThrough = 1, kBegins = 2;
 
-// Writes ``sum * scale`` to (or adds it to) elements [c, c + N) of table row v.
-template <int TT, int N>
+// Elements [c, c + N) of table row v.
+template <int TT>
+__device__ __forceinline__ typename Elem<TT>::T *table_row(const EmbeddingGradArgs &g, int64_t v,
+                                                           int64_t c) {
+    return static_cast<typename Elem<TT>::T *>(g.dtable) + v * g.table_ld + c;
+}
+
+// Writes ``sum * scale`` to elements [c, c + N) of table row v, or with ACC adds it to what
+// they were.
+template <int TT, int N, bool ACC>
 __device__ __forceinline__ void finish_row(const EmbeddingGradArgs &g, int64_t v, int64_t c,
-                                           const float *sum) {
-    using TE = typename Elem<TT>::T;
+                                           const float *sum, const Raw<TT, N> &before) {
     if (!fa_in_bounds(v, 1, g.vocab) || !fa_in_bounds(c, N, g.dim)) return;
-    TE *row = static_cast<TE *>(g.dtable) + v * g.table_ld + c;
+    typename Elem<TT>::T *row = table_row<TT>(g, v, c);
     float y[N];
-    if (g.accumulate) {
-        load_n<TT, N>(row, y);
+    if (ACC) {
+        before.widen(y);
 #pragma unroll
         for (int j = 0; j < N; ++j) y[j] = fmaf(sum[j], g.scale, y[j]);
     } else {
@@ -353,13 +416,12 @@ __device__ __forceinline__ void store_partial(float *p, const float *x) {
         for (int j = 0; j < N; ++j) p[j] = x[j];
     }
 }
-// (another CTA's: from L2)
 template <int N>
 __device__ __forceinline__ void load_partial(const float *p, float *x) {
     if constexpr (N % 4 == 0) {
 #pragma unroll
         for (int j = 0; j < N; j += 4) {
-            const float4 f = __ldcg(reinterpret_cast<const float4 *>(p + j));
+            const float4 f = *reinterpret_cast<const float4 *>(p + j);
             x[j] = f.x;
             x[j + 1] = f.y;
             x[j + 2] = f.z;
@@ -367,17 +429,38 @@ __device__ __forceinline__ void load_partial(const float *p, float *x) {
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = __ldcg(p + j);
+        for (int j = 0; j < N; ++j) x[j] = p[j];
     }
 }
 
-// CTA (u, slab): unit u's tokens, columns of slab.  A run that began before the unit
+// The last token of the run of ``key`` that goes through token ``from``, by a warp: the lanes
+// probe further and further ahead, then the stretch that the end is in, 31 points at a time.
+__device__ __forceinline__ int64_t run_end(const uint32_t *keys, int64_t tokens, int64_t from,
+                                           uint32_t key, int lane) {
+    const auto same = [&](int64_t i) { return i < tokens && keys[i] == key; };
+    int64_t lo = from, hi = from + (int64_t(1) << 31);  // same(lo), not same(hi)
+    const unsigned far = __ballot_sync(0xffffffffu, same(from + (int64_t(1) << lane)));
+    const int k = far == 0xffffffffu ? 32 : __ffs(~far) - 1;
+    if (k < 32) hi = from + (int64_t(1) << k);
+    if (k > 0) lo = from + (int64_t(1) << (k - 1));
+    while (hi - lo > 1) {
+        const int64_t step = (hi - lo + 31) / 32;
+        const unsigned on = __ballot_sync(0xffffffffu, lo + (lane + 1) * step < hi &&
+                                                           same(lo + (lane + 1) * step));
+        const int n = __popc(on);  // the run is sorted: a prefix of the points
+        hi = min(hi, lo + (n + 1) * step);
+        lo += n * step;
+    }
+    return lo;
+}
+
+// CTA (u, slab): unit u's runs, columns of slab.  A long run that began before the unit
 // leaves its sum in partial[u][0], one that goes on after it in partial[u][1] (a run
 // that does both, in [0]).
-template <int DT, int TT, bool VEC>
-__global__ void __launch_bounds__(kSumThreads, 4) sum_units_kernel(SumArgs a) {
+template <int DT, int TT, bool VEC, bool ACC>
+__global__ void __launch_bounds__(kSumThreads, ACC ? 4 : 5) sum_units_kernel(SumArgs a) {
+    constexpr int kSumAhead = ACC ? 4 : 6;  // rows a thread has in flight, of dout and the table
     constexpr int N = kGroup<DT, TT, VEC>;
-    constexpr int kAhead = 8;  // rows in flight
     constexpr uint32_t kNone = 0xffffffffu;  // no id: ids are below 2^31
     using DE = typename Elem<DT>::T;
     const EmbeddingGradArgs &g = a.g;
@@ -385,150 +468,129 @@ __global__ void __launch_bounds__(kSumThreads, 4) sum_units_kernel(SumArgs a) {
     fa_allow_dependents();
     const int64_t c = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * N;
     const int64_t u = blockIdx.x, first = u * kSumUnit;
-    __shared__ uint32_t key[kSumUnit];
-    __shared__ uint32_t pos[kSumUnit];
-    __shared__ uint32_t ends;       // bit i: token i is its run's last here
-    __shared__ bool began, goes;    // the first run began before the unit; the last goes on
-    __shared__ bool with_last, with_next;  // and is shared with that one unit only
-    __shared__ bool add_last, add_next;    // whose sum came first: this CTA adds both
+    __shared__ uint32_t key[2 * kSumUnit], pos[2 * kSumUnit];
+    __shared__ uint64_t ends;         // bit i: token i is its run's last here
+    __shared__ int begin, end;        // the tokens to add
+    __shared__ int head_end, tail;    // where a long head ends; the token that leaves a long run
+    static_assert(kSumUnit == 32, "a warp holds a unit");
     if (threadIdx.x < 32) {
+        constexpr unsigned kAll = 0xffffffffu;
         const int lane = threadIdx.x;
-        const auto key_at = [&](int64_t i) { return i >= 0 && i < g.tokens ? a.keys[i] : kNone; };
-        const uint32_t k = key_at(first + lane);
-        // lanes 0 to 3: the tokens on both sides of the units before and after this one
-        const uint32_t around =
-            key_at(lane == 0   ? first - 1
-                   : lane == 1 ? first - kSumUnit - 1
-                   : lane == 2 ? first + kSumUnit
-                   : lane == 3 ? first + 2 * kSumUnit
-                               : -1);
-        pos[lane] = first + lane < g.tokens ? a.pos[first + lane] : 0u;
-        key[lane] = k < g.vocab ? k : kNone;
-        const uint32_t head = __shfl_sync(0xffffffffu, k, 0), tail = __shfl_sync(0xffffffffu, k, 31);
-        const uint32_t after = __shfl_sync(0xffffffffu, around, 2);
-        uint32_t next = __shfl_down_sync(0xffffffffu, k, 1);
-        if (lane == 31) next = after;
-        const uint32_t e = __ballot_sync(0xffffffffu, next != k || lane == 31);
-        const bool in = __shfl_sync(0xffffffffu, around, 0) == head && head < g.vocab;
-        const bool on = after == tail && tail < g.vocab;
-        const bool one = e == 0x80000000u;  // one run: only the last token ends one
-        const bool before_last = __shfl_sync(0xffffffffu, around, 1) == head;
-        const bool after_next = __shfl_sync(0xffffffffu, around, 3) == tail;
+        const auto key_at = [&](int64_t i) {
+            const uint32_t k = i >= 0 && i < g.tokens ? a.keys[i] : kNone;
+            return k < g.vocab ? k : kNone;
+        };
+        const uint32_t prev = key_at(first - 32 + lane), own = key_at(first + lane),
+                       next = key_at(first + 32 + lane);
+        const uint32_t own_pos = first + lane < g.tokens ? a.pos[first + lane] : 0u;
+        const uint32_t next_pos = first + 32 + lane < g.tokens ? a.pos[first + 32 + lane] : 0u;
+        key[lane] = own;
+        key[32 + lane] = next;
+        pos[lane] = own_pos;
+        pos[32 + lane] = next_pos;
+        const uint32_t h = __shfl_sync(kAll, own, 0), t = __shfl_sync(kAll, own, 31);
+        // tokens of the first run before, in and after the unit; of the last run in and after it
+        const auto from_low = [](unsigned same) { return same == kAll ? 32 : __ffs(~same) - 1; };
+        const int h_before = __clz(~__ballot_sync(kAll, prev == h));
+        const int h_in = from_low(__ballot_sync(kAll, own == h));
+        const int t_in = __clz(~__ballot_sync(kAll, own == t));
+        const int t_after = from_low(__ballot_sync(kAll, next == t));
+        const bool in = h != kNone && h_before > 0, on = t != kNone && t_after > 0;
+        const bool h_long = in && h_before + h_in + (h_in == 32 ? t_after : 0) > 32;
+        const bool t_long = on && (t_in == 32 ? h_before : 0) + t_in + t_after > 32;
+        const int valid = __popc(__ballot_sync(kAll, own != kNone));
+        const int to = on && !t_long ? 32 + t_after : valid;
+        uint32_t after = __shfl_down_sync(kAll, own, 1);
+        const uint32_t next0 = __shfl_sync(kAll, next, 0);
+        const uint32_t after_next = __shfl_down_sync(kAll, next, 1);
+        if (lane == 31) after = to > 32 ? next0 : kNone;
+        const uint64_t e = __ballot_sync(kAll, own != after) |
+                           static_cast<uint64_t>(
+                               __ballot_sync(kAll, next != after_next || lane == 31)) << 32;
         if (lane == 0) {
             ends = e;
-            began = in;
-            goes = on;
-            with_last = in && !(one && on) && !before_last;
-            with_next = on && !(one && in) && !after_next;
-            if (blockIdx.y == 0)
-                a.shared[u] = in && on && one ? kThrough : on && after_next ? kBegins : 0u;
+            begin = in && !h_long ? h_in : 0;  // a short run is the unit's before
+            end = to;
+            head_end = h_long ? h_in : 0;
+            tail = t_long ? 31 : -1;
         }
-    }
-    __syncthreads();
-    const bool here = c < g.dim;
-    const uint32_t last = ends;
-    bool began_before = began;
-    const bool goes_on = goes;
-    if (here) {
-        const DE *dout = static_cast<const DE *>(g.dout) + c;
-        float sum[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) sum[j] = 0.f;
-#pragma unroll 1
-        for (int i0 = 0; i0 < kSumUnit && key[i0] != kNone; i0 += kAhead) {
-            Raw<DT, N> rows[kAhead];
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (key[i0 + k] != kNone && fa_in_bounds(c, N, g.dim) &&
-                    fa_in_bounds(pos[i0 + k], 1, g.tokens))
-                    rows[k].load(dout + static_cast<int64_t>(pos[i0 + k]) * g.dout_ld);
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int i = i0 + k;
-                const uint32_t v = key[i];
-                if (v == kNone) break;  // tokens without an id come last
-                float x[N];
-                rows[k].widen(x);
-#pragma unroll
-                for (int j = 0; j < N; ++j) sum[j] += x[j];
-                if (!(last >> i & 1u)) continue;
-                const bool on = i == kSumUnit - 1 && goes_on;
-                if (began_before || on)
-                    store_partial<N>(a.partial + (2 * u + (began_before ? 0 : 1)) * g.dim + c, sum);
-                else
-                    finish_row<TT, N>(g, v, c, sum);
-                began_before = false;
-#pragma unroll
-                for (int j = 0; j < N; ++j) sum[j] = 0.f;
+        if (blockIdx.y == 0 && t_long && !(in && t_in == 32)) {  // begins here, and goes on
+            const int64_t last = run_end(a.keys, g.tokens, first + 32, t, lane);
+            if (lane == 0) {
+                const uint32_t k = atomicAdd(a.long_runs, 1u);
+                if (fa_in_bounds(k, 1, a.units))
+                    a.runs[k] = LongRun{static_cast<uint32_t>(u),
+                                        static_cast<uint32_t>(last / kSumUnit), t};
             }
         }
     }
-    if (!with_last && !with_next) return;  // the same for the whole CTA
-    // partial sums are in memory before they are counted, and the other's read after
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) {
-        uint32_t *arrived = a.arrived + blockIdx.y * a.units;
-        add_last = with_last && atomicAdd(&arrived[u - 1], 1u) == 1u;
-        add_next = with_next && atomicAdd(&arrived[u], 1u) == 1u;
-        __threadfence();
-    }
-    __syncthreads();
-    if (!here) return;
-    const auto add_pair = [&](int64_t w, uint32_t v) {  // the run across the end of unit w
-        float x[N], y[N];
-        load_partial<N>(a.partial + (2 * w + 1) * g.dim + c, x);
-        load_partial<N>(a.partial + 2 * (w + 1) * g.dim + c, y);
+    if (c >= g.dim) return;
+    const DE *dout = static_cast<const DE *>(g.dout) + c;
+    const uint64_t last = ends;
+    const int to = end;
+    float sum[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] += y[j];
-        finish_row<TT, N>(g, v, c, x);
-    };
-    if (add_last) add_pair(u - 1, key[0]);
-    if (add_next) add_pair(u, key[kSumUnit - 1]);
+    for (int j = 0; j < N; ++j) sum[j] = 0.f;
+#pragma unroll 1
+    for (int i0 = begin; i0 < to; i0 += kSumAhead) {
+        Raw<DT, N> rows[kSumAhead];
+        Raw<TT, N> before[ACC ? kSumAhead : 1];  // the table's rows of the runs that end here
+#pragma unroll
+        for (int k = 0; k < kSumAhead; ++k)
+            if (i0 + k < to && fa_in_bounds(c, N, g.dim) && fa_in_bounds(pos[i0 + k], 1, g.tokens)) {
+                rows[k].load(dout + static_cast<int64_t>(pos[i0 + k]) * g.dout_ld);
+                if (ACC && (last >> (i0 + k) & 1u) && fa_in_bounds(key[i0 + k], 1, g.vocab))
+                    before[ACC ? k : 0].load(table_row<TT>(g, key[i0 + k], c));
+            }
+#pragma unroll
+        for (int k = 0; k < kSumAhead; ++k) {
+            const int i = i0 + k;
+            if (i >= to) break;
+            float x[N];
+            rows[k].widen(x);
+#pragma unroll
+            for (int j = 0; j < N; ++j) sum[j] += x[j];
+            if (!(last >> i & 1u)) continue;
+            if (i < head_end || i == tail)
+                store_partial<N>(a.partial + (2 * u + (i < head_end ? 0 : 1)) * g.dim + c, sum);
+            else
+                finish_row<TT, N, ACC>(g, key[i], c, sum, before[ACC ? k : 0]);
+#pragma unroll
+            for (int j = 0; j < N; ++j) sum[j] = 0.f;
+        }
+    }
 }
 
-// Runs of three units and more, in columns [32 N blockIdx.y, + 32 N).  Each warp of a CTA looks
-// whether one unit began such a run; the CTA's warps then add each of these runs together,
-// each a stretch of its partial sums in unit order, and the stretches' sums in order.
-template <int DT, int TT, bool VEC>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_units_kernel(SumArgs a) {
+// The long runs: a CTA at a time adds one in columns [32 N slab, + 32 N), its warps each a
+// stretch of the partial sums in unit order, then the stretches' sums in order.
+template <int DT, int TT, bool VEC, bool ACC>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_units_kernel(SumArgs a, uint32_t slabs) {
     constexpr int N = kGroup<DT, TT, VEC>;
     const EmbeddingGradArgs &g = a.g;
-    __shared__ int64_t last_unit[kJoinWarps];  // of the run that the warp's unit began (0: none)
     __shared__ float stretch[kJoinWarps][32 * N];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kJoinWarps, mine = u0 + warp;
-    const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * N;
     fa_grid_dependency_wait();
     fa_allow_dependents();
-    int64_t end = 0;
-    {
-        const auto through = [&](int64_t w) { return w < a.units && a.shared[w] == kThrough; };
-        const bool next = through(mine + 1 + lane);  // asked for together with the unit's own
-        if (mine < a.units && a.shared[mine] == kBegins) {
-            end = mine + 1;
-            unsigned on = __ballot_sync(0xffffffffu, next);
-            while (on == 0xffffffffu) {
-                end += 32;
-                on = __ballot_sync(0xffffffffu, through(end + lane));
-            }
-            end += __ffs(~on) - 1;
-        }
-    }
-    if (lane == 0) last_unit[warp] = end;
-    __syncthreads();
-    const bool here = c < g.dim;
-    for (int k = 0; k < kJoinWarps; ++k) {
-        if (!last_unit[k]) continue;  // the same for the whole CTA
-        const int64_t u = u0 + k, each = (last_unit[k] - u + kJoinWarps - 1) / kJoinWarps;
-        const int64_t w1 = min(u + (warp + 1) * each, last_unit[k]);
+    const int64_t work = static_cast<int64_t>(*a.long_runs) * slabs;
+    for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
+        const int64_t k = i / slabs;
+        if (!fa_in_bounds(k, 1, a.units)) break;
+        const LongRun run = a.runs[k];
+        const int64_t c = ((i - k * slabs) * 32 + lane) * N;
+        const int64_t u = run.first, each = (run.last - u + kJoinWarps - 1) / kJoinWarps;
+        const int64_t w0 = u + 1 + warp * each, w1 = min(w0 + each - 1, int64_t(run.last));
+        const bool here = c < g.dim;
         float sum[N];
+        Raw<TT, N> before;
+        if (ACC && warp == 0 && here && fa_in_bounds(run.key, 1, g.vocab))
+            before.load(table_row<TT>(g, run.key, c));
 #pragma unroll
         for (int j = 0; j < N; ++j) sum[j] = 0.f;
         if (here) {
             if (warp == 0) load_partial<N>(a.partial + (2 * u + 1) * g.dim + c, sum);
-#pragma unroll 4
-            for (int64_t w = u + 1 + warp * each; w <= w1; ++w) {
+#pragma unroll 8
+            for (int64_t w = w0; w <= w1; ++w) {
                 float x[N];
                 if (!fa_in_bounds(w, 1, a.units)) break;
                 load_partial<N>(a.partial + 2 * w * g.dim + c, x);
@@ -540,10 +602,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_units_kernel(SumArgs a) 
         for (int j = 0; j < N; ++j) stretch[warp][j * 32 + lane] = sum[j];
         __syncthreads();
         if (warp == 0 && here) {
+#pragma unroll
             for (int w = 1; w < kJoinWarps; ++w)
 #pragma unroll
                 for (int j = 0; j < N; ++j) sum[j] += stretch[w][j * 32 + lane];
-            finish_row<TT, N>(g, a.keys[(u + 1) * kSumUnit], c, sum);
+            finish_row<TT, N, ACC>(g, run.key, c, sum, before);
         }
         __syncthreads();
     }
@@ -603,21 +666,21 @@ cudaError_t launch_embedding_lookup(const LookupArgs &a, fa_itype idt, fa_dtype 
     });
 }
 
-EmbeddingScratch embedding_scratch_layout(int64_t tokens, int64_t dim) {
+EmbeddingScratch embedding_scratch_layout(int64_t tokens, int64_t vocab, int64_t dim) {
     EmbeddingScratch s;
     s.chunks = (tokens + kSortChunk - 1) / kSortChunk;
     s.units = (tokens + kSumUnit - 1) / kSumUnit;
     s.sorted_words = round_up(tokens, 4);
-    // slabs of the sums' kernel: a column a thread at most
-    s.counters = s.units * ((dim + kSumThreads - 1) / kSumThreads);
-    s.bytes = 4 * (s.sorted_words * (s.chunks > 1 ? 4 : 2) + round_up(s.units, 4) +
-                   round_up(s.counters, 4) + s.units * 2 * round_up(dim, 4));
+    s.claim_words = round_up(vocab, 4);
+    s.run_words = 4 + round_up(3 * s.units, 4);  // their number, and the runs
+    s.bytes = 4 * (s.sorted_words * (s.chunks > 1 ? 4 : 2) + s.claim_words + s.run_words +
+                   s.units * 2 * round_up(dim, 4));
     return s;
 }
 
 cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, fa_dtype ddt,
                                       fa_dtype tdt, cudaStream_t stream) {
-    const EmbeddingScratch s = embedding_scratch_layout(g.tokens, g.dim);
+    const EmbeddingScratch s = embedding_scratch_layout(g.tokens, g.vocab, g.dim);
     uint32_t *keys = static_cast<uint32_t *>(g.scratch), *pos = keys + s.sorted_words;
     uint32_t *chunk_keys = keys, *chunk_pos = pos;
     uint32_t *end = pos + s.sorted_words;
@@ -636,23 +699,47 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
         sa.pos = chunk_pos;
         int bits = 1;
         while (g.vocab >> bits) ++bits;  // vocab itself is a key
-        sa.passes = (bits + 8) / 9;
+        sa.passes = (bits + kMostDigitBits - 1) / kMostDigitBits;
         sa.digit_bits = (bits + sa.passes - 1) / sa.passes;
         sa.chunks = static_cast<unsigned>(s.chunks);
         sa.ctas = s.chunks > 1 ? kSortChunk / kSortSlots
                                : static_cast<unsigned>(
                                      std::max<int64_t>(1, (g.tokens + kSortSlots - 1) / kSortSlots));
         const int64_t elem = tdt == FA_F32 ? 4 : 2;
-        const bool flat = g.table_ld == g.dim;
+        // Rows of ids that occur are written anyway: zeroed before too, they cost a second
+        // write.  Above 16 MB of them at most, that costs more than finding them (3 us; the
+        // rows of 65536 tokens in a table of 131 MB: 11 us).
+        const bool claim =
+            !g.accumulate && std::min(g.tokens, g.vocab) * g.dim * elem > (int64_t(16) << 20);
+        uint32_t *claims = claim ? end : nullptr;
+        const bool flat = g.table_ld == g.dim && !claim;
         sa.zero.p = static_cast<char *>(g.dtable);
-        sa.zero.rows = flat ? 1 : g.vocab;
+        sa.zero.rows = g.accumulate ? 0 : flat ? 1 : g.vocab;
         sa.zero.bytes = (flat ? g.vocab * g.dim : g.dim) * elem;
         sa.zero.ld = g.table_ld * elem;
-        sa.arrived = end + round_up(s.units, 4);
-        sa.counters = s.counters;
-        // enough CTAs to zero the table at the memory's rate, 64 KB each at least
-        const int64_t zeroing =
-            g.accumulate ? 0 : std::min<int64_t>(2 * 152, g.vocab * g.dim * elem / 65536 + 1);
+        sa.zero.claims = claims;
+        sa.long_runs = end + s.claim_words;
+        if (claim) {
+            cudaError_t err = for_itype(idt, [&](auto it) {
+                claim_kernel<it()><<<static_cast<unsigned>((g.tokens + 255) / 256), 256, 0, stream>>>(
+                    g.ids, claims, g.tokens, g.vocab, g.padding_idx);
+                return cudaGetLastError();
+            });
+            if (err != cudaSuccess) return err;
+        }
+        // The first rows are asked into L2 meanwhile (32 MB: 2 to 6 us of 90; 96 MB would push
+        // out the zeros that L2 still holds), unless they are shorter than a few lines.
+        const int64_t row_bytes = g.dim * (ddt == FA_F32 ? 4 : 2);
+        sa.prefetch.p = static_cast<const char *>(g.dout);
+        sa.prefetch.rows =
+            row_bytes < 512 ? 0 : std::min(g.tokens, (int64_t(32) << 20) / row_bytes);
+        sa.prefetch.bytes = row_bytes;
+        sa.prefetch.ld = g.dout_ld * (ddt == FA_F32 ? 4 : 2);
+        // enough CTAs to zero the table, or to ask for rows, at the memory's rate; 64 KB each
+        // at least
+        const int64_t beside = (g.accumulate ? 0 : g.vocab * g.dim * elem) +
+                               sa.prefetch.rows * row_bytes;
+        const int64_t zeroing = std::min<int64_t>(2 * 152, beside / 65536 + !g.accumulate);
         const int64_t zero_clusters = (zeroing + sa.ctas - 1) / sa.ctas;
         const auto go = [&](auto it, auto item) {
             auto kernel = sort_chunk_kernel<it(), decltype(item)>;
@@ -664,7 +751,7 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
             if (e != cudaSuccess) return e;
             return launch_clusters(
                 kernel, dim3(static_cast<unsigned>((sa.chunks + zero_clusters) * sa.ctas)),
-                dim3(kSortThreads), kSmem, sa.ctas, false, stream, sa);
+                dim3(kSortThreads), kSmem, sa.ctas, claim, stream, sa);
         };
         cudaError_t err = for_itype(idt, [&](auto it) {
             return g.vocab < 65536 ? go(it, uint32_t{}) : go(it, uint64_t{});
@@ -685,32 +772,36 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
     a.g = g;
     a.keys = keys;
     a.pos = pos;
-    a.shared = end;
-    a.arrived = end + round_up(s.units, 4);
-    a.partial = reinterpret_cast<float *>(a.arrived + round_up(s.counters, 4));
+    a.long_runs = end + s.claim_words;
+    a.runs = reinterpret_cast<LongRun *>(a.long_runs + 4);
+    a.partial = reinterpret_cast<float *>(a.long_runs + s.run_words);
     a.units = s.units;
     const bool vec = vector_rows(g.dout, g.dout_ld, ddt, g.dtable, g.table_ld, tdt, g.dim);
     return for_dtype(ddt, [&](auto dd) {
         return for_dtype(tdt, [&](auto td) {
-            const auto go = [&](auto v) {
-                constexpr bool VEC = decltype(v)::value;
+            const auto go = [&](auto v, auto acc) {
+                constexpr bool VEC = decltype(v)::value, ACC = decltype(acc)::value;
                 constexpr int N = kGroup<dd(), td(), VEC>;
                 const int64_t groups = (g.dim + N - 1) / N;
                 const int threads = static_cast<int>(
                     groups < kSumThreads ? round_up(groups, 32) : kSumThreads);
                 const int64_t slabs = (groups + threads - 1) / threads;
                 cudaError_t e = launch_dependent(
-                    sum_units_kernel<dd(), td(), VEC>,
+                    sum_units_kernel<dd(), td(), VEC, ACC>,
                     dim3(static_cast<unsigned>(a.units), static_cast<unsigned>(slabs)),
                     dim3(threads), 0, stream, a);
-                if (e != cudaSuccess || a.units < 3) return e;
-                return launch_dependent(
-                    join_units_kernel<dd(), td(), VEC>,
-                    dim3(static_cast<unsigned>((a.units - 2 + kJoinWarps - 1) / kJoinWarps),
-                         static_cast<unsigned>((groups + 31) / 32)),
-                    dim3(kJoinWarps * 32), 0, stream, a);
+                if (e != cudaSuccess || a.units < 2) return e;
+                const uint32_t join_slabs = static_cast<uint32_t>((groups + 31) / 32);
+                // a long run takes two units at least
+                const int64_t most = std::min<int64_t>(a.units / 2 * join_slabs, 8 * 152);
+                return launch_dependent(join_units_kernel<dd(), td(), VEC, ACC>,
+                                        dim3(static_cast<unsigned>(most)), dim3(kJoinWarps * 32),
+                                        0, stream, a, join_slabs);
             };
-            return vec ? go(std::true_type{}) : go(std::false_type{});
+            const std::true_type yes{};
+            const std::false_type no{};
+            if (vec) return g.accumulate ? go(yes, yes) : go(yes, no);
+            return g.accumulate ? go(no, yes) : go(no, no);
         });
     });
 }

@@ -141,7 +141,7 @@ struct RowSum {
 
 // Merges what the warps of the CTAs of a cluster hold of a row; every thread returns the
 // row's.  The maximum first, so that a part is rebased once.  ``part``: shared, [warps];
-// ``whole``: shared, one per CTA.
+// ``whole``: shared, one per CTA.  The caller ends with leave_row.
 __device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, RowSum *whole,
                                             const Share &sh) {
     constexpr int warps = kRowThreads / 32;
@@ -170,7 +170,7 @@ __device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, Ro
         cluster.sync();
         w = lane < static_cast<int>(sh.split()) ? *cluster.map_shared_rank(whole, lane)
                                            : RowSum{-INFINITY, 0.f};
-        cluster.sync();  // no CTA leaves while another reads its part
+        cluster.barrier_arrive();  // has read the others' parts: see leave_row
         top = w.top;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -179,6 +179,11 @@ __device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, Ro
     }
     if (row.top == -INFINITY) row.s = NAN;  // no finite logit
     return row;
+}
+
+// Before a CTA that has called merge_row ends: no CTA leaves while another reads its part.
+__device__ __forceinline__ void leave_row(const Share &sh) {
+    if (sh.log2 > 0) cg::this_cluster().barrier_wait();
 }
 
 // logp of the label from its logit and the row's statistics, rounded once: the product and
@@ -381,6 +386,7 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2
         logp[t] = label_logp(Elem<DT>::widen(row[label]), r, x.scale);
         if (lse) reinterpret_cast<float2 *>(lse)[t] = make_float2(r.top, r.s);
     }
+    leave_row(sh);
 }
 
 // Rows are taken from the last to the first: the pass that made the statistics left the
@@ -429,12 +435,15 @@ __device__ __forceinline__ float softplus(float z) {
 
 // One CTA per pair: a half of it for each sequence's sum, the pair's loss and the
 // coefficient of each of its tokens.  Tokens of no sequence are zeroed by the first and the
-// last pair's CTA.
+// last pair's CTA.  Up to kPairCluster pairs are one cluster, whose first CTA takes the mean
+// of their losses (a launch less); more leave it to preference_mean_kernel.
+constexpr unsigned kPairCluster = 8;
 template <int IT>
 __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(PreferenceArgs a) {
     constexpr int kHalf = kPairThreads / 2, kWarps = kHalf / 32;
     __shared__ Sum2 part[2][kWarps];
     __shared__ int counts[2][kWarps];
+    __shared__ float my_loss;
     const int64_t pair = blockIdx.x;
     const int q = threadIdx.x / kHalf, tid = threadIdx.x % kHalf, lane = tid & 31;
     const auto clamped = [&](int64_t j) {
@@ -483,7 +492,8 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(Preferenc
     const float d = dz * a.beta / static_cast<float>(a.pairs);
     if (threadIdx.x == 0) {
         const float keep = (1.f - e) * softplus(-z);
-        a.pair_loss[pair] = e > 0.f ? keep + e * softplus(z) : keep;
+        my_loss = e > 0.f ? keep + e * softplus(z) : keep;
+        a.pair_loss[pair] = my_loss;
         a.rewards[2 * pair] = a.beta * mean[0];
         a.rewards[2 * pair + 1] = a.beta * mean[1];
     }
@@ -495,6 +505,15 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(Preferenc
         for (int64_t t = tid; t < lo; t += kHalf) a.dlogp[t] = 0.f;
     if (pair == a.pairs - 1 && q == 1)
         for (int64_t t = hi + tid; t < a.tokens; t += kHalf) a.dlogp[t] = 0.f;
+    if (gridDim.x > kPairCluster) return;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    if (pair == 0 && threadIdx.x == 0) {
+        Sum2 total;
+        for (unsigned r = 0; r < gridDim.x; ++r) total.add(*cluster.map_shared_rank(&my_loss, r));
+        *a.loss = total.value() / static_cast<float>(gridDim.x);
+    }
+    cluster.sync();  // no CTA leaves while the first reads its loss
 }
 
 // The mean over the pairs, by one CTA (no pairs: 0, and no token has a coefficient).
@@ -695,7 +714,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
         }
         coef = o.dlogp * (in.weight / denom) * a.grad_factor;
     }
-    if (!out) return;
+    if (!out) return leave_row(sh);
     __syncthreads();
     if constexpr (HELD > 0) {
         if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
@@ -725,10 +744,11 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
             }
             if (label_is_mine<DT>(label, sp, part, sh))
                 out[label] = E::round(fmaf(e(label_logit), w, c));
-            return;
+            return leave_row(sh);
         }
     }
     row_gradient<DT>(row, out, n, a.x, r, coef, label, sh);
+    leave_row(sh);
 }
 
 // The sums over the tokens, by a cluster of CTAs: each adds its tokens, the first adds the
@@ -847,10 +867,12 @@ cudaError_t launch_token_logprobs_gradient(const LogitGradArgs &a, fa_dtype dt, 
 cudaError_t launch_preference(const PreferenceArgs &a, fa_itype lt, cudaStream_t stream) {
     return for_itype(lt, [&](auto i) {
         if (a.pairs > 0) {
-            cudaError_t err = launch_dependent(preference_pair_kernel<i()>,
-                                               dim3(static_cast<unsigned>(a.pairs)),
-                                               dim3(kPairThreads), 0, stream, a);
-            if (err != cudaSuccess) return err;
+            const bool whole = a.pairs <= kPairCluster;
+            const unsigned pairs = static_cast<unsigned>(a.pairs);
+            cudaError_t err =
+                launch_clusters(preference_pair_kernel<i()>, dim3(pairs), dim3(kPairThreads), 0,
+                                whole ? pairs : 1, true, stream, a);
+            if (err != cudaSuccess || whole) return err;
         }
         return launch_dependent(preference_mean_kernel, dim3(1), dim3(kPairThreads), 0, stream, a);
     });

@@ -185,7 +185,7 @@ fa_status fa_embedding_scratch(int64_t tokens, int64_t vocab, int64_t dim, int64
     if (tokens < 0 || vocab < 0 || dim < 0 || tokens > kMaxCount || vocab >= kMaxCount ||
         dim > kMaxDim)
         return FA_ERR_SIZE;
-    *bytes = fa::embedding_scratch_layout(tokens, dim).bytes;
+    *bytes = fa::embedding_scratch_layout(tokens, vocab, dim).bytes;
     return FA_OK;
 }
 

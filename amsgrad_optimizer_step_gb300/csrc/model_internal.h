@@ -49,14 +49,15 @@ cudaError_t launch_embedding_lookup(const LookupArgs &a, fa_itype idt, fa_dtype 
 struct EmbeddingScratch {
     int64_t chunks;  // runs of kSortChunk tokens that one cluster sorts
     int64_t units;   // runs of kSumUnit sorted tokens that one CTA adds
-    int64_t counters;      // of the sums' kernel
+    int64_t claim_words;   // a token of each id
+    int64_t run_words;     // the list of long runs
     int64_t sorted_words;  // 32-bit words of one sorted array (tokens, rounded up to 4)
     int64_t bytes;
 };
 constexpr int kSortSlots = 4096;             // tokens in one CTA's shared memory
 constexpr int kSortChunk = 16 * kSortSlots;  // in a cluster's
-constexpr int kSumUnit = 32;                // (a warp's ballot holds one)
-EmbeddingScratch embedding_scratch_layout(int64_t tokens, int64_t dim);
+constexpr int kSumUnit = 32;
+EmbeddingScratch embedding_scratch_layout(int64_t tokens, int64_t vocab, int64_t dim);
 
 struct EmbeddingGradArgs {
     const void *ids;

@@ -66,8 +66,8 @@ class FaPolicy(ctypes.Structure):
     _fields_ = [("old_logp", c_vp), ("advantages", c_vp), ("ref_logp", c_vp), ("weights", c_vp),
                 ("clip_low", c_f64), ("clip_high", c_f64), ("kl_coef", c_f64),
                 ("denominator", c_f64), ("grad_scale", c_f64), ("summary", c_vp),
-                ("logp", c_vp), ("token_loss", c_vp), ("token_kl", c_vp), ("dlogits", c_vp),
-                ("dlogits_ld", c_i64)]
+                ("logp", c_vp), ("token_loss", c_vp), ("token_kl", c_vp), ("lse", c_vp),
+                ("dlogp", c_vp), ("dlogits", c_vp), ("dlogits_ld", c_i64)]
 
 
 P = c_vp

@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a) {
     // a thread's items are 32 apart: a warp's are consecutive, taken in rounds
     const int first = warp * 32 * kSortItems + lane;
     const auto finish = [&](int i, Item x) {  // the i-th of the sorted chunk
-        if (i >= n || !fa_in_bounds(chunk + i, 1, a.tokens)) return;
+        if (!fa_in_bounds(chunk + i, 1, a.tokens)) return;
         a.keys[chunk + i] = static_cast<uint32_t>(x >> 16);
         a.pos[chunk + i] = static_cast<uint32_t>(chunk + static_cast<uint16_t>(x));
     };
@@ -219,13 +219,15 @@ __global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a) {
 #pragma unroll
     for (int j = 0; j < kSortItems; ++j) {
         const int i = static_cast<int>(rank) * kSortSlots + first + 32 * j;
-        item[j] = ~Item(0);  // past the end: came last, and stays last
+        item[j] = 0;
         if (i < n && fa_in_bounds(chunk + i, 1, a.tokens)) {
             const int64_t id = load_id<IT>(a.ids, chunk + i);
             const bool known = id >= 0 && id < a.vocab && id != a.padding_idx;
             item[j] = static_cast<Item>(known ? id : a.vocab) << 16 | static_cast<Item>(i);
         }
     }
+    // places from n on stay empty: a CTA's tokens are its first ``held``, in every pass
+    const int held = min(max(n - static_cast<int>(rank) * kSortSlots, 0), kSortSlots);
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = 16 + pass * a.digit_bits;
         const auto digit = [&](Item x) { return static_cast<int>(x >> shift) & (digits - 1); };
@@ -235,10 +237,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a) {
         uint16_t before[kSortItems];  // tokens of the digit before this one in the warp
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
+            if (warp * 32 * kSortItems + 32 * j >= held) break;  // the whole warp
             const int d = digit(item[j]);
+            const bool in = first + 32 * j < held;
             // the lanes with this digit, from a ballot of each of its bits (with match.any a
             // sort of 4096 tokens took 2 us more)
-            unsigned same = 0xffffffffu;
+            unsigned same = __ballot_sync(0xffffffffu, in);
 #pragma unroll
             for (int b = 0; b < kMostDigitBits; ++b) {
                 const bool bit = d >> b & 1;
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a) {
             const int ahead = __popc(same & ((1u << lane) - 1));
             const uint16_t c = s.count[warp][d];
             __syncwarp();
-            if (ahead == 0) s.count[warp][d] = static_cast<uint16_t>(c + __popc(same));
+            if (in && ahead == 0) s.count[warp][d] = static_cast<uint16_t>(c + __popc(same));
             __syncwarp();
             before[j] = static_cast<uint16_t>(c + ahead);
         }
@@ -300,6 +304,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a) {
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
+            if (first + 32 * j >= held) continue;
             const int at = s.count[warp][digit(item[j])] + before[j];
             if (fa_in_bounds(at, 1, kSortSlots)) s.own[at] = item[j];
         }
@@ -308,8 +313,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a) {
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
             const int i = t + j * kSortThreads;
+            if (i >= held) break;
             const Item x = s.own[i];
-            const int at = s.base[digit(x)] + i;  // < ctas * kSortSlots
+            const int at = s.base[digit(x)] + i;  // < n
             if (!fa_in_bounds(at, 1, static_cast<int64_t>(a.ctas) * kSortSlots)) continue;
             if (last)
                 finish(at, x);

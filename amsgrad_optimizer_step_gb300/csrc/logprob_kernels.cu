@@ -186,14 +186,53 @@ __device__ __forceinline__ void leave_row(const Share &sh) {
     if (sh.log2 > 0) cg::this_cluster().barrier_wait();
 }
 
-// logp of the label from its logit and the row's statistics, rounded once: the product and
-// the difference in two parts each.
+// x + y exactly, as the rounded sum and what the rounding left.
+__device__ __forceinline__ Sum2 two_sum(float x, float y) {
+    Sum2 s;
+    s.hi = x + y;
+    const float b = s.hi - x;
+    s.lo = (x - (s.hi - b)) + (y - b);
+    return s;
+}
+
+// ln s for a normal s >= 1, within 4e-9 of it: s = 2^e m with m from 1/sqrt 2 to sqrt 2, and
+// ln m = 2 atanh r, r = (m - 1) / (m + 1), by its series (|r| < 0.172: the term left out is
+// below 2^-40 of the first).
+__device__ __forceinline__ Sum2 log_parts(float s) {
+    const int e = (__float_as_int(s) - __float_as_int(0.70710678f)) >> 23;
+    const float m = __int_as_float(__float_as_int(s) - (e << 23)), f = static_cast<float>(e);
+    const float num = m - 1.f;  // exact
+    const Sum2 den = two_sum(m, 1.f);
+    const float r = __fdiv_rn(num, den.hi);
+    const float r_lo = __fdividef(fmaf(-r, den.lo, fmaf(-r, den.hi, num)), den.hi);
+    const float q = r * r;
+    float p = 1.f / 15.f;  // 1/3 + q/5 + ... + q^6/15
+    p = fmaf(p, q, 1.f / 13.f);
+    p = fmaf(p, q, 1.f / 11.f);
+    p = fmaf(p, q, 1.f / 9.f);
+    p = fmaf(p, q, 1.f / 7.f);
+    p = fmaf(p, q, 1.f / 5.f);
+    p = fmaf(p, q, 1.f / 3.f);
+    // ln 2 in two parts, the first short enough that e times it is exact
+    constexpr float kLn2Hi = 0.693145751953125f, kLn2Lo = 1.4286068203094172e-06f;
+    Sum2 l = two_sum(f * kLn2Hi, 2.f * r);
+    l.lo += fmaf(f, kLn2Lo, 2.f * fmaf(q * r, p, r_lo));
+    return two_sum(l.hi, l.lo);
+}
+
+// logp of the label from its logit and the row's statistics, rounded once.  exp2_fast comes
+// out low on average: the sum of a row's terms but the top's (which is 1) by 3.5e-8 to 4.1e-8
+// of them, over rows of 32000 logits of each type, so that log-probabilities were as much too
+// high; the middle of that is taken off.
 __device__ __forceinline__ float label_logp(float x, const RowSum &r, float scale) {
-    const float d = x - r.top, log_s = logf(r.s);
-    if (!(d > -1e30f)) return d * scale - log_s;  // the parts would not be finite
+    constexpr float kTermsLow = 3.8e-8f;
+    const float d = x - r.top;
+    // outside this the parts would not be finite
+    if (!(d > -1e30f) || !(r.s >= 1.f) || !(r.s < 1e30f)) return d * scale - logf(r.s);
+    const Sum2 log_s = log_parts(r.s);
     const float p = d * scale, p_lo = fmaf(d, scale, -p);
-    const float y = p - log_s, b = y - p;
-    return y + ((p - (y - b)) - (log_s + b) + p_lo);
+    const Sum2 y = two_sum(p, -log_s.hi);
+    return y.hi + (y.lo + (p_lo - log_s.lo - kTermsLow * (1.f - __fdividef(1.f, r.s))));
 }
 
 template <int IT>
@@ -636,6 +675,8 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
             a.logp[t] = 0.f;
             a.token_loss[t] = 0.f;
             a.token_kl[t] = 0.f;
+            if (a.lse) reinterpret_cast<float2 *>(a.lse)[t] = make_float2(0.f, 1.f);
+            if (a.dlogp) a.dlogp[t] = 0.f;
         }
         if (out) row_zeros<DT>(out, n, sh);
         if (divisor == kFromKernel) fa_grid_dependency_wait();
@@ -707,12 +748,15 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
             a.logp[t] = logp;
             a.token_loss[t] = o.loss;
             a.token_kl[t] = o.kl;
+            if (a.lse) reinterpret_cast<float2 *>(a.lse)[t] = make_float2(r.top, r.s);
         }
         if (divisor == kFromKernel) {
             fa_grid_dependency_wait();
             denom = a.summary[3];
         }
-        coef = o.dlogp * (in.weight / denom) * a.grad_factor;
+        const float dlogp = o.dlogp * (in.weight / denom);
+        if (a.dlogp && sh.first()) a.dlogp[t] = dlogp;
+        coef = dlogp * a.grad_factor;
     }
     if (!out) return leave_row(sh);
     __syncthreads();
@@ -903,7 +947,7 @@ cudaError_t launch_policy(const PolicyArgs &a, fa_dtype dt, fa_itype lt, cudaStr
             // Every CTA counts the labels itself when they are few (a launch less); else one
             // kernel does before the rows'.
             constexpr int64_t kFewLabels = 2048;
-            const bool counts = a.dlogits && a.denominator == 0.f;
+            const bool counts = (a.dlogits || a.dlogp) && a.denominator == 0.f;
             const Divisor divisor = !counts                     ? kGiven
                                     : a.x.tokens <= kFewLabels ? kCountHere
                                                                : kFromKernel;

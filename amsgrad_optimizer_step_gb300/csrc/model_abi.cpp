@@ -358,17 +358,20 @@ fa_status fa_policy_loss(const fa_logits *x, const fa_policy *p, void *stream) {
         FA_TRY(check_device_ptr(p->logp, dev, 4));
         FA_TRY(check_device_ptr(p->token_loss, dev, 4));
         FA_TRY(check_device_ptr(p->token_kl, dev, 4));
+        if (p->lse) FA_TRY(check_device_ptr(p->lse, dev, 8));
+        if (p->dlogp) FA_TRY(check_device_ptr(p->dlogp, dev, 4));
         if (p->dlogits) FA_TRY(check_dlogits(x, p->dlogits, p->dlogits_ld, dev));
     }
     const int64_t b = x->tokens * 4;
     const Matrix outs[] = {
         vec(p->summary, 16), vec(p->logp, b), vec(p->token_loss, b), vec(p->token_kl, b),
+        vec(p->lse, 2 * b), vec(p->dlogp, b),
         mat(p->dlogits, x->tokens, x->vocab, p->dlogits_ld, dtype_bytes(x->dtype))};
     const Matrix ins[] = {labels_vec(x),       vec(p->old_logp, b), vec(p->advantages, b),
                           vec(p->ref_logp, b), vec(p->weights, b)};
-    FA_TRY(check_outputs(outs, 5, ins, 5));
+    FA_TRY(check_outputs(outs, 7, ins, 5));
     const Matrix logits[] = {logits_matrix(x)};
-    FA_TRY(check_outputs(outs, 4, logits, 1));  // dlogits: checked above
+    FA_TRY(check_outputs(outs, 6, logits, 1));  // dlogits: checked above
     TraceRange trace("fa_policy_loss");
     fa::PolicyArgs a;
     a.x = logits_args(x);
@@ -385,6 +388,8 @@ fa_status fa_policy_loss(const fa_logits *x, const fa_policy *p, void *stream) {
     a.logp = p->logp;
     a.token_loss = p->token_loss;
     a.token_kl = p->token_kl;
+    a.lse = p->lse;
+    a.dlogp = p->dlogp;
     a.dlogits = p->dlogits;
     a.dlogits_ld = p->dlogits_ld;
     return cuda_status(

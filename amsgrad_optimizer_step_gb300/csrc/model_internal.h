@@ -113,6 +113,7 @@ struct PolicyArgs {
     float denominator;  // 0: the number of counted tokens, from summary[3]
     float grad_factor;  // logit_scale * grad_scale
     float *summary, *logp, *token_loss, *token_kl;
+    float *lse, *dlogp;  // or nullptr
     void *dlogits;
     int64_t dlogits_ld;
 };

@@ -237,9 +237,12 @@ def fa_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.T
                    weights: Optional[torch.Tensor] = None,
                    dlogits: Optional[torch.Tensor] = None, clip_low: float = 0.2,
                    clip_high: float = 0.2, kl_coef: float = 0.0, denominator: float = 0.0,
-                   logit_scale: float = 1.0, grad_scale: float = 1.0, stream=None) -> None:
+                   logit_scale: float = 1.0, grad_scale: float = 1.0,
+                   lse: Optional[torch.Tensor] = None, dlogp: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
     """Clipped policy loss with a KL term; with dlogits (which may be the logits) the
-    gradient too, in the same pass.  denominator 0 divides by the counted tokens."""
+    gradient too, in the same pass.  denominator 0 divides by the counted tokens.  lse and
+    dlogp keep what fa_token_logprobs_gradient takes, for a gradient later."""
     n = logits.shape[0]
     f32 = torch.float32
     x = _logits(logits, labels, logit_scale)
@@ -251,6 +254,8 @@ def fa_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.T
         _vector("summary", out.summary, 4, f32), _vector("logp", out.logp, n, f32),
         _vector("token_loss", out.token_loss, n, f32),
         _vector("token_kl", out.token_kl, n, f32),
+        None if lse is None else _vector("lse", lse, 2 * n, f32),
+        None if dlogp is None else _vector("dlogp", dlogp, n, f32),
         None if dlogits is None else dlogits.data_ptr(),
         0 if dlogits is None else _dlogits(logits, dlogits))
     check("fa_policy_loss",

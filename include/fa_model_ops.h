@@ -167,6 +167,9 @@ typedef struct fa_policy {
     float *logp;              /* [tokens], as fa_token_logprobs                               */
     float *token_loss;        /* [tokens], 0 where not counted                                */
     float *token_kl;          /* [tokens], 0 where not counted                                */
+    float *lse;               /* [tokens][2] as fa_token_logprobs, or NULL                    */
+    float *dlogp;             /* [tokens]: dloss / dlogp, or NULL: with lse, the gradient can */
+                              /* be taken later, by fa_token_logprobs_gradient                */
     void *dlogits;            /* [tokens, vocab] of the logits' type, or NULL: no gradient;   */
     int64_t dlogits_ld;       /* may be the logits themselves (same pointer and ld)           */
 } fa_policy;

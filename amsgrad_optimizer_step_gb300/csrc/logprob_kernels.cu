@@ -27,8 +27,11 @@ namespace cg = cooperative_groups;
 
 FA_BOUNDS_COUNTER(g_logprob_oob)
 
-constexpr int kRowThreads = 256;
 constexpr int kBatch = 4;  // 16-byte vectors a thread takes at a time
+// A row's kernels are compiled for CTAs of NT = 32, 64, 128 and 256 threads: a row of few
+// vectors is a warp's, without barriers, and many CTAs share an SM (65536 rows of 1000 BF16
+// logits by 256 threads each took 330 us, nine tenths of it in starting and joining them).
+constexpr int kMostThreads = 256;
 
 // A row cut for 16-byte accesses: head scalars up to the first boundary, then nvec
 // vectors, then the scalars left over.
@@ -142,9 +145,10 @@ struct RowSum {
 // Merges what the warps of the CTAs of a cluster hold of a row; every thread returns the
 // row's.  The maximum first, so that a part is rebased once.  ``part``: shared, [warps];
 // ``whole``: shared, one per CTA.  The caller ends with leave_row.
+template <int NT>
 __device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, RowSum *whole,
                                             const Share &sh) {
-    constexpr int warps = kRowThreads / 32;
+    constexpr int warps = NT / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const auto warp_total = [](float s) {
 #pragma unroll
@@ -153,17 +157,20 @@ __device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, Ro
     };
     float lo, hi;
     unpair(acc.sum, lo, hi);
-    const float s = warp_total(lo + hi);
-    if (lane == 0) part[warp] = RowSum{acc.top, s};
-    __syncthreads();
-    // every warp adds the warps' parts alike
-    RowSum w = lane < warps ? part[lane] : RowSum{-INFINITY, 0.f};
+    RowSum row{acc.top, warp_total(lo + hi)}, w;
     Exponent e = acc.e;
-    float top = w.top;
+    float top;
+    if constexpr (warps > 1) {
+        if (lane == 0) part[warp] = row;
+        __syncthreads();
+        // every warp adds the warps' parts alike
+        w = lane < warps ? part[lane] : RowSum{-INFINITY, 0.f};
+        top = w.top;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    e.set(top);
-    RowSum row{top, warp_total(w.at(e))};
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        e.set(top);
+        row = RowSum{top, warp_total(w.at(e))};
+    }
     if (sh.log2 > 0) {
         cg::cluster_group cluster = cg::this_cluster();
         if (threadIdx.x == 0) *whole = row;
@@ -235,9 +242,8 @@ __device__ __forceinline__ float label_logp(float x, const RowSum &r, float scal
     return y.hi + (y.lo + (p_lo - log_s.lo - kTermsLow * (1.f - __fdividef(1.f, r.s))));
 }
 
-template <int IT>
 __device__ __forceinline__ bool load_label(const LogitsArgs &x, int64_t t, int64_t *label) {
-    *label = load_id<IT>(x.labels, t);
+    *label = x.wide_labels ? load_id<FA_I64>(x.labels, t) : load_id<FA_I32>(x.labels, t);
     return *label >= 0 && *label < x.vocab;
 }
 
@@ -277,28 +283,28 @@ __device__ __forceinline__ uint4 gradient_vector(const uint4 &r, const Exponent 
 
 // Whether this thread writes the label's element of the row: it then reads the logit before
 // it writes anything, and the element, c (1 - p), last.
-template <int DT>
+template <int DT, int NT>
 __device__ __forceinline__ bool label_is_mine(int64_t label, const RowSpan &sp,
                                               const RowPart &part, const Share &sh) {
     const int at = static_cast<int>(label), t = threadIdx.x;
     if (at < sp.head) return sh.first() && t == at;
     if (at >= sp.tail) return sh.last() && t == at - sp.tail;
     const int i = (at - sp.head) / Elem<DT>::kVec - part.begin;
-    return i >= 0 && i < part.count && i % kRowThreads == t;
+    return i >= 0 && i < part.count && i % NT == t;
 }
 
-// f(i, whole batch) for the vectors i, i + kRowThreads, ... of a thread in batches of N: whole
+// f(i, whole batch) for the vectors i, i + NT, ... of a thread in batches of N: whole
 // ones first, without a check of each vector, then one that may be cut short.
-template <int N, typename F>
+template <int NT, int N, typename F>
 __device__ __forceinline__ void for_batches(int count, F f) {
     int i0 = 0;
-    for (; i0 + N * kRowThreads <= count; i0 += N * kRowThreads) f(i0, std::true_type{});
+    for (; i0 + N * NT <= count; i0 += N * NT) f(i0, std::true_type{});
     if (i0 < count) f(i0, std::false_type{});
 }
 
 // dlogits of (a part of) one row from global memory.  The output may be the row itself:
 // every element is read before it is written, by the thread that writes it.
-template <int DT>
+template <int DT, int NT>
 __device__ __forceinline__ void row_gradient(const void *row, void *out, int64_t n,
                                              const LogitsArgs &a, RowSum r, float c,
                                              int64_t label, const Share &sh) {
@@ -311,28 +317,28 @@ __device__ __forceinline__ void row_gradient(const void *row, void *out, int64_t
     const int tid = threadIdx.x;
     if ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) {
         // not co-aligned: element by element
-        for (int64_t i = sh.rank * kRowThreads + tid; i < n; i += sh.split() * kRowThreads)
+        for (int64_t i = sh.rank * NT + tid; i < n; i += sh.split() * NT)
             if (fa_in_bounds(i, 1, n))
                 y[i] = E::round(fmaf(e(E::widen(x[i])), w, i == label ? c : 0.f));
         return;
     }
     const RowSpan sp = row_span<DT>(row, n);
     const RowPart part(sp, sh);
-    const bool mine = label_is_mine<DT>(label, sp, part, sh);
+    const bool mine = label_is_mine<DT, NT>(label, sp, part, sh);
     const float label_logit = mine ? E::widen(x[label]) : 0.f;
     row_ends(sp, n, sh, [&](int i) { y[i] = E::round(e(E::widen(x[i])) * w); });
     const uint4 *q = reinterpret_cast<const uint4 *>(x + sp.head) + part.begin + tid;
     uint4 *o = reinterpret_cast<uint4 *>(y + sp.head) + part.begin + tid;
-    for_batches<kBatch>(part.count, [&](int i0, auto whole) {
+    for_batches<NT, kBatch>(part.count, [&](int i0, auto whole) {
         uint4 v[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int i = i0 + j * kRowThreads;
+            const int i = i0 + j * NT;
             if ((decltype(whole)::value || i + tid < part.count) && part.in_bounds(i + tid)) v[j] = __ldcs(q + i);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int i = i0 + j * kRowThreads;
+            const int i = i0 + j * NT;
             if ((decltype(whole)::value || i + tid < part.count) && part.in_bounds(i + tid))
                 __stcs(o + i, gradient_vector<DT>(v[j], e, w));
         }
@@ -377,11 +383,11 @@ __device__ __forceinline__ uint4 no_vector() {
 }
 
 // The softmax statistics of a row by the CTAs of a cluster, read from global memory.
-template <int DT>
+template <int DT, int NT>
 __device__ __forceinline__ RowSum row_softmax(const void *row, const LogitsArgs &a,
                                               const Share &sh) {
     using T = typename Elem<DT>::T;
-    __shared__ RowSum parts[kRowThreads / 32], whole;
+    __shared__ RowSum parts[NT / 32], whole;
     const RowSpan sp = row_span<DT>(row, a.vocab);
     Softmax acc(a);
     add_ends<DT>(acc, row, sp, a.vocab, sh);
@@ -389,30 +395,30 @@ __device__ __forceinline__ RowSum row_softmax(const void *row, const LogitsArgs 
     const int tid = threadIdx.x;
     const uint4 *q =
         reinterpret_cast<const uint4 *>(static_cast<const T *>(row) + sp.head) + part.begin + tid;
-    for_batches<kBatch>(part.count, [&](int i0, auto full) {
+    for_batches<NT, kBatch>(part.count, [&](int i0, auto full) {
         if (!decltype(full)::value && i0 + (tid & ~31) >= part.count) return;  // whole warps
         uint4 r[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int i = i0 + j * kRowThreads;
+            const int i = i0 + j * NT;
             r[j] = (decltype(full)::value || i + tid < part.count) && part.in_bounds(i + tid)
                        ? __ldg(q + i)
                        : no_vector<DT>();
         }
         acc.add<DT, kBatch>(r);
     });
-    return merge_row(acc, parts, &whole, sh);
+    return merge_row<NT>(acc, parts, &whole, sh);
 }
 
-template <int DT, int IT>
-__global__ void __launch_bounds__(kRowThreads)
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT)
 token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2) {
     using T = typename Elem<DT>::T;
     fa_allow_dependents();
     const Share sh(split_log2);
     const int64_t t = sh.row;
     int64_t label;
-    if (!load_label<IT>(x, t, &label)) {
+    if (!load_label(x, t, &label)) {
         if (sh.first() && threadIdx.x == 0) {
             logp[t] = 0.f;
             if (lse) reinterpret_cast<float2 *>(lse)[t] = make_float2(0.f, 1.f);
@@ -420,7 +426,7 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2
         return;
     }
     const T *row = static_cast<const T *>(x.logits) + t * x.ld;
-    const RowSum r = row_softmax<DT>(row, x, sh);
+    const RowSum r = row_softmax<DT, NT>(row, x, sh);
     if (sh.first() && threadIdx.x == 0) {
         logp[t] = label_logp(Elem<DT>::widen(row[label]), r, x.scale);
         if (lse) reinterpret_cast<float2 *>(lse)[t] = make_float2(r.top, r.s);
@@ -430,15 +436,15 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2
 
 // Rows are taken from the last to the first: the pass that made the statistics left the
 // last rows in L2.
-template <int DT, int IT>
-__global__ void __launch_bounds__(kRowThreads)
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT)
 logprob_gradient_kernel(LogitGradArgs a, unsigned split_log2) {
     using T = typename Elem<DT>::T;
     const Share sh(split_log2);
     const int64_t t = a.x.tokens - 1 - sh.row;
     T *out = static_cast<T *>(a.dlogits) + t * a.dlogits_ld;
     int64_t label;
-    if (!load_label<IT>(a.x, t, &label)) {
+    if (!load_label(a.x, t, &label)) {
         row_zeros<DT>(out, a.x.vocab, sh);
         return;
     }
@@ -446,7 +452,7 @@ logprob_gradient_kernel(LogitGradArgs a, unsigned split_log2) {
     const float2 l = reinterpret_cast<const float2 *>(a.lse)[t];
     const RowSum r{l.x, l.y};
     const float c = a.dlogp[t] * a.factor * (a.grad_loss ? *a.grad_loss : 1.f);
-    row_gradient<DT>(row, out, a.x.vocab, a.x, r, c, label, sh);
+    row_gradient<DT, NT>(row, out, a.x.vocab, a.x, r, c, label, sh);
 }
 
 // ---- preference loss ------------------------------------------------------------
@@ -621,13 +627,12 @@ __device__ __forceinline__ PolicyTerms policy_terms(const PolicyArgs &a, const P
 }
 
 // Counted tokens among the labels, by the whole CTA; every thread returns their number.
-template <int IT>
 __device__ __forceinline__ int count_labels(const LogitsArgs &x) {
     __shared__ int total[32];
     int n = 0;
     for (int64_t t = threadIdx.x; t < x.tokens; t += blockDim.x) {
         int64_t label;
-        n += load_label<IT>(x, t, &label);
+        n += load_label(x, t, &label);
     }
     n = __reduce_add_sync(0xffffffffu, n);
     if ((threadIdx.x & 31) == 0) total[threadIdx.x / 32] = n;
@@ -638,10 +643,9 @@ __device__ __forceinline__ int count_labels(const LogitsArgs &x) {
 }
 
 // summary[3] = the number of counted tokens, for the rows' kernel.
-template <int IT>
 __global__ void __launch_bounds__(kSummaryThreads) policy_count_kernel(PolicyArgs a) {
     fa_allow_dependents();
-    const int n = count_labels<IT>(a.x);
+    const int n = count_labels(a.x);
     if (threadIdx.x == 0) a.summary[3] = static_cast<float>(n);
 }
 
@@ -654,13 +658,13 @@ enum Divisor { kGiven, kFromKernel, kCountHere };
 // fourth to registers (four CTAs of 64 KB rows then fit an SM instead of three).  The
 // gradient is made from there: one read and one write of the logits.  HELD == 0 (rows wider
 // than a cluster holds, or no gradient): the row is read again.
-template <int DT, int IT, int HELD>
-__global__ void __launch_bounds__(kRowThreads, 4)
+template <int DT, int NT, int HELD>
+__global__ void __launch_bounds__(NT, NT == 32 ? 32 : 1024 / NT)
 policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
     using E = Elem<DT>;
     using T = typename E::T;
-    extern __shared__ uint4 slot[];  // [3 * HELD][kRowThreads]
-    __shared__ RowSum parts[kRowThreads / 32], whole;
+    extern __shared__ uint4 slot[];  // [3 * HELD][NT]
+    __shared__ RowSum parts[NT / 32], whole;
     __shared__ float coef;
     const Share sh(split_log2);
     const int64_t t = sh.row, n = a.x.vocab;
@@ -670,7 +674,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
     // earlier work of the stream had ended: only its reader waits for it.
     fa_allow_dependents();
     int64_t label;
-    if (!load_label<IT>(a.x, t, &label)) {
+    if (!load_label(a.x, t, &label)) {
         if (sh.first() && tid == 0) {
             a.logp[t] = 0.f;
             a.token_loss[t] = 0.f;
@@ -684,9 +688,9 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
     }
     const T *row = static_cast<const T *>(a.x.logits) + t * a.x.ld;
     const RowSpan sp = row_span<DT>(row, n);
-    const RowPart part(sp, sh);  // HELD: at most 4 * HELD * kRowThreads vectors
+    const RowPart part(sp, sh);  // HELD: at most 4 * HELD * NT vectors
     const uint4 *q = reinterpret_cast<const uint4 *>(row + sp.head) + part.begin + tid;
-    constexpr int kGroup = HELD * kRowThreads;
+    constexpr int kGroup = HELD * NT;
     constexpr int kRegs = HELD > 0 ? HELD : 1;
     uint4 held[kRegs];
     if constexpr (HELD > 0) {
@@ -694,7 +698,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
         for (int g = 0; g < 3; ++g) {
 #pragma unroll
             for (int j = 0; j < HELD; ++j) {
-                const int i = g * kGroup + j * kRowThreads;
+                const int i = g * kGroup + j * NT;
                 if (i + tid < part.count && part.in_bounds(i + tid))
                     copy_async16(slot + i + tid, q + i);
             }
@@ -702,7 +706,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
         }
 #pragma unroll
         for (int j = 0; j < HELD; ++j) {
-            const int i = 3 * kGroup + j * kRowThreads;
+            const int i = 3 * kGroup + j * NT;
             held[j] = i + tid < part.count && part.in_bounds(i + tid) ? __ldcs(q + i)
                                                                      : no_vector<DT>();
         }
@@ -712,7 +716,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
     const PolicyToken in(a, first ? t : 0);
     const float label_logit = E::widen(row[label]);
     float denom = a.denominator;
-    if (divisor == kCountHere) denom = static_cast<float>(count_labels<IT>(a.x));
+    if (divisor == kCountHere) denom = static_cast<float>(count_labels(a.x));
 
     RowSum r;
     if constexpr (HELD > 0) {
@@ -725,7 +729,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
             uint4 v[kRegs];
 #pragma unroll
             for (int j = 0; j < HELD; ++j) {
-                const int i = i0 + j * kRowThreads + tid;
+                const int i = i0 + j * NT + tid;
                 v[j] = full || i < part.count ? slot[i] : no_vector<DT>();
             }
             acc.add<DT, HELD>(v);
@@ -737,9 +741,9 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
         copy_async_wait<0>();
         group(2);
         if (3 * kGroup + (tid & ~31) < part.count) acc.add<DT, HELD>(held);
-        r = merge_row(acc, parts, &whole, sh);
+        r = merge_row<NT>(acc, parts, &whole, sh);
     } else {
-        r = row_softmax<DT>(row, a.x, sh);
+        r = row_softmax<DT, NT>(row, a.x, sh);
     }
     if (first) {
         const float logp = label_logp(label_logit, r, a.x.scale);
@@ -769,29 +773,29 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
             const auto write = [&](int i, const uint4 &v) {
                 if (part.in_bounds(i + tid)) __stcs(o + i, gradient_vector<DT>(v, e, w));
             };
-            if (3 * kGroup + (HELD - 1) * kRowThreads + tid < part.count) {  // all of its vectors
+            if (3 * kGroup + (HELD - 1) * NT + tid < part.count) {  // all of its vectors
 #pragma unroll 1
                 for (int g = 0; g < 3; ++g)
 #pragma unroll
                     for (int j = 0; j < HELD; ++j)
-                        write(g * kGroup + j * kRowThreads, slot[g * kGroup + j * kRowThreads + tid]);
+                        write(g * kGroup + j * NT, slot[g * kGroup + j * NT + tid]);
 #pragma unroll
-                for (int j = 0; j < HELD; ++j) write(3 * kGroup + j * kRowThreads, held[j]);
+                for (int j = 0; j < HELD; ++j) write(3 * kGroup + j * NT, held[j]);
             } else {
 #pragma unroll 1
-                for (int i = 0; i < 3 * kGroup && i + tid < part.count; i += kRowThreads)
+                for (int i = 0; i < 3 * kGroup && i + tid < part.count; i += NT)
                     write(i, slot[i + tid]);
 #pragma unroll
                 for (int j = 0; j < HELD; ++j)
-                    if (3 * kGroup + j * kRowThreads + tid < part.count)
-                        write(3 * kGroup + j * kRowThreads, held[j]);
+                    if (3 * kGroup + j * NT + tid < part.count)
+                        write(3 * kGroup + j * NT, held[j]);
             }
-            if (label_is_mine<DT>(label, sp, part, sh))
+            if (label_is_mine<DT, NT>(label, sp, part, sh))
                 out[label] = E::round(fmaf(e(label_logit), w, c));
             return leave_row(sh);
         }
     }
-    row_gradient<DT>(row, out, n, a.x, r, coef, label, sh);
+    row_gradient<DT, NT>(row, out, n, a.x, r, coef, label, sh);
     leave_row(sh);
 }
 
@@ -802,7 +806,6 @@ struct PolicySums {
     Sum2 loss, kl;
     int n, clipped;
 };
-template <int IT>
 __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyArgs a) {
     __shared__ Sum2 parts[2][kSummaryThreads / 32];
     __shared__ int counts[2];
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyA
     for (int64_t t = blockIdx.x * kSummaryThreads + threadIdx.x; t < a.x.tokens;
          t += ctas * kSummaryThreads) {
         int64_t label;
-        const bool counted = load_label<IT>(a.x, t, &label);
+        const bool counted = load_label(a.x, t, &label);
         const PolicyToken in(a, t);  // loaded beside the label
         const float token_loss = a.token_loss[t], token_kl = a.token_kl[t], logp = a.logp[t];
         if (!counted) continue;
@@ -864,6 +867,16 @@ unsigned split_for(int64_t tokens, int64_t nvec, int64_t least, unsigned log2) {
     return log2;
 }
 
+// Calls f with the threads of a CTA that has ``nvec`` vectors of a row: sixteen vectors a
+// thread, as far as the sizes go.
+template <typename F>
+cudaError_t for_threads(int64_t nvec, F f) {
+    if (nvec <= 16 * 32) return f(std::integral_constant<int, 32>{});
+    if (nvec <= 16 * 64) return f(std::integral_constant<int, 64>{});
+    if (nvec <= 16 * 128) return f(std::integral_constant<int, 128>{});
+    return f(std::integral_constant<int, kMostThreads>{});
+}
+
 }  // namespace
 
 cudaError_t logprob_bounds_violations(unsigned long long *count, bool clear) {
@@ -879,30 +892,29 @@ cudaError_t logprob_bounds_violations(unsigned long long *count, bool clear) {
 #endif
 }
 
-cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, fa_itype lt, float *logp,
-                                  float *lse, cudaStream_t stream) {
+cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, float *logp, float *lse,
+                                  cudaStream_t stream) {
     return for_dtype(dt, [&](auto d) {
-        return for_itype(lt, [&](auto i) {
-            const unsigned log2 =
-                split_for(x.tokens, x.vocab / Elem<d()>::kVec, kBatch * kRowThreads, 0);
-            if (x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;
-            return launch_clusters(token_logprobs_kernel<d(), i()>,
-                                   dim3(static_cast<unsigned>(x.tokens << log2)),
-                                   dim3(kRowThreads), 0, 1u << log2, false, stream, x, logp, lse,
-                                   log2);
+        const int64_t nvec = x.vocab / Elem<d()>::kVec;
+        const unsigned log2 = split_for(x.tokens, nvec, kBatch * kMostThreads, 0);
+        if (x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;
+        return for_threads(nvec >> log2, [&](auto nt) {
+            return launch_clusters(token_logprobs_kernel<d(), nt()>,
+                                   dim3(static_cast<unsigned>(x.tokens << log2)), dim3(nt()), 0,
+                                   1u << log2, false, stream, x, logp, lse, log2);
         });
     });
 }
 
-cudaError_t launch_token_logprobs_gradient(const LogitGradArgs &a, fa_dtype dt, fa_itype lt,
+cudaError_t launch_token_logprobs_gradient(const LogitGradArgs &a, fa_dtype dt,
                                            cudaStream_t stream) {
     return for_dtype(dt, [&](auto d) {
-        return for_itype(lt, [&](auto i) {
-            const unsigned log2 =
-                split_for(a.x.tokens, a.x.vocab / Elem<d()>::kVec, kBatch * kRowThreads, 0);
-            if (a.x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;
-            logprob_gradient_kernel<d(), i()>
-                <<<static_cast<unsigned>(a.x.tokens << log2), kRowThreads, 0, stream>>>(a, log2);
+        const int64_t nvec = a.x.vocab / Elem<d()>::kVec;
+        const unsigned log2 = split_for(a.x.tokens, nvec, kBatch * kMostThreads, 0);
+        if (a.x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;
+        return for_threads(nvec >> log2, [&](auto nt) {
+            logprob_gradient_kernel<d(), nt()>
+                <<<static_cast<unsigned>(a.x.tokens << log2), nt(), 0, stream>>>(a, log2);
             return cudaGetLastError();
         });
     });
@@ -924,60 +936,57 @@ cudaError_t launch_preference(const PreferenceArgs &a, fa_itype lt, cudaStream_t
 
 namespace {
 
-template <int DT, int IT, int HELD>
+template <int DT, int NT, int HELD>
 cudaError_t launch_policy_rows(const PolicyArgs &a, unsigned log2, Divisor divisor,
                                cudaStream_t stream) {
-    constexpr int kSmem = 3 * HELD * kRowThreads * 16;
-    auto kernel = policy_row_kernel<DT, IT, HELD>;
+    constexpr int kSmem = 3 * HELD * NT * 16;
+    auto kernel = policy_row_kernel<DT, NT, HELD>;
     if (kSmem >= 48 * 1024) {  // with the static part, past what needs no asking
         cudaError_t err =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (err != cudaSuccess) return err;
     }
-    return launch_clusters(kernel,
-                           dim3(static_cast<unsigned>(a.x.tokens << log2)), dim3(kRowThreads),
+    return launch_clusters(kernel, dim3(static_cast<unsigned>(a.x.tokens << log2)), dim3(NT),
                            kSmem, 1u << log2, divisor == kFromKernel, stream, a, log2, divisor);
 }
 
 }  // namespace
 
-cudaError_t launch_policy(const PolicyArgs &a, fa_dtype dt, fa_itype lt, cudaStream_t stream) {
-    return for_itype(lt, [&](auto i) {
-        if (a.x.tokens > 0) {
-            // Every CTA counts the labels itself when they are few (a launch less); else one
-            // kernel does before the rows'.
-            constexpr int64_t kFewLabels = 2048;
-            const bool counts = (a.dlogits || a.dlogp) && a.denominator == 0.f;
-            const Divisor divisor = !counts                     ? kGiven
-                                    : a.x.tokens <= kFewLabels ? kCountHere
-                                                               : kFromKernel;
-            if (divisor == kFromKernel) {
-                policy_count_kernel<i()><<<1, kSummaryThreads, 0, stream>>>(a);
-                cudaError_t err = cudaGetLastError();
-                if (err != cudaSuccess) return err;
-            }
-            cudaError_t err = for_dtype(dt, [&](auto d) {
-                constexpr int64_t kMost = 4 * 4 * kRowThreads;  // vectors a CTA holds
-                const int64_t nvec = a.x.vocab / Elem<d()>::kVec;
-                unsigned log2 = 0;
-                while (log2 < 3 && nvec > kMost << log2) ++log2;
-                const bool held = a.dlogits && nvec <= kMost << log2;
-                log2 = split_for(a.x.tokens, nvec, kRowThreads, held ? log2 : 0);
-                if (a.x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;
-                const int64_t each = (nvec + (int64_t(1) << log2) - 1) >> log2;
-                if (!held) return launch_policy_rows<d(), i(), 0>(a, log2, divisor, stream);
-                if (each <= kMost / 4)
-                    return launch_policy_rows<d(), i(), 1>(a, log2, divisor, stream);
-                if (each <= kMost / 2)
-                    return launch_policy_rows<d(), i(), 2>(a, log2, divisor, stream);
-                return launch_policy_rows<d(), i(), 4>(a, log2, divisor, stream);
+cudaError_t launch_policy(const PolicyArgs &a, fa_dtype dt, cudaStream_t stream) {
+    if (a.x.tokens > 0) {
+        cudaError_t err = for_dtype(dt, [&](auto d) {
+            constexpr int64_t kMost = 4 * 4 * kMostThreads;  // vectors a CTA holds
+            const int64_t nvec = a.x.vocab / Elem<d()>::kVec;
+            unsigned log2 = 0;
+            while (log2 < 3 && nvec > kMost << log2) ++log2;
+            const bool held = a.dlogits && nvec <= kMost << log2;
+            log2 = split_for(a.x.tokens, nvec, kMostThreads, held ? log2 : 0);
+            if (a.x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;
+            const int64_t each = (nvec + (int64_t(1) << log2) - 1) >> log2;
+            return for_threads(each, [&](auto nt) {
+                // Every CTA counts the labels itself when that is a few loads a thread (a
+                // launch less); else one kernel does before the rows'.
+                const bool counts = (a.dlogits || a.dlogp) && a.denominator == 0.f;
+                const Divisor divisor = !counts                   ? kGiven
+                                        : a.x.tokens <= 8 * nt() ? kCountHere
+                                                                 : kFromKernel;
+                if (divisor == kFromKernel) {
+                    policy_count_kernel<<<1, kSummaryThreads, 0, stream>>>(a);
+                    cudaError_t e = cudaGetLastError();
+                    if (e != cudaSuccess) return e;
+                }
+                if (!held) return launch_policy_rows<d(), nt(), 0>(a, log2, divisor, stream);
+                // (rows of up to four vectors a lane of one warp)
+                if (nt() == 32 && each <= 4 * 32)
+                    return launch_policy_rows<d(), 32, 1>(a, log2, divisor, stream);
+                return launch_policy_rows<d(), nt(), 4>(a, log2, divisor, stream);
             });
-            if (err != cudaSuccess) return err;
-        }
-        const unsigned ctas = a.x.tokens > 2 * kSummaryThreads ? kSummaryCtas : 1;
-        return launch_clusters(policy_summary_kernel<i()>, dim3(ctas), dim3(kSummaryThreads), 0,
-                               ctas, true, stream, a);
-    });
+        });
+        if (err != cudaSuccess) return err;
+    }
+    const unsigned ctas = a.x.tokens > 2 * kSummaryThreads ? kSummaryCtas : 1;
+    return launch_clusters(policy_summary_kernel, dim3(ctas), dim3(kSummaryThreads), 0, ctas, true,
+                           stream, a);
 }
 
 }  // namespace fa

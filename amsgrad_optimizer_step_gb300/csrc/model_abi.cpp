@@ -120,6 +120,7 @@ fa::LogitsArgs logits_args(const fa_logits *x) {
     fa::LogitsArgs a;
     a.logits = x->logits;
     a.labels = x->labels;
+    a.wide_labels = x->ltype == FA_I64;
     a.tokens = x->tokens;
     a.vocab = x->vocab;
     a.ld = x->ld;
@@ -247,7 +248,7 @@ fa_status fa_token_logprobs(const fa_logits *x, float *logp, float *lse, void *s
     const Matrix ins[] = {logits_matrix(x), labels_vec(x)};
     FA_TRY(check_outputs(outs, 2, ins, 2));
     TraceRange trace("fa_token_logprobs");
-    return cuda_status(fa::launch_token_logprobs(logits_args(x), x->dtype, x->ltype, logp, lse,
+    return cuda_status(fa::launch_token_logprobs(logits_args(x), x->dtype, logp, lse,
                                                  static_cast<cudaStream_t>(stream)));
 }
 
@@ -279,8 +280,7 @@ fa_status fa_token_logprobs_gradient(const fa_logits *x, const float *lse, const
     a.factor = static_cast<float>(grad_scale * x->logit_scale);
     a.dlogits = dlogits;
     a.dlogits_ld = dlogits_ld;
-    return cuda_status(fa::launch_token_logprobs_gradient(a, x->dtype, x->ltype,
-                                                          static_cast<cudaStream_t>(stream)));
+    return cuda_status(fa::launch_token_logprobs_gradient(a, x->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 fa_status fa_preference_loss(const fa_logits *x, const fa_preference *p, void *stream) {
@@ -315,8 +315,7 @@ fa_status fa_preference_loss(const fa_logits *x, const fa_preference *p, void *s
     TraceRange trace("fa_preference_loss");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (x->tokens > 0)
-        FA_TRY(cuda_status(fa::launch_token_logprobs(logits_args(x), x->dtype, x->ltype, p->logp,
-                                                     p->lse, s)));
+        FA_TRY(cuda_status(fa::launch_token_logprobs(logits_args(x), x->dtype, p->logp, p->lse, s)));
     fa::PreferenceArgs a;
     a.labels = x->labels;
     a.tokens = x->tokens;
@@ -392,8 +391,7 @@ fa_status fa_policy_loss(const fa_logits *x, const fa_policy *p, void *stream) {
     a.dlogp = p->dlogp;
     a.dlogits = p->dlogits;
     a.dlogits_ld = p->dlogits_ld;
-    return cuda_status(
-        fa::launch_policy(a, x->dtype, x->ltype, static_cast<cudaStream_t>(stream)));
+    return cuda_status(fa::launch_policy(a, x->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 // ---- gated activation -------------------------------------------------------------

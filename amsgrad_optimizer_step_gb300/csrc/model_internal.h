@@ -75,12 +75,13 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &a, fa_itype idt, 
 struct LogitsArgs {
     const void *logits;
     const void *labels;
+    bool wide_labels;  // int64
     int64_t tokens, vocab, ld;
     float scale;  // logit_scale
     float k, k_lo;  // logit_scale * log2(e) as an FP32 value and its residual
 };
-cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, fa_itype lt, float *logp,
-                                  float *lse, cudaStream_t stream);
+cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, float *logp, float *lse,
+                                  cudaStream_t stream);
 
 struct LogitGradArgs {
     LogitsArgs x;
@@ -91,7 +92,7 @@ struct LogitGradArgs {
     void *dlogits;
     int64_t dlogits_ld;
 };
-cudaError_t launch_token_logprobs_gradient(const LogitGradArgs &a, fa_dtype dt, fa_itype lt,
+cudaError_t launch_token_logprobs_gradient(const LogitGradArgs &a, fa_dtype dt,
                                            cudaStream_t stream);
 
 struct PreferenceArgs {
@@ -117,7 +118,7 @@ struct PolicyArgs {
     void *dlogits;
     int64_t dlogits_ld;
 };
-cudaError_t launch_policy(const PolicyArgs &a, fa_dtype dt, fa_itype lt, cudaStream_t stream);
+cudaError_t launch_policy(const PolicyArgs &a, fa_dtype dt, cudaStream_t stream);
 
 // ---- gated activation -------------------------------------------------------------
 struct GatedForwardArgs {

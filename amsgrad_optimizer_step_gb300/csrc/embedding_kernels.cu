@@ -55,11 +55,11 @@ constexpr int kGroup =
 // ---- lookup --------------------------------------------------------------------
 
 // 2^lanes_log2 lanes take a token's stretch (blockIdx.y) of kLookupGroups groups each: a row's
-// loads are in flight together once its id is there.
-template <int TT, int OT, int IT, bool VEC>
+// loads are in flight together once its id is there.  Rows aligned for whole groups.
+template <int TT, int OT, int IT>
 __global__ void __launch_bounds__(kLookupThreads)
 lookup_kernel(LookupArgs a, int groups, int lanes_log2) {
-    constexpr int N = kGroup<TT, OT, VEC>;
+    constexpr int N = kGroup<TT, OT, true>;
     using TE = typename Elem<TT>::T;
     using OE = typename Elem<OT>::T;
     const int64_t thread = static_cast<int64_t>(blockIdx.x) * kLookupThreads + threadIdx.x;
@@ -85,6 +85,54 @@ lookup_kernel(LookupArgs a, int groups, int lanes_log2) {
 #pragma unroll
         for (int j = 0; j < N; ++j) x[k][j] = known ? x[k][j] * a.scale : 0.f;
         store_n<OT, N>(out + static_cast<int64_t>(g) * N, x[k]);
+    }
+}
+
+// The same for rows that begin anywhere: groups begin at the output's 16-byte lines, wherever
+// their elements lie in the table's; what is left of a row before and after them goes
+// element by element, an element a lane (65536 rows of 2047 BF16: 154 us with single
+// elements throughout).
+template <int TT, int OT, int IT>
+__global__ void __launch_bounds__(kLookupThreads) lookup_any_kernel(LookupArgs a, int lanes_log2) {
+    constexpr int N = kGroup<TT, OT, true>, kGroups = 2;
+    using TE = typename Elem<TT>::T;
+    using OE = typename Elem<OT>::T;
+    const int64_t thread = static_cast<int64_t>(blockIdx.x) * kLookupThreads + threadIdx.x;
+    const int64_t t = thread >> lanes_log2;
+    if (t >= a.tokens) return;
+    const int lanes = 1 << lanes_log2, lane = threadIdx.x & (lanes - 1);
+    const int dim = static_cast<int>(a.dim);
+    const int64_t id = load_id<IT>(a.ids, t);
+    const bool known = id >= 0 && id < a.vocab;
+    const TE *row = static_cast<const TE *>(a.table) + (known ? id : 0) * a.table_ld;
+    OE *out = static_cast<OE *>(a.out) + t * a.out_ld;
+    const Span table(a.table, ((a.vocab - 1) * a.table_ld + a.dim) * sizeof(TE));
+    const int past = static_cast<int>(reinterpret_cast<uintptr_t>(out) & 15);
+    const int head = min(dim, past ? (16 - past) / static_cast<int>(sizeof(OE)) : 0);
+    const int groups = (dim - head) / N, tail = head + groups * N;
+    if (blockIdx.y == 0)
+        for (int i = lane; i < head + dim - tail; i += lanes) {
+            const int e = i < head ? i : i - head + tail;
+            if (fa_in_bounds(e, 1, dim))
+                out[e] = Elem<OT>::round(known ? Elem<TT>::widen(row[e]) * a.scale : 0.f);
+        }
+    const int g0 = (blockIdx.y * kGroups << lanes_log2) + lane;
+    RawAny<TT, N> x[kGroups];
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        const int g = g0 + k * lanes;
+        if (known && g < groups && fa_in_bounds(head + g * N, N, dim))
+            x[k].load(row + head + g * N, N, table);
+    }
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        const int g = g0 + k * lanes;
+        if (g >= groups || !fa_in_bounds(head + g * N, N, dim)) break;
+        float y[N];
+        x[k].widen(y);
+#pragma unroll
+        for (int j = 0; j < N; ++j) y[j] = known ? y[j] * a.scale : 0.f;
+        store_n<OT, N>(out + head + g * N, y);
     }
 }
 
@@ -465,7 +513,8 @@ __device__ __forceinline__ int64_t run_end(const uint32_t *keys, int64_t tokens,
 // that does both, in [0]).
 template <int DT, int TT, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kSumThreads, ACC ? 4 : 5) sum_units_kernel(SumArgs a) {
-    constexpr int kSumAhead = ACC ? 4 : 6;  // rows a thread has in flight, of dout and the table
+    // rows a thread has in flight, of dout and the table: more of single elements
+    constexpr int kSumAhead = VEC ? (ACC ? 4 : 6) : 16;
     constexpr int N = kGroup<DT, TT, VEC>;
     constexpr uint32_t kNone = 0xffffffffu;  // no id: ids are below 2^31
     using DE = typename Elem<DT>::T;
@@ -650,23 +699,22 @@ cudaError_t launch_embedding_lookup(const LookupArgs &a, fa_itype idt, fa_dtype 
     return for_dtype(tdt, [&](auto td) {
         return for_dtype(odt, [&](auto od) {
             return for_itype(idt, [&](auto id) {
-                const auto go = [&](auto v) {
-                    constexpr bool VEC = decltype(v)::value;
-                    const int64_t groups = a.dim / kGroup<td(), od(), VEC>;
-                    int lanes_log2 = 0;
-                    while (lanes_log2 < 5 && (int64_t(kLookupGroups) << lanes_log2) < groups)
-                        ++lanes_log2;
-                    const int64_t ctas = ((a.tokens << lanes_log2) + kLookupThreads - 1) /
-                                         kLookupThreads;
-                    const int64_t stretch = int64_t(kLookupGroups) << lanes_log2;
-                    const int64_t stretches = (groups + stretch - 1) / stretch;
-                    if (ctas > kMaxGridX || stretches > 65535) return cudaErrorInvalidConfiguration;
-                    lookup_kernel<td(), od(), id(), VEC>
-                        <<<dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(stretches)),
-                           kLookupThreads, 0, stream>>>(a, static_cast<int>(groups), lanes_log2);
-                    return cudaGetLastError();
-                };
-                return vec ? go(std::true_type{}) : go(std::false_type{});
+                const int64_t groups = (a.dim - 1) / kGroup<td(), od(), true> + 1;
+                const int64_t in_flight = vec ? kLookupGroups : 2;
+                int log2 = 0;
+                while (log2 < 5 && in_flight << log2 < groups) ++log2;
+                const int64_t ctas = ((a.tokens << log2) + kLookupThreads - 1) / kLookupThreads;
+                const int64_t stretch = in_flight << log2;
+                const int64_t stretches = (groups + stretch - 1) / stretch;
+                if (ctas > kMaxGridX || stretches > 65535) return cudaErrorInvalidConfiguration;
+                const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(stretches));
+                if (vec)
+                    lookup_kernel<td(), od(), id()><<<grid, kLookupThreads, 0, stream>>>(
+                        a, static_cast<int>(groups), log2);
+                else
+                    lookup_any_kernel<td(), od(), id()>
+                        <<<grid, kLookupThreads, 0, stream>>>(a, log2);
+                return cudaGetLastError();
             });
         });
     });

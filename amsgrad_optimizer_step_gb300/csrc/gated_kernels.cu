@@ -76,36 +76,52 @@ struct Activation<FA_GELU_TANH> {
     }
 };
 
-// A lane's run of eight columns [c, c + 8) of a row: one 16-byte access (two for FP32) when
-// the rows are aligned and the columns all exist, element accesses otherwise; columns past
-// the end read as 0 and are not written.
-template <int DT, bool VEC>
-__device__ __forceinline__ Raw<DT, kRun> load_run(const void *base, int64_t row, int64_t ld,
-                                                  int64_t c, int64_t cols) {
-    using E = Elem<DT>;
-    const typename E::T *p = static_cast<const typename E::T *>(base) + row * ld + c;
-    Raw<DT, kRun> x;
-    if (VEC && c + kRun <= cols) {
-        if (fa_in_bounds(c, kRun, cols)) x.load(p);
-    } else {
-        float y[kRun];
-#pragma unroll
-        for (int j = 0; j < kRun; ++j) y[j] = c + j < cols ? E::widen(p[j]) : 0.f;
-        x.from(y);  // exact: they came from this type
-    }
-    return x;
+// A lane's run of eight columns [c, c + 8) of a row.  ALIGNED: one 16-byte access (two for
+// FP32) when the columns all exist, element accesses otherwise; else the 16-byte lines that the
+// run touches (see RawAny, store_any).  Columns past the end read as 0 and are not written.
+__device__ __forceinline__ int valid_cols(int64_t c, int64_t cols) {
+    return c + kRun <= cols ? kRun : c < cols ? static_cast<int>(cols - c) : 0;
 }
-template <int DT, bool VEC>
-__device__ __forceinline__ void store_run(void *base, int64_t row, int64_t ld, int64_t c,
-                                          int64_t cols, const float *x) {
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ Raw<DT, kRun> load_run(const MatrixArgs &m, int64_t row, int64_t c) {
     using E = Elem<DT>;
-    typename E::T *p = static_cast<typename E::T *>(base) + row * ld + c;
-    if (VEC && c + kRun <= cols) {
-        if (fa_in_bounds(c, kRun, cols)) store_n<DT, kRun>(p, x);
-    } else {
+    const typename E::T *p = static_cast<const typename E::T *>(m.p) + row * m.ld + c;
+    const int valid = valid_cols(c, m.cols);
+    if (valid && !fa_in_bounds(c, valid, m.cols)) return {};
+    if constexpr (ALIGNED) {
+        Raw<DT, kRun> x;
+        if (c + kRun <= m.cols) {
+            x.load(p);
+        } else {
+            float y[kRun];
 #pragma unroll
-        for (int j = 0; j < kRun; ++j)
-            if (c + j < cols) p[j] = E::round(x[j]);
+            for (int j = 0; j < kRun; ++j) y[j] = j < valid ? E::widen(p[j]) : 0.f;
+            x.from(y);  // exact: they came from this type
+        }
+        return x;
+    } else {
+        RawAny<DT, kRun> x;
+        x.load(p, valid, Span(m.p, ((m.rows - 1) * m.ld + m.cols) * sizeof(typename E::T)));
+        return x.raw();
+    }
+}
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void store_run(const MatrixArgs &m, int64_t row, int64_t c,
+                                          const float *x, unsigned lanes) {
+    using E = Elem<DT>;
+    typename E::T *p = static_cast<typename E::T *>(m.p) + row * m.ld + c;
+    int valid = valid_cols(c, m.cols);
+    if (valid && !fa_in_bounds(c, valid, m.cols)) valid = 0;
+    if constexpr (ALIGNED) {
+        if (c + kRun <= m.cols) {
+            store_n<DT, kRun>(p, x);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kRun; ++j)
+                if (j < valid) p[j] = E::round(x[j]);
+        }
+    } else {
+        store_any<DT, kRun>(p, x, valid, lanes, kLanes);
     }
 }
 
@@ -144,8 +160,8 @@ __device__ __forceinline__ void decode(uint2 codes, float scale, uint64_t *x) {
     }
 }
 
-template <int DT, int ACT, bool VEC, bool KEEP>
-__global__ void __launch_bounds__(kGatedThreads, VEC && DT != FA_F32 ? 5 : 2)
+template <int DT, int ACT, bool ALIGNED, bool KEEP>
+__global__ void __launch_bounds__(kGatedThreads, DT == FA_F32 ? 2 : ALIGNED ? 5 : 4)
 gated_forward_kernel(GatedForwardArgs a) {
     const uint32_t b = (blockIdx.x * kGatedThreads + threadIdx.x) / kLanes;
     const int lane = threadIdx.x % kLanes;
@@ -156,12 +172,12 @@ gated_forward_kernel(GatedForwardArgs a) {
                           kCheckpointBlock + lane * kRun;
     Raw<DT, kRun> g[2], u[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) g[r] = load_run<DT, VEC>(a.gate, row, a.gate_ld, c + r * kRunStride, a.cols);
+    for (int r = 0; r < 2; ++r) g[r] = load_run<DT, ALIGNED>(a.gate, row, c + r * kRunStride);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) u[r] = load_run<DT, VEC>(a.up, row, a.up_ld, c + r * kRunStride, a.cols);
+    for (int r = 0; r < 2; ++r) u[r] = load_run<DT, ALIGNED>(a.up, row, c + r * kRunStride);
     float inv_g = 0.f, inv_u = 0.f;
+    const unsigned lanes = 0xffu << (threadIdx.x & 24);
     if (KEEP) {
-        const unsigned lanes = 0xffu << (threadIdx.x & 24);
         float tg = max_nan(g[0].magnitude(), g[1].magnitude());
         float tu = max_nan(u[0].magnitude(), u[1].magnitude());
 #pragma unroll
@@ -194,12 +210,13 @@ gated_forward_kernel(GatedForwardArgs a) {
         for (int j = 0; j < kRun; j += 2)
             unpair(mul2(Activation<ACT>::value(pair(x[j], x[j + 1])), pair(y[j], y[j + 1])), x[j],
                    x[j + 1]);
-        store_run<DT, VEC>(a.h, row, a.h_ld, c + r * kRunStride, a.cols, x);
+        store_run<DT, ALIGNED>(a.h, row, c + r * kRunStride, x, lanes);
     }
 }
 
-template <int DT, int ACT, bool VEC>
-__global__ void __launch_bounds__(kGatedThreads) gated_backward_kernel(GatedBackwardArgs a) {
+template <int DT, int ACT, bool ALIGNED>
+__global__ void __launch_bounds__(kGatedThreads, DT == FA_F32 || ALIGNED ? 2 : 4)
+gated_backward_kernel(GatedBackwardArgs a) {
     const uint32_t b = (blockIdx.x * kGatedThreads + threadIdx.x) / kLanes;
     const int lane = threadIdx.x % kLanes;
     const int64_t n = a.rows * a.blocks;
@@ -208,13 +225,14 @@ __global__ void __launch_bounds__(kGatedThreads) gated_backward_kernel(GatedBack
     const int64_t c = static_cast<int64_t>(b - row * static_cast<uint32_t>(a.blocks)) *
                           kCheckpointBlock + lane * kRun;
     const int8_t *code = a.codes + static_cast<int64_t>(b) * kCheckpointBlock + lane * kRun;
+    const unsigned lanes = 0xffu << (threadIdx.x & 24);
     uint2 qg[2], qu[2];
     Raw<DT, kRun> d[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         qg[r] = __ldcs(reinterpret_cast<const uint2 *>(code + r * kRunStride));
         qu[r] = __ldcs(reinterpret_cast<const uint2 *>(code + n * kCheckpointBlock + r * kRunStride));
-        d[r] = load_run<DT, VEC>(a.dh, row, a.dh_ld, c + r * kRunStride, a.cols);
+        d[r] = load_run<DT, ALIGNED>(a.dh, row, c + r * kRunStride);
     }
     const float sg = a.scales[b], su = a.scales[n + b];
 #pragma unroll
@@ -234,16 +252,17 @@ __global__ void __launch_bounds__(kGatedThreads) gated_backward_kernel(GatedBack
             unpair(mul2(dh, act), du[j], du[j + 1]);
             unpair(mul2(act, u[j / 2]), h[j], h[j + 1]);
         }
-        store_run<DT, VEC>(a.dgate, row, a.dgate_ld, c + r * kRunStride, a.cols, dg);
-        store_run<DT, VEC>(a.dup, row, a.dup_ld, c + r * kRunStride, a.cols, du);
-        if (a.h) store_run<DT, VEC>(a.h, row, a.h_ld, c + r * kRunStride, a.cols, h);
+        store_run<DT, ALIGNED>(a.dgate, row, c + r * kRunStride, dg, lanes);
+        store_run<DT, ALIGNED>(a.dup, row, c + r * kRunStride, du, lanes);
+        if (a.h.p) store_run<DT, ALIGNED>(a.h, row, c + r * kRunStride, h, lanes);
     }
 }
 
 // Whether 16-byte accesses at multiples of eight columns are aligned in every row.
-bool vector_rows(const void *p, int64_t ld, fa_dtype dt) {
-    const int64_t row_bytes = ld * (dt == FA_F32 ? 4 : 2);
-    return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_bytes % 16 == 0);
+bool aligned_rows(const MatrixArgs &m, fa_dtype dt) {
+    const int64_t row_bytes = m.ld * (dt == FA_F32 ? 4 : 2);
+    return !m.p || (reinterpret_cast<uintptr_t>(m.p) % 16 == 0 &&
+                    (m.rows < 2 || row_bytes % 16 == 0));
 }
 
 template <typename F>
@@ -270,8 +289,7 @@ cudaError_t gated_bounds_violations(unsigned long long *count, bool clear) {
 cudaError_t launch_gated_forward(const GatedForwardArgs &a, fa_dtype dt, fa_activation act,
                                  cudaStream_t stream) {
     const int64_t ctas = (a.rows * a.blocks * kLanes + kGatedThreads - 1) / kGatedThreads;
-    const bool vec = vector_rows(a.gate, a.gate_ld, dt) && vector_rows(a.up, a.up_ld, dt) &&
-                     vector_rows(a.h, a.h_ld, dt);
+    const bool vec = aligned_rows(a.gate, dt) && aligned_rows(a.up, dt) && aligned_rows(a.h, dt);
     return for_dtype(dt, [&](auto d) {
         return for_activation(act, [&](auto ac) {
             auto *kernel = vec ? a.codes ? gated_forward_kernel<d(), ac(), true, true>
@@ -287,8 +305,8 @@ cudaError_t launch_gated_forward(const GatedForwardArgs &a, fa_dtype dt, fa_acti
 cudaError_t launch_gated_backward(const GatedBackwardArgs &a, fa_dtype dt, fa_activation act,
                                   cudaStream_t stream) {
     const int64_t ctas = (a.rows * a.blocks * kLanes + kGatedThreads - 1) / kGatedThreads;
-    const bool vec = vector_rows(a.dh, a.dh_ld, dt) && vector_rows(a.dgate, a.dgate_ld, dt) &&
-                     vector_rows(a.dup, a.dup_ld, dt) && vector_rows(a.h, a.h_ld, dt);
+    const bool vec = aligned_rows(a.dh, dt) && aligned_rows(a.dgate, dt) &&
+                     aligned_rows(a.dup, dt) && aligned_rows(a.h, dt);
     return for_dtype(dt, [&](auto d) {
         return for_activation(act, [&](auto ac) {
             auto *kernel = vec ? gated_backward_kernel<d(), ac(), true>

@@ -20,7 +20,7 @@ using fa::TraceRange;
 using fa::valid_dtype;
 
 constexpr int64_t kMaxCount = 0x7fffffff;        // tokens, ids, rows: the grid's limit
-constexpr int64_t kMaxDim = int64_t(1) << 22;       // of an embedding: the grid's other limit
+constexpr int64_t kMaxDim = int64_t(1) << 21;       // of an embedding: the grid's other limit
 constexpr int64_t kMaxElements = int64_t(1) << 56;  // of one matrix: byte offsets stay in 64 bits
 constexpr int64_t kMaxBlocks = int64_t(1) << 28;    // of a checkpoint: 8 lanes each, in one grid
 constexpr double kLog2E = 1.4426950408889634;
@@ -436,16 +436,12 @@ fa_status fa_gated_forward(int64_t rows, int64_t cols, const void *gate, int64_t
     FA_TRY(check_outputs(outs, 3, ins, 2));
     TraceRange trace("fa_gated_forward");
     fa::GatedForwardArgs a;
-    a.gate = gate;
-    a.up = up;
-    a.h = h;
+    a.gate = {const_cast<void *>(gate), rows, cols, gate_ld};
+    a.up = {const_cast<void *>(up), rows, cols, up_ld};
+    a.h = {h, rows, cols, h_ld};
     a.codes = codes;
     a.scales = scales;
     a.rows = rows;
-    a.cols = cols;
-    a.gate_ld = gate_ld;
-    a.up_ld = up_ld;
-    a.h_ld = h_ld;
     a.blocks = (cols + fa::kCheckpointBlock - 1) / fa::kCheckpointBlock;
     a.by_blocks = fa::Divider(static_cast<uint32_t>(a.blocks));
     return cuda_status(
@@ -483,16 +479,11 @@ fa_status fa_gated_backward(int64_t rows, int64_t cols, const int8_t *codes, con
     fa::GatedBackwardArgs a;
     a.codes = codes;
     a.scales = scales;
-    a.dh = dh;
-    a.dgate = dgate;
-    a.dup = dup;
-    a.h = h;
+    a.dh = {const_cast<void *>(dh), rows, cols, dh_ld};
+    a.dgate = {dgate, rows, cols, dgate_ld};
+    a.dup = {dup, rows, cols, dup_ld};
+    a.h = {h, rows, cols, h_ld};
     a.rows = rows;
-    a.cols = cols;
-    a.dh_ld = dh_ld;
-    a.dgate_ld = dgate_ld;
-    a.dup_ld = dup_ld;
-    a.h_ld = h_ld;
     a.blocks = (cols + fa::kCheckpointBlock - 1) / fa::kCheckpointBlock;
     a.by_blocks = fa::Divider(static_cast<uint32_t>(a.blocks));
     return cuda_status(

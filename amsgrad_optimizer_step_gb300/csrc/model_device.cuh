@@ -171,6 +171,20 @@ __device__ __forceinline__ void load_n(const typename Elem<DT>::T *p, float *x) 
     }
 }
 
+// N FP32 values (whole vectors) rounded and packed into words.
+template <int DT, int N>
+__device__ __forceinline__ void pack_words(const float *x, uint32_t *w) {
+    using E = Elem<DT>;
+#pragma unroll
+    for (int k = 0; k < N / E::kVec; ++k) {
+        const uint4 r = E::pack(x + k * E::kVec);
+        w[4 * k] = r.x;
+        w[4 * k + 1] = r.y;
+        w[4 * k + 2] = r.z;
+        w[4 * k + 3] = r.w;
+    }
+}
+
 // N elements as they lie in memory, to be widened later: half the registers for 16-bit types.
 template <int DT, int N>
 struct Raw {
@@ -209,6 +223,119 @@ struct Raw {
         return E::template magnitude<kWords>(r);
     }
 };
+
+// ---- runs of elements at any element-aligned address ----------------------------------
+
+// Words [0, W) of ``cat`` moved down by ``bytes`` (0 to 15, a multiple of two); cat holds W + 4.
+template <int W>
+__device__ __forceinline__ void move_down(const uint32_t *cat, int bytes, uint32_t *out) {
+    uint32_t a[W + 3], b[W + 1];
+#pragma unroll
+    for (int i = 0; i < W + 3; ++i) a[i] = bytes & 4 ? cat[i + 1] : cat[i];
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) b[i] = bytes & 8 ? a[i + 2] : a[i];
+#pragma unroll
+    for (int i = 0; i < W; ++i) out[i] = __funnelshift_r(b[i], b[i + 1], 8 * (bytes & 2));
+}
+
+// Bytes that 16-byte reads may touch: those of the 16-byte lines inside an array.
+struct Span {
+    uintptr_t lo, hi;
+
+    __host__ __device__ Span(const void *p, int64_t bytes)
+        : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + bytes) {}
+};
+
+// N elements (whole vectors) from any address, as they lie in memory: the 16-byte lines
+// around them where those are inside the array (what else is in them is not used), else
+// element by element.
+template <int DT, int N>
+struct RawAny {
+    using E = Elem<DT>;
+    static constexpr int kWords = N / E::kVec * 4;
+    uint32_t cat[kWords + 4];
+    int bytes;  // from the first word to the first element
+
+    // The first ``valid`` of the elements exist; the others are 0.
+    __device__ __forceinline__ void load(const typename E::T *p, int valid, const Span &in) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p), line = at & ~uintptr_t(15);
+        bytes = static_cast<int>(at - line);
+        if (valid == N && line >= in.lo && line + 4 * kWords + (bytes ? 16 : 0) <= in.hi) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(line);
+#pragma unroll
+            for (int k = 0; k <= kWords / 4; ++k) {
+                uint4 r = make_uint4(0u, 0u, 0u, 0u);
+                if (k < kWords / 4 || bytes) r = __ldg(q + k);
+                cat[4 * k] = r.x;
+                cat[4 * k + 1] = r.y;
+                cat[4 * k + 2] = r.z;
+                cat[4 * k + 3] = r.w;
+            }
+            return;
+        }
+        bytes = 0;
+        float x[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = j < valid ? E::widen(p[j]) : 0.f;
+        pack_words<DT, N>(x, cat);  // exact: they came from this type
+#pragma unroll
+        for (int k = kWords; k < kWords + 4; ++k) cat[k] = 0u;
+    }
+    __device__ __forceinline__ Raw<DT, N> raw() const {
+        uint32_t w[kWords];
+        move_down<kWords>(cat, bytes, w);
+        Raw<DT, N> x;
+#pragma unroll
+        for (int k = 0; k < kWords / 4; ++k)
+            x.r[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        return x;
+    }
+    __device__ __forceinline__ void widen(float *x) const { raw().widen(x); }
+};
+
+// Stores the runs of N elements that consecutive lanes hold of one row, lane after lane, from
+// any address on: each lane writes the 16-byte lines that begin in the run before its own
+// with what that lane has of them, and only the ends of the lanes' whole stretch go element
+// by element.  ``p``: where this lane's run belongs; ``valid``: how many of its elements exist
+// (N, but for the last lanes).  All lanes of ``lanes`` call it, in groups of ``width``.
+template <int DT, int N>
+__device__ __forceinline__ void store_any(typename Elem<DT>::T *p, const float *x, int valid,
+                                          unsigned lanes, int width) {
+    using E = Elem<DT>;
+    constexpr int W = N / E::kVec * 4, kSize = sizeof(typename E::T);
+    const int bytes = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+    uint32_t cat[W + 4];  // the end of the run before, then this one
+    pack_words<DT, N>(x, cat + 4);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) cat[k] = __shfl_up_sync(lanes, cat[W + k], 1, width);
+    const int lane = (threadIdx.x & 31) & (width - 1);
+    // whole: this lane writes its lines from the one that its run begins in
+    const bool whole = valid == N && (lane > 0 || bytes == 0);
+    const bool next_whole = __shfl_down_sync(lanes, whole, 1, width) && lane < width - 1 &&
+                            (lanes >> ((threadIdx.x & 31) + 1) & 1u);
+    int from = 0, to = valid;  // elements left to write one by one
+    if (whole) {
+        uint32_t w[W];
+        // bytes == 0: the lines are the run's own
+        if (bytes == 0) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k] = cat[4 + k];
+        } else {
+            move_down<W>(cat, 16 - bytes, w);
+        }
+        uint4 *q = reinterpret_cast<uint4 *>(reinterpret_cast<uintptr_t>(p) - bytes);
+#pragma unroll
+        for (int k = 0; k < W / 4; ++k)
+            __stcs(q + k, make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+        from = N - bytes / kSize;  // what the next lane's first line holds
+        to = next_whole ? from : N;
+    } else if (valid == N && next_whole) {
+        to = N - bytes / kSize;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (j >= from && j < to) p[j] = E::round(x[j]);
+}
 
 // load_n for rows that others read too (kept in L2).
 template <int DT, int N>

@@ -121,12 +121,15 @@ struct PolicyArgs {
 cudaError_t launch_policy(const PolicyArgs &a, fa_dtype dt, cudaStream_t stream);
 
 // ---- gated activation -------------------------------------------------------------
+struct MatrixArgs {
+    void *p;
+    int64_t rows, cols, ld;
+};
 struct GatedForwardArgs {
-    const void *gate, *up;
-    void *h;
+    MatrixArgs gate, up, h;
     int8_t *codes;  // nullptr: no checkpoint
     float *scales;
-    int64_t rows, cols, gate_ld, up_ld, h_ld, blocks;
+    int64_t rows, blocks;
     Divider by_blocks;
 };
 cudaError_t launch_gated_forward(const GatedForwardArgs &a, fa_dtype dt, fa_activation act,
@@ -135,9 +138,8 @@ cudaError_t launch_gated_forward(const GatedForwardArgs &a, fa_dtype dt, fa_acti
 struct GatedBackwardArgs {
     const int8_t *codes;
     const float *scales;
-    const void *dh;
-    void *dgate, *dup, *h;  // h may be nullptr
-    int64_t rows, cols, dh_ld, dgate_ld, dup_ld, h_ld, blocks;
+    MatrixArgs dh, dgate, dup, h;  // h.p may be nullptr
+    int64_t rows, blocks;
     Divider by_blocks;
 };
 cudaError_t launch_gated_backward(const GatedBackwardArgs &a, fa_dtype dt, fa_activation act,

@@ -437,7 +437,7 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2
 // Rows are taken from the last to the first: the pass that made the statistics left the
 // last rows in L2.
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 1536 / NT)
 logprob_gradient_kernel(LogitGradArgs a, unsigned split_log2) {
     using T = typename Elem<DT>::T;
     const Share sh(split_log2);
@@ -630,6 +630,7 @@ __device__ __forceinline__ PolicyTerms policy_terms(const PolicyArgs &a, const P
 __device__ __forceinline__ int count_labels(const LogitsArgs &x) {
     __shared__ int total[32];
     int n = 0;
+#pragma unroll 8
     for (int64_t t = threadIdx.x; t < x.tokens; t += blockDim.x) {
         int64_t label;
         n += load_label(x, t, &label);

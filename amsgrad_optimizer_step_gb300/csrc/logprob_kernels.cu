@@ -242,9 +242,13 @@ __device__ __forceinline__ float label_logp(float x, const RowSum &r, float scal
     return y.hi + (y.lo + (p_lo - log_s.lo - kTermsLow * (1.f - __fdividef(1.f, r.s))));
 }
 
+// A token's label; whether it is counted.  Both types by 32-bit words, so that the kernels
+// are compiled once for them: a counted label's upper word is zero.
 __device__ __forceinline__ bool load_label(const LogitsArgs &x, int64_t t, int64_t *label) {
-    *label = x.wide_labels ? load_id<FA_I64>(x.labels, t) : load_id<FA_I32>(x.labels, t);
-    return *label >= 0 && *label < x.vocab;
+    const unsigned *word = static_cast<const unsigned *>(x.labels) + (t << x.wide_labels);
+    const unsigned low = word[0], high = x.wide_labels ? word[1] : 0u;
+    *label = low;
+    return high == 0 && low < static_cast<unsigned>(x.vocab);
 }
 
 // The part of a row's vectors that a CTA takes.
@@ -437,7 +441,7 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2
 // Rows are taken from the last to the first: the pass that made the statistics left the
 // last rows in L2.
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT, 1536 / NT)
+__global__ void __launch_bounds__(NT, NT == 32 ? 32 : 1536 / NT)
 logprob_gradient_kernel(LogitGradArgs a, unsigned split_log2) {
     using T = typename Elem<DT>::T;
     const Share sh(split_log2);
@@ -630,7 +634,6 @@ __device__ __forceinline__ PolicyTerms policy_terms(const PolicyArgs &a, const P
 __device__ __forceinline__ int count_labels(const LogitsArgs &x) {
     __shared__ int total[32];
     int n = 0;
-#pragma unroll 8
     for (int64_t t = threadIdx.x; t < x.tokens; t += blockDim.x) {
         int64_t label;
         n += load_label(x, t, &label);

@@ -406,7 +406,7 @@ __device__ __forceinline__ RowSum row_softmax(const void *row, const LogitsArgs 
         for (int j = 0; j < kBatch; ++j) {
             const int i = i0 + j * NT;
             r[j] = (decltype(full)::value || i + tid < part.count) && part.in_bounds(i + tid)
-                       ? __ldg(q + i)
+                       ? q[i]
                        : no_vector<DT>();
         }
         acc.add<DT, kBatch>(r);
@@ -415,7 +415,7 @@ __device__ __forceinline__ RowSum row_softmax(const void *row, const LogitsArgs 
 }
 
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, NT == 32 ? 32 : 1536 / NT)
 token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2) {
     using T = typename Elem<DT>::T;
     fa_allow_dependents();
@@ -430,9 +430,11 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2
         return;
     }
     const T *row = static_cast<const T *>(x.logits) + t * x.ld;
+    const bool first = sh.first() && threadIdx.x == 0;
+    const float label_logit = first ? Elem<DT>::widen(row[label]) : 0.f;  // before the sum
     const RowSum r = row_softmax<DT, NT>(row, x, sh);
-    if (sh.first() && threadIdx.x == 0) {
-        logp[t] = label_logp(Elem<DT>::widen(row[label]), r, x.scale);
+    if (first) {
+        logp[t] = label_logp(label_logit, r, x.scale);
         if (lse) reinterpret_cast<float2 *>(lse)[t] = make_float2(r.top, r.s);
     }
     leave_row(sh);

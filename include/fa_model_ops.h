@@ -58,8 +58,9 @@ fa_status fa_embedding_lookup(int64_t tokens, const void *ids, fa_itype idt, con
 
 /* Scratch of fa_embedding_gradient in bytes, into *bytes (the pages
  * have no counterpart): the tokens sorted by id, and FP32 partial sums of the ids
- * whose tokens several blocks share.  Host only; FA_ERR_SIZE for a negative count or
- * one above 2^31 - 1 tokens or ids. */
+ * whose tokens several blocks share.  Host only; FA_ERR_SIZE for a negative count, more
+ * than 2^31 - 1 tokens, 2^31 - 2 ids or 2^21 columns (of a lookup: the same tokens and
+ * columns, and any vocab). */
 fa_status fa_embedding_scratch(int64_t tokens, int64_t vocab, int64_t dim, int64_t *bytes);
 
 /*
@@ -193,7 +194,8 @@ fa_status fa_policy_loss(const fa_logits *x, const fa_policy *a, void *stream);
 /* Size of the checkpoint of a [rows, cols] gated activation (the pages
  * have no counterpart): its codes in bytes, 2 * rows * pitch with pitch = cols rounded up to
  * 128 (gate [rows, pitch], then up), and its scales in FP32 elements, 2 * rows *
- * pitch / 128 (in the same order).  Host only. */
+ * pitch / 128 (in the same order).  Host only; FA_ERR_SIZE for a negative count or
+ * more than 2^28 blocks (rows * pitch / 128), which the calls below refuse too. */
 fa_status fa_checkpoint_size(int64_t rows, int64_t cols, int64_t *code_bytes,
                              int64_t *scale_elements);
 

@@ -33,9 +33,10 @@ namespace {
 
 FA_BOUNDS_COUNTER(g_embedding_oob)
 
+namespace cg = cooperative_groups;
+
 constexpr int kLookupThreads = 256;
 constexpr int kLookupGroups = 4;  // 16-byte groups a lane has in flight
-namespace cg = cooperative_groups;
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -55,7 +56,9 @@ constexpr int kGroup =
 // ---- lookup --------------------------------------------------------------------
 
 // 2^lanes_log2 lanes take a token's stretch (blockIdx.y) of kLookupGroups groups each: a row's
-// loads are in flight together once its id is there.  Rows aligned for whole groups.
+// loads are in flight together once its id is there.  Rows aligned for whole groups.  The
+// writes bound it, and the reads of the rows that occur: 65536 tokens of 2048 BF16 from a table
+// of 131 MB take 53 us, 6.1 TB/s of both (the table's 55 MB that L2 does not hold are read once).
 template <int TT, int OT, int IT>
 __global__ void __launch_bounds__(kLookupThreads)
 lookup_kernel(LookupArgs a, int groups, int lanes_log2) {
@@ -90,7 +93,7 @@ lookup_kernel(LookupArgs a, int groups, int lanes_log2) {
 
 // The same for rows that begin anywhere: groups begin at the output's 16-byte lines, wherever
 // their elements lie in the table's; what is left of a row before and after them goes
-// element by element, an element a lane (65536 rows of 2047 BF16: 154 us with single
+// element by element, an element a lane (65536 rows of 2047 BF16: 78 us; 154 us with single
 // elements throughout).
 template <int TT, int OT, int IT>
 __global__ void __launch_bounds__(kLookupThreads) lookup_any_kernel(LookupArgs a, int lanes_log2) {
@@ -232,7 +235,9 @@ struct SortSmem {
     uint32_t warp_total[2][kSortWarps];
 };
 
-// The first chunks' clusters sort; the CTAs after them zero the table meanwhile.
+// The first chunks' clusters sort; the CTAs after them zero the table meanwhile.  Latency
+// bounds the sort, not its 0.8 MB: barriers of the cluster, ballots, prefix sums (65536 tokens
+// and 32000 ids, two digits: 18.5 us; 4096 tokens: 12.3; 333: 8.3).
 template <int IT, typename Item>
 __global__ void __launch_bounds__(kSortThreads) sort_chunk_kernel(SortArgs a) {
     fa_allow_dependents();
@@ -508,6 +513,8 @@ __device__ __forceinline__ int64_t run_end(const uint32_t *keys, int64_t tokens,
     return lo;
 }
 
+// Bound by its reads and writes: 65536 rows of 2048 BF16 summed into 32000 take 53 us, 7.1
+// TB/s, with up to six rows' loads of a thread in flight.
 // CTA (u, slab): unit u's runs, columns of slab.  A long run that began before the unit
 // leaves its sum in partial[u][0], one that goes on after it in partial[u][1] (a run
 // that does both, in [0]).
@@ -618,7 +625,9 @@ __global__ void __launch_bounds__(kSumThreads, ACC ? 4 : 5) sum_units_kernel(Sum
 }
 
 // The long runs: a CTA at a time adds one in columns [32 N slab, + 32 N), its warps each a
-// stretch of the partial sums in unit order, then the stretches' sums in order.
+// stretch of the partial sums in unit order, then the stretches' sums in order.  The partial
+// sums (10 MB for 65536 Zipf-distributed tokens of 2048) are still in L2: about 5 us, in the
+// wake of the sums.
 template <int DT, int TT, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_units_kernel(SumArgs a, uint32_t slabs) {
     constexpr int N = kGroup<DT, TT, VEC>;
@@ -761,8 +770,9 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
                                      std::max<int64_t>(1, (g.tokens + kSortSlots - 1) / kSortSlots));
         const int64_t elem = tdt == FA_F32 ? 4 : 2;
         // Rows of ids that occur are written anyway: zeroed before too, they cost a second
-        // write.  Above 16 MB of them at most, that costs more than finding them (3 us; the
-        // rows of 65536 tokens in a table of 131 MB: 11 us).
+        // write.  Above 16 MB of them at most, that costs more than finding them (3.3 us; of
+        // 65536 tokens in a table of 131 MB, it shortens the sort's stage, which zeroes,
+        // from 26 us to 21).
         const bool claim =
             !g.accumulate && std::min(g.tokens, g.vocab) * g.dim * elem > (int64_t(16) << 20);
         uint32_t *claims = claim ? end : nullptr;

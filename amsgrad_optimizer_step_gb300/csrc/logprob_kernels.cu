@@ -8,6 +8,13 @@
 // exp(scale (x - top)) is 2^(k d) with d = x - top (exact for 16-bit logits) and k = scale
 // log2(e) in two FP32 parts: k d is rounded once.  With k in one part the log-probabilities
 // were 2e-8 of a row's spread off, all the same way.
+//
+// Reads and writes of the logits bound them: one read for the log-probabilities (7296 rows of
+// 32000: FP32 134 us, 7.0 TB/s; FP16 73 us, 6.4 TB/s, with the issue slots 57 % busy: 59
+// instructions on eight elements), a second read and the write for their gradient (7.0 TB/s),
+// and one of each for the policy loss, which holds the row on chip between its sum and its
+// gradient (16384 rows of 32000 BF16: 326 us, 6.1 TB/s).  The preference loss cannot: a
+// token's coefficient needs every row of its pair.
 #include <algorithm>
 #include <type_traits>
 
@@ -51,8 +58,8 @@ __host__ __device__ __forceinline__ RowSpan row_span(const void *row, int64_t n)
     return r;
 }
 
-// One of the 2^log2 CTAs that take a row together, and the row.  (Powers of two: divisions
-// by a number known at run time were a fifth of a CTA's instructions.)
+// One of the 2^log2 CTAs that take a row together, and the row.  (Powers of two: with
+// divisions by a number known at run time the log-probabilities executed 6 % more.)
 struct Share {
     unsigned rank, log2;
     int64_t row;
@@ -440,8 +447,10 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2
     leave_row(sh);
 }
 
-// Rows are taken from the last to the first: the pass that made the statistics left the
-// last rows in L2.
+// One pass over the rows with no sum in it: 64 bytes of loads a thread, their gradient, and
+// the stores; read and write bound it (4980 rows of 32000 BF16, a quarter of them zeros: 80 us,
+// 7.0 TB/s).  Rows are taken from the last to the first: the pass that made the statistics
+// left the last rows in L2.
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT, NT == 32 ? 32 : 1536 / NT)
 logprob_gradient_kernel(LogitGradArgs a, unsigned split_log2) {
@@ -661,9 +670,13 @@ enum Divisor { kGiven, kFromKernel, kCountHere };
 // One row by a cluster of 2^split_log2 CTAs.  HELD > 0: each CTA's part of the row, at most
 // 4 * HELD vectors a thread, is read once and held on chip: three groups of HELD vectors
 // come to shared memory asynchronously, so that the sum begins when the first has come, the
-// fourth to registers (four CTAs of 64 KB rows then fit an SM instead of three).  The
-// gradient is made from there: one read and one write of the logits.  HELD == 0 (rows wider
-// than a cluster holds, or no gradient): the row is read again.
+// fourth to registers (four CTAs of 64 KB rows then fit an SM instead of three: 65,536
+// registers and 192 KB of shared memory).  The gradient is made from there: one read and one
+// write of the logits, which bound it (16384 rows of 32000 BF16: 326 us with the sums over
+// the tokens, 6.1 TB/s; the sum of one CTA and the writes of another overlap, what does not is
+// the last wave).  Rows past 64 KB go to clusters (1111 rows of 131072 BF16, four CTAs each:
+// 109 us, 5.1 TB/s: 7.3 waves are run as eight, and the parts wait for one another twice).
+// HELD == 0 (rows wider than a cluster holds, or no gradient): the row is read again.
 template <int DT, int NT, int HELD>
 __global__ void __launch_bounds__(NT, NT == 32 ? 32 : 1024 / NT)
 policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
@@ -806,7 +819,8 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
 }
 
 // The sums over the tokens, by a cluster of CTAs: each adds its tokens, the first adds the
-// CTAs' sums in order.
+// CTAs' sums in order.  Bound by its own latencies: 6 us for 1111 tokens by one CTA, 8 us for
+// 4096 by eight (alone, with cold caches).
 constexpr unsigned kSummaryCtas = 8;
 struct PolicySums {
     Sum2 loss, kl;
@@ -904,7 +918,11 @@ cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, float *logp,
         const int64_t nvec = x.vocab / Elem<d()>::kVec;
         const unsigned log2 = split_for(x.tokens, nvec, kBatch * kMostThreads, 0);
         if (x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;
-        return for_threads(nvec >> log2, [&](auto nt) {
+        // From 24 rows an SM on, twice the vectors a thread: fewer warps begin and join (3648
+        // rows of 32000 FP16: 40.9 us against 41.7; 912 rows, no longer one wave: 14.8
+        // against 14.6; the gradient, which joins nothing, gains nothing).
+        const int longer = x.tokens >= 24 * 152;
+        return for_threads(nvec >> (log2 + longer), [&](auto nt) {
             return launch_clusters(token_logprobs_kernel<d(), nt()>,
                                    dim3(static_cast<unsigned>(x.tokens << log2)), dim3(nt()), 0,
                                    1u << log2, false, stream, x, logp, lse, log2);

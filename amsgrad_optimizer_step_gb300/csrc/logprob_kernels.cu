@@ -13,7 +13,7 @@
 // 32000: FP32 134 us, 7.0 TB/s; FP16 73 us, 6.4 TB/s, with the issue slots 57 % busy: 59
 // instructions on eight elements), a second read and the write for their gradient (7.0 TB/s),
 // and one of each for the policy loss, which holds the row on chip between its sum and its
-// gradient (16384 rows of 32000 BF16: 326 us, 6.1 TB/s).  The preference loss cannot: a
+// gradient (16384 rows of 32000 BF16: 317 us, 6.3 TB/s).  The preference loss cannot: a
 // token's coefficient needs every row of its pair.
 #include <algorithm>
 #include <type_traits>
@@ -149,12 +149,21 @@ struct RowSum {
     }
 };
 
+// The CTAs that take a row together write to one another's shared memory: each says here,
+// early, that it runs; merge_row waits for all of them.
+__device__ __forceinline__ void enter_row(const Share &sh) {
+    if (sh.log2 > 0) cg::this_cluster().barrier_arrive();
+}
+
 // Merges what the warps of the CTAs of a cluster hold of a row; every thread returns the
-// row's.  The maximum first, so that a part is rebased once.  ``part``: shared, [warps];
-// ``whole``: shared, one per CTA.  The caller ends with leave_row.
+// row's.  Every warp sends its part to every CTA, so that the cluster waits once and reads only
+// its own memory, and each part is rebased once, to the row's maximum (merged in each CTA first
+// and then read from one another's memory, 1111 policy rows of 131072 BF16 took 110 us instead
+// of 104, 1999 of 100003 FP32 411 us instead of 359).  ``part``: shared,
+// [kMostSplit * warps].  After enter_row.
+constexpr int kMostSplit = 8;
 template <int NT>
-__device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, RowSum *whole,
-                                            const Share &sh) {
+__device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, const Share &sh) {
     constexpr int warps = NT / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const auto warp_total = [](float s) {
@@ -164,40 +173,31 @@ __device__ __forceinline__ RowSum merge_row(const Softmax &acc, RowSum *part, Ro
     };
     float lo, hi;
     unpair(acc.sum, lo, hi);
-    RowSum row{acc.top, warp_total(lo + hi)}, w;
-    Exponent e = acc.e;
-    float top;
-    if constexpr (warps > 1) {
-        if (lane == 0) part[warp] = row;
-        __syncthreads();
-        // every warp adds the warps' parts alike
-        w = lane < warps ? part[lane] : RowSum{-INFINITY, 0.f};
-        top = w.top;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        e.set(top);
-        row = RowSum{top, warp_total(w.at(e))};
-    }
+    RowSum row{acc.top, warp_total(lo + hi)};
     if (sh.log2 > 0) {
         cg::cluster_group cluster = cg::this_cluster();
-        if (threadIdx.x == 0) *whole = row;
+        cluster.barrier_wait();  // the other CTAs run
+        if (lane < static_cast<int>(sh.split()))
+            *cluster.map_shared_rank(part + sh.rank * warps + warp, lane) = row;
         cluster.sync();
-        w = lane < static_cast<int>(sh.split()) ? *cluster.map_shared_rank(whole, lane)
-                                           : RowSum{-INFINITY, 0.f};
-        cluster.barrier_arrive();  // has read the others' parts: see leave_row
-        top = w.top;
+    } else if constexpr (warps > 1) {
+        if (lane == 0) part[warp] = row;
+        __syncthreads();
+    }
+    if (warps > 1 || sh.log2 > 0) {  // every warp adds the parts alike
+        const int parts = warps << sh.log2;
+        const RowSum none{-INFINITY, 0.f};
+        const RowSum w = lane < parts ? part[lane] : none;
+        const RowSum v = lane + 32 < parts ? part[lane + 32] : none;
+        float top = fmaxf(w.top, v.top);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        Exponent e = acc.e;
         e.set(top);
-        row = RowSum{top, warp_total(w.at(e))};
+        row = RowSum{top, warp_total(w.at(e) + v.at(e))};
     }
     if (row.top == -INFINITY) row.s = NAN;  // no finite logit
     return row;
-}
-
-// Before a CTA that has called merge_row ends: no CTA leaves while another reads its part.
-__device__ __forceinline__ void leave_row(const Share &sh) {
-    if (sh.log2 > 0) cg::this_cluster().barrier_wait();
 }
 
 // x + y exactly, as the rounded sum and what the rounding left.
@@ -398,7 +398,7 @@ template <int DT, int NT>
 __device__ __forceinline__ RowSum row_softmax(const void *row, const LogitsArgs &a,
                                               const Share &sh) {
     using T = typename Elem<DT>::T;
-    __shared__ RowSum parts[NT / 32], whole;
+    __shared__ RowSum parts[kMostSplit * NT / 32];
     const RowSpan sp = row_span<DT>(row, a.vocab);
     Softmax acc(a);
     add_ends<DT>(acc, row, sp, a.vocab, sh);
@@ -418,7 +418,7 @@ __device__ __forceinline__ RowSum row_softmax(const void *row, const LogitsArgs 
         }
         acc.add<DT, kBatch>(r);
     });
-    return merge_row<NT>(acc, parts, &whole, sh);
+    return merge_row<NT>(acc, parts, sh);
 }
 
 template <int DT, int NT>
@@ -436,6 +436,7 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2
         }
         return;
     }
+    enter_row(sh);
     const T *row = static_cast<const T *>(x.logits) + t * x.ld;
     const bool first = sh.first() && threadIdx.x == 0;
     const float label_logit = first ? Elem<DT>::widen(row[label]) : 0.f;  // before the sum
@@ -444,7 +445,6 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2
         logp[t] = label_logp(label_logit, r, x.scale);
         if (lse) reinterpret_cast<float2 *>(lse)[t] = make_float2(r.top, r.s);
     }
-    leave_row(sh);
 }
 
 // One pass over the rows with no sum in it: 64 bytes of loads a thread, their gradient, and
@@ -672,10 +672,10 @@ enum Divisor { kGiven, kFromKernel, kCountHere };
 // come to shared memory asynchronously, so that the sum begins when the first has come, the
 // fourth to registers (four CTAs of 64 KB rows then fit an SM instead of three: 65,536
 // registers and 192 KB of shared memory).  The gradient is made from there: one read and one
-// write of the logits, which bound it (16384 rows of 32000 BF16: 326 us with the sums over
-// the tokens, 6.1 TB/s; the sum of one CTA and the writes of another overlap, what does not is
+// write of the logits, which bound it (16384 rows of 32000 BF16: 317 us with the sums over
+// the tokens, 6.3 TB/s; the sum of one CTA and the writes of another overlap, what does not is
 // the last wave).  Rows past 64 KB go to clusters (1111 rows of 131072 BF16, four CTAs each:
-// 109 us, 5.1 TB/s: 7.3 waves are run as eight, and the parts wait for one another twice).
+// 104 us, 5.3 TB/s: 7.3 waves are run as eight, and the parts wait for one another).
 // HELD == 0 (rows wider than a cluster holds, or no gradient): the row is read again.
 template <int DT, int NT, int HELD>
 __global__ void __launch_bounds__(NT, NT == 32 ? 32 : 1024 / NT)
@@ -683,7 +683,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
     using E = Elem<DT>;
     using T = typename E::T;
     extern __shared__ uint4 slot[];  // [3 * HELD][NT]
-    __shared__ RowSum parts[NT / 32], whole;
+    __shared__ RowSum parts[kMostSplit * NT / 32];
     __shared__ float coef;
     const Share sh(split_log2);
     const int64_t t = sh.row, n = a.x.vocab;
@@ -705,6 +705,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
         if (divisor == kFromKernel) fa_grid_dependency_wait();
         return;
     }
+    enter_row(sh);
     const T *row = static_cast<const T *>(a.x.logits) + t * a.x.ld;
     const RowSpan sp = row_span<DT>(row, n);
     const RowPart part(sp, sh);  // HELD: at most 4 * HELD * NT vectors
@@ -760,7 +761,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
         copy_async_wait<0>();
         group(2);
         if (3 * kGroup + (tid & ~31) < part.count) acc.add<DT, HELD>(held);
-        r = merge_row<NT>(acc, parts, &whole, sh);
+        r = merge_row<NT>(acc, parts, sh);
     } else {
         r = row_softmax<DT, NT>(row, a.x, sh);
     }
@@ -781,7 +782,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
         if (a.dlogp && sh.first()) a.dlogp[t] = dlogp;
         coef = dlogp * a.grad_factor;
     }
-    if (!out) return leave_row(sh);
+    if (!out) return;
     __syncthreads();
     if constexpr (HELD > 0) {
         if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
@@ -811,11 +812,10 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
             }
             if (label_is_mine<DT, NT>(label, sp, part, sh))
                 out[label] = E::round(fmaf(e(label_logit), w, c));
-            return leave_row(sh);
+            return;
         }
     }
     row_gradient<DT, NT>(row, out, n, a.x, r, coef, label, sh);
-    leave_row(sh);
 }
 
 // The sums over the tokens, by a cluster of CTAs: each adds its tokens, the first adds the
@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyA
 // CTAs a row is split over (their logarithm) so that a call of few tokens covers the GPU:
 // doubled while the grid is under two CTAs an SM and each still has ``least`` vectors.
 unsigned split_for(int64_t tokens, int64_t nvec, int64_t least, unsigned log2) {
-    while (log2 < 3 && (tokens << log2) < 2 * 152 && nvec >> (log2 + 1) >= least) ++log2;
+    while (1 << log2 < kMostSplit && (tokens << log2) < 2 * 152 && nvec >> (log2 + 1) >= least) ++log2;
     return log2;
 }
 
@@ -982,7 +982,7 @@ cudaError_t launch_policy(const PolicyArgs &a, fa_dtype dt, cudaStream_t stream)
             constexpr int64_t kMost = 4 * 4 * kMostThreads;  // vectors a CTA holds
             const int64_t nvec = a.x.vocab / Elem<d()>::kVec;
             unsigned log2 = 0;
-            while (log2 < 3 && nvec > kMost << log2) ++log2;
+            while (1 << log2 < kMostSplit && nvec > kMost << log2) ++log2;
             const bool held = a.dlogits && nvec <= kMost << log2;
             log2 = split_for(a.x.tokens, nvec, kMostThreads, held ? log2 : 0);
             if (a.x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;

@@ -35,10 +35,15 @@ namespace cg = cooperative_groups;
 FA_BOUNDS_COUNTER(g_logprob_oob)
 
 constexpr int kBatch = 4;  // 16-byte vectors a thread takes at a time
-// A row's kernels are compiled for CTAs of NT = 32, 64, 128 and 256 threads: a row of few
-// vectors is a warp's, without barriers, and many CTAs share an SM (65536 rows of 1000 BF16
-// logits by 256 threads each took 330 us, nine tenths of it in starting and joining them).
+// A row's kernels are compiled for NT = 32, 64, 128 and 256 threads a row: a row of few
+// vectors is a warp's, without barriers (65536 policy rows of 1000 BF16 logits by 256 threads
+// each took 330 us, nine tenths of it in starting and joining them).  A CTA has one row, or
+// kWarpRows of a warp each where there are many: an SM runs no more than 32 CTAs (the
+// log-probabilities of 65536 rows of 1000 BF16: 70 us by CTAs of one warp, 34 by four).
 constexpr int kMostThreads = 256;
+constexpr int kWarpRows = 4;
+template <int NT>
+constexpr int kBlockThreads = NT == 32 ? 32 * kWarpRows : NT;
 
 // A row cut for 16-byte accesses: head scalars up to the first boundary, then nvec
 // vectors, then the scalars left over.
@@ -64,8 +69,10 @@ struct Share {
     unsigned rank, log2;
     int64_t row;
 
-    __device__ __forceinline__ explicit Share(unsigned log2_)
-        : rank(blockIdx.x & ((1u << log2_) - 1)), log2(log2_), row(blockIdx.x >> log2_) {}
+    __device__ __forceinline__ explicit Share(unsigned log2_, bool warp_rows = false)
+        : rank(blockIdx.x & ((1u << log2_) - 1)), log2(log2_), row(blockIdx.x >> log2_) {
+        if (warp_rows) row = row * blockDim.y + threadIdx.y;
+    }
     __device__ __forceinline__ unsigned split() const { return 1u << log2; }
     __device__ __forceinline__ bool first() const { return rank == 0; }
     __device__ __forceinline__ bool last() const { return rank == split() - 1; }
@@ -422,12 +429,13 @@ __device__ __forceinline__ RowSum row_softmax(const void *row, const LogitsArgs 
 }
 
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT, NT == 32 ? 32 : 1536 / NT)
+__global__ void __launch_bounds__(kBlockThreads<NT>, 1536 / kBlockThreads<NT>)
 token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2) {
     using T = typename Elem<DT>::T;
     fa_allow_dependents();
-    const Share sh(split_log2);
+    const Share sh(split_log2, NT == 32);
     const int64_t t = sh.row;
+    if (NT == 32 && t >= x.tokens) return;
     int64_t label;
     if (!load_label(x, t, &label)) {
         if (sh.first() && threadIdx.x == 0) {
@@ -452,11 +460,12 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2
 // 7.0 TB/s).  Rows are taken from the last to the first: the pass that made the statistics
 // left the last rows in L2.
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT, NT == 32 ? 32 : 1536 / NT)
+__global__ void __launch_bounds__(kBlockThreads<NT>, 1536 / kBlockThreads<NT>)
 logprob_gradient_kernel(LogitGradArgs a, unsigned split_log2) {
     using T = typename Elem<DT>::T;
-    const Share sh(split_log2);
+    const Share sh(split_log2, NT == 32);
     const int64_t t = a.x.tokens - 1 - sh.row;
+    if (NT == 32 && t < 0) return;
     T *out = static_cast<T *>(a.dlogits) + t * a.dlogits_ld;
     int64_t label;
     if (!load_label(a.x, t, &label)) {
@@ -641,26 +650,30 @@ __device__ __forceinline__ PolicyTerms policy_terms(const PolicyArgs &a, const P
     return o;
 }
 
-// Counted tokens among the labels, by the whole CTA; every thread returns their number.
+// Counted tokens among the labels, by a warp (WARP) or the whole CTA; every thread returns
+// their number.
+template <bool WARP>
 __device__ __forceinline__ int count_labels(const LogitsArgs &x) {
-    __shared__ int total[32];
     int n = 0;
     for (int64_t t = threadIdx.x; t < x.tokens; t += blockDim.x) {
         int64_t label;
         n += load_label(x, t, &label);
     }
     n = __reduce_add_sync(0xffffffffu, n);
-    if ((threadIdx.x & 31) == 0) total[threadIdx.x / 32] = n;
-    __syncthreads();
-    n = 0;
-    for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) n += total[w];
+    if constexpr (!WARP) {
+        __shared__ int total[32];
+        if ((threadIdx.x & 31) == 0) total[threadIdx.x / 32] = n;
+        __syncthreads();
+        n = 0;
+        for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) n += total[w];
+    }
     return n;
 }
 
 // summary[3] = the number of counted tokens, for the rows' kernel.
 __global__ void __launch_bounds__(kSummaryThreads) policy_count_kernel(PolicyArgs a) {
     fa_allow_dependents();
-    const int n = count_labels(a.x);
+    const int n = count_labels<false>(a.x);
     if (threadIdx.x == 0) a.summary[3] = static_cast<float>(n);
 }
 
@@ -678,15 +691,17 @@ enum Divisor { kGiven, kFromKernel, kCountHere };
 // 104 us, 5.3 TB/s: 7.3 waves are run as eight, and the parts wait for one another).
 // HELD == 0 (rows wider than a cluster holds, or no gradient): the row is read again.
 template <int DT, int NT, int HELD>
-__global__ void __launch_bounds__(NT, NT == 32 ? 32 : 1024 / NT)
+__global__ void __launch_bounds__(kBlockThreads<NT>,
+                                  (HELD == 1 ? 1280 : 1024) / kBlockThreads<NT>)
 policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
     using E = Elem<DT>;
     using T = typename E::T;
-    extern __shared__ uint4 slot[];  // [3 * HELD][NT]
+    extern __shared__ uint4 slots[];  // [3 * HELD][NT], for each row
+    uint4 *slot = NT == 32 ? slots + threadIdx.y * (3 * HELD * NT) : slots;
     __shared__ RowSum parts[kMostSplit * NT / 32];
-    __shared__ float coef;
-    const Share sh(split_log2);
+    const Share sh(split_log2, NT == 32);
     const int64_t t = sh.row, n = a.x.vocab;
+    if (NT == 32 && t >= a.x.tokens) return;
     const int tid = threadIdx.x;
     T *out = a.dlogits ? static_cast<T *>(a.dlogits) + t * a.dlogits_ld : nullptr;
     // Nothing here but summary[3] comes from the counting kernel, which began after all
@@ -736,7 +751,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
     const PolicyToken in(a, first ? t : 0);
     const float label_logit = E::widen(row[label]);
     float denom = a.denominator;
-    if (divisor == kCountHere) denom = static_cast<float>(count_labels(a.x));
+    if (divisor == kCountHere) denom = static_cast<float>(count_labels<NT == 32>(a.x));
 
     RowSum r;
     if constexpr (HELD > 0) {
@@ -765,6 +780,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
     } else {
         r = row_softmax<DT, NT>(row, a.x, sh);
     }
+    float coef = 0.f;
     if (first) {
         const float logp = label_logp(label_logit, r, a.x.scale);
         const PolicyTerms o = policy_terms(a, in, logp);
@@ -783,7 +799,14 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
         coef = dlogp * a.grad_factor;
     }
     if (!out) return;
-    __syncthreads();
+    if constexpr (NT == 32) {
+        coef = __shfl_sync(0xffffffffu, coef, 0);
+    } else {
+        __shared__ float shared_coef;
+        if (first) shared_coef = coef;
+        __syncthreads();
+        coef = shared_coef;
+    }
     if constexpr (HELD > 0) {
         if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
             const Exponent e(a.x, r.top);
@@ -887,6 +910,16 @@ unsigned split_for(int64_t tokens, int64_t nvec, int64_t least, unsigned log2) {
     return log2;
 }
 
+// CTAs and threads for ``tokens`` rows by clusters of 2^log2 CTAs of nt threads a row: with
+// more rows of a warp than an SM runs CTAs, kWarpRows to a CTA.
+struct RowGrid {
+    dim3 ctas, threads;
+    RowGrid(int64_t tokens, int nt, unsigned log2) : threads(nt) {
+        if (nt == 32 && log2 == 0 && tokens > 32 * 152) threads.y = kWarpRows;
+        ctas = dim3(static_cast<unsigned>((tokens + threads.y - 1) / threads.y << log2));
+    }
+};
+
 // Calls f with the threads of a CTA that has ``nvec`` vectors of a row: sixteen vectors a
 // thread, as far as the sizes go.
 template <typename F>
@@ -923,8 +956,8 @@ cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, float *logp,
         // against 14.6; the gradient, which joins nothing, gains nothing).
         const int longer = x.tokens >= 24 * 152;
         return for_threads(nvec >> (log2 + longer), [&](auto nt) {
-            return launch_clusters(token_logprobs_kernel<d(), nt()>,
-                                   dim3(static_cast<unsigned>(x.tokens << log2)), dim3(nt()), 0,
+            const RowGrid g(x.tokens, nt(), log2);
+            return launch_clusters(token_logprobs_kernel<d(), nt()>, g.ctas, g.threads, 0,
                                    1u << log2, false, stream, x, logp, lse, log2);
         });
     });
@@ -937,8 +970,8 @@ cudaError_t launch_token_logprobs_gradient(const LogitGradArgs &a, fa_dtype dt,
         const unsigned log2 = split_for(a.x.tokens, nvec, kBatch * kMostThreads, 0);
         if (a.x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;
         return for_threads(nvec >> log2, [&](auto nt) {
-            logprob_gradient_kernel<d(), nt()>
-                <<<static_cast<unsigned>(a.x.tokens << log2), nt(), 0, stream>>>(a, log2);
+            const RowGrid g(a.x.tokens, nt(), log2);
+            logprob_gradient_kernel<d(), nt()><<<g.ctas, g.threads, 0, stream>>>(a, log2);
             return cudaGetLastError();
         });
     });
@@ -970,8 +1003,9 @@ cudaError_t launch_policy_rows(const PolicyArgs &a, unsigned log2, Divisor divis
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (err != cudaSuccess) return err;
     }
-    return launch_clusters(kernel, dim3(static_cast<unsigned>(a.x.tokens << log2)), dim3(NT),
-                           kSmem, 1u << log2, divisor == kFromKernel, stream, a, log2, divisor);
+    const RowGrid g(a.x.tokens, NT, log2);
+    return launch_clusters(kernel, g.ctas, g.threads, kSmem * g.threads.y, 1u << log2,
+                           divisor == kFromKernel, stream, a, log2, divisor);
 }
 
 }  // namespace

@@ -263,6 +263,19 @@ def test_logprobs_layouts(dt, vocab, layout):
     check_logprobs(logits, labels, layout=layout, in_place=True)
 
 
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("tokens,vocab", [(4865, 1), (5003, 67), (5003, 1003), (4866, 4096),
+                                          (3649, 5001)])
+def test_logprobs_many_rows(dt, tokens, vocab):
+    """More rows than the SMs run blocks: several to a block, the last one not full."""
+    g = gen(tokens + vocab)
+    logits = randn(g, tokens, vocab, dtype=DTYPES[dt], sigma=3.0)
+    labels = torch.randint(0, vocab, (tokens,), device=DEV, generator=g)
+    labels[torch.rand(tokens, device=DEV, generator=g) < 0.2] = -100
+    check_logprobs(logits, labels)
+    check_logprobs(logits, labels.to(torch.int32), scale=0.7, layout=(3, 1))
+
+
 @pytest.mark.parametrize("vocab", [100_003, 131_072, 262_147])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_logprobs_wide_rows(dt, vocab):
@@ -581,6 +594,15 @@ def test_policy_lengths(tokens):
     check_policy(logits, labels, old, adv, ref)         # watched, not added
     check_policy(logits, labels, old, adv, None, w, denominator=float(tokens))
     check_policy(logits, labels.to(torch.int32), old, adv, lo=0.0, hi=0.0, off_edge=1e-3)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("tokens,vocab", [(4865, 1), (5003, 67), (5003, 1003), (4866, 4096)])
+def test_policy_many_rows(dt, tokens, vocab):
+    logits, labels, old, adv, ref, w = rollout(tokens + vocab, tokens, vocab, dt)
+    check_policy(logits, labels, old, adv, ref, kl=0.05)
+    check_policy(logits, labels, old, adv, ref, w, kl=0.1, denominator=float(tokens),
+                 in_place=True)
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))

@@ -14,6 +14,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import model_ops as ops
 
@@ -22,9 +23,12 @@ __all__ = ["embedding", "gated_activation", "gated_down", "token_logprobs", "pre
 
 
 def _flat(x: torch.Tensor) -> torch.Tensor:
-    """A matrix of the last dimension's rows (a copy where the strides do not allow a view)."""
-    y = x.reshape(-1, x.shape[-1])
-    return y if y.shape[1] <= 1 or y.stride(1) == 1 else y.contiguous()
+    """A matrix of the last dimension's rows: a view where rows are adjacent elements and do not
+    overlap, else a copy (the gradient of a sum over rows is one row expanded)."""
+    rows, cols = x.shape[:-1].numel(), x.shape[-1]
+    y = x.reshape(rows, cols)
+    dense = (cols <= 1 or y.stride(1) == 1) and (rows <= 1 or y.stride(0) >= cols)
+    return y if dense else y.contiguous()
 
 
 class _Embedding(torch.autograd.Function):
@@ -39,6 +43,7 @@ class _Embedding(torch.autograd.Function):
         return out.view(*ids.shape, weight.shape[1])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         (ids,) = ctx.saved_tensors
         (vocab, dim), dtype = ctx.table
@@ -68,16 +73,20 @@ class _Gated(torch.autograd.Function):
         gate, up = _halves(_flat(gate_up))
         h = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
         keep = ctx.needs_input_grad[0]
-        ctx.checkpoint = ops.checkpoint_buffer(*gate.shape, gate.device) if keep else None
-        ops.fa_gated_forward(gate, up, h, ctx.checkpoint, activation)
+        checkpoint = ops.checkpoint_buffer(*gate.shape, gate.device) if keep else None
+        ops.fa_gated_forward(gate, up, h, checkpoint, activation)
+        if keep:  # given back with the graph's other tensors once the backward pass has run
+            ctx.save_for_backward(checkpoint.codes, checkpoint.scales)
         ctx.activation, ctx.shape = activation, gate_up.shape
         return h.view(*gate_up.shape[:-1], gate.shape[1])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh):
         dh = _flat(dh)
+        checkpoint = ops.Checkpoint(*ctx.saved_tensors, dh.shape[1])
         grad = torch.empty((dh.shape[0], 2 * dh.shape[1]), dtype=dh.dtype, device=dh.device)
-        ops.fa_gated_backward(ctx.checkpoint, dh, *_halves(grad), None, ctx.activation)
+        ops.fa_gated_backward(checkpoint, dh, *_halves(grad), None, ctx.activation)
         return grad.view(ctx.shape), None
 
 
@@ -93,20 +102,23 @@ class _GatedDown(torch.autograd.Function):
         gate, up = _halves(_flat(gate_up))
         h = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
         keep = any(ctx.needs_input_grad[:2])
-        ctx.checkpoint = ops.checkpoint_buffer(*gate.shape, gate.device) if keep else None
-        ops.fa_gated_forward(gate, up, h, ctx.checkpoint, activation)
-        ctx.save_for_backward(weight)
+        checkpoint = ops.checkpoint_buffer(*gate.shape, gate.device) if keep else None
+        ops.fa_gated_forward(gate, up, h, checkpoint, activation)
+        if keep:
+            ctx.save_for_backward(weight, checkpoint.codes, checkpoint.scales)
         ctx.activation, ctx.shape = activation, gate_up.shape
         return (h @ weight.t()).view(*gate_up.shape[:-1], weight.shape[0])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
-        (weight,) = ctx.saved_tensors
+        weight, *kept = ctx.saved_tensors
         dy = _flat(dy)
         dh = dy @ weight
+        checkpoint = ops.Checkpoint(*kept, dh.shape[1])
         grad = torch.empty((dh.shape[0], 2 * dh.shape[1]), dtype=dh.dtype, device=dh.device)
         h = torch.empty_like(dh) if ctx.needs_input_grad[1] else None
-        ops.fa_gated_backward(ctx.checkpoint, dh, *_halves(grad), h, ctx.activation)
+        ops.fa_gated_backward(checkpoint, dh, *_halves(grad), h, ctx.activation)
         return grad.view(ctx.shape), None if h is None else dy.t() @ h, None
 
 
@@ -142,6 +154,7 @@ class _TokenLogprobs(torch.autograd.Function):
         return logp.view(labels.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dlogp):
         logits, labels, lse = ctx.saved_tensors
         return _gradient(ctx, logits, labels, lse, dlogp.reshape(-1).float().contiguous(),
@@ -168,6 +181,7 @@ class _PreferenceLoss(torch.autograd.Function):
         return out.loss.view(()), out.rewards
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss, _):
         grad = _gradient(ctx, *ctx.saved_tensors, dloss.reshape(1).float())
         return (grad.view(ctx.shape),) + (None,) * 7
@@ -202,6 +216,7 @@ class _PolicyLoss(torch.autograd.Function):
         return loss, stats
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss, _):
         grad = _gradient(ctx, *ctx.saved_tensors, dloss.reshape(1).float())
         return (grad.view(ctx.shape),) + (None,) * 10

@@ -62,7 +62,7 @@ def _rows(name: str, t: torch.Tensor, shape) -> int:
     row, col = t.stride()
     if col == 1 and row >= shape[1]:
         return row
-    if col != 1 and shape[1] > 1:
+    if col != 1 and shape[1] > 1 and shape[0] > 0:
         raise ValueError(f"{name}: the elements of a row must be adjacent")
     if shape[0] > 1 and row < shape[1]:
         raise ValueError(f"{name}: overlapping or broadcast rows")

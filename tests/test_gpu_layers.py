@@ -78,6 +78,78 @@ def test_gated_layers(layers, kind):
     assert bool(((w.grad.double() - dw).abs() <= 100 * U32 * (1 + dw.abs())).all())
 
 
+def test_gradients_that_are_expanded(layers):
+    """Gradients of sums and means come as one row, or one element, expanded."""
+    w = randn(20, 40, 24).requires_grad_()
+    ids = torch.arange(30, device=DEV) % 7
+    c = randn(21, 24)
+    (dw,) = torch.autograd.grad(layers.embedding(ids, w).sum(0), w, c)
+    count = torch.bincount(ids, minlength=40)[:, None]
+    assert_close(dw, count.double() * c.double(), 31 * U32 * count * c.abs(), "embedding")
+    gu = randn(22, 15, 2 * 130).requires_grad_()
+    down = randn(23, 24, 130).requires_grad_()
+    rows = randn(24, 130).expand(15, 130)
+    ones = randn(25, 24).expand(15, 24)
+    for run, d, inputs in ((lambda: layers.gated_activation(gu), rows, (gu,)),
+                           (lambda: layers.gated_down(gu, down), ones, (gu, down))):
+        for x, y in zip(torch.autograd.grad(run(), inputs, d),
+                        torch.autograd.grad(run(), inputs, d.contiguous())):
+            assert torch.equal(x, y)
+    logits = randn(26, 9, 50).requires_grad_()
+    labels = torch.arange(9, device=DEV)
+    one = torch.tensor([0.25], device=DEV)
+    x, y = (torch.autograd.grad(layers.token_logprobs(logits, labels), logits, d)[0]
+            for d in (one.expand(9), one.expand(9).contiguous()))
+    assert torch.equal(x, y)
+
+
+def test_gradients_of_gradients_are_refused(layers):
+    """The backward passes are not differentiable: asked for twice, they say so."""
+    w = randn(30, 11, 8).requires_grad_()
+    gu = randn(31, 5, 16).requires_grad_()
+    logits = randn(32, 5, 11).requires_grad_()
+    ids = torch.arange(5, device=DEV)
+    flat = torch.zeros(5, device=DEV)
+    for y, x in ((layers.embedding(ids, w).square().sum(), w),
+                 (layers.gated_activation(gu).square().sum(), gu),
+                 (layers.gated_down(gu, w).square().sum(), gu),
+                 (layers.token_logprobs(logits, ids).square().sum(), logits),
+                 (layers.policy_loss(logits, ids, flat, flat + 1.0)[0].square(), logits),
+                 (layers.preference_loss(logits, ids, torch.tensor([0, 3, 5], device=DEV), flat,
+                                         )[0].square(), logits)):
+        (g,) = torch.autograd.grad(y, x, create_graph=True)
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(g.sum(), x)
+
+
+def test_a_checkpoint_is_given_back_after_the_backward_pass(layers):
+    gu = randn(33, 512, 2 * 2048).requires_grad_()
+    h = layers.gated_activation(gu)
+    dh, gu.grad = torch.ones_like(h), torch.zeros_like(gu)
+    before = torch.cuda.memory_allocated()
+    h.backward(dh)
+    freed = before - torch.cuda.memory_allocated()
+    assert freed >= 2 * 512 * 2048  # the codes, though h and its graph live on
+    with pytest.raises(RuntimeError):
+        h.backward(dh)
+
+
+def test_layers_with_nothing(layers):
+    w = randn(34, 6, 8).requires_grad_()
+    none = torch.empty(0, dtype=torch.int64, device=DEV)
+    (g,) = torch.autograd.grad(layers.embedding(none, w).sum(), w)
+    assert torch.equal(g, torch.zeros_like(g))
+    for shape in ((0, 16), (3, 0, 16), (3, 0)):
+        gu = torch.empty(shape, device=DEV, requires_grad=True)
+        h = layers.gated_activation(gu)
+        assert h.shape == (*shape[:-1], shape[-1] // 2)
+        (g,) = torch.autograd.grad(h.sum(), gu)
+        assert g.shape == gu.shape
+    logits = torch.empty((0, 7), device=DEV, requires_grad=True)
+    (g,) = torch.autograd.grad(layers.token_logprobs(logits, none).sum(), logits)
+    assert g.shape == (0, 7)
+
+
 def test_gated_down_keeps_eight_bits(layers):
     """What lives from the forward to the backward pass of gated_down: two bytes a column and a
     scale for 128 of them, for gate and up together, not their six bytes and the activation."""

@@ -688,7 +688,7 @@ enum Divisor { kGiven, kFromKernel, kCountHere };
 // write of the logits, which bound it (16384 rows of 32000 BF16: 317 us with the sums over
 // the tokens, 6.3 TB/s; the sum of one CTA and the writes of another overlap, what does not is
 // the last wave).  Rows past 64 KB go to clusters (1111 rows of 131072 BF16, four CTAs each:
-// 104 us, 5.3 TB/s: 7.3 waves are run as eight, and the parts wait for one another).
+// 103 us, 5.4 TB/s: 7.3 waves are run as eight, and the parts wait for one another).
 // HELD == 0 (rows wider than a cluster holds, or no gradient): the row is read again.
 template <int DT, int NT, int HELD>
 __global__ void __launch_bounds__(kBlockThreads<NT>,
@@ -843,25 +843,22 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
 
 // The sums over the tokens, by a cluster of CTAs: each adds its tokens, the first adds the
 // CTAs' sums in order.  Bound by its own latencies: 6 us for 1111 tokens by one CTA, 8 us for
-// 4096 by eight (alone, with cold caches).
+// 4096 by eight (alone, with cold caches and a CTA-wide sum after the other; all sums in one
+// pass take 0.8 us off a call of 1111).
 constexpr unsigned kSummaryCtas = 8;
 struct PolicySums {
     Sum2 loss, kl;
-    int n, clipped;
+    int n = 0, clipped = 0;
 };
 __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyArgs a) {
-    __shared__ Sum2 parts[2][kSummaryThreads / 32];
-    __shared__ int counts[2];
-    __shared__ PolicySums sums;
-    cg::cluster_group cluster = cg::this_cluster();
-    const unsigned ctas = gridDim.x;
-    if (threadIdx.x < 2) counts[threadIdx.x] = 0;
+    __shared__ PolicySums parts[kSummaryThreads / 32], sums;
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
     fa_grid_dependency_wait();
     Sum2 loss, kl;
     int n = 0, clipped = 0;
 #pragma unroll 2
-    for (int64_t t = blockIdx.x * kSummaryThreads + threadIdx.x; t < a.x.tokens;
-         t += ctas * kSummaryThreads) {
+    for (int64_t t = blockIdx.x * blockDim.x + threadIdx.x; t < a.x.tokens;
+         t += gridDim.x * blockDim.x) {
         int64_t label;
         const bool counted = load_label(a.x, t, &label);
         const PolicyToken in(a, t);  // loaded beside the label
@@ -874,21 +871,21 @@ __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyA
         clipped += r * in.adv > fminf(fmaxf(r, a.clip_lo), a.clip_hi) * in.adv;
         ++n;
     }
-    loss = cta_sum2(loss, parts[0]);
-    kl = cta_sum2(kl, parts[1]);
-    n = __reduce_add_sync(0xffffffffu, n);
-    clipped = __reduce_add_sync(0xffffffffu, clipped);
-    if ((threadIdx.x & 31) == 0) {  // whole numbers: any order
-        atomicAdd(&counts[0], n);
-        atomicAdd(&counts[1], clipped);
-    }
+    const auto by_warp = [](const PolicySums &s) {
+        return PolicySums{warp_sum2(s.loss), warp_sum2(s.kl), __reduce_add_sync(0xffffffffu, s.n),
+                          __reduce_add_sync(0xffffffffu, s.clipped)};
+    };
+    PolicySums all = by_warp(PolicySums{loss, kl, n, clipped});
+    if (lane == 0) parts[threadIdx.x / 32] = all;
     __syncthreads();
-    if (threadIdx.x == 0) sums = PolicySums{loss, kl, counts[0], counts[1]};
-    cluster.sync();
+    if (threadIdx.x < 32) {
+        all = by_warp(lane < warps ? parts[lane] : PolicySums{});
+        if (lane == 0) sums = all;
+    }
+    if (gridDim.x > 1) cg::this_cluster().sync();
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        PolicySums all = sums;
-        for (unsigned r = 1; r < ctas; ++r) {
-            const PolicySums *o = cluster.map_shared_rank(&sums, r);
+        for (unsigned r = 1; r < gridDim.x; ++r) {
+            const PolicySums *o = cg::this_cluster().map_shared_rank(&sums, r);
             all.loss.add(o->loss);
             all.kl.add(o->kl);
             all.n += o->n;
@@ -900,7 +897,8 @@ __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyA
         a.summary[2] = static_cast<float>(all.clipped) / by;
         a.summary[3] = count;
     }
-    cluster.sync();  // no CTA leaves while the first reads its sums
+    // no CTA leaves while the first reads its sums
+    if (gridDim.x > 1) cg::this_cluster().sync();
 }
 
 // CTAs a row is split over (their logarithm) so that a call of few tokens covers the GPU:
@@ -1043,7 +1041,9 @@ cudaError_t launch_policy(const PolicyArgs &a, fa_dtype dt, cudaStream_t stream)
         if (err != cudaSuccess) return err;
     }
     const unsigned ctas = a.x.tokens > 2 * kSummaryThreads ? kSummaryCtas : 1;
-    return launch_clusters(policy_summary_kernel, dim3(ctas), dim3(kSummaryThreads), 0, ctas, true,
+    const unsigned warps = static_cast<unsigned>(
+        std::min<int64_t>(std::max<int64_t>(1, (a.x.tokens + 31) / 32), kSummaryThreads / 32));
+    return launch_clusters(policy_summary_kernel, dim3(ctas), dim3(32 * warps), 0, ctas, true,
                            stream, a);
 }
 

@@ -48,8 +48,8 @@ def sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".h")]
-    hdrs += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
+    hdrs = [os.path.join(d, f) for d in (CSRC, INCLUDE) for f in os.listdir(d)
+            if f.endswith((".h", ".cuh"))]
     return sources() + hdrs + [os.path.abspath(__file__)]
 
 

@@ -74,7 +74,11 @@ struct Activation<FA_GELU_TANH> {
         return mul2(g, gate(g, mul2(g, g)));
     }
     static __device__ __forceinline__ void with_slope(uint64_t g, uint64_t &a, uint64_t &da) {
-        const uint64_t q = mul2(g, g), s = gate(g, q);
+        // The square stops at 2^60 (|g| = 2^30, where the sigmoid has long been 0 or 1): infinite
+        // from |g| = 2^64 on, it made the slope 0 * inf.
+        float lo, hi;
+        unpair(mul2(g, g), lo, hi);
+        const uint64_t q = pair(fminf(lo, 0x1p60f), fminf(hi, 0x1p60f)), s = gate(g, q);
         a = mul2(g, s);
         const uint64_t rest = mul2(a, fma2(s, both(-1.f), both(1.f)));
         da = fma2(rest, fma2(q, both(3.f * kB), both(kA)), s);

@@ -615,7 +615,7 @@ __device__ __forceinline__ float kl_term(float d) {
         p = fmaf(p, d, 0.5f);
         return d * d * p;
     }
-    return expm1f(d) - d;
+    return d == INFINITY ? d : expm1f(d) - d;  // its limit, where the label's logit is -inf
 }
 
 // A token's inputs, and what its log-probability makes of them.

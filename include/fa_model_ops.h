@@ -179,7 +179,7 @@ typedef struct fa_policy {
  * Clipped policy loss with a KL term, and its gradient in the same pass (the pages
  * have no counterpart): with r = exp(logp - old_logp), A the advantage, d = ref_logp
  * - logp,
- *   token_kl = exp(d) - d - 1,
+ *   token_kl = exp(d) - d - 1 (infinite where d is),
  *   token_loss = -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A) + kl_coef * token_kl,
  *   loss = sum_t weights_t * token_loss_t / denominator,
  *   dlogits as fa_token_logprobs_gradient with dlogp = weights / denominator *

@@ -1,12 +1,15 @@
 """Values at the ends of the types' range through the model-side operators."""
 
+import math
+
 import pytest
 import torch
 
 import amsgrad_optimizer_step_gb300 as fa
 import model_reference as R
+import test_gpu_model_ops as M
 from model_reference import DTYPES, U32
-from test_gpu_model_ops import DEV, NAN, gen, randn
+from test_gpu_model_ops import DEV, INF, NAN, gen, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +48,17 @@ def test_gates_whose_square_overflows(dt, top, kind):
                       (again, a * u), (dg, x * u * on), (du, x * a)):
         R.assert_close(got[:, :128], want, 8 * U32 * want.abs(), kind)
     assert all(bool(torch.isfinite(t).all()) for t in (h, dg, du, again))
+
+
+# ---- policy loss ------------------------------------------------------------------------
+
+def test_the_kl_term_of_a_masked_label_is_infinite():
+    """exp(d) - d - 1 at d = +inf (the reference model allows a label that the logits mask) and
+    at d = -inf is infinite, as towards it; of two infinities NaN."""
+    logits, labels, old, adv, ref, _ = M.rollout(12, 4, 67, hidden=0.0)
+    for t in (0, 1):
+        logits[t, labels[t]] = -INF
+    ref[:3] = torch.tensor([-3.0, -INF, -INF], device=DEV)
+    b, _ = M.run_policy(logits, labels, old, adv, ref_logp=ref, kl_coef=0.05)
+    assert b.token_kl[0].item() == INF and math.isnan(b.token_kl[1].item())
+    assert b.token_kl[2].item() == INF and math.isfinite(b.token_kl[3].item())

@@ -626,6 +626,11 @@ struct PolicyToken {
         : old_logp(a.old_logp[t]), adv(a.advantages[t]), ref_logp(a.ref_logp ? a.ref_logp[t] : 0.f),
           weight(a.weights ? a.weights[t] : 1.f) {}
 };
+// w * x for an advantage or a weight w: nothing where w is 0, beside a ratio or a loss past
+// FP32's range too (0 * inf would make the loss and the token's gradient row NaN); a NaN stays.
+__device__ __forceinline__ float scaled(float w, float x) {
+    return w == 0.f && fabsf(x) == INFINITY ? 0.f : w * x;
+}
 struct PolicyTerms {
     float loss, kl, dlogp;  // dlogp: d loss / d logp
     bool clipped;
@@ -633,7 +638,8 @@ struct PolicyTerms {
 __device__ __forceinline__ PolicyTerms policy_terms(const PolicyArgs &a, const PolicyToken &in,
                                                     float logp) {
     const float r = expf(logp - in.old_logp);
-    const float free = r * in.adv, held = fminf(fmaxf(r, a.clip_lo), a.clip_hi) * in.adv;
+    const float free = scaled(in.adv, r);
+    const float held = fminf(fmaxf(r, a.clip_lo), a.clip_hi) * in.adv;
     PolicyTerms o;
     o.clipped = free > held;
     o.loss = o.clipped ? -held : -free;  // a NaN ratio is not clipped, and stays
@@ -794,7 +800,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
             fa_grid_dependency_wait();
             denom = a.summary[3];
         }
-        const float dlogp = o.dlogp * (in.weight / denom);
+        const float dlogp = scaled(in.weight / denom, o.dlogp);
         if (a.dlogp && sh.first()) a.dlogp[t] = dlogp;
         coef = dlogp * a.grad_factor;
     }
@@ -864,7 +870,7 @@ __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyA
         const PolicyToken in(a, t);  // loaded beside the label
         const float token_loss = a.token_loss[t], token_kl = a.token_kl[t], logp = a.logp[t];
         if (!counted) continue;
-        loss.add(in.weight * token_loss);
+        loss.add(scaled(in.weight, token_loss));
         kl.add(token_kl);
         // the ratio and the clip as the rows' kernel took them
         const float r = expf(logp - in.old_logp);

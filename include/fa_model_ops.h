@@ -184,7 +184,9 @@ typedef struct fa_policy {
  *   loss = sum_t weights_t * token_loss_t / denominator,
  *   dlogits as fa_token_logprobs_gradient with dlogp = weights / denominator *
  *     (kl_coef * (1 - exp(d)) - (r A where r A <= the clamped product, else 0)).
- * A token whose clamped product is the smaller counts as clipped.  Sums over
+ * A token whose clamped product is the smaller counts as clipped.  A token with
+ * advantage or weight 0 adds nothing by it where its ratio, its loss or its slope is
+ * infinite (past FP32, or a label whose logit is -Inf); a NaN stays.  Sums over
  * tokens are held as an FP32 value and its residual.  The logits are read once.  tokens == 0: summary 0.
  */
 fa_status fa_policy_loss(const fa_logits *x, const fa_policy *a, void *stream);

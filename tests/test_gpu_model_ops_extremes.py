@@ -52,6 +52,22 @@ def test_gates_whose_square_overflows(dt, top, kind):
 
 # ---- policy loss ------------------------------------------------------------------------
 
+def overflowing(vocab, dtype="f32"):
+    """Tokens 0 to 4: ratios past FP32 with advantage 0 and 1, then a weight of 0 beside an
+    overflowing loss, an overflowing KL term and a masked label; the rest as they come."""
+    logits, labels, old, adv, ref, w = M.rollout(11, 40, vocab, dtype, hidden=0.0)
+    logp = R.logprobs(logits, labels, 1.0)[0]
+    w = w + 0.1
+    old[:3] = (logp[:3] - 100.0).float()
+    ref = (logp + 0.3).float()
+    adv[:3] = torch.tensor([0.0, 1.0, -1.0], device=DEV)
+    w[2:5] = 0.0
+    ref[3] = logp[3].float() + 200.0
+    logits[4, labels[4]] = -INF
+    ref[4] = 0.0
+    return logits, labels, old, adv, ref, w
+
+
 def test_the_kl_term_of_a_masked_label_is_infinite():
     """exp(d) - d - 1 at d = +inf (the reference model allows a label that the logits mask) and
     at d = -inf is infinite, as towards it; of two infinities NaN."""
@@ -62,3 +78,45 @@ def test_the_kl_term_of_a_masked_label_is_infinite():
     b, _ = M.run_policy(logits, labels, old, adv, ref_logp=ref, kl_coef=0.05)
     assert b.token_kl[0].item() == INF and math.isnan(b.token_kl[1].item())
     assert b.token_kl[2].item() == INF and math.isfinite(b.token_kl[3].item())
+
+
+@pytest.mark.parametrize("vocab", [67, 1003, 32_000])
+@pytest.mark.parametrize("denominator", [0.0, 13.0])
+def test_nothing_times_an_overflow_is_nothing(vocab, denominator):
+    """A token without an advantage or without a weight adds nothing to the loss and has no
+    gradient, where its ratio or its loss is past FP32 too: as the formula in 64 bits has it."""
+    logits, labels, old, adv, ref, w = overflowing(vocab)
+    b, d = M.run_policy(logits, labels, old, adv, ref_logp=ref, weights=w, kl_coef=0.05,
+                        clip_high=0.28, denominator=denominator)
+    assert torch.isfinite(b.token_loss[:2]).all()
+    assert bool((b.token_loss[2:5] == INF).all())
+    keep = torch.ones(40, dtype=torch.bool, device=DEV)
+    keep[4] = False  # infinite in 64 bits as well; the others are the formula's
+    logp, p = R.logprobs(logits, labels, 1.0)
+    want = R.policy(torch.where(keep, logp, logp.new_tensor(-1.0)), keep | ~keep, old, adv,
+                    torch.where(keep, ref, -1.0), w, 0.2, 0.28, 0.05, denominator)
+    finite = w.double() * want["token_loss"].abs()
+    # 60 units of a log-probability's error, through ratios that are at most e of one another
+    assert abs(b.loss.item() - want["loss"].item()) <= 400 * U32 * finite.sum().item() / (
+        denominator or 40)
+    assert not d[2:5].any() and bool(torch.isfinite(d).all())
+    grad = R.logprobs_gradient(logits, labels, p, want["dlogp"], 1.0)
+    assert bool(((d.double() - grad).abs() <= 400 * U32 * (
+        want["dlogp"].abs().max())).all())
+    # the gradient taken later
+    lse, dlogp = torch.empty(40, 2, device=DEV), torch.empty(40, device=DEV)
+    M.run_policy(logits, labels, old, adv, grad=False, ref_logp=ref, weights=w, kl_coef=0.05,
+                 clip_high=0.28, denominator=denominator, lse=lse, dlogp=dlogp)
+    assert not dlogp[2:5].any() and bool(torch.isfinite(dlogp).all())
+
+
+def test_a_nan_is_not_hidden_by_a_zero():
+    logits, labels, old, adv, ref, w = overflowing(300)
+    for make in ("advantage", "weight"):
+        x, a, v = logits.clone(), adv.clone(), w.clone()
+        x[7, 3] = NAN
+        a[7] = 0.0 if make == "advantage" else 1.0
+        v[7] = 0.0 if make == "weight" else 1.0
+        b, d = M.run_policy(x, labels, old, a, ref_logp=ref, weights=v, kl_coef=0.05)
+        assert math.isnan(b.loss.item()) and bool(torch.isnan(d[7]).all())
+        assert bool(torch.isfinite(d[8:]).all())

@@ -97,7 +97,9 @@ def gated_activation(gate_up: torch.Tensor, activation: str = "silu") -> torch.T
 
 
 class _GatedDown(torch.autograd.Function):
+    # its matrix products, in both passes, in the type that autocast has for the forward pass
     @staticmethod
+    @torch.amp.custom_fwd(device_type="cuda")
     def forward(ctx, gate_up, weight, activation):
         gate, up = _halves(_flat(gate_up))
         h = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
@@ -111,6 +113,7 @@ class _GatedDown(torch.autograd.Function):
 
     @staticmethod
     @once_differentiable
+    @torch.amp.custom_bwd(device_type="cuda")
     def backward(ctx, dy):
         weight, *kept = ctx.saved_tensors
         dy = _flat(dy)
@@ -126,7 +129,7 @@ def gated_down(gate_up: torch.Tensor, weight: torch.Tensor,
                activation: str = "silu") -> torch.Tensor:
     """(act(gate) * up) @ weight.T.  Between the passes it holds an 8-bit checkpoint of gate and
     up alone: the activation itself, which the weight's gradient needs, is made again from it
-    in the same pass as their gradients."""
+    in the same pass as their gradients.  Under autocast the product is one of autocast's."""
     return _GatedDown.apply(gate_up, weight, activation)
 
 

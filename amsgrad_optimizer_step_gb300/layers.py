@@ -60,6 +60,10 @@ def embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
     return _Embedding.apply(ids, weight, scale, -1 if padding_idx is None else padding_idx)
 
 
+# needs_input_grad of the two functions below says only which inputs require a gradient; whether
+# any will be taken (no_grad, inference_mode) is asked outside: a forward method runs with
+# gradients off in every mode.
+
 def _halves(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     cols = x.shape[1] // 2
     if x.shape[1] != 2 * cols:
@@ -69,10 +73,10 @@ def _halves(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
 
 class _Gated(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, gate_up, activation):
+    def forward(ctx, gate_up, activation, grad_enabled):
         gate, up = _halves(_flat(gate_up))
         h = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
-        keep = ctx.needs_input_grad[0]
+        keep = grad_enabled and ctx.needs_input_grad[0]
         checkpoint = ops.checkpoint_buffer(*gate.shape, gate.device) if keep else None
         ops.fa_gated_forward(gate, up, h, checkpoint, activation)
         if keep:  # given back with the graph's other tensors once the backward pass has run
@@ -87,23 +91,23 @@ class _Gated(torch.autograd.Function):
         checkpoint = ops.Checkpoint(*ctx.saved_tensors, dh.shape[1])
         grad = torch.empty((dh.shape[0], 2 * dh.shape[1]), dtype=dh.dtype, device=dh.device)
         ops.fa_gated_backward(checkpoint, dh, *_halves(grad), None, ctx.activation)
-        return grad.view(ctx.shape), None
+        return grad.view(ctx.shape), None, None
 
 
 def gated_activation(gate_up: torch.Tensor, activation: str = "silu") -> torch.Tensor:
     """act(gate) * up of a projection whose last dimension holds gate and up side by side, which
-    are kept in 8 bits for the backward pass."""
-    return _Gated.apply(gate_up, activation)
+    are kept in 8 bits for the backward pass (nothing is kept where there will be none)."""
+    return _Gated.apply(gate_up, activation, torch.is_grad_enabled())
 
 
 class _GatedDown(torch.autograd.Function):
     # its matrix products, in both passes, in the type that autocast has for the forward pass
     @staticmethod
     @torch.amp.custom_fwd(device_type="cuda")
-    def forward(ctx, gate_up, weight, activation):
+    def forward(ctx, gate_up, weight, activation, grad_enabled):
         gate, up = _halves(_flat(gate_up))
         h = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
-        keep = any(ctx.needs_input_grad[:2])
+        keep = grad_enabled and any(ctx.needs_input_grad[:2])
         checkpoint = ops.checkpoint_buffer(*gate.shape, gate.device) if keep else None
         ops.fa_gated_forward(gate, up, h, checkpoint, activation)
         if keep:
@@ -122,7 +126,7 @@ class _GatedDown(torch.autograd.Function):
         grad = torch.empty((dh.shape[0], 2 * dh.shape[1]), dtype=dh.dtype, device=dh.device)
         h = torch.empty_like(dh) if ctx.needs_input_grad[1] else None
         ops.fa_gated_backward(checkpoint, dh, *_halves(grad), h, ctx.activation)
-        return grad.view(ctx.shape), None if h is None else dy.t() @ h, None
+        return grad.view(ctx.shape), None if h is None else dy.t() @ h, None, None
 
 
 def gated_down(gate_up: torch.Tensor, weight: torch.Tensor,
@@ -130,7 +134,7 @@ def gated_down(gate_up: torch.Tensor, weight: torch.Tensor,
     """(act(gate) * up) @ weight.T.  Between the passes it holds an 8-bit checkpoint of gate and
     up alone: the activation itself, which the weight's gradient needs, is made again from it
     in the same pass as their gradients.  Under autocast the product is one of autocast's."""
-    return _GatedDown.apply(gate_up, weight, activation)
+    return _GatedDown.apply(gate_up, weight, activation, torch.is_grad_enabled())
 
 
 def _gradient(ctx, logits, labels, lse, dlogp, grad_loss):

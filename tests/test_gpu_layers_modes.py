@@ -69,3 +69,20 @@ def test_gated_down_with_one_gradient_under_autocast(layers):
         y.float().sum().backward()
         assert bool(torch.isfinite(x.grad).all())
         x.requires_grad_(False)
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_no_checkpoint_without_gradients(layers, monkeypatch, mode):
+    """Parameters that would have a gradient, in a pass that has none: nothing is kept, and the
+    results are the training pass's bit for bit."""
+    gu = randn(6, 9, 2 * 130).requires_grad_()
+    w = randn(7, 24, 130).requires_grad_()
+    want = layers.gated_activation(gu).detach(), layers.gated_down(gu, w).detach()
+
+    def refuse(*args):
+        raise AssertionError("a checkpoint is made")
+    monkeypatch.setattr(layers.ops, "checkpoint_buffer", refuse)
+    with mode():
+        got = layers.gated_activation(gu), layers.gated_down(gu, w)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)

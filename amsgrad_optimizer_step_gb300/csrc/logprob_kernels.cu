@@ -5,9 +5,9 @@
 //   top = max_v x_v,  s = sum_v exp(scale (x_v - top)),
 //   logp = scale (x_label - top) - ln s,
 //   dlogits_v = c (1[v = label] - exp(scale (x_v - top)) / s).
-// exp(scale (x - top)) is 2^(k d) with d = x - top (exact for 16-bit logits) and k = scale
-// log2(e) in two FP32 parts: k d is rounded once.  With k in one part the log-probabilities
-// were 2e-8 of a row's spread off, all the same way.
+// exp(scale (x - top)) is 2^(k d) with d = x - top (rounded for FP32 logits, close to exact for
+// 16-bit ones) and k = scale log2(e) in two FP32 parts.  With k in one part the
+// log-probabilities were 2e-8 of a row's spread off, all the same way.
 //
 // Reads and writes of the logits bound them: one read for the log-probabilities (7296 rows of
 // 32000: FP32 134 us, 7.0 TB/s; FP16 73 us, 6.4 TB/s, with the issue slots 57 % busy: 59
@@ -100,6 +100,16 @@ struct Exponent {
     }
 };
 
+// exp2_fast truncates: its values are low by half a unit in the last place on average, which
+// over mantissas of every size is 2^-25 / ln 2 = 4.3e-8 of a sum (measured: 3.5e-8 to 5.5e-8, rows
+// of 100 to 131072 logits of each type).  v + kHalfUnit * v, rounded, is one unit above v
+// where v's mantissa is above 4/3 and v elsewhere: the same 4.3e-8 on average, and 1 and 2 stay,
+// so that sums of equal terms are exact.  Taken over sums of two terms (of one: 46.98 us instead of
+// 46.68 for a preference loss of 3648 rows of 32000 FP16; of none: 45.93, and every log-probability
+// 4.5e-8 too high).  What it leaves is below 1e-8, or 2.5e-8 in rows of nine logits; rows whose
+// logits are multiples of 1/2 have too few arguments for an average, and up to 4.2e-8.
+constexpr float kHalfUnit = 1.5f * 0x1p-25f;
+
 // The running maximum and the sum of 2^(k (x - top)) over the elements a warp has seen: the
 // maximum is the warp's, so that it rises for all lanes at once (and seldom: after the
 // first vectors, once in n times for n times the elements); each lane has its own sum, in
@@ -126,7 +136,8 @@ struct Softmax {
     // A scalar per lane (-inf: none).
     __device__ __forceinline__ void add1(float x) {
         raise(x);
-        sum = add2(sum, pair(e(x), 0.f));
+        const float y = e(x);
+        sum = add2(sum, pair(fmaf(y, kHalfUnit, y), 0.f));
     }
     template <int DT, int N>
     __device__ __forceinline__ void add(const uint4 *r) {
@@ -140,7 +151,10 @@ struct Softmax {
             float x[V];
             Elem<DT>::unpack(r[i], x);
 #pragma unroll
-            for (int j = 0; j < V; j += 2) some = add2(some, e.of_pair(x[j], x[j + 1]));
+            for (int j = 0; j < V; j += 4) {
+                const uint64_t v = add2(e.of_pair(x[j], x[j + 1]), e.of_pair(x[j + 2], x[j + 3]));
+                some = add2(some, fma2(v, pair(kHalfUnit, kHalfUnit), v));
+            }
         }
         sum = add2(sum, some);
     }
@@ -241,19 +255,16 @@ __device__ __forceinline__ Sum2 log_parts(float s) {
     return two_sum(l.hi, l.lo);
 }
 
-// logp of the label from its logit and the row's statistics, rounded once.  exp2_fast comes
-// out low on average: the sum of a row's terms but the top's (which is 1) by 3.5e-8 to 4.1e-8
-// of them, over rows of 32000 logits of each type, so that log-probabilities were as much too
-// high; the middle of that is taken off.
+// logp of the label from its logit and the row's statistics, with one rounding of its own (d is
+// rounded before it where the logits are FP32, and s is an FP32 sum).
 __device__ __forceinline__ float label_logp(float x, const RowSum &r, float scale) {
-    constexpr float kTermsLow = 3.8e-8f;
     const float d = x - r.top;
     // outside this the parts would not be finite
     if (!(d > -1e30f) || !(r.s >= 1.f) || !(r.s < 1e30f)) return d * scale - logf(r.s);
     const Sum2 log_s = log_parts(r.s);
     const float p = d * scale, p_lo = fmaf(d, scale, -p);
     const Sum2 y = two_sum(p, -log_s.hi);
-    return y.hi + (y.lo + (p_lo - log_s.lo - kTermsLow * (1.f - __fdividef(1.f, r.s))));
+    return y.hi + (y.lo + (p_lo - log_s.lo));
 }
 
 // A token's label; whether it is counted.  Both types by 32-bit words, so that the kernels

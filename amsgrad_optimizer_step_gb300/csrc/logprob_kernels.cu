@@ -256,13 +256,14 @@ __device__ __forceinline__ Sum2 log_parts(float s) {
 }
 
 // logp of the label from its logit and the row's statistics, with one rounding of its own (d is
-// rounded before it where the logits are FP32, and s is an FP32 sum).
-__device__ __forceinline__ float label_logp(float x, const RowSum &r, float scale) {
+// rounded before it where the logits are FP32, and s is an FP32 sum).  The scale is in two
+// parts, as k is: rounded, 0.7 made the log-probabilities 1e-7 too high.
+__device__ __forceinline__ float label_logp(float x, const RowSum &r, const LogitsArgs &a) {
     const float d = x - r.top;
     // outside this the parts would not be finite
-    if (!(d > -1e30f) || !(r.s >= 1.f) || !(r.s < 1e30f)) return d * scale - logf(r.s);
+    if (!(d > -1e30f) || !(r.s >= 1.f) || !(r.s < 1e30f)) return d * a.scale - logf(r.s);
     const Sum2 log_s = log_parts(r.s);
-    const float p = d * scale, p_lo = fmaf(d, scale, -p);
+    const float p = d * a.scale, p_lo = fmaf(d, a.scale_lo, fmaf(d, a.scale, -p));
     const Sum2 y = two_sum(p, -log_s.hi);
     return y.hi + (y.lo + (p_lo - log_s.lo));
 }
@@ -461,7 +462,7 @@ token_logprobs_kernel(LogitsArgs x, float *logp, float *lse, unsigned split_log2
     const float label_logit = first ? Elem<DT>::widen(row[label]) : 0.f;  // before the sum
     const RowSum r = row_softmax<DT, NT>(row, x, sh);
     if (first) {
-        logp[t] = label_logp(label_logit, r, x.scale);
+        logp[t] = label_logp(label_logit, r, x);
         if (lse) reinterpret_cast<float2 *>(lse)[t] = make_float2(r.top, r.s);
     }
 }
@@ -799,7 +800,7 @@ policy_row_kernel(PolicyArgs a, unsigned split_log2, Divisor divisor) {
     }
     float coef = 0.f;
     if (first) {
-        const float logp = label_logp(label_logit, r, a.x.scale);
+        const float logp = label_logp(label_logit, r, a.x);
         const PolicyTerms o = policy_terms(a, in, logp);
         if (sh.first()) {
             a.logp[t] = logp;

@@ -125,6 +125,7 @@ fa::LogitsArgs logits_args(const fa_logits *x) {
     a.vocab = x->vocab;
     a.ld = x->ld;
     a.scale = static_cast<float>(x->logit_scale);
+    a.scale_lo = static_cast<float>(x->logit_scale - a.scale);
     // k rounded down, so that its residual is positive: -inf times either part is -inf
     const double k = x->logit_scale * kLog2E;
     a.k = static_cast<float>(k);

@@ -77,8 +77,8 @@ struct LogitsArgs {
     const void *labels;
     bool wide_labels;  // int64
     int64_t tokens, vocab, ld;
-    float scale;  // logit_scale
-    float k, k_lo;  // logit_scale * log2(e) as an FP32 value and its residual
+    float scale, scale_lo;  // logit_scale as an FP32 value and its residual
+    float k, k_lo;          // logit_scale * log2(e) in the same way
 };
 cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, float *logp, float *lse,
                                   cudaStream_t stream);

@@ -50,14 +50,14 @@ def assert_mean(e, bound):
 
 @pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("rows,vocab", [(20_000, 1000), (8000, 32_000)])
-@pytest.mark.parametrize("sigma", [0.3, 2.0])
-def test_errors_have_no_sign(dt, rows, vocab, sigma):
-    """Rows of a language model's kind: neither the exponential nor the rounding of k = log2(e)
-    shows in the mean of s or of logp."""
+@pytest.mark.parametrize("sigma,scale", [(0.3, 1.0), (2.0, 1.0), (2.0, 0.7), (1.0, 1.9)])
+def test_errors_have_no_sign(dt, rows, vocab, sigma, scale):
+    """Rows of a language model's kind, at scales whose k = scale log2(e) rounds by different
+    parts: neither the exponential nor k's rounding shows in the mean of s or of logp."""
     g = gen(vocab)
     logits = randn(g, rows, vocab, dtype=DTYPES[dt], sigma=sigma)
     labels = torch.randint(0, vocab, (rows,), device=DEV, generator=g)
-    of_s, of_logp = errors(logits, labels)
+    of_s, of_logp = errors(logits, labels, scale)
     assert_mean(of_s, MEAN)
     assert_mean(of_logp, MEAN)
 

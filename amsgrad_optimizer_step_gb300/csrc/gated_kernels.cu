@@ -39,7 +39,9 @@ __device__ __forceinline__ float reciprocal(float x) {
 }
 __device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
 
-// sigmoid(-t / log2(e)) of a pair: 1 / (1 + 2^t).
+// sigmoid(-t / log2(e)) of a pair: 1 / (1 + 2^t).  A result below 2^-126 is 0: what it costs is
+// below 1.1e-36 (a reciprocal of subnormal results, and 2^t past 2^128, would lengthen every
+// element for it).
 __device__ __forceinline__ uint64_t sigmoid2(uint64_t t) {
     float lo, hi;
     unpair(t, lo, hi);

@@ -209,7 +209,9 @@ fa_status fa_checkpoint_size(int64_t rows, int64_t cols, int64_t *code_bytes,
  * in FP32 (ties to even), so a code stands for code * scale, within a / 254 of x (and
  * FP32 rounding).  A block with a < 2^-100 is stored as zeros; one with a NaN or an
  * infinity has scale NaN, so that what the backward pass makes of it is NaN and the
- * gradient statistics skip the step.  Columns past cols hold code 0.  codes NULL (and
+ * gradient statistics skip the step.  The sigmoid's values below 2^-126 count as
+ * zero: act and act' are 0 for silu gates below -87.3 (|act| < 1.1e-36 there) and tanh-GELU
+ * gates below -10 (1.2e-37).  Columns past cols hold code 0.  codes NULL (and
  * scales NULL): no checkpoint is kept.  gate and up may be halves of one matrix.
  * rows == 0 or cols == 0: nothing is launched or checked.
  */

@@ -50,6 +50,19 @@ def test_gates_whose_square_overflows(dt, top, kind):
     assert all(bool(torch.isfinite(t).all()) for t in (h, dg, du, again))
 
 
+@pytest.mark.parametrize("kind,bound", [("silu", 1.1e-36), ("gelu_tanh", 1.3e-37)])
+def test_the_range_where_the_activation_comes_out_as_zero(kind, bound):
+    """The sigmoid's values below 2^-126 count as zero.  |act| is the gate's magnitude times
+    that at most: 89 for silu (past ln 2^128 the value itself is smaller), 11 for the tanh form."""
+    gate = torch.linspace(-130.0, 0.0, 128 * 64, device=DEV).view(64, 128)
+    one = torch.ones_like(gate)
+    h = torch.empty_like(gate)
+    fa.fa_gated_forward(gate, one, h, None, kind)
+    want = R.act(gate.double(), kind)[0]
+    terms = M.act_terms(gate.double(), kind) * want.abs()
+    assert bool(((h.double() - want).abs() <= bound + terms).all())
+
+
 # ---- policy loss ------------------------------------------------------------------------
 
 def overflowing(vocab, dtype="f32"):

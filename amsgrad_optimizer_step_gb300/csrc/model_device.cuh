@@ -157,20 +157,6 @@ __device__ __forceinline__ void store_n(typename Elem<DT>::T *p, const float *x)
     }
 }
 
-// Loads N consecutive elements of DT as FP32 (the counterpart of store_n).
-template <int DT, int N>
-__device__ __forceinline__ void load_n(const typename Elem<DT>::T *p, float *x) {
-    constexpr int V = Elem<DT>::kVec;
-    if constexpr (N % V == 0) {
-#pragma unroll
-        for (int j = 0; j < N; j += V)
-            Elem<DT>::unpack(__ldcs(reinterpret_cast<const uint4 *>(p + j)), x + j);
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = Elem<DT>::widen(p[j]);
-    }
-}
-
 // N FP32 values (whole vectors) rounded and packed into words.
 template <int DT, int N>
 __device__ __forceinline__ void pack_words(const float *x, uint32_t *w) {
@@ -337,7 +323,8 @@ __device__ __forceinline__ void store_any(typename Elem<DT>::T *p, const float *
         if (j >= from && j < to) p[j] = E::round(x[j]);
 }
 
-// load_n for rows that others read too (kept in L2).
+// Loads N consecutive elements of DT as FP32 (the counterpart of store_n), of rows that others
+// read too (kept in L2).
 template <int DT, int N>
 __device__ __forceinline__ void read_n(const typename Elem<DT>::T *p, float *x) {
     constexpr int V = Elem<DT>::kVec;

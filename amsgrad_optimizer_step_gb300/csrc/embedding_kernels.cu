@@ -803,7 +803,7 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
         // at least
         const int64_t beside = (g.accumulate ? 0 : g.vocab * g.dim * elem) +
                                sa.prefetch.rows * row_bytes;
-        const int64_t zeroing = std::min<int64_t>(2 * 152, beside / 65536 + !g.accumulate);
+        const int64_t zeroing = std::min<int64_t>(2 * kSms, beside / 65536 + !g.accumulate);
         const int64_t zero_clusters = (zeroing + sa.ctas - 1) / sa.ctas;
         const auto go = [&](auto it, auto item) {
             auto kernel = sort_chunk_kernel<it(), decltype(item)>;
@@ -857,7 +857,7 @@ cudaError_t launch_embedding_gradient(const EmbeddingGradArgs &g, fa_itype idt, 
                 if (e != cudaSuccess || a.units < 2) return e;
                 const uint32_t join_slabs = static_cast<uint32_t>((groups + 31) / 32);
                 // a long run takes two units at least
-                const int64_t most = std::min<int64_t>(a.units / 2 * join_slabs, 8 * 152);
+                const int64_t most = std::min<int64_t>(a.units / 2 * join_slabs, 8 * kSms);
                 return launch_dependent(join_units_kernel<dd(), td(), VEC, ACC>,
                                         dim3(static_cast<unsigned>(most)), dim3(kJoinWarps * 32),
                                         0, stream, a, join_slabs);

@@ -922,7 +922,7 @@ __global__ void __launch_bounds__(kSummaryThreads) policy_summary_kernel(PolicyA
 // CTAs a row is split over (their logarithm) so that a call of few tokens covers the GPU:
 // doubled while the grid is under two CTAs an SM and each still has ``least`` vectors.
 unsigned split_for(int64_t tokens, int64_t nvec, int64_t least, unsigned log2) {
-    while (1 << log2 < kMostSplit && (tokens << log2) < 2 * 152 && nvec >> (log2 + 1) >= least) ++log2;
+    while (1 << log2 < kMostSplit && (tokens << log2) < 2 * kSms && nvec >> (log2 + 1) >= least) ++log2;
     return log2;
 }
 
@@ -931,7 +931,7 @@ unsigned split_for(int64_t tokens, int64_t nvec, int64_t least, unsigned log2) {
 struct RowGrid {
     dim3 ctas, threads;
     RowGrid(int64_t tokens, int nt, unsigned log2) : threads(nt) {
-        if (nt == 32 && log2 == 0 && tokens > 32 * 152) threads.y = kWarpRows;
+        if (nt == 32 && log2 == 0 && tokens > 32 * kSms) threads.y = kWarpRows;
         ctas = dim3(static_cast<unsigned>((tokens + threads.y - 1) / threads.y << log2));
     }
 };
@@ -970,7 +970,7 @@ cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, float *logp,
         // From 24 rows an SM on, twice the vectors a thread: fewer warps begin and join (3648
         // rows of 32000 FP16: 40.9 us against 41.7; 912 rows, no longer one wave: 14.8
         // against 14.6; the gradient, which joins nothing, gains nothing).
-        const int longer = x.tokens >= 24 * 152;
+        const int longer = x.tokens >= 24 * kSms;
         return for_threads(nvec >> (log2 + longer), [&](auto nt) {
             const RowGrid g(x.tokens, nt(), log2);
             return launch_clusters(token_logprobs_kernel<d(), nt()>, g.ctas, g.threads, 0,

@@ -13,6 +13,7 @@
 namespace fa {
 
 constexpr int kCheckpointBlock = FA_CHECKPOINT_BLOCK;
+constexpr int kSms = 152;  // a GB300's, which the sizes of grids and their thresholds count in
 
 // Division of a number below 2^31 by a constant: the high word of a product with the
 // divisor's inverse, rounded up, at 31 + ceil(log2 d) fractional bits.

@@ -56,7 +56,8 @@ class _Embedding(torch.autograd.Function):
 def embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
               padding_idx: Optional[int] = None) -> torch.Tensor:
     """scale * weight[ids]; ids outside the table give zeros, and they and ``padding_idx`` no
-    gradient."""
+    gradient.  ``padding_idx`` is an id as it stands in ``ids``: a negative one is outside the
+    table like every negative id (it does not count from the table's end)."""
     return _Embedding.apply(ids, weight, scale, -1 if padding_idx is None else padding_idx)
 
 

@@ -86,3 +86,14 @@ def test_no_checkpoint_without_gradients(layers, monkeypatch, mode):
         got = layers.gated_activation(gu), layers.gated_down(gu, w)
     for x, y in zip(got, want):
         assert torch.equal(x, y)
+
+
+def test_a_padding_id_is_an_id_as_it_stands(layers):
+    """padding_idx is compared with the ids: a negative one is outside the table like any other
+    negative id, and no row loses its gradient for it."""
+    w = randn(8, 5, 8).requires_grad_()
+    ids = torch.tensor([4, -1, 0, 4], device=DEV)
+    (got,) = torch.autograd.grad(layers.embedding(ids, w, padding_idx=-1).sum(), w)
+    assert got.sum(1).tolist() == [8.0, 0.0, 0.0, 0.0, 16.0]
+    (got,) = torch.autograd.grad(layers.embedding(ids, w, padding_idx=4).sum(), w)
+    assert got.sum(1).tolist() == [8.0, 0.0, 0.0, 0.0, 0.0]

@@ -49,7 +49,8 @@ __device__ __forceinline__ uint64_t sigmoid2(uint64_t t) {
     return pair(reciprocal(lo), reciprocal(hi));
 }
 
-// The activation of a pair and its derivative.
+// The activation of a pair and its derivative.  ``square``: 1, or 0 where the gate may be above
+// 2^63 and is 2^55 at least or 0 (see gated_backward_kernel).
 template <int ACT>
 struct Activation;
 
@@ -58,7 +59,8 @@ struct Activation<FA_SILU> {
     static __device__ __forceinline__ uint64_t value(uint64_t g) {
         return mul2(g, sigmoid2(mul2(g, both(-kLog2E))));
     }
-    static __device__ __forceinline__ void with_slope(uint64_t g, uint64_t &a, uint64_t &da) {
+    static __device__ __forceinline__ void with_slope(uint64_t g, float, uint64_t &a,
+                                                      uint64_t &da) {
         const uint64_t s = sigmoid2(mul2(g, both(-kLog2E)));
         a = mul2(g, s);
         da = fma2(a, fma2(s, both(-1.f), both(1.f)), s);  // s (1 + g (1 - s))
@@ -75,12 +77,9 @@ struct Activation<FA_GELU_TANH> {
     static __device__ __forceinline__ uint64_t value(uint64_t g) {
         return mul2(g, gate(g, mul2(g, g)));
     }
-    static __device__ __forceinline__ void with_slope(uint64_t g, uint64_t &a, uint64_t &da) {
-        // The square stops at 2^60 (|g| = 2^30, where the sigmoid has long been 0 or 1): infinite
-        // from |g| = 2^64 on, it made the slope 0 * inf.
-        float lo, hi;
-        unpair(mul2(g, g), lo, hi);
-        const uint64_t q = pair(fminf(lo, 0x1p60f), fminf(hi, 0x1p60f)), s = gate(g, q);
+    static __device__ __forceinline__ void with_slope(uint64_t g, float square, uint64_t &a,
+                                                      uint64_t &da) {
+        const uint64_t q = mul2(g, mul2(g, both(square))), s = gate(g, q);
         a = mul2(g, s);
         const uint64_t rest = mul2(a, fma2(s, both(-1.f), both(1.f)));
         da = fma2(rest, fma2(q, both(3.f * kB), both(kA)), s);
@@ -226,7 +225,9 @@ gated_forward_kernel(GatedForwardArgs a) {
 }
 
 template <int DT, int ACT, bool ALIGNED>
-__global__ void __launch_bounds__(kGatedThreads, DT == FA_F32 || ALIGNED ? 2 : 4)
+__global__ void __launch_bounds__(kGatedThreads, DT == FA_F32 && ACT == FA_GELU_TANH ? 3
+                                                 : DT == FA_F32 || ALIGNED           ? 2
+                                                                                     : 4)
 gated_backward_kernel(GatedBackwardArgs a) {
     const uint32_t b = (blockIdx.x * kGatedThreads + threadIdx.x) / kLanes;
     const int lane = threadIdx.x % kLanes;
@@ -246,6 +247,11 @@ gated_backward_kernel(GatedBackwardArgs a) {
         d[r] = load_run<DT, ALIGNED>(a.dh, row, c + r * kRunStride);
     }
     const float sg = a.scales[b], su = a.scales[n + b];
+    // From 2^64 on a gate's square is infinite and its slope would be 0 * inf.  A scale of 2^55
+    // makes every code but 0 so large that the sigmoid is 0 or 1 without the square.  (8192 x 5632,
+    // tanh form: a bound on each square took BF16 73 us and FP32 160; a branch 81 and 145; this
+    // takes 73 and 138, FP32 in 80 registers a thread, 159 in 92.)
+    const float square = sg >= 0x1p55f ? 0.f : 1.f;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         uint64_t g[kRun / 2], u[kRun / 2];
@@ -256,7 +262,7 @@ gated_backward_kernel(GatedBackwardArgs a) {
 #pragma unroll
         for (int j = 0; j < kRun; j += 2) {
             uint64_t act, slope;
-            Activation<ACT>::with_slope(g[j / 2], act, slope);
+            Activation<ACT>::with_slope(g[j / 2], square, act, slope);
             const uint64_t dh = pair(x[j], x[j + 1]);
             // |act'| < 1.13: overflows only where the gradient does
             unpair(mul2(mul2(dh, slope), u[j / 2]), dg[j], dg[j + 1]);

@@ -513,8 +513,9 @@ __device__ __forceinline__ int64_t run_end(const uint32_t *keys, int64_t tokens,
     return lo;
 }
 
-// Bound by its reads and writes: 65536 rows of 2048 BF16 summed into 32000 take 53 us, 7.1
-// TB/s, with up to six rows' loads of a thread in flight.
+// Bound by its reads and writes: 65536 rows of 2048 BF16 with Zipf-distributed ids, summed into
+// the 13100 rows that occur, take 53 us: 332 MB with the partial sums, 6.3 TB/s, with up to six
+// rows' loads of a thread in flight.
 // CTA (u, slab): unit u's runs, columns of slab.  A long run that began before the unit
 // leaves its sum in partial[u][0], one that goes on after it in partial[u][1] (a run
 // that does both, in [0]).

@@ -10,10 +10,10 @@
 // log-probabilities were 2e-8 of a row's spread off, all the same way.
 //
 // Reads and writes of the logits bound them: one read for the log-probabilities (7296 rows of
-// 32000: FP32 134 us, 7.0 TB/s; FP16 73 us, 6.4 TB/s, with the issue slots 57 % busy: 59
-// instructions on eight elements), a second read and the write for their gradient (7.0 TB/s),
+// 32000: FP32 134 us, 7.0 TB/s; FP16 and BF16 74 us, 6.3 TB/s, with the issue slots 53 % busy: 52
+// instructions on eight elements), a second read and the write for their gradient (6.7 TB/s),
 // and one of each for the policy loss, which holds the row on chip between its sum and its
-// gradient (16384 rows of 32000 BF16: 317 us, 6.3 TB/s).  The preference loss cannot: a
+// gradient (16384 rows of 32000 BF16: 318 us, 6.3 TB/s).  The preference loss cannot: a
 // token's coefficient needs every row of its pair.
 #include <algorithm>
 #include <type_traits>
@@ -39,7 +39,7 @@ constexpr int kBatch = 4;  // 16-byte vectors a thread takes at a time
 // vectors is a warp's, without barriers (65536 policy rows of 1000 BF16 logits by 256 threads
 // each took 330 us, nine tenths of it in starting and joining them).  A CTA has one row, or
 // kWarpRows of a warp each where there are many: an SM runs no more than 32 CTAs (the
-// log-probabilities of 65536 rows of 1000 BF16: 70 us by CTAs of one warp, 34 by four).
+// log-probabilities of 65536 rows of 1000 BF16: 70 us by CTAs of one warp, 33 by four).
 constexpr int kMostThreads = 256;
 constexpr int kWarpRows = 4;
 template <int NT>
@@ -104,10 +104,10 @@ struct Exponent {
 // over mantissas of every size is 2^-25 / ln 2 = 4.3e-8 of a sum (measured: 3.5e-8 to 5.5e-8, rows
 // of 100 to 131072 logits of each type).  v + kHalfUnit * v, rounded, is one unit above v
 // where v's mantissa is above 4/3 and v elsewhere: the same 4.3e-8 on average, and 1 and 2 stay,
-// so that sums of equal terms are exact.  Taken over sums of two terms (of one: 46.98 us instead of
-// 46.68 for a preference loss of 3648 rows of 32000 FP16; of none: 45.93, and every log-probability
-// 4.5e-8 too high).  What it leaves is below 1e-8, or 2.5e-8 in rows of nine logits; rows whose
-// logits are multiples of 1/2 have too few arguments for an average, and up to 4.2e-8.
+// so that sums of equal terms are exact.  Taken over sums of two terms (a preference loss of 3501
+// counted rows of 32000 FP16: 46.7 us; of every term 47.0; not at all 45.9, and every
+// log-probability 4.5e-8 too high).  What it leaves is below 1e-8, or 2.5e-8 in rows of nine logits;
+// rows whose logits are multiples of 1/2 have too few arguments for an average, and up to 4.2e-8.
 constexpr float kHalfUnit = 1.5f * 0x1p-25f;
 
 // The running maximum and the sum of 2^(k (x - top)) over the elements a warp has seen: the
@@ -703,7 +703,7 @@ enum Divisor { kGiven, kFromKernel, kCountHere };
 // come to shared memory asynchronously, so that the sum begins when the first has come, the
 // fourth to registers (four CTAs of 64 KB rows then fit an SM instead of three: 65,536
 // registers and 192 KB of shared memory).  The gradient is made from there: one read and one
-// write of the logits, which bound it (16384 rows of 32000 BF16: 317 us with the sums over
+// write of the logits, which bound it (16384 rows of 32000 BF16: 318 us with the sums over
 // the tokens, 6.3 TB/s; the sum of one CTA and the writes of another overlap, what does not is
 // the last wave).  Rows past 64 KB go to clusters (1111 rows of 131072 BF16, four CTAs each:
 // 103 us, 5.4 TB/s: 7.3 waves are run as eight, and the parts wait for one another).
@@ -968,8 +968,8 @@ cudaError_t launch_token_logprobs(const LogitsArgs &x, fa_dtype dt, float *logp,
         const unsigned log2 = split_for(x.tokens, nvec, kBatch * kMostThreads, 0);
         if (x.tokens << log2 > kMaxGridX) return cudaErrorInvalidConfiguration;
         // From 24 rows an SM on, twice the vectors a thread: fewer warps begin and join (3648
-        // rows of 32000 FP16: 40.9 us against 41.7; 912 rows, no longer one wave: 14.8
-        // against 14.6; the gradient, which joins nothing, gains nothing).
+        // rows of 32000 FP16: 40.9 us against 41.6, BF16 39.8 against 41.8; 912 rows, no longer
+        // one wave, FP16: 15.2 against 14.6; the gradient, which joins nothing, gains nothing).
         const int longer = x.tokens >= 24 * kSms;
         return for_threads(nvec >> (log2 + longer), [&](auto nt) {
             const RowGrid g(x.tokens, nt(), log2);

@@ -207,7 +207,7 @@ fa_status fa_checkpoint_size(int64_t rows, int64_t cols, int64_t *code_bytes,
  * consecutive columns of a row are one block: with a its largest magnitude,
  *   scale = a / 127,  code = rint(x * (127 / a))
  * in FP32 (ties to even), so a code stands for code * scale, within a / 254 of x (and
- * FP32 rounding).  A block with a < 2^-100 is stored as zeros; one with a NaN or an
+ * FP32 rounding, by which 127 * scale is infinite where a is FP32's largest number).  A block with a < 2^-100 is stored as zeros; one with a NaN or an
  * infinity has scale NaN, so that what the backward pass makes of it is NaN and the
  * gradient statistics skip the step.  The sigmoid's values below 2^-126 count as
  * zero: act and act' are 0 for silu gates below -87.3 (|act| < 1.1e-36 there) and tanh-GELU

@@ -42,8 +42,7 @@
 // launched the ordinary way it returns at once.  Every kernel launched through
 // launch_dependent calls it before its first global-memory access, so starting
 // early never reads anything stale: what overlaps is launch latency, CTA
-// scheduling and shared-memory setup.  (launch_clusters in model_internal.h names the
-// two kernels that wait later, and why they may.)
+// scheduling and shared-memory setup.
 #if defined(__CUDACC__)
 __device__ __forceinline__ void fa_grid_dependency_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");

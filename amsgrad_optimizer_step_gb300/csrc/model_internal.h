@@ -155,11 +155,12 @@ cudaError_t gated_bounds_violations(unsigned long long *count, bool clear);
 #if defined(__CUDACC__)
 // Launches ``kernel`` in clusters of ``cluster`` CTAs (1: none), as a programmatic
 // dependent of the kernel before it or not.  A dependent waits (fa_grid_dependency_wait)
-// before its first access to global memory, as those of launch_dependent do, with two exceptions: policy_row_kernel waits only
-// to read the count of the kernel before it, and the sorting CTAs of sort_chunk_kernel do not
-// wait at all.  Both are launched so behind a kernel of the same call that is itself an
-// ordinary launch, so that all earlier work of the stream has ended when it begins, and that
-// reads nothing they write and writes nothing they read without waiting.
+// before its first access to global memory, as those of launch_dependent do, with two
+// exceptions: policy_row_kernel waits only to read the count of the kernel before it, and
+// the sorting CTAs of sort_chunk_kernel do not wait at all.  Both are launched so behind a
+// kernel of the same call that is itself an ordinary launch, so that all earlier work of the
+// stream has ended when it begins, and that reads nothing they write and writes nothing they
+// read without waiting.
 template <typename... Params, typename... Args>
 inline cudaError_t launch_clusters(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
                                    unsigned cluster, bool dependent, cudaStream_t stream,

@@ -70,6 +70,40 @@ class FaPolicy(ctypes.Structure):
                 ("dlogp", c_vp), ("dlogits", c_vp), ("dlogits_ld", c_i64)]
 
 
+class FaDropoutKey(ctypes.Structure):
+    _fields_ = [("p", c_f64), ("seed", c_u64), ("offset", c_u64), ("counter", c_vp)]
+
+
+class FaJoin(ctypes.Structure):
+    _fields_ = [("rows", c_i64), ("cols", c_i64), ("dtype", c_i32), ("stream_dtype", c_i32),
+                ("weight_dtype", c_i32), ("post_norm", c_i32), ("branch", c_vp),
+                ("branch_ld", c_i64), ("post_weight", c_vp), ("pre_weight", c_vp),
+                ("gate", c_vp), ("gate_ld", c_i64), ("groups", c_i64),
+                ("residual_scale", c_f64), ("branch_scale", c_f64), ("eps", c_f64),
+                ("weight_offset", c_f64), ("dropout", c_vp)]
+
+
+class FaJoinGradient(ctypes.Structure):
+    _fields_ = [("out", c_vp), ("out_ld", c_i64), ("post_rstd", c_vp), ("pre_rstd", c_vp),
+                ("dout", c_vp), ("dout_ld", c_i64), ("dnormed", c_vp), ("dnormed_ld", c_i64),
+                ("dresidual", c_vp), ("dresidual_ld", c_i64), ("dbranch", c_vp),
+                ("dbranch_ld", c_i64), ("dpost_weight", c_vp), ("dpre_weight", c_vp),
+                ("dgate", c_vp), ("dgate_ld", c_i64), ("scratch", c_vp),
+                ("scratch_bytes", c_i64)]
+
+
+class FaRouter(ctypes.Structure):
+    _fields_ = [("tokens", c_i64), ("experts", c_i64), ("logits", c_vp), ("dtype", c_i32),
+                ("ld", c_i64), ("counted", c_vp), ("top_k", c_i32), ("renormalise", c_i32),
+                ("weight_scale", c_f64), ("balance_coef", c_f64), ("z_coef", c_f64)]
+
+
+class FaRouting(ctypes.Structure):
+    _fields_ = [("chosen", c_vp), ("weights", c_vp), ("lse", c_vp), ("counts", c_vp),
+                ("mean_prob", c_vp), ("summary", c_vp), ("scratch", c_vp),
+                ("scratch_bytes", c_i64)]
+
+
 P = c_vp
 PI64 = ctypes.POINTER(c_i64)
 PU64 = ctypes.POINTER(c_u64)
@@ -140,6 +174,17 @@ SIGNATURES = {
                                  P]),
     "fa_gated_backward": (c_i32, [c_i64, c_i64, P, P, c_i32, P, c_i64, c_i32, P, c_i64, P, c_i64,
                                   P, c_i64, P]),
+    # fa_block_ops.h
+    "fa_dropout": (c_i32, [c_i64, c_i64, P, c_i64, c_i32, ctypes.POINTER(FaDropoutKey), P, c_i64,
+                           P]),
+    "fa_block_join": (c_i32, [ctypes.POINTER(FaJoin), P, c_i64, P, c_i64, P, c_i64, P, P, P]),
+    "fa_block_join_scratch": (c_i32, [c_i64, c_i64, c_i64, PI64]),
+    "fa_block_join_gradient": (c_i32, [ctypes.POINTER(FaJoin), ctypes.POINTER(FaJoinGradient),
+                                       P]),
+    "fa_route_scratch": (c_i32, [c_i64, c_i64, PI64]),
+    "fa_route": (c_i32, [ctypes.POINTER(FaRouter), ctypes.POINTER(FaRouting), P]),
+    "fa_route_gradient": (c_i32, [ctypes.POINTER(FaRouter), ctypes.POINTER(FaRouting), P, P, P,
+                                  c_i64, P]),
 }
 
 _LIB = None

@@ -28,6 +28,7 @@
 
 #include "fused_adamw.h"
 #include "abi_checks.h"
+#include "block_internal.h"
 #include "internal.h"
 #include "model_internal.h"
 
@@ -369,7 +370,10 @@ fa_status fa_bounds_check_report(int32_t *enabled, uint64_t *violations, int32_t
     unsigned long long total = 0;
     for (auto *count : {fa::update_bounds_violations, fa::stats_bounds_violations,
                         fa::staged_bounds_violations, fa::embedding_bounds_violations,
-                        fa::logprob_bounds_violations, fa::gated_bounds_violations}) {
+                        fa::logprob_bounds_violations, fa::gated_bounds_violations,
+                        fa::dropout_bounds_violations, fa::join_bounds_violations,
+                        fa::join_gradient_bounds_violations,
+                        fa::join_gradient_f32_bounds_violations, fa::route_bounds_violations}) {
         unsigned long long n = 0;
         if (count(&n, clear != 0) != cudaSuccess) {
             cudaGetLastError();

@@ -1,0 +1,141 @@
+// Internal interface between the C-ABI host layer of the residual blocks' operators
+// (block_abi.cpp) and their kernels (dropout_kernels.cu, join_kernels.cu,
+// route_kernels.cu).
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "fa_block_ops.h"
+#include "internal.h"
+#include "model_internal.h"
+
+namespace fa {
+
+// ---- dropout -------------------------------------------------------------------
+struct DropArgs {
+    uint32_t threshold;  // 16 bits are kept from threshold >> 16 on; 2^32 - 1: none is
+    uint32_t key[2];
+    uint64_t offset;
+    const uint64_t *counter;  // or nullptr
+    float scale;              // of what is kept
+};
+struct DropoutArgs {
+    MatrixArgs x, out;
+    int64_t blocks;  // of 64 columns
+    Divider by_blocks;
+    DropArgs drop;
+};
+cudaError_t launch_dropout(const DropoutArgs &a, fa_dtype dt, cudaStream_t stream);
+
+// ---- the join of a block to the residual stream -------------------------------------
+struct JoinArgs {
+    MatrixArgs branch, residual, out, normed;  // p nullptr where there is none
+    const void *post_weight, *pre_weight, *gate;
+    int64_t gate_ld;
+    int64_t rows, cols;
+    uint32_t group_rows;  // rows that share a row of the gate
+    Divider by_group;
+    bool wide_weights;  // FP32 (else the branch's type)
+    bool vec_weights;   // every row of them starts on a 16-byte boundary
+    bool post_norm, dropped;
+    float residual_scale, branch_scale, eps, weight_offset;
+    float *post_rstd, *pre_rstd;  // or nullptr
+    DropArgs drop;
+};
+cudaError_t launch_block_join(const JoinArgs &a, fa_dtype dt, fa_dtype st, cudaStream_t stream);
+
+// How the gradient cuts the rows: CTAs of consecutive rows, each with FP32 sums of its own.
+struct JoinPlan {
+    int64_t chunk;  // rows of a CTA
+    int64_t ctas;
+    int64_t pitch;  // columns of one row of sums
+    int64_t parts;  // rows of sums of a CTA
+    int64_t bytes;
+};
+JoinPlan join_plan(int64_t rows, int64_t cols, int64_t groups);
+
+// Threads of a row of the gradient and runs of a thread: one up to 4096 columns, two up to 8192
+// (the columns' sums are two registers a column); 0: more, in shared memory.
+struct JoinShape {
+    int threads, runs;
+};
+JoinShape join_shape(int64_t cols);
+
+struct JoinGradArgs {
+    JoinArgs j;  // branch, weights, gate, scales; post_rstd and pre_rstd are read
+    MatrixArgs out, dout, dnormed, dresidual, dbranch;  // p nullptr where there is none
+    void *dpost_weight, *dpre_weight, *dgate;
+    int64_t dgate_ld, groups;
+    float *sums;
+    JoinPlan plan;
+    int32_t stages;  // of the kernel's ring (set by the launch)
+};
+cudaError_t launch_block_join_gradient(const JoinGradArgs &a, fa_dtype dt, fa_dtype st,
+                                       cudaStream_t stream);
+cudaError_t launch_block_join_gradient_f32(const JoinGradArgs &a, fa_dtype dt,
+                                           cudaStream_t stream);
+
+// ---- the router ------------------------------------------------------------------------
+struct RoutePlan {
+    int64_t ctas;
+    int64_t bytes;
+};
+RoutePlan route_plan(int64_t tokens, int64_t experts);
+
+struct RouteArgs {
+    MatrixArgs logits;
+    const uint8_t *counted;
+    int32_t top_k;
+    Divider by_k;
+    bool renormalise;
+    float weight_scale, balance_coef, z_coef;
+    int32_t *chosen;
+    float *weights, *lse;
+    int32_t *counts;
+    float *mean_prob, *summary;
+    void *scratch;
+    RoutePlan plan;
+};
+cudaError_t launch_route(const RouteArgs &a, fa_dtype dt, cudaStream_t stream);
+
+struct RouteGradArgs {
+    RouteArgs r;
+    const float *dweights, *grad_loss;  // or nullptr
+    MatrixArgs dlogits;
+};
+cudaError_t launch_route_gradient(const RouteGradArgs &a, fa_dtype dt, cudaStream_t stream);
+
+cudaError_t dropout_bounds_violations(unsigned long long *count, bool clear);
+cudaError_t join_bounds_violations(unsigned long long *count, bool clear);
+cudaError_t join_gradient_bounds_violations(unsigned long long *count, bool clear);
+cudaError_t join_gradient_f32_bounds_violations(unsigned long long *count, bool clear);
+cudaError_t route_bounds_violations(unsigned long long *count, bool clear);
+
+// Calls f with the validated types of the branch and of the stream.
+template <typename F>
+inline cudaError_t for_stream_dtype(fa_dtype dt, fa_dtype st, F f) {
+    return for_dtype(dt, [&](auto d) {
+        return st == FA_F32 ? f(d, std::integral_constant<int, FA_F32>{}) : f(d, d);
+    });
+}
+
+// Defines a file's ``name``_bounds_violations over its counter.
+#if FA_BOUNDS_CHECK
+#define FA_BOUNDS_VIOLATIONS(name, counter)                                    \
+    cudaError_t name(unsigned long long *count, bool clear) {                  \
+        cudaError_t err = cudaMemcpyFromSymbol(count, counter, sizeof(*count)); \
+        if (err != cudaSuccess || !clear) return err;                          \
+        const unsigned long long zero = 0;                                     \
+        return cudaMemcpyToSymbol(counter, &zero, sizeof(zero));               \
+    }
+#else
+#define FA_BOUNDS_VIOLATIONS(name, counter)                 \
+    cudaError_t name(unsigned long long *count, bool) {     \
+        *count = 0;                                         \
+        return cudaSuccess;                                 \
+    }
+#endif
+
+}  // namespace fa

@@ -17,17 +17,16 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
-#include "model_device.cuh"
-#include "model_internal.h"
+
+FA_BOUNDS_COUNTER(g_gated_oob)
+
+#include "model_runs.cuh"
 
 namespace fa {
 namespace {
 
-FA_BOUNDS_COUNTER(g_gated_oob)
-
 constexpr int kGatedThreads = 256;
 constexpr int kLanes = 8;                         // per block of columns
-constexpr int kRun = 8;                           // consecutive columns of a lane
 constexpr int kRunStride = kCheckpointBlock / 2;  // between its two runs
 constexpr float kTiny = 0x1p-100f;                // blocks below it are stored as zeros
 constexpr float kLog2E = 1.4426950408889634f;
@@ -85,55 +84,6 @@ struct Activation<FA_GELU_TANH> {
         da = fma2(rest, fma2(q, both(3.f * kB), both(kA)), s);
     }
 };
-
-// A lane's run of eight columns [c, c + 8) of a row.  ALIGNED: one 16-byte access (two for
-// FP32) when the columns all exist, element accesses otherwise; else the 16-byte lines that the
-// run touches (see RawAny, store_any).  Columns past the end read as 0 and are not written.
-__device__ __forceinline__ int valid_cols(int64_t c, int64_t cols) {
-    return c + kRun <= cols ? kRun : c < cols ? static_cast<int>(cols - c) : 0;
-}
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ Raw<DT, kRun> load_run(const MatrixArgs &m, int64_t row, int64_t c) {
-    using E = Elem<DT>;
-    const typename E::T *p = static_cast<const typename E::T *>(m.p) + row * m.ld + c;
-    const int valid = valid_cols(c, m.cols);
-    if (valid && !fa_in_bounds(c, valid, m.cols)) return {};
-    if constexpr (ALIGNED) {
-        Raw<DT, kRun> x;
-        if (c + kRun <= m.cols) {
-            x.load(p);
-        } else {
-            float y[kRun];
-#pragma unroll
-            for (int j = 0; j < kRun; ++j) y[j] = j < valid ? E::widen(p[j]) : 0.f;
-            x.from(y);  // exact: they came from this type
-        }
-        return x;
-    } else {
-        RawAny<DT, kRun> x;
-        x.load(p, valid, Span(m.p, ((m.rows - 1) * m.ld + m.cols) * sizeof(typename E::T)));
-        return x.raw();
-    }
-}
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ void store_run(const MatrixArgs &m, int64_t row, int64_t c,
-                                          const float *x, unsigned lanes) {
-    using E = Elem<DT>;
-    typename E::T *p = static_cast<typename E::T *>(m.p) + row * m.ld + c;
-    int valid = valid_cols(c, m.cols);
-    if (valid && !fa_in_bounds(c, valid, m.cols)) valid = 0;
-    if constexpr (ALIGNED) {
-        if (c + kRun <= m.cols) {
-            store_n<DT, kRun>(p, x);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kRun; ++j)
-                if (j < valid) p[j] = E::round(x[j]);
-        }
-    } else {
-        store_any<DT, kRun>(p, x, valid, lanes, kLanes);
-    }
-}
 
 // The larger of two magnitudes; NaN where either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -220,7 +170,7 @@ gated_forward_kernel(GatedForwardArgs a) {
         for (int j = 0; j < kRun; j += 2)
             unpair(mul2(Activation<ACT>::value(pair(x[j], x[j + 1])), pair(y[j], y[j + 1])), x[j],
                    x[j + 1]);
-        store_run<DT, ALIGNED>(a.h, row, c + r * kRunStride, x, lanes);
+        store_run<DT, ALIGNED>(a.h, row, c + r * kRunStride, x, lanes, kLanes);
     }
 }
 
@@ -269,17 +219,10 @@ gated_backward_kernel(GatedBackwardArgs a) {
             unpair(mul2(dh, act), du[j], du[j + 1]);
             unpair(mul2(act, u[j / 2]), h[j], h[j + 1]);
         }
-        store_run<DT, ALIGNED>(a.dgate, row, c + r * kRunStride, dg, lanes);
-        store_run<DT, ALIGNED>(a.dup, row, c + r * kRunStride, du, lanes);
-        if (a.h.p) store_run<DT, ALIGNED>(a.h, row, c + r * kRunStride, h, lanes);
+        store_run<DT, ALIGNED>(a.dgate, row, c + r * kRunStride, dg, lanes, kLanes);
+        store_run<DT, ALIGNED>(a.dup, row, c + r * kRunStride, du, lanes, kLanes);
+        if (a.h.p) store_run<DT, ALIGNED>(a.h, row, c + r * kRunStride, h, lanes, kLanes);
     }
-}
-
-// Whether 16-byte accesses at multiples of eight columns are aligned in every row.
-bool aligned_rows(const MatrixArgs &m, fa_dtype dt) {
-    const int64_t row_bytes = m.ld * (dt == FA_F32 ? 4 : 2);
-    return !m.p || (reinterpret_cast<uintptr_t>(m.p) % 16 == 0 &&
-                    (m.rows < 2 || row_bytes % 16 == 0));
 }
 
 template <typename F>

@@ -1,0 +1,35 @@
+// The gradient of a join whose stream has the branch's type, and how it cuts the rows.
+#include "join_gradient.cuh"
+
+namespace fa {
+
+FA_BOUNDS_VIOLATIONS(join_gradient_bounds_violations, g_join_gradient_oob)
+
+JoinShape join_shape(int64_t cols) {
+    const int64_t runs = (cols + kRun - 1) / kRun;
+    const int r = runs <= kMaxThreads ? 1 : 2;
+    const int64_t threads = ((runs + r - 1) / r + 31) / 32 * 32;
+    if (threads > kMaxThreads) return {kMaxThreads, 0};
+    return {static_cast<int>(threads), r};
+}
+
+JoinPlan join_plan(int64_t rows, int64_t cols, int64_t groups) {
+    JoinPlan p{0, 0, 0, 0, 0};
+    if (rows == 0 || cols == 0) return p;
+    const int64_t ctas = kSms * (kMaxThreads / join_shape(cols).threads);
+    p.chunk = (rows + ctas - 1) / ctas;
+    p.ctas = (rows + p.chunk - 1) / p.chunk;
+    p.pitch = (cols + kRun - 1) / kRun * kRun;
+    p.parts = groups > 0 ? 4 : 2;
+    p.bytes = p.ctas * p.parts * p.pitch * 4;
+    return p;
+}
+
+cudaError_t launch_block_join_gradient(const JoinGradArgs &a, fa_dtype dt, fa_dtype st,
+                                       cudaStream_t stream) {
+    if (st == FA_F32) return launch_block_join_gradient_f32(a, dt, stream);
+    return dt == FA_F16 ? launch_gradient<FA_F16, FA_F16>(a, stream)
+                        : launch_gradient<FA_BF16, FA_BF16>(a, stream);
+}
+
+}  // namespace fa

@@ -245,11 +245,12 @@ def _routing(out: RouteBuffers, tokens: int, experts: int) -> tuple[FaRouting, i
     f32, i32 = torch.float32, torch.int32
     pairs = _vector("chosen", out.chosen, tokens * k, i32), _vector("weights", out.weights,
                                                                     tokens * k, f32)
-    if out.summary is None:
+    if out.lse is None:
         return FaRouting(*pairs), k
-    return FaRouting(*pairs, _vector("lse", out.lse, 2 * tokens, f32),
-                     _vector("counts", out.counts, experts, i32),
-                     _vector("mean_prob", out.mean_prob, experts, f32),
+    kept = _vector("lse", out.lse, 2 * tokens, f32), _vector("counts", out.counts, experts, i32)
+    if out.summary is None:  # what a gradient reads
+        return FaRouting(*pairs, *kept), k
+    return FaRouting(*pairs, *kept, _vector("mean_prob", out.mean_prob, experts, f32),
                      _vector("summary", out.summary, 4, f32),
                      _vector("scratch", out.scratch, out.scratch.numel(), torch.uint8),
                      out.scratch.numel()), k
@@ -276,7 +277,7 @@ def fa_route_gradient(logits: torch.Tensor, out: RouteBuffers, dlogits: torch.Te
     """dlogits of grad_loss (a device scalar) * loss + sum of dweights * weights, from what
     fa_route wrote with the same arguments."""
     tokens, experts = _matrix("logits", logits)
-    if out.summary is None:
+    if out.lse is None:
         raise ValueError("the buffers are those of a pass without a loss: nothing was kept")
     r, k = _routing(out, tokens, experts)
     x = _router(logits, k, counted, renormalise, weight_scale, balance_coef, z_coef)

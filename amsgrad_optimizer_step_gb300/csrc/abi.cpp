@@ -353,12 +353,17 @@ const char *fa_status_string(fa_status s) {
 
 fa_status fa_device_error(int32_t *flag, int32_t clear) {
     if (!flag) return FA_ERR_NULL;
-    int v = 0;
-    if (fa::update_pipeline_error(&v, clear != 0) != cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_CUDA;
+    int set = 0;
+    for (auto *read : {fa::update_pipeline_error, fa::join_gradient_error,
+                       fa::join_gradient_f32_error}) {
+        int v = 0;
+        if (read(&v, clear != 0) != cudaSuccess) {
+            cudaGetLastError();
+            return FA_ERR_CUDA;
+        }
+        set |= v;
     }
-    *flag = v;
+    *flag = set;
     return FA_OK;
 }
 

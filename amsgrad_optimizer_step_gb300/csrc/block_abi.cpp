@@ -30,8 +30,10 @@ DropArgs drop_args(const fa_dropout_key *k) {
     const auto q = static_cast<uint32_t>(std::nearbyint(65536.0 * k->p));
     DropArgs d;
     d.threshold = q < 65536 ? q << 16 : 0xffffffffu;
-    d.key[0] = static_cast<uint32_t>(k->seed);
-    d.key[1] = static_cast<uint32_t>(k->seed >> 32);
+    for (uint32_t r = 0; r < static_cast<uint32_t>(kPhiloxRounds); ++r) {
+        d.key[r][0] = static_cast<uint32_t>(k->seed) + r * 0x9E3779B9u;
+        d.key[r][1] = static_cast<uint32_t>(k->seed >> 32) + r * 0xBB67AE85u;
+    }
     d.offset = k->offset;
     d.counter = k->counter;
     d.scale = q < 65536 ? static_cast<float>(65536.0 / (65536.0 - q)) : 0.f;
@@ -224,7 +226,7 @@ fa_status fa_block_join_scratch(int64_t rows, int64_t cols, int64_t groups, int6
     if (!bytes) return FA_ERR_NULL;
     if (rows < 0 || rows > kMaxCount || cols < 0 || cols > FA_JOIN_MAX_COLS || groups < 0)
         return FA_ERR_SIZE;
-    *bytes = join_plan(rows, cols, groups).bytes;
+    *bytes = join_plan(rows, cols, groups, 8).bytes;
     return FA_OK;
 }
 
@@ -246,9 +248,13 @@ fa_status fa_block_join_gradient(const fa_join *j, const fa_join_gradient *g, vo
     if (g->dbranch) FA_TRY(check_matrix(rows, cols, g->dbranch_ld));
     if (g->dgate) FA_TRY(check_matrix(j->groups, cols, g->dgate_ld));
     if (cols == 0) return FA_OK;
+    const int element_bytes =
+        2 * static_cast<int>(dtype_bytes(j->dtype) + dtype_bytes(j->stream_dtype));
+    const JoinPlan plan = join_plan(rows, cols, g->dgate ? j->groups : 0, element_bytes);
     const bool sums = g->dpost_weight || g->dpre_weight || g->dgate;
-    const JoinPlan plan = join_plan(rows, cols, g->dgate ? j->groups : 0);
-    if (rows > 0 && sums && g->scratch_bytes < plan.bytes) return FA_ERR_SIZE;
+    int64_t need = 0;
+    FA_TRY(fa_block_join_scratch(rows, cols, g->dgate ? j->groups : 0, &need));
+    if (rows > 0 && sums && g->scratch_bytes < need) return FA_ERR_SIZE;
     int dev;
     FA_TRY(stream_device(stream, &dev));
     const size_t e = dtype_bytes(j->dtype), s = dtype_bytes(j->stream_dtype),
@@ -275,7 +281,7 @@ fa_status fa_block_join_gradient(const fa_join *j, const fa_join_gradient *g, vo
                            vec(g->dpost_weight, row_bytes),
                            vec(g->dpre_weight, row_bytes),
                            mat(g->dgate, j->groups, cols, g->dgate_ld, w),
-                           vec(sums ? g->scratch : nullptr, plan.bytes)};
+                           vec(sums ? g->scratch : nullptr, need)};
     const Matrix ins[] = {mat(j->branch, rows, cols, j->branch_ld, e),
                           mat(pre ? g->out : nullptr, rows, cols, g->out_ld, s),
                           mat(g->dout, rows, cols, g->dout_ld, s),

@@ -14,9 +14,10 @@
 namespace fa {
 
 // ---- dropout -------------------------------------------------------------------
+constexpr int kPhiloxRounds = 10;
 struct DropArgs {
     uint32_t threshold;  // 16 bits are kept from threshold >> 16 on; 2^32 - 1: none is
-    uint32_t key[2];
+    uint32_t key[kPhiloxRounds][2];  // of each round
     uint64_t offset;
     const uint64_t *counter;  // or nullptr
     float scale;              // of what is kept
@@ -46,22 +47,32 @@ struct JoinArgs {
 };
 cudaError_t launch_block_join(const JoinArgs &a, fa_dtype dt, fa_dtype st, cudaStream_t stream);
 
-// How the gradient cuts the rows: CTAs of consecutive rows, each with FP32 sums of its own.
+// How the gradient cuts the rows into CTAs, each with FP32 sums of its own.  element_bytes: of a
+// column over the four matrices that it reads (8 at least, which gives the most CTAs).
 struct JoinPlan {
-    int64_t chunk;  // rows of a CTA
+    int64_t chunk;  // rows of a CTA at most
     int64_t ctas;
     int64_t pitch;  // columns of one row of sums
     int64_t parts;  // rows of sums of a CTA
     int64_t bytes;
 };
-JoinPlan join_plan(int64_t rows, int64_t cols, int64_t groups);
+JoinPlan join_plan(int64_t rows, int64_t cols, int64_t groups, int element_bytes);
 
-// Threads of a row of the gradient and runs of a thread: one up to 4096 columns, two up to 8192
-// (the columns' sums are two registers a column); 0: more, in shared memory.
+// Threads of a row of the gradient and runs of a thread: one up to 6144 columns, two up to 8192
+// (the columns' sums are two registers a column); 0: more, with the sums in shared memory.
 struct JoinShape {
     int threads, runs;
 };
 JoinShape join_shape(int64_t cols);
+constexpr int kJoinThreads = 768;  // of a row of one run a thread, and of an SM
+// CTAs of the gradient on an SM, for rows of ``row_bytes`` over the four matrices that it reads:
+// as many as have room for two rows each on their way, beside the weights (64 bytes a run).
+constexpr int kSmShared = 228 * 1024;  // of an SM, of which a CTA has 2 KB for other things
+inline int join_ctas_per_sm(const JoinShape &shape, int row_bytes) {
+    int n = shape.threads < kJoinThreads ? kJoinThreads / shape.threads : 1;
+    while (n > 1 && kSmShared / n - 2048 - 64 * shape.runs * shape.threads < 2 * row_bytes) --n;
+    return n;
+}
 
 struct JoinGradArgs {
     JoinArgs j;  // branch, weights, gate, scales; post_rstd and pre_rstd are read
@@ -106,6 +117,11 @@ struct RouteGradArgs {
     MatrixArgs dlogits;
 };
 cudaError_t launch_route_gradient(const RouteGradArgs &a, fa_dtype dt, cudaStream_t stream);
+
+// Reads (and optionally clears) the flag that the gradient of a join sets when a bounded wait for
+// a row gives up.  Waits for the device.
+cudaError_t join_gradient_error(int *flag, bool clear);
+cudaError_t join_gradient_f32_error(int *flag, bool clear);
 
 cudaError_t dropout_bounds_violations(unsigned long long *count, bool clear);
 cudaError_t join_bounds_violations(unsigned long long *count, bool clear);

@@ -18,12 +18,11 @@
 
 FA_BOUNDS_COUNTER(g_join_gradient_oob)
 
+#include "bulk_rows.cuh"
 #include "join_device.cuh"
 
 namespace fa {
 namespace {
-
-constexpr int kRingBytes = 220 * 1024;
 
 // One row's four matrices as a thread holds them.
 template <int DT, int ST, int R>
@@ -32,85 +31,105 @@ struct GradRow {
     Raw<DT, kRun> dn[R], y[R];
 };
 
-template <int DT>
-__device__ __forceinline__ void zero(Raw<DT, kRun> &x) {
-#pragma unroll
-    for (int k = 0; k < Raw<DT, kRun>::kWords; ++k) x.r[k] = make_uint4(0u, 0u, 0u, 0u);
-}
+__device__ int g_join_gradient_error;  // a wait for a row ran out
 
-// The rows on their way: a ring in shared memory of two to four rows, every thread's vectors in
-// slots of its own, copied asynchronously by the thread that reads them (no barrier is needed).
+// The rows on their way: a ring of up to four rows, the four matrices' one behind another, each as
+// long as the threads' runs reach.  What nothing is copied to (columns past the end, matrices that
+// are not there) stays 0, so that a thread reads its runs without asking.  The row's reduction is
+// between the last read of a slot and the copies of a later row into it.
 template <int DT, int ST, int R>
 struct Ring {
     static constexpr int kMost = 4;
-    static constexpr int kS = Raw<ST, kRun>::kWords, kD = Raw<DT, kRun>::kWords;
-    static constexpr int kVectors = 2 * R * (kS + kD);  // of 16 bytes, a thread's for one row
+    static constexpr int kS = Raw<ST, kRun>::kWords, kD = Raw<DT, kRun>::kWords;  // of 16 bytes
+    static constexpr int kVectors = 2 * R * (kS + kD);  // of a row, per thread
 
-    static int bytes(int threads) { return kVectors * threads * 16; }  // of one row
+    static int bytes(int threads) { return 16 * kVectors * threads; }  // of a row
     // Rows that the ring has room for (below two there is none).
-    static int stages(int threads) {
-        const int n = kRingBytes / bytes(threads);
+    static int stages(int threads, int ctas, int weights) {
+        const int n = (kSmShared / ctas - 2048 - weights) / bytes(threads);
         return n < kMost ? n : kMost;
     }
-    // Waits for the oldest row but ``stages`` - 2 later ones.
-    static __device__ __forceinline__ void wait(int stages) {
-        if (stages == 4)
-            copy_async_wait<2>();
-        else if (stages == 3)
-            copy_async_wait<1>();
-        else
-            copy_async_wait<0>();
+    // By one thread: asks for a row.
+    static __device__ __forceinline__ void issue(const JoinGradArgs &a, int64_t row, uint4 *slot,
+                                                 uint64_t *bar) {
+        if (!fa_in_bounds(row, 1, a.j.rows)) return;
+        const int runs = static_cast<int>(a.j.cols) / kRun, reach = R * blockDim.x;
+        const uint32_t s = 16 * kS * runs, d = 16 * kD * runs;
+        row_expect(bar, (a.dout.p ? s : 0) + (a.out.p ? s : 0) + (a.dnormed.p ? d : 0) +
+                            (a.j.branch.p ? d : 0));
+        const auto copy = [&](const MatrixArgs &m, int size, uint32_t bytes, int at) {
+            if (m.p)
+                row_copy(slot + at * reach, static_cast<const char *>(m.p) + row * m.ld * size,
+                         bytes, bar);
+        };
+        copy(a.dout, 2 * kS, s, 0);
+        copy(a.out, 2 * kS, s, kS);
+        copy(a.dnormed, 2 * kD, d, 2 * kS);
+        copy(a.j.branch, 2 * kD, d, 2 * kS + kD);
     }
-    template <int DD>
-    static __device__ __forceinline__ void ask(const MatrixArgs &m, int64_t row, int64_t c,
-                                               uint4 *slot) {
-        constexpr int W = Raw<DD, kRun>::kWords;
-        if (!m.p || c >= m.cols || !fa_in_bounds(c, kRun, m.cols)) return;
-        const auto *p = static_cast<const typename Elem<DD>::T *>(m.p) + row * m.ld + c;
+    template <int W, typename T>
+    static __device__ __forceinline__ void take(const uint4 *at, T &x) {
 #pragma unroll
-        for (int k = 0; k < W; ++k)
-            copy_async16(slot + k * blockDim.x, reinterpret_cast<const uint4 *>(p) + k);
+        for (int k = 0; k < W; ++k) x.r[k] = at[k];
     }
-    static __device__ __forceinline__ uint4 *stage(uint4 *ring, int s) {
-        return ring + static_cast<size_t>(s) * kVectors * blockDim.x + threadIdx.x;
-    }
-    // Asks for a row (nothing past the last one) and closes the group.
-    static __device__ __forceinline__ void issue(const JoinGradArgs &a, int64_t row, int64_t last,
-                                                 uint4 *slot) {
-        if (row < last) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int64_t c = (static_cast<int64_t>(r) * blockDim.x + threadIdx.x) * kRun;
-                uint4 *at = slot + r * 2 * (kS + kD) * blockDim.x;
-                ask<ST>(a.dout, row, c, at);
-                ask<ST>(a.out, row, c, at + kS * blockDim.x);
-                ask<DT>(a.dnormed, row, c, at + 2 * kS * blockDim.x);
-                ask<DT>(a.j.branch, row, c, at + (2 * kS + kD) * blockDim.x);
-            }
-        }
-        copy_async_commit();
-    }
-    template <int DD>
-    static __device__ __forceinline__ void take(bool there, const uint4 *slot,
-                                                Raw<DD, kRun> &x) {
-        zero(x);
-        if (!there) return;
-#pragma unroll
-        for (int k = 0; k < Raw<DD, kRun>::kWords; ++k) x.r[k] = slot[k * blockDim.x];
-    }
-    static __device__ __forceinline__ void read(const JoinGradArgs &a, const uint4 *slot,
-                                                GradRow<DT, ST, R> &g) {
+    static __device__ __forceinline__ void read(const uint4 *slot, GradRow<DT, ST, R> &g) {
+        const int reach = R * blockDim.x;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const bool in = (static_cast<int64_t>(r) * blockDim.x + threadIdx.x) * kRun < a.j.cols;
-            const uint4 *at = slot + r * 2 * (kS + kD) * blockDim.x;
-            take(in && a.dout.p, at, g.dout[r]);
-            take(in && a.out.p, at + kS * blockDim.x, g.x[r]);
-            take(in && a.dnormed.p, at + 2 * kS * blockDim.x, g.dn[r]);
-            take(in && a.j.branch.p, at + (2 * kS + kD) * blockDim.x, g.y[r]);
+            const int q = r * blockDim.x + threadIdx.x;
+            take<kS>(slot + q * kS, g.dout[r]);
+            take<kS>(slot + kS * reach + q * kS, g.x[r]);
+            take<kD>(slot + 2 * kS * reach + q * kD, g.dn[r]);
+            take<kD>(slot + (2 * kS + kD) * reach + q * kD, g.y[r]);
         }
     }
 };
+
+// Three sums over a warp, halving what a lane carries at each of the first steps: six shuffles
+// instead of fifteen.  The sums end in lanes 0 to 7, 8 to 15 and 16 to 23.
+__device__ __forceinline__ float warp_sum3(float s1, float s2, float s3) {
+    const bool h16 = threadIdx.x & 16, h8 = threadIdx.x & 8;
+    float a = h16 ? s3 : s1, b = h16 ? 0.f : s2;
+    a += __shfl_xor_sync(0xffffffffu, h16 ? s1 : s3, 16);
+    b += __shfl_xor_sync(0xffffffffu, h16 ? s2 : 0.f, 16);
+    float c = h8 ? b : a;
+    c += __shfl_xor_sync(0xffffffffu, h8 ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    return c;
+}
+
+// The same over a row's threads, in every one.  ``part``: 24 floats for each sum and for nothing
+// (those of no warp 0), not in use by the call before.  True where one of the threads says
+// ``failed``.
+constexpr int kPartWarps = kJoinThreads / 32;
+__device__ __forceinline__ bool row_sum3(float &s1, float &s2, float &s3, float *part,
+                                         bool failed) {
+    float c = warp_sum3(s1, s2, s3);
+    const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
+    if (warps > 1) {
+        if (lane % 8 == 0) part[lane / 8 * kPartWarps + threadIdx.x / 32] = c;
+        failed = __syncthreads_or(failed);
+        // eight lanes take a sum's warps, eight at a time
+        const float *const mine = part + lane / 8 * kPartWarps + lane % 8;
+        c = mine[0];
+        for (int w = 8; w < warps; w += 8) c += mine[w];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    } else {
+        failed = __any_sync(0xffffffffu, failed);
+    }
+    s1 = __shfl_sync(0xffffffffu, c, 0);
+    s2 = __shfl_sync(0xffffffffu, c, 8);
+    s3 = __shfl_sync(0xffffffffu, c, 16);
+    return failed;
+}
+
+__device__ __forceinline__ float sum_of_pair(uint64_t p) {
+    float lo, hi;
+    unpair(p, lo, hi);
+    return lo + hi;
+}
 
 template <int DT>
 __device__ __forceinline__ void store_weight(void *p, bool wide, int64_t at, float x) {
@@ -124,91 +143,126 @@ __device__ __forceinline__ void store_weight(void *p, bool wide, int64_t at, flo
 enum { kPost = 0, kPre = 1, kHead = 2, kTail = 3 };
 
 // RING: rows of whole, aligned runs that go through the ring; else each row is read when its turn
-// comes, from any address.
-template <int DT, int ST, int R, bool RING>
-__global__ void __launch_bounds__(kMaxThreads) join_gradient_kernel(JoinGradArgs a) {
+// comes, from any address.  ALL: both norms, the branch and every matrix's gradient are there
+// (what a training step asks for, without a question a row).  DROP: false where nothing is dropped.
+template <int DT, int ST, int R, bool RING, bool ALL, bool DROP>
+__global__ void __launch_bounds__(R == 1 ? kJoinThreads : kMaxThreads)
+join_gradient_kernel(JoinGradArgs a) {
     extern __shared__ uint4 ring[];
-    __shared__ float part[2][3][kMaxThreads / 32];
+    __shared__ __align__(16) float part[2][4 * kPartWarps];
     using Rows = Ring<DT, ST, R>;
-    const int64_t first = blockIdx.x * a.plan.chunk;
-    const int64_t last = first + a.plan.chunk < a.j.rows ? first + a.plan.chunk : a.j.rows;
-    const bool pre = a.dnormed.p, branch = a.j.branch.p, post = a.j.post_norm && branch;
-    const int64_t blocks = (a.j.cols + kRun - 1) / kRun;
-    const float inv_cols = 1.f / static_cast<float>(a.j.cols);
-    const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
-    int64_t c[R];
-    int valid[R];
+    __shared__ uint64_t bars[Rows::kMost];
+    // the CTA's rows: first, first + stride, ...
+    const bool own_gate = a.j.gate && a.j.group_rows < a.j.rows;
+    const int64_t stride = own_gate ? 1 : gridDim.x;
+    const int64_t first = own_gate ? blockIdx.x * a.plan.chunk : blockIdx.x;
+    const int64_t end = own_gate && first + a.plan.chunk < a.j.rows ? first + a.plan.chunk : a.j.rows;
+    const int count = static_cast<int>((end - first + stride - 1) / stride);
+    const bool pre = ALL || a.dnormed.p, branch = ALL || a.j.branch.p;
+    const bool post = ALL || (a.j.post_norm && branch), dropped = DROP && (ALL || a.j.dropped);
+    const int cols = static_cast<int>(a.j.cols), runs = (cols + kRun - 1) / kRun;
+    const float inv_cols = 1.f / static_cast<float>(cols);
+    const int lane = threadIdx.x % 32;
+    for (int i = threadIdx.x; i < 2 * 4 * kPartWarps; i += blockDim.x) part[0][i] = 0.f;
+    const int row_vectors = RING ? Rows::kVectors * blockDim.x : 0;
+    if (RING) {
+        if (runs < R * static_cast<int>(blockDim.x) || !a.dout.p || !pre || !branch) {
+            for (int i = threadIdx.x; i < a.stages * row_vectors; i += blockDim.x)
+                ring[i] = make_uint4(0u, 0u, 0u, 0u);
+            shared_writes_before_copies();
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < a.stages; ++i) row_barrier_init(bars + i);
+            row_barriers_ready();
+            for (int i = 0; i < a.stages && i < count; ++i)
+                Rows::issue(a, first + i * stride, ring + i * row_vectors, bars + i);
+        }
+    }
+    __syncthreads();
+    const float scale = dropped ? a.j.branch_scale * a.j.drop.scale : a.j.branch_scale;
+    const uint64_t call = dropped ? drop_call(a.j.drop) : 0;
+    // the thread's weights, in slots of its own: w_pre, then scale * gate * w_post, of each run
+    float4 *const kept_weights =
+        reinterpret_cast<float4 *>(ring + a.stages * row_vectors) + threadIdx.x;
+    const auto keep = [&](int which, int r, const float *w) {
+        float4 *const at = kept_weights + (4 * r + 2 * which) * blockDim.x;
+        at[0] = make_float4(w[0], w[1], w[2], w[3]);
+        at[blockDim.x] = make_float4(w[4], w[5], w[6], w[7]);
+    };
+    const auto fetch = [&](int which, int r, uint64_t *w) {
+        const float4 *const at = kept_weights + (4 * r + 2 * which) * blockDim.x;
+        const float4 lo = at[0], hi = at[blockDim.x];
+        w[0] = pair(lo.x, lo.y);
+        w[1] = pair(lo.z, lo.w);
+        w[2] = pair(hi.x, hi.y);
+        w[3] = pair(hi.z, hi.w);
+    };
+    uint64_t sum_k[R][kPairs] = {}, sum_p[R][kPairs] = {};
+    // the weights of run r: what: a weight or the gate's row, ``offset`` added
+    const auto weights = [&](const void *p, int64_t row0, int r, float offset, float *w) {
+        const int c = (r * blockDim.x + threadIdx.x) * kRun;
+        load_weights<DT>(a.j, p, row0 + c, valid_cols(c, cols), offset, w);
+    };
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        c[r] = (static_cast<int64_t>(r) * blockDim.x + threadIdx.x) * kRun;
-        valid[r] = valid_cols(c[r], a.j.cols);
+        float w[kRun];
+        weights(pre ? a.j.pre_weight : nullptr, 0, r, a.j.weight_offset, w);
+        keep(0, r, w);
     }
-    if (RING) {
-#pragma unroll
-        for (int s = 0; s < Rows::kMost - 1; ++s)
-            if (s < a.stages - 1) Rows::issue(a, first + s, last, Rows::stage(ring, s));
-    }
-    const float scale = a.j.dropped ? a.j.branch_scale * a.j.drop.scale : a.j.branch_scale;
-    const uint64_t call = a.j.dropped ? drop_call(a.j.drop) : 0;
-    float wp[R][kRun], aw[R][kRun];  // w_pre; scale * gate * w_post
-    float sum_k[R][kRun] = {}, sum_p[R][kRun] = {};
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        load_weights<DT>(a.j, pre ? a.j.pre_weight : nullptr, c[r], valid[r],
-                               a.j.weight_offset, wp[r]);
     float *const sums = a.sums + blockIdx.x * a.plan.parts * a.plan.pitch;
-    // the gate's group of the first row, and how many of its rows are left
-    int64_t group = a.j.gate ? a.j.by_group.quotient(static_cast<uint32_t>(first)) : 0;
-    int64_t group_first = a.j.gate ? group * a.j.group_rows : first;
-    int64_t group_last = a.j.gate ? group_first + a.j.group_rows : last;
+    // the gate's group of the row, and the turns that its rows begin and end with (where a group is
+    // all rows, the first CTA counts as the one that begins it)
+    int64_t group = own_gate ? a.j.by_group.quotient(static_cast<uint32_t>(first)) : 0;
+    int64_t group_begin = own_gate ? group * a.j.group_rows - first : -static_cast<int64_t>(blockIdx.x);
+    int64_t group_end = own_gate ? group_begin + a.j.group_rows : gridDim.x == 1 ? count : count + 1;
     bool flushed = false;
 
     const auto new_group = [&] {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float w[kRun];
-            load_weights<DT>(a.j, post ? a.j.post_weight : nullptr, c[r],
-                                   valid[r], a.j.weight_offset, aw[r]);
-            load_weights<DT>(a.j, a.j.gate, group * a.j.gate_ld + c[r],
-                                   valid[r], 0.f, w);
+            float w[kRun], g[kRun];
+            weights(post ? a.j.post_weight : nullptr, 0, r, a.j.weight_offset, w);
+            weights(a.j.gate, group * a.j.gate_ld, r, 0.f, g);
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) aw[r][j] *= scale * w[j];
+            for (int j = 0; j < kRun; ++j) w[j] *= scale * g[j];
+            keep(1, r, w);
         }
     };
     // The group's sums: whole where all its rows are this CTA's, else a part of them.
     const auto flush = [&] {
-        const bool begun_here = group_first >= first, whole = begun_here && group_last <= last;
+        const bool begun_here = group_begin >= 0, whole = begun_here && group_end <= count;
         float *const gate_part = sums + (begun_here ? kTail : kHead) * a.plan.pitch;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float w[kRun];
+            const int c = (r * blockDim.x + threadIdx.x) * kRun, valid = valid_cols(c, cols);
+            float w[kRun], k[kRun];
+            from_pairs(sum_k[r], k);
             if (a.dpost_weight) {
-                load_weights<DT>(a.j, a.j.gate, group * a.j.gate_ld + c[r],
-                                       valid[r], 0.f, w);
+                weights(a.j.gate, group * a.j.gate_ld, r, 0.f, w);
+                float *const at = sums + kPost * a.plan.pitch + c;
 #pragma unroll
                 for (int j = 0; j < kRun; ++j)
-                    if (j < valid[r]) {
-                        float *at = sums + kPost * a.plan.pitch + c[r] + j;
-                        const float x = scale * w[j] * sum_k[r][j];
-                        *at = flushed ? *at + x : x;
+                    if (j < valid) {
+                        const float x = scale * w[j] * k[j];
+                        at[j] = flushed ? at[j] + x : x;
                     }
             }
             if (a.dgate) {
-                load_weights<DT>(a.j, post ? a.j.post_weight : nullptr, c[r],
-                                       valid[r], a.j.weight_offset, w);
+                weights(post ? a.j.post_weight : nullptr, 0, r, a.j.weight_offset, w);
 #pragma unroll
                 for (int j = 0; j < kRun; ++j)
-                    if (j < valid[r]) {
-                        const float x = scale * w[j] * sum_k[r][j];
+                    if (j < valid) {
+                        const float x = scale * w[j] * k[j];
                         if (whole)
                             store_weight<DT>(a.dgate, a.j.wide_weights,
-                                             group * a.dgate_ld + c[r] + j, x);
+                                             group * a.dgate_ld + c + j, x);
                         else
-                            gate_part[c[r] + j] = x;
+                            gate_part[c + j] = x;
                     }
             }
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) sum_k[r][j] = 0.f;
+            for (int j = 0; j < kPairs; ++j) sum_k[r][j] = 0;
         }
         flushed = true;
     };
@@ -216,125 +270,161 @@ __global__ void __launch_bounds__(kMaxThreads) join_gradient_kernel(JoinGradArgs
     if (branch) new_group();
     float rp_lane = 0.f, rq_lane = 1.f;
     int stage = 0;
+    uint32_t parity = 0;
+    bool failed = false;
     fa_allow_dependents();
-    for (int64_t row = first; row < last; ++row) {
-        const int64_t n = row - first;
+    int64_t row = first;
+    using S = typename Elem<ST>::T;
+    using D = typename Elem<DT>::T;
+    S *to_residual = static_cast<S *>(a.dresidual.p) + first * a.dresidual.ld + threadIdx.x * kRun;
+    D *to_branch = static_cast<D *>(a.dbranch.p) + first * a.dbranch.ld + threadIdx.x * kRun;
+    const int64_t residual_step = stride * a.dresidual.ld, branch_step = stride * a.dbranch.ld;
+    for (int n = 0; n < count;
+         ++n, row += stride, to_residual += residual_step, to_branch += branch_step) {
         if (n % 32 == 0) {  // the inverse roots of 32 rows, a lane each
-            const bool in = row + lane < last;
-            if (pre) rp_lane = in ? a.j.pre_rstd[row + lane] : 0.f;
-            if (post) rq_lane = in ? a.j.post_rstd[row + lane] : 0.f;
+            const int64_t at = row + lane * stride;
+            if (pre) rp_lane = at < end ? a.j.pre_rstd[at] : 0.f;
+            if (post) rq_lane = at < end ? a.j.post_rstd[at] : 0.f;
         }
         const float rp = __shfl_sync(0xffffffffu, rp_lane, n % 32);
         const float rq = __shfl_sync(0xffffffffu, rq_lane, n % 32);
-        if (row == group_last) {
+        if (n == group_end) {
             if (branch) flush();
             ++group;
-            group_first = group_last;
-            group_last += a.j.group_rows;
+            group_begin = group_end;
+            group_end += a.j.group_rows;
             if (branch) new_group();
         }
         GradRow<DT, ST, R> g;
         if (RING) {
-            Rows::wait(a.stages);
-            Rows::read(a, Rows::stage(ring, stage), g);
-            // the slot read a row ago is free
-            Rows::issue(a, row + a.stages - 1, last,
-                        Rows::stage(ring, stage == 0 ? a.stages - 1 : stage - 1));
-            stage = stage == a.stages - 1 ? 0 : stage + 1;
+            failed = !row_wait(bars + stage, parity);
+            Rows::read(ring + stage * row_vectors, g);
         } else {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                if (a.dout.p) g.dout[r] = load_run<ST, RING>(a.dout, row, c[r]);
-                else zero(g.dout[r]);
-                if (a.out.p) g.x[r] = load_run<ST, RING>(a.out, row, c[r]);
-                else zero(g.x[r]);
-                if (pre) g.dn[r] = load_run<DT, RING>(a.dnormed, row, c[r]);
-                else zero(g.dn[r]);
-                if (branch) g.y[r] = load_run<DT, RING>(a.j.branch, row, c[r]);
-                else zero(g.y[r]);
+                const int c = (r * blockDim.x + threadIdx.x) * kRun;
+                zero(g.dout[r]);
+                zero(g.x[r]);
+                zero(g.dn[r]);
+                zero(g.y[r]);
+                if (a.dout.p) g.dout[r] = load_run<ST, false>(a.dout, row, c);
+                if (a.out.p) g.x[r] = load_run<ST, false>(a.out, row, c);
+                if (pre) g.dn[r] = load_run<DT, false>(a.dnormed, row, c);
+                if (branch) g.y[r] = load_run<DT, false>(a.j.branch, row, c);
             }
         }
-        float s1 = 0.f, s2 = 0.f, s3 = 0.f;
-        float t[R][kRun];
-        Kept kept[R];
+        // ym: the kept yh; am: the weights of the kept ones
+        uint64_t t[R][kPairs], ym[R][kPairs], am[R][kPairs];
+        uint64_t s1 = 0, s2 = 0, s3 = 0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (a.j.dropped)
-                kept[r].draw(a.j.drop, row * blocks + c[r] / kRun, call);
-            else
-                kept[r].all();
-            float dn[kRun], x[kRun], y[kRun];
-            g.dout[r].widen(t[r]);
-            g.dn[r].widen(dn);
-            g.x[r].widen(x);
-            g.y[r].widen(y);
+            uint64_t x[kPairs];
+            widen_pairs<ST>(g.dout[r], t[r]);
+            widen_pairs<ST>(g.x[r], x);
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) {
-                const float d = dn[j] * wp[r][j], xh = x[j] * rp;
-                s1 = fmaf(d, xh, s1);
-                t[r][j] = fmaf(rp, d, t[r][j]);
-                if (post) {
-                    const float v = kept[r](j, a.j.drop.threshold) ? y[j] * rq : 0.f;
-                    const float q = v * aw[r][j];
-                    s2 = fmaf(q, t[r][j], s2);
-                    s3 = fmaf(q, xh, s3);
+            for (int j = 0; j < kPairs; ++j) x[j] = mul2(x[j], both(rp));
+            if (pre) {
+                uint64_t d[kPairs], wp[kPairs];
+                widen_pairs<DT>(g.dn[r], d);
+                fetch(0, r, wp);
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) {
+                    sum_p[r][j] = fma2(d[j], x[j], sum_p[r][j]);
+                    d[j] = mul2(d[j], wp[j]);
+                    t[r][j] = fma2(d[j], both(rp), t[r][j]);
+                    s1 = fma2(d[j], x[j], s1);
                 }
+            }
+            widen_pairs<DT>(g.y[r], ym[r]);
+            fetch(1, r, am[r]);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) ym[r][j] = mul2(ym[r][j], both(rq));
+            if (dropped) {
+                Kept kept;
+                kept.draw(a.j.drop, static_cast<uint64_t>(row) * runs + (r * blockDim.x + threadIdx.x),
+                          call);
+                kept.mask(ym[r], a.j.drop.threshold);
+                kept.mask(am[r], a.j.drop.threshold);
+            }
+            if (post) {
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) {
+                    const uint64_t q = mul2(ym[r][j], am[r][j]);
+                    s2 = fma2(q, t[r][j], s2);
+                    s3 = fma2(q, x[j], s3);
+                }
+            }
+        }
+        float back = 0.f, mean = 0.f;  // times xh: taken off t; times yh: taken off dbranch
+        float f1 = sum_of_pair(s1), f2 = sum_of_pair(s2), f3 = sum_of_pair(s3);
+        // (the other part is still being read)
+        failed = row_sum3(f1, f2, f3, part[n % 2], failed);
+        if (RING) {
+            if (failed) break;
+            // every thread has read its part of the slot
+            if (threadIdx.x == 0 && n + a.stages < count)
+                Rows::issue(a, row + a.stages * stride, ring + stage * row_vectors, bars + stage);
+            if (++stage == a.stages) {
+                stage = 0;
+                parity ^= 1;
             }
         }
         if (pre || post) {
-            s1 = warp_sum(s1);
-            if (post) {
-                s2 = warp_sum(s2);
-                s3 = warp_sum(s3);
-            }
-            if (warps > 1) {
-                float(*p)[kMaxThreads / 32] = part[n % 2];  // the other one is still being read
-                if (lane == 0) {
-                    p[0][threadIdx.x / 32] = s1;
-                    p[1][threadIdx.x / 32] = s2;
-                    p[2][threadIdx.x / 32] = s3;
-                }
-                __syncthreads();
-                s1 = s2 = s3 = 0.f;
-                for (int w = 0; w < warps; ++w) {
-                    s1 += p[0][w];
-                    s2 += p[1][w];
-                    s3 += p[2][w];
-                }
-            }
+            back = rp * (f1 * inv_cols);
+            mean = (f2 - back * f3) * inv_cols * rq;
         }
-        const float back = rp * (s1 * inv_cols);            // times xh: taken off t
-        const float mean = (s2 - back * s3) * inv_cols * rq;  // times yh: taken off dbranch
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float dn[kRun], x[kRun], y[kRun], dr[kRun], db[kRun];
-            g.dn[r].widen(dn);
-            g.x[r].widen(x);
-            g.y[r].widen(y);
+            uint64_t x[kPairs], y[kPairs], dr[kPairs], db[kPairs];
+            widen_pairs<ST>(g.x[r], x);
+            widen_pairs<DT>(g.y[r], y);
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) {
-                const float xh = x[j] * rp;
-                const float total = pre ? fmaf(-back, xh, t[r][j]) : t[r][j];
-                sum_p[r][j] = fmaf(dn[j], xh, sum_p[r][j]);
-                dr[j] = a.j.residual_scale * total;
-                const bool on = kept[r](j, a.j.drop.threshold);
-                const float yh = y[j] * rq;
-                sum_k[r][j] = fmaf(on ? yh : 0.f, on ? total : 0.f, sum_k[r][j]);
-                db[j] = on ? total * aw[r][j] : 0.f;
-                if (post) db[j] = fmaf(db[j], rq, -yh * mean);
+            for (int j = 0; j < kPairs; ++j) {
+                const uint64_t total =
+                    pre ? fma2(mul2(x[j], both(rp)), both(-back), t[r][j]) : t[r][j];
+                dr[j] = mul2(total, both(a.j.residual_scale));
+                sum_k[r][j] = fma2(ym[r][j], total, sum_k[r][j]);
+                db[j] = mul2(total, am[r][j]);
+                if (post)
+                    db[j] = fma2(mul2(y[j], both(rq)), both(-mean), mul2(db[j], both(rq)));
             }
-            if (a.dresidual.p)
-                store_run<ST, RING>(a.dresidual, row, c[r], dr, 0xffffffffu, 32);
-            if (a.dbranch.p) store_run<DT, RING>(a.dbranch, row, c[r], db, 0xffffffffu, 32);
+            const int q = r * blockDim.x + threadIdx.x;
+            float v[kRun];
+            if (ALL || a.dresidual.p) {
+                from_pairs(dr, v);
+                if (!RING)
+                    store_run<ST, false>(a.dresidual, row, q * kRun, v, 0xffffffffu, 32);
+                else if (q < runs && fa_in_bounds(q * kRun, kRun, cols))
+                    store_n<ST, kRun>(to_residual + r * blockDim.x * kRun, v);
+            }
+            if (ALL || a.dbranch.p) {
+                from_pairs(db, v);
+                if (!RING)
+                    store_run<DT, false>(a.dbranch, row, q * kRun, v, 0xffffffffu, 32);
+                else if (q < runs && fa_in_bounds(q * kRun, kRun, cols))
+                    store_n<DT, kRun>(to_branch + r * blockDim.x * kRun, v);
+            }
         }
+    }
+    if (RING && failed) {  // the same in every thread
+        if (threadIdx.x == 0) {
+            atomicExch(&g_join_gradient_error, 1);
+            // the copies that are still on their way to this CTA's memory
+            for (int i = 0; i < a.stages; ++i) row_wait(bars + i, i < stage ? parity ^ 1 : parity);
+        }
+        return;
     }
     if (branch && (a.dpost_weight || a.dgate)) flush();
     if (a.dpre_weight) {
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r) {
+            const int c = (r * blockDim.x + threadIdx.x) * kRun, valid = valid_cols(c, cols);
+            float v[kRun];
+            from_pairs(sum_p[r], v);
 #pragma unroll
             for (int j = 0; j < kRun; ++j)
-                if (j < valid[r]) sums[kPre * a.plan.pitch + c[r] + j] = sum_p[r][j];
+                if (j < valid) sums[kPre * a.plan.pitch + c + j] = v[j];
+        }
     }
 }
 
@@ -494,11 +584,11 @@ __global__ void __launch_bounds__(kMaxThreads) join_gradient_wide_kernel(JoinGra
                 sums[kPre * a.plan.pitch + q * kRun + j] = sum_p[q * kRun + j];
 }
 
-// Joins the CTAs' sums in order.  A block takes 32 columns of one result, eight runs of CTAs
+// Joins the CTAs' sums in order.  A block takes 32 columns of one result, 16 runs of CTAs
 // side by side.  blockIdx.y: the first weight, the second, then the gate's groups, or (where
 // there are more groups than CTAs) the border before each CTA, whose group it joins if it is
 // the group's first border.
-constexpr int kJoinSlices = 8;
+constexpr int kJoinSlices = 16;
 template <int DT>
 __global__ void __launch_bounds__(32 * kJoinSlices) join_sums_kernel(JoinGradArgs a) {
     __shared__ float part[kJoinSlices][32];
@@ -524,6 +614,7 @@ __global__ void __launch_bounds__(32 * kJoinSlices) join_sums_kernel(JoinGradArg
     float s = 0.f;
     if (col < a.j.cols) {
         // a group's first CTA began it: its part is the tail
+#pragma unroll 8
         for (int64_t c = c0 + threadIdx.y; c <= c1; c += kJoinSlices) {
             const int row = what == kHead && c == c0 ? kTail : what;
             const int64_t at = (c * p.parts + row) * p.pitch + col;
@@ -554,11 +645,20 @@ template <int DT, int ST, int R>
 cudaError_t launch_gradient_rows(const JoinGradArgs &a, bool vec, int threads,
                                  cudaStream_t stream) {
     JoinGradArgs args = a;
-    args.stages = Ring<DT, ST, R>::stages(threads);
-    if (vec && args.stages >= 2)
-        return launch_rows(join_gradient_kernel<DT, ST, R, true>, args, threads,
-                           args.stages * Ring<DT, ST, R>::bytes(threads), stream);
-    return launch_rows(join_gradient_kernel<DT, ST, R, false>, args, threads, 0, stream);
+    const int weights = 4 * R * threads * static_cast<int>(sizeof(float4));
+    const int row_bytes = Ring<DT, ST, R>::bytes(threads);
+    args.stages = Ring<DT, ST, R>::stages(threads, join_ctas_per_sm({threads, R}, row_bytes), weights);
+    if (vec && args.stages >= 2) {
+        const size_t smem = weights + args.stages * row_bytes;
+        const bool all = a.j.post_norm && a.dnormed.p && a.dout.p && a.dresidual.p && a.dbranch.p;
+        auto *kernel = !all         ? join_gradient_kernel<DT, ST, R, true, false, true>
+                       : a.j.dropped ? join_gradient_kernel<DT, ST, R, true, true, true>
+                                     : join_gradient_kernel<DT, ST, R, true, true, false>;
+        return launch_rows(kernel, args, threads, smem, stream);
+    }
+    args.stages = 0;
+    return launch_rows(join_gradient_kernel<DT, ST, R, false, false, true>, args, threads, weights,
+                       stream);
 }
 
 template <int DT, int ST>
@@ -581,6 +681,13 @@ cudaError_t launch_gradient(const JoinGradArgs &a, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>((a.j.cols + 31) / 32),
                     static_cast<unsigned>(2 + groups));
     return launch_dependent(join_sums_kernel<DT>, grid, dim3(32, kJoinSlices), 0, stream, a);
+}
+
+cudaError_t read_row_error(int *flag, bool clear) {
+    const cudaError_t e = cudaMemcpyFromSymbol(flag, g_join_gradient_error, sizeof(int));
+    if (e != cudaSuccess || !clear) return e;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_join_gradient_error, &zero, sizeof(int));
 }
 
 }  // namespace

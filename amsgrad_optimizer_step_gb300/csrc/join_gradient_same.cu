@@ -5,23 +5,26 @@ namespace fa {
 
 FA_BOUNDS_VIOLATIONS(join_gradient_bounds_violations, g_join_gradient_oob)
 
+cudaError_t join_gradient_error(int *flag, bool clear) { return read_row_error(flag, clear); }
+
 JoinShape join_shape(int64_t cols) {
-    const int64_t runs = (cols + kRun - 1) / kRun;
-    const int r = runs <= kMaxThreads ? 1 : 2;
-    const int64_t threads = ((runs + r - 1) / r + 31) / 32 * 32;
-    if (threads > kMaxThreads) return {kMaxThreads, 0};
-    return {static_cast<int>(threads), r};
+    const int runs = static_cast<int>((cols + kRun - 1) / kRun);
+    if (runs <= kJoinThreads) return {(runs + 31) / 32 * 32, 1};
+    if (runs <= 2 * kMaxThreads) return {(runs + 63) / 64 * 32, 2};
+    return {kMaxThreads, 0};
 }
 
-JoinPlan join_plan(int64_t rows, int64_t cols, int64_t groups) {
+JoinPlan join_plan(int64_t rows, int64_t cols, int64_t groups, int element_bytes) {
     JoinPlan p{0, 0, 0, 0, 0};
     if (rows == 0 || cols == 0) return p;
-    const int64_t ctas = kSms * (kMaxThreads / join_shape(cols).threads);
+    const JoinShape shape = join_shape(cols);
+    const int reach = kRun * shape.threads * (shape.runs ? shape.runs : 1);
+    const int64_t ctas = kSms * join_ctas_per_sm(shape, reach * element_bytes);
     p.chunk = (rows + ctas - 1) / ctas;
     p.ctas = (rows + p.chunk - 1) / p.chunk;
     p.pitch = (cols + kRun - 1) / kRun * kRun;
     p.parts = groups > 0 ? 4 : 2;
-    p.bytes = p.ctas * p.parts * p.pitch * 4;
+    p.bytes = (ctas < rows ? ctas : rows) * p.parts * p.pitch * 4;
     return p;
 }
 

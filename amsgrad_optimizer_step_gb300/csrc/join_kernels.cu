@@ -1,8 +1,13 @@
 // The join of a block's output to the residual stream, with the norms behind and before it.
 //
-// A row belongs to one CTA (several short rows to one, a warp each); thread i holds the runs of
-// eight columns i, i + threads, ... of it in registers, so the stream is read once and both
-// norms' sums are taken from what is there.
+// A row belongs to a team of warps.  The work is bound by issue slots before it is by memory (a
+// row a CTA and a run of eight columns a lane took 684 instructions a warp's run, 90 us for 16384 x
+// 2048 BF16 of which the memory needs 40), so what is done once a row is spread over several
+// runs a lane, the arithmetic is in packed pairs, and the weights lie widened and multiplied
+// together in shared memory for all rows of a CTA.  A lane's runs of the next row are on their
+// way to shared memory, to slots that nobody else reads, while it works on those of this one; the
+// stream as it is stored waits there for the second norm.  The loops over a lane's runs are
+// rolled: unrolled over eight of them, the code no longer fitted the instruction caches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -16,156 +21,371 @@ FA_BOUNDS_COUNTER(g_join_oob)
 namespace fa {
 namespace {
 
-constexpr int kRowWarps = 4;       // short rows to a CTA
+constexpr int kTeamThreads = 1024;  // of a CTA and an SM at most, in 64 registers each
+constexpr int kMaxWarps = 32;
+constexpr int kMostShared = 220 * 1024;
 constexpr float kHuge = 0x1p-70f;  // rows whose squares pass FP32 are summed at this scale
 
-// The sum over a row's threads (blockDim.x of them), in every one.  ``part``: one float per
-// warp, not in use by the call before.
-__device__ __forceinline__ float row_sum(float x, float *part) {
+// The sum over a team's lanes, in every one.  ``part``: four floats for each four warps, not in
+// use by the call before.
+__device__ __forceinline__ float team_sum(float x, float *part) {
     x = warp_sum(x);
     if (blockDim.x == 32) return x;
+    const unsigned warps = blockDim.x / 32;
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = x;
-    __syncthreads();
+    team_sync();
     float s = 0.f;
-    for (unsigned w = 0; w < blockDim.x / 32; ++w) s += part[w];
+    for (unsigned w = 0; w < warps; w += 4) {  // (what no warp wrote is 0)
+        const float4 v = *reinterpret_cast<const float4 *>(part + w);
+        s += (v.x + v.y) + (v.z + v.w);
+    }
     return s;
 }
 
-__device__ __forceinline__ float inverse_root(float sum, float cols, float eps) {
-    return __frsqrt_rn(__fdiv_rn(sum, cols) + eps);
+// 1 / sqrt(mean) within two units in the last place.
+__device__ __forceinline__ float inverse_root(float mean) {
+    const float y = rsqrtf(mean);
+    const float e = fmaf(-mean * y, y, 1.f);
+    return mean < INFINITY ? fmaf(0.5f * y, e, y) : y;
 }
 
-// 1 / sqrt(mean square + eps) of the row that the threads hold.
-template <int R>
-__device__ __forceinline__ float row_rstd(const float (*x)[kRun], float cols, float eps,
-                                          float *part, float *part_again) {
-    float s = 0.f;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int j = 0; j < kRun; ++j) s = fmaf(x[r][j], x[r][j], s);
-    s = row_sum(s, part);
-    if (s < INFINITY) return inverse_root(s, cols, eps);
-    // squares past FP32 (or an infinity or NaN, which stays one); eps does not matter to them
-    s = 0.f;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int j = 0; j < kRun; ++j) {
-            const float y = x[r][j] * kHuge;
-            s = fmaf(y, y, s);
-        }
-    return inverse_root(row_sum(s, part_again), cols, 0.f) * kHuge;
+__device__ __forceinline__ float sum_of_pairs(uint64_t a, uint64_t b) {
+    float x, y;
+    unpair(add2(a, b), x, y);
+    return x + y;
 }
 
-template <int DT, int ST, int R, bool ALIGNED>
-__global__ void __launch_bounds__(R == 1 ? 256 : kMaxThreads) join_kernel(JoinArgs a) {
-    __shared__ float part[4][kMaxThreads / 32];
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    if (row >= a.rows) return;  // a whole warp: rows share no barrier
-    const float cols = static_cast<float>(a.cols);
-    int64_t c[R];
-    int valid[R];
-    Raw<DT, kRun> ry[R];
-    Raw<ST, kRun> rr[R];
+__device__ __forceinline__ void add_squares(const uint64_t *p, uint64_t *s) {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) s[j % 2] = fma2(p[j], p[j], s[j % 2]);
+}
+
+// 1 / sqrt(mean square + eps) of the row that a team holds, R runs a lane.
+template <int DT, int R>
+__device__ __forceinline__ float team_rstd(const Raw<DT, kRun> *x, float inv_cols, float eps,
+                                           float *part) {
+    uint64_t s[2] = {}, p[kPairs];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        c[r] = (static_cast<int64_t>(r) * blockDim.x + threadIdx.x) * kRun;
-        valid[r] = valid_cols(c[r], a.cols);
-        if (a.branch.p) ry[r] = load_run<DT, ALIGNED>(a.branch, row, c[r]);
+        widen_pairs<DT>(x[r], p);
+        add_squares(p, s);
     }
+    float sum = team_sum(sum_of_pairs(s[0], s[1]), part);
+    if (sum < INFINITY) return inverse_root(fmaf(sum, inv_cols, eps));
+    // squares past FP32 (or an infinity or NaN, which stays one); eps does not matter to them
+    s[0] = s[1] = 0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) rr[r] = load_run<ST, ALIGNED>(a.residual, row, c[r]);
-    float y[R][kRun], x[R][kRun];
-    if (a.branch.p) {
+    for (int r = 0; r < R; ++r) {
+        widen_pairs<DT>(x[r], p);
 #pragma unroll
-        for (int r = 0; r < R; ++r) ry[r].widen(y[r]);
+        for (int j = 0; j < kPairs; ++j) p[j] = mul2(p[j], both(kHuge));
+        add_squares(p, s);
+    }
+    sum = team_sum(sum_of_pairs(s[0], s[1]), part + 4 * kMaxWarps);
+    return inverse_root(sum * inv_cols) * kHuge;
+}
+
+// Two sums' places in turn: one is written again only after a wait for those who read it.
+struct Parts {
+    float at[2][2 * 4 * kMaxWarps];
+};
+__device__ __forceinline__ void clear_parts(Parts &parts, int thread, int threads) {
+    for (int i = thread; i < 2 * 2 * 4 * kMaxWarps; i += threads) parts.at[0][i] = 0.f;
+}
+
+// out and the branch's share of it, of one run: p = alpha * p + f.
+__device__ __forceinline__ void join_pairs(uint64_t alpha, uint64_t *p, const uint64_t *f) {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) p[j] = fma2(alpha, p[j], f[j]);
+}
+
+// Many rows.  blockDim: the lanes of a team, the teams; R runs a lane.  VEC: rows of whole, aligned
+// runs (else they are read from any address).  RING: the runs of the team's next row are asked for
+// while it works on this one.  DROP: false where nothing is dropped.
+template <int DT, int ST, int R, bool VEC, bool RING, bool DROP>
+__global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool stage) {
+    constexpr int kD = Raw<DT, kRun>::kWords, kS = Raw<ST, kRun>::kWords;
+    extern __shared__ float4 staged[];
+    __shared__ Parts parts;
+    const int cols = static_cast<int>(a.cols), runs = (cols + kRun - 1) / kRun;
+    const float inv_cols = 1.f / static_cast<float>(cols);
+    const int q0 = threadIdx.x, lanes = blockDim.x;  // this lane's runs: q0, q0 + lanes, ...
+    const int threads = blockDim.x * blockDim.y, thread = threadIdx.y * lanes + q0;
+    const bool branch = a.branch.p, dropped = DROP && a.dropped;
+    const bool own_gate = a.gate && (!stage || a.group_rows < a.rows);  // read row by row
+    // the weights, as two planes of four columns of each run: the scale of the branch with its
+    // norm's weight and a gate that all rows share, and the second norm's weight
+    float4 *const plane_post = staged, *const plane_pre = staged + 2 * runs;
+    const float scale = dropped ? a.drop.scale * a.branch_scale : a.branch_scale;
+    for (int q = thread; stage && q < runs; q += threads) {
+        const int valid = valid_cols(q * kRun, cols);
+        float w[kRun], g[kRun];
+        load_weights<DT>(a, a.post_norm ? a.post_weight : nullptr, q * kRun, valid,
+                         a.weight_offset, w);
+        load_weights<DT>(a, own_gate ? nullptr : a.gate, q * kRun, valid, 0.f, g);
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) w[j] *= scale * g[j];
+        plane_post[q] = make_float4(w[0], w[1], w[2], w[3]);
+        plane_post[q + runs] = make_float4(w[4], w[5], w[6], w[7]);
+        load_weights<DT>(a, a.pre_weight, q * kRun, valid, a.weight_offset, w);
+        plane_pre[q] = make_float4(w[0], w[1], w[2], w[3]);
+        plane_pre[q + runs] = make_float4(w[4], w[5], w[6], w[7]);
+    }
+    clear_parts(parts, thread, threads);
+    // a lane's slots: the branch's and the stream's runs, of two rows; those of no run stay 0
+    uint4 *const ring = reinterpret_cast<uint4 *>(staged + (stage ? 4 * runs : 0)) + thread;
+    const int run_stride = (kD + kS) * threads;
+    if (RING)
+        for (int k = 0; k < 2 * R * (kD + kS); ++k)
+            ring[k * threads] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    const auto weights = [&](const float4 *plane, int q, uint64_t *w) {
+        if (stage) {
+            if (q >= runs) q = 0;  // not used
+            const float4 lo = plane[q], hi = plane[q + runs];
+            w[0] = pair(lo.x, lo.y);
+            w[1] = pair(lo.z, lo.w);
+            w[2] = pair(hi.x, hi.y);
+            w[3] = pair(hi.z, hi.w);
+        } else {
+            const bool post = plane == plane_post;
+            float x[kRun];
+            load_weights<DT>(a, !post ? a.pre_weight : a.post_norm ? a.post_weight : nullptr,
+                             q * kRun, valid_cols(q * kRun, cols), a.weight_offset, x);
+            to_pairs(x, w);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j)
+                if (post) w[j] = mul2(w[j], both(scale));
+        }
+    };
+    const auto ask = [&](int64_t row, int slot) {
+        if (row < a.rows) {
+            uint4 *at = ring + slot * R * run_stride;
+#pragma unroll
+            for (int r = 0; r < R; ++r, at += run_stride) {
+                const int q = q0 + r * lanes;
+                if (q >= runs || !fa_in_bounds(q * kRun, kRun, cols)) continue;
+                if (branch) ask_run<DT>(a.branch, row, q, at, threads);
+                ask_run<ST>(a.residual, row, q, at + kD * threads, threads);
+            }
+        }
+        copy_async_commit();
+    };
+    const uint64_t call = dropped ? drop_call(a.drop) : 0;
+    const uint64_t alpha = both(a.residual_scale);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int team_part = threadIdx.y * ((lanes / 32 + 3) / 4 * 4);
+    int turn = 0, slot = 0;  // of the sums' places; of this row
+    if (RING) ask(row, slot);
+    for (; row < a.rows; row += step) {
+        Raw<DT, kRun> y[R];
+        Raw<ST, kRun> x[R];
+        if (RING) {
+            ask(row + step, slot ^ 1);  // that slot was read a row ago
+            copy_async_wait<1>();
+            const uint4 *at = ring + slot * R * run_stride;
+            slot ^= 1;
+#pragma unroll
+            for (int r = 0; r < R; ++r, at += run_stride) {
+                take_run(at, threads, y[r]);
+                take_run(at + kD * threads, threads, x[r]);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                zero(y[r]);
+                if (branch) y[r] = read_run<DT, VEC>(a.branch, row, q0 + r * lanes, runs);
+                x[r] = read_run<ST, VEC>(a.residual, row, q0 + r * lanes, runs);
+            }
+        }
         float rstd = 1.f;
         if (a.post_norm) {
-            rstd = row_rstd<R>(y, cols, a.eps, part[0], part[1]);
-            if (a.post_rstd && threadIdx.x == 0) a.post_rstd[row] = rstd;
+            rstd = team_rstd<DT, R>(y, inv_cols, a.eps, parts.at[turn] + team_part);
+            turn ^= 1;
+            if (a.post_rstd && q0 == 0) a.post_rstd[row] = rstd;
         }
-        const int64_t group = a.gate ? a.by_group.quotient(static_cast<uint32_t>(row)) : 0;
-        const uint64_t call = a.dropped ? drop_call(a.drop) : 0;
-        const float scale = a.dropped ? a.drop.scale * a.branch_scale : a.branch_scale;
-        const int64_t blocks = (a.cols + kRun - 1) / kRun;
+        const uint64_t root = both(rstd);
+        const int64_t group = own_gate ? a.by_group.quotient(static_cast<uint32_t>(row)) : 0;
+        uint64_t block = static_cast<uint64_t>(row) * runs + q0;
+#pragma unroll
+        for (int r = 0; r < R; ++r, block += lanes) {
+            const int q = q0 + r * lanes;
+            uint64_t p[kPairs];
+            widen_pairs<ST>(x[r], p);
+            if (branch) {
+                uint64_t f[kPairs], w[kPairs];
+                widen_pairs<DT>(y[r], f);
+                weights(plane_post, q, w);
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) f[j] = mul2(mul2(f[j], root), w[j]);
+                if (own_gate) {
+                    float g[kRun];
+                    load_weights<DT>(a, a.gate, group * a.gate_ld + q * kRun,
+                                     valid_cols(q * kRun, cols), 0.f, g);
+                    to_pairs(g, w);
+#pragma unroll
+                    for (int j = 0; j < kPairs; ++j) f[j] = mul2(f[j], w[j]);
+                }
+                if (dropped) {
+                    Kept kept;
+                    kept.draw(a.drop, block, call);
+                    kept.mask(f, a.drop.threshold);
+                }
+                join_pairs(alpha, p, f);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) p[j] = mul2(alpha, p[j]);
+            }
+            float v[kRun];
+            from_pairs(p, v);
+            x[r].from(v);  // as it is stored
+            if (VEC) {
+                if (a.out.p && q < runs) store_raw<ST>(a.out, row, q * kRun, x[r]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kRun; ++j)  // what is not there adds nothing to the sum
+                    if (q * kRun + j >= cols) v[j] = 0.f;
+                x[r].from(v);
+                if (a.out.p) store_run<ST, false>(a.out, row, q * kRun, v, 0xffffffffu, 32);
+            }
+            if (VEC && q >= runs) zero(x[r]);
+        }
+        if (!a.normed.p) continue;
+        // the norm is that of the stored values
+        rstd = team_rstd<ST, R>(x, inv_cols, a.eps, parts.at[turn] + team_part);
+        turn ^= 1;
+        if (a.pre_rstd && q0 == 0) a.pre_rstd[row] = rstd;
+        const uint64_t root_pre = both(rstd);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float w[kRun];
-            if (a.post_norm) {
-                load_weights<DT>(a, a.post_weight, c[r], valid[r],
-                                          a.weight_offset, w);
+            const int q = q0 + r * lanes;
+            uint64_t p[kPairs], w[kPairs];
+            widen_pairs<ST>(x[r], p);
+            weights(plane_pre, q, w);
 #pragma unroll
-                for (int j = 0; j < kRun; ++j) y[r][j] *= rstd * w[j];
+            for (int j = 0; j < kPairs; ++j) p[j] = mul2(mul2(p[j], root_pre), w[j]);
+            float v[kRun];
+            from_pairs(p, v);
+            if (VEC) {
+                Raw<DT, kRun> n;
+                n.from(v);
+                if (q < runs) store_raw<DT>(a.normed, row, q * kRun, n);
+            } else {
+                store_run<DT, false>(a.normed, row, q * kRun, v, 0xffffffffu, 32);
             }
-            if (a.gate) {
-                load_weights<DT>(a, a.gate, group * a.gate_ld + c[r],
-                                          valid[r], 0.f, w);
-#pragma unroll
-                for (int j = 0; j < kRun; ++j) y[r][j] *= w[j];
-            }
-            if (a.dropped) {
-                Kept kept;
-                kept.draw(a.drop, row * blocks + c[r] / kRun, call);
-#pragma unroll
-                for (int j = 0; j < kRun; ++j)
-                    if (!kept(j, a.drop.threshold)) y[r][j] = 0.f;
-            }
-            rr[r].widen(x[r]);
-#pragma unroll
-            for (int j = 0; j < kRun; ++j)
-                x[r][j] = fmaf(a.residual_scale, x[r][j], scale * y[r][j]);
         }
+    }
+}
+
+// Few rows: a row a CTA and a run a lane, the shortest way through a row.
+template <int DT, int ST>
+__global__ void __launch_bounds__(32 * kMaxWarps) join_few_kernel(JoinArgs a, bool vec) {
+    __shared__ Parts parts;
+    const int cols = static_cast<int>(a.cols), runs = (cols + kRun - 1) / kRun;
+    const float inv_cols = 1.f / static_cast<float>(cols);
+    const float scale = a.dropped ? a.drop.scale * a.branch_scale : a.branch_scale;
+    const int64_t row = blockIdx.x;
+    const int q = threadIdx.x, c = q * kRun, valid = valid_cols(c, cols);
+    Raw<DT, kRun> y;
+    zero(y);
+    if (a.branch.p)
+        y = vec ? read_run<DT, true>(a.branch, row, q, runs)
+                : read_run<DT, false>(a.branch, row, q, runs);
+    const Raw<ST, kRun> x = vec ? read_run<ST, true>(a.residual, row, q, runs)
+                                : read_run<ST, false>(a.residual, row, q, runs);
+    const int64_t group = a.gate ? a.by_group.quotient(static_cast<uint32_t>(row)) : 0;
+    float w[kRun], g[kRun], w_pre[kRun];
+    load_weights<DT>(a, a.post_norm ? a.post_weight : nullptr, c, valid, a.weight_offset, w);
+    load_weights<DT>(a, a.gate, group * a.gate_ld + c, valid, 0.f, g);
+    load_weights<DT>(a, a.pre_weight, c, valid, a.weight_offset, w_pre);
+    clear_parts(parts, threadIdx.x, blockDim.x);
+    __syncthreads();
+    uint64_t p[kPairs], f[kPairs];
+    float rstd = 1.f;
+    widen_pairs<DT>(y, f);
+    if (a.post_norm) {
+        rstd = team_rstd<DT, 1>(&y, inv_cols, a.eps, parts.at[0]);
+        if (a.post_rstd && q == 0) a.post_rstd[row] = rstd;
+    }
+    widen_pairs<ST>(x, p);
+    if (a.branch.p) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j)
+            f[j] = mul2(mul2(f[j], both(rstd)), pair(w[2 * j] * (scale * g[2 * j]),
+                                                     w[2 * j + 1] * (scale * g[2 * j + 1])));
+        if (a.dropped) {
+            Kept kept;
+            kept.draw(a.drop, static_cast<uint64_t>(row) * runs + q, drop_call(a.drop));
+            kept.mask(f, a.drop.threshold);
+        }
+        join_pairs(both(a.residual_scale), p, f);
     } else {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            rr[r].widen(x[r]);
+        for (int j = 0; j < kPairs; ++j) p[j] = mul2(both(a.residual_scale), p[j]);
+    }
+    float v[kRun];
+    from_pairs(p, v);
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) x[r][j] *= a.residual_scale;
+    for (int j = 0; j < kRun; ++j)
+        if (j >= valid) v[j] = 0.f;
+    const auto store = [&](const MatrixArgs &m, auto type) {
+        if (vec)
+            store_run<decltype(type)::value, true>(m, row, c, v, 0xffffffffu, 32);
+        else
+            store_run<decltype(type)::value, false>(m, row, c, v, 0xffffffffu, 32);
+    };
+    if (a.out.p) store(a.out, std::integral_constant<int, ST>{});
+    if (!a.normed.p) return;
+    Raw<ST, kRun> stored;
+    stored.from(v);
+    widen_pairs<ST>(stored, p);
+    rstd = team_rstd<ST, 1>(&stored, inv_cols, a.eps, parts.at[1]);
+    if (a.pre_rstd && q == 0) a.pre_rstd[row] = rstd;
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j)
+        p[j] = mul2(mul2(p[j], both(rstd)), pair(w_pre[2 * j], w_pre[2 * j + 1]));
+    from_pairs(p, v);
+    store(a.normed, std::integral_constant<int, DT>{});
+}
+
+template <int DT, int ST, int R, bool VEC, bool RING, bool DROP>
+cudaError_t launch_as(const JoinArgs &a, dim3 block, size_t smem, bool stage,
+                      cudaStream_t stream) {
+    auto *kernel = join_kernel<DT, ST, R, VEC, RING, DROP>;
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    int64_t grid = (a.rows + block.y - 1) / block.y;
+    if (grid > kSms) grid = kSms;  // the SMs are full, and the weights are staged once
+    kernel<<<static_cast<unsigned>(grid), block, smem, stream>>>(a, stage);
+    return cudaGetLastError();
+}
+
+template <int DT, int ST, int R, bool VEC>
+cudaError_t launch_many(const JoinArgs &a, cudaStream_t stream) {
+    const int runs = static_cast<int>((a.cols + kRun - 1) / kRun);
+    const int warps = (runs + 32 * R - 1) / (32 * R), teams = kTeamThreads / 32 / warps;
+    const int weights = 4 * static_cast<int>(sizeof(float4)) * runs;
+    const bool stage = weights <= kMostShared;
+    const dim3 block(32 * warps, warps > 1 && teams > 16 ? 16 : teams);  // 16: a barrier each
+    if constexpr (VEC && ST != FA_F32) {
+        // The ring, where it has room for three quarters of the teams.  16384 x 2048 BF16 took 57 us
+        // with it and 63 without.  Runs of FP32 are two vectors 32 bytes apart, which the copies
+        // to shared memory fetch as half sectors: 10922 x 2048 of BF16 and FP32 took 65 and 53.
+        const int team = 2 * 16 * R * 32 * warps *
+                         (Raw<DT, kRun>::kWords + Raw<ST, kRun>::kWords);
+        int room = (kMostShared - weights) / team;
+        if (room > static_cast<int>(block.y)) room = block.y;
+        if (4 * room >= 3 * static_cast<int>(block.y)) {
+            const dim3 fewer(block.x, room);
+            const size_t smem = weights + static_cast<size_t>(team) * room;
+            return a.dropped
+                       ? launch_as<DT, ST, R, true, true, true>(a, fewer, smem, true, stream)
+                       : launch_as<DT, ST, R, true, true, false>(a, fewer, smem, true, stream);
         }
     }
-    if (a.out.p) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            store_run<ST, ALIGNED>(a.out, row, c[r], x[r], 0xffffffffu, 32);
-    }
-    if (!a.normed.p) return;
-    // the norm is that of the stored values
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        rr[r].from(x[r]);
-        rr[r].widen(x[r]);
-    }
-    const float rstd = row_rstd<R>(x, cols, a.eps, part[2], part[3]);
-    if (a.pre_rstd && threadIdx.x == 0) a.pre_rstd[row] = rstd;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        float w[kRun];
-        load_weights<DT>(a, a.pre_weight, c[r], valid[r], a.weight_offset,
-                                  w);
-#pragma unroll
-        for (int j = 0; j < kRun; ++j) x[r][j] *= rstd * w[j];
-        store_run<DT, ALIGNED>(a.normed, row, c[r], x[r], 0xffffffffu, 32);
-    }
-}
-
-// Threads of a row and runs of a thread.
-struct Shape {
-    int threads, runs;
-};
-Shape forward_shape(int64_t cols) {
-    const int64_t runs = (cols + kRun - 1) / kRun;
-    const int r = runs <= 256 ? 1 : runs <= 1024 ? 2 : 4;
-    return {static_cast<int>(((runs + r - 1) / r + 31) / 32 * 32), r};
-}
-
-template <typename F>
-cudaError_t for_runs(int runs, F f) {
-    switch (runs) {
-        case 1: return f(std::integral_constant<int, 1>{});
-        case 2: return f(std::integral_constant<int, 2>{});
-        default: return f(std::integral_constant<int, 4>{});
-    }
+    return launch_as<DT, ST, R, VEC, false, true>(a, block, stage ? weights : 0, stage, stream);
 }
 
 }  // namespace
@@ -173,18 +393,23 @@ cudaError_t for_runs(int runs, F f) {
 FA_BOUNDS_VIOLATIONS(join_bounds_violations, g_join_oob)
 
 cudaError_t launch_block_join(const JoinArgs &a, fa_dtype dt, fa_dtype st, cudaStream_t stream) {
-    const Shape shape = forward_shape(a.cols);
-    const dim3 block(shape.threads, shape.threads == 32 ? kRowWarps : 1);
-    const unsigned grid = static_cast<unsigned>((a.rows + block.y - 1) / block.y);
-    const bool vec = aligned_rows(a.branch, dt) && aligned_rows(a.residual, st) &&
-                     aligned_rows(a.out, st) && aligned_rows(a.normed, dt);
+    const bool vec = a.cols % kRun == 0 && aligned_rows(a.branch, dt) &&
+                     aligned_rows(a.residual, st) && aligned_rows(a.out, st) &&
+                     aligned_rows(a.normed, dt);
+    // few rows: fewer than four warps an SM with a run a lane
+    const int64_t warps = ((a.cols + kRun - 1) / kRun + 31) / 32;
     return for_stream_dtype(dt, st, [&](auto d, auto s) {
-        return for_runs(shape.runs, [&](auto r) {
-            auto *kernel = vec ? join_kernel<d(), s(), r(), true>
-                               : join_kernel<d(), s(), r(), false>;
-            kernel<<<grid, block, 0, stream>>>(a);
+        if (warps <= kMaxWarps && a.rows * warps < 4 * kSms) {
+            join_few_kernel<d(), s()><<<static_cast<unsigned>(a.rows),
+                                        static_cast<unsigned>(32 * warps), 0, stream>>>(a, vec);
             return cudaGetLastError();
-        });
+        }
+        // two runs a lane are what 64 registers hold of the work on them
+        if (warps == 1)
+            return vec ? launch_many<d(), s(), 1, true>(a, stream)
+                       : launch_many<d(), s(), 1, false>(a, stream);
+        return vec ? launch_many<d(), s(), 2, true>(a, stream)
+                   : launch_many<d(), s(), 2, false>(a, stream);
     });
 }
 

@@ -156,7 +156,8 @@ const char *fa_status_string(fa_status status);
  * wait in that pipeline is bounded (about a second), and a wait that gives up
  * sets a device flag, drains its own copies and ends the kernel early (its
  * outputs are then incomplete: discard them, as [FA-ja] "低レベルの使用" asks of
- * any device failure).  This reads the flag of the current device into *flag
+ * any device failure).  So does the gradient of a block's join (fa_block_ops.h) with its
+ * rows.  This reads the flag of the current device into *flag
  * (0 = no wait ever gave up) and clears it when clear != 0.  Waits for the
  * device; FA_ERR_CUDA if it cannot be read.  The pipeline is this library's;
  * the pages have no counterpart. */

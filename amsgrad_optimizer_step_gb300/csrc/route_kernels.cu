@@ -1,12 +1,18 @@
 // The router of gated experts: choice, weights, counts and the balance loss of tokens from
 // their logits, and the logits' gradient.
 //
-// A token's row belongs to a group of 1 to 32 lanes, eight experts a lane (up to 256 experts;
-// 16 or 32 beyond), in registers.  The choice takes the largest key top_k times: keys are
-// integers in the logits' order, and for 16-bit types carry the expert's number below them, so
-// that one maximum over the group gives both the logit and the expert, ties to the lower number.
-// The first key is the row's maximum, which the softmax is taken from.  Sums over tokens stay
-// with the lane that holds the expert, then go by CTA and in order.
+// A token's row belongs to a group of 1 to 32 lanes, up to 16 experts a lane (32 beyond 512), in
+// registers.  Up to eight experts are chosen from lists: every lane sorts its keys once, keeping
+// eight, and a choice is the maximum of the lists' heads, whose lane moves on to its next.  Keys are
+// integers in the logits' order with the expert's number in their low bits, so that one maximum
+// gives the expert, ties to the lower number: those of 16-bit logits hold the whole logit, those
+// of FP32 its upper bits, and where two of the keys that matter agree in these (one token in some
+// hundred) the warp chooses again by whole logits, an expert at a time, which is also how more
+// than eight are chosen.  Sums over tokens stay with the lane that holds the expert, then go by
+// CTA and in order.
+//
+// Instructions bound it, not memory: 65536 tokens, 8 of 128 experts, BF16, took 51 us with a
+// maximum over all keys for every choice, of which the bytes need 3.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -22,68 +28,24 @@ namespace fa {
 namespace {
 
 constexpr int kRouteThreads = 256;
+constexpr int kRouteCtas = 3;  // on an SM: what 80 registers a thread allow
 constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kGradThreads = 256;
+constexpr int kListed = 8;  // keys of a lane's list, and experts chosen from lists at most
+constexpr float kLog2E = 1.4426950408889634f;
 
 // Keys in the order of the logits: larger logits have larger keys, -0 and 0 the same one, and
-// every NaN the largest.  0 is below every key.
-template <int DT>
-struct Key;
-
-template <>
-struct Key<FA_F32> {
-    static constexpr bool kNumbered = false;
-    static __device__ __forceinline__ uint32_t of(float x, int) {
-        const uint32_t b = __float_as_uint(x + 0.f);  // -0 becomes 0
-        const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
-        return x != x ? 0xffffffffu : k;
-    }
-    static __device__ __forceinline__ float logit(uint32_t k) {
-        return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
-    }
-};
-
-// The upper 16 bits of the widened logit hold a BF16; an FP16 keeps its own bits.
-template <int DT>
-struct Key16 {
-    static constexpr bool kNumbered = true;
-    static __device__ __forceinline__ uint32_t of(float x, int expert) {
-        const typename Elem<DT>::T e = Elem<DT>::round(x + 0.f);  // exact
-        const uint32_t b = *reinterpret_cast<const uint16_t *>(&e);
-        uint32_t k = b & 0x8000u ? ~b & 0xffffu : b | 0x8000u;
-        if (x != x) k = 0xffffu;
-        return k << 16 | (0xffffu - static_cast<uint32_t>(expert));
-    }
-    static __device__ __forceinline__ float logit(uint32_t k) {
-        k >>= 16;
-        const uint16_t b = static_cast<uint16_t>(k & 0x8000u ? k ^ 0x8000u : ~k);
-        return Elem<DT>::widen(*reinterpret_cast<const typename Elem<DT>::T *>(&b));
-    }
-};
-template <>
-struct Key<FA_F16> : Key16<FA_F16> {};
-template <>
-struct Key<FA_BF16> : Key16<FA_BF16> {};
-
-// N experts of a token, as they lie in memory; those past the end are -infinity.
-template <int DT, int N>
-__device__ __forceinline__ void load_logits(const MatrixArgs &m, int64_t row, int c, bool vec,
-                                            float *x) {
-    using T = typename Elem<DT>::T;
-    const T *p = static_cast<const T *>(m.p) + row * m.ld + c;
-    const int left = static_cast<int>(m.cols) - c, valid = left < 0 ? 0 : left < N ? left : N;
-    if (valid && !fa_in_bounds(c, valid, m.cols)) return;
-    if (vec && valid == N) {
-        Raw<DT, N> r;
-        r.load(p);
-        r.widen(x);
-    } else {
-        RawAny<DT, N> r;
-        r.load(p, valid, Span(m.p, ((m.rows - 1) * m.ld + m.cols) * sizeof(T)));
-        r.widen(x);
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-        if (j >= valid) x[j] = -INFINITY;
+// every NaN the largest (an addition's NaN is 0x7fffffff, whatever went in).
+__device__ __forceinline__ uint32_t whole_key(float x) {
+    const uint32_t b = __float_as_uint(__fadd_rn(x, 0.f));  // -0 becomes 0
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+// With the expert's number in the low BITS, ten at most: the widened 16-bit types have 13 or 16
+// zeros there.
+template <int BITS>
+__device__ __forceinline__ uint32_t numbered_key(float x, int expert) {
+    constexpr uint32_t kNumber = (1u << BITS) - 1;
+    return (whole_key(x) & ~kNumber) | (kNumber - static_cast<uint32_t>(expert));
 }
 
 template <int L>
@@ -99,6 +61,82 @@ __device__ __forceinline__ uint32_t group_max(uint32_t x) {
     return x;
 }
 
+__device__ __forceinline__ void order(uint32_t &a, uint32_t &b) {
+    const uint32_t hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+// Eight keys, the largest first (Batcher's odd-even merge network: 19 exchanges).
+__device__ __forceinline__ void sort8(uint32_t *k) {
+    order(k[0], k[1]), order(k[2], k[3]), order(k[4], k[5]), order(k[6], k[7]);
+    order(k[0], k[2]), order(k[1], k[3]), order(k[4], k[6]), order(k[5], k[7]);
+    order(k[1], k[2]), order(k[5], k[6]);
+    order(k[0], k[4]), order(k[1], k[5]), order(k[2], k[6]), order(k[3], k[7]);
+    order(k[2], k[4]), order(k[3], k[5]);
+    order(k[1], k[2]), order(k[3], k[4]), order(k[5], k[6]);
+}
+// The largest eight of two such lists, in a: the larger ones of a and of b backwards rise and
+// fall once, which three steps sort.
+__device__ __forceinline__ void merge8(uint32_t *a, const uint32_t *b) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = max(a[j], b[7 - j]);
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (!(j & d)) order(a[j], a[j + d]);
+}
+
+// A lane's experts: R runs of eight, L runs apart.
+template <int L>
+__device__ __forceinline__ int expert_of(int part, int j) {
+    return ((j / kRun) * L + part) * kRun + j % kRun;
+}
+template <int DT, int L, int R>
+__device__ __forceinline__ void load_logits(const MatrixArgs &m, int64_t row, int part, bool vec,
+                                            float *x) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int c = (r * L + part) * kRun;
+        const Raw<DT, kRun> raw =
+            vec ? load_run<DT, true>(m, row, c) : load_run<DT, false>(m, row, c);
+        raw.widen(x + r * kRun);
+    }
+    if (L * R * kRun == m.cols) return;
+#pragma unroll
+    for (int j = 0; j < R * kRun; ++j)
+        if (expert_of<L>(part, j) >= m.cols) x[j] = -INFINITY;
+}
+
+// Calls take(i, expert) in every lane of a group for the choices i < k, by whole logits.
+template <int L, int N, typename Take>
+__device__ __forceinline__ void choose_whole(const float *x, int part, int experts, int k,
+                                             Take take) {
+    uint32_t gone = 0;  // of this lane's
+    for (int i = 0; i < k; ++i) {
+        uint32_t best = 0;
+        int mine = 0x7fffffff;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int e = expert_of<L>(part, j);
+            const uint32_t key = e < experts && !(gone >> j & 1u) ? whole_key(x[j]) : 0u;
+            if (key > best) {
+                best = key;
+                mine = e;
+            }
+        }
+        const uint32_t top = group_max<L>(best);
+        if (best != top) mine = 0x7fffffff;
+        int e = mine;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) e = min(e, __shfl_xor_sync(0xffffffffu, e, o));
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (expert_of<L>(part, j) == e) gone |= 1u << j;
+        take(i, e);
+    }
+}
+
 // What a CTA leaves of its tokens: per expert the probabilities' sum and the count, then z's sum
 // and the counted tokens.
 struct RouteSums {
@@ -106,6 +144,8 @@ struct RouteSums {
     int32_t *count;  // [ctas][experts]
     float *z;        // [ctas]
     int32_t *tokens;  // [ctas]
+    float *dot;      // of the joining CTAs: sums of counts * mean probability
+    int32_t *joined;  // how many of them are done
 };
 __host__ __device__ inline RouteSums route_sums(void *scratch, int64_t ctas, int64_t experts) {
     RouteSums s;
@@ -113,29 +153,30 @@ __host__ __device__ inline RouteSums route_sums(void *scratch, int64_t ctas, int
     s.count = reinterpret_cast<int32_t *>(s.prob + ctas * experts);
     s.z = reinterpret_cast<float *>(s.count + ctas * experts);
     s.tokens = reinterpret_cast<int32_t *>(s.z + ctas);
+    s.dot = reinterpret_cast<float *>(s.tokens + ctas);
+    s.joined = reinterpret_cast<int32_t *>(s.dot + FA_ROUTE_MAX_EXPERTS / 8);
     return s;
 }
 
-// L lanes a token, N experts a lane.
-template <int DT, int L, int N>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a, bool vec) {
-    constexpr int kTokens = 32 / L;  // of a warp's turn
+// L lanes a token, R runs of eight experts a lane.  LISTED: at most kListed are chosen.
+template <int DT, int L, int R, bool LISTED>
+__global__ void __launch_bounds__(kRouteThreads, R < 4 ? kRouteCtas : 2)
+route_kernel(RouteArgs a, bool vec) {
+    constexpr int kTokens = 32 / L, N = R * kRun;  // tokens of a warp's turn; a lane's experts
+    constexpr int kBits = 31 - __builtin_clz(L * N);
+    constexpr int kItems = ((LISTED ? kListed : FA_ROUTE_MAX_CHOSEN) + L - 1) / L;  // of a lane
     extern __shared__ uint32_t shared[];
-    // a warp's choices before they are written: the experts and their exponentials, then each
-    // token's factor
+    int32_t *const count = reinterpret_cast<int32_t *>(shared);  // the CTA's
     const int k = a.top_k, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int sub = lane / L, part = lane % L;
-    uint32_t *const my = shared + warp * kTokens * (2 * k + 1);
-    int32_t *const expert = reinterpret_cast<int32_t *>(my);
-    float *const weight = reinterpret_cast<float *>(my + kTokens * k);
-    float *const factor = weight + kTokens * k;
-    // then the CTA's counts
-    int32_t *const count = reinterpret_cast<int32_t *>(shared + kRouteWarps * kTokens * (2 * k + 1));
     const int64_t tokens = a.logits.rows;
     const int experts = static_cast<int>(a.logits.cols);
     const bool sums = a.summary != nullptr;
     if (sums) {
         for (int e = threadIdx.x; e < experts; e += kRouteThreads) count[e] = 0;
+        // how many CTAs have joined the sums, for the kernel that does
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            *route_sums(a.scratch, gridDim.x, experts).joined = 0;
         __syncthreads();
     }
     float prob[N] = {}, z = 0.f;
@@ -146,64 +187,86 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a, bool 
         const int64_t t = t0 + sub;
         const bool on = t < tokens && (!a.counted || a.counted[t]);
         float x[N];
-        uint32_t key[N];
         if (on) {
-            load_logits<DT, N>(a.logits, t, part * N, vec, x);
+            load_logits<DT, L, R>(a.logits, t, part, vec, x);
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) x[j] = 0.f;
         }
+        int item[kItems];  // the choices part, part + L, ... of the token
+        const auto take = [&](int i, int e) {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            key[j] = part * N + j < experts ? Key<DT>::of(x[j], part * N + j) : 0u;
-        float top = 0.f, picked = 0.f;
-        for (int i = 0; i < k; ++i) {
-            uint32_t best = key[0];
+            for (int s = 0; s < kItems; ++s)
+                if (i == s * L + part) item[s] = e;
+        };
+        bool again = !LISTED;
+        if (LISTED) {
+            constexpr uint32_t kNumber = (1u << kBits) - 1;
+            uint32_t key[N];
+            // (what is past the last expert is -infinity, and its number is behind all that there are)
 #pragma unroll
-            for (int j = 1; j < N; ++j) best = max(best, key[j]);
-            const uint32_t mine = best;
-            best = group_max<L>(best);
-            int e = 0;
-            if (Key<DT>::kNumbered) {
-                e = static_cast<int>(0xffffu - (best & 0xffffu));
+            for (int j = 0; j < N; ++j) key[j] = numbered_key<kBits>(x[j], expert_of<L>(part, j));
 #pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (key[j] == best) key[j] = 0u;
-            } else {
-                // the first lane that has the key, and its first expert with it
-                const unsigned have = __ballot_sync(0xffffffffu, mine == best);
-                const int winner = __ffs(static_cast<int>(have >> (sub * L))) - 1;
-                bool found = part != winner;
+            for (int r = 0; r < R; ++r) sort8(key + r * kRun);
 #pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (!found && key[j] == best) {
-                        key[j] = 0u;
-                        e = part * N + j;
-                        found = true;
-                    }
-                e = __shfl_sync(0xffffffffu, e, winner, L);
+            for (int r = 1; r < R; ++r) merge8(key, key + r * kRun);
+            uint32_t before = 0xffffffffu;
+            bool same = false;
+#pragma unroll
+            for (int i = 0; i <= kListed; ++i) {
+                // (FP32 asks for one more, which the last choice has to be above)
+                if (i > k || (i == k && (DT != FA_F32 || k == experts))) break;
+                const uint32_t best = group_max<L>(key[0]);
+                if (DT == FA_F32) same |= i > 0 && (best | kNumber) == (before | kNumber);
+                before = best;
+                if (i == k) break;
+                take(i, static_cast<int>(kNumber - (best & kNumber)));
+                if (key[0] == best) {  // the keys are distinct: one lane of the group
+#pragma unroll
+                    for (int j = 0; j < kListed - i; ++j)  // as far as later choices reach
+                        key[j] = j + 1 < kListed ? key[j + 1] : 0u;
+                }
             }
-            const float logit = Key<DT>::logit(best);
-            if (i == 0) top = logit;
-            const float ex = expf(logit - top);
-            picked += ex;
-            if (part == 0) {
-                expert[sub * k + i] = on ? e : -1;
-                weight[sub * k + i] = ex;
-                if (sums && on) atomicAdd(count + e, 1);
-            }
+            if (DT == FA_F32) again = __any_sync(0xffffffffu, same && on);
         }
+        if (again) choose_whole<L, N>(x, part, experts, k, take);
+        float top = x[0];
+#pragma unroll
+        for (int j = 1; j < N; ++j) top = fmaxf(top, x[j]);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         float total = 0.f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            x[j] = expf(x[j] - top);
+            x[j] = exp2_fast((x[j] - top) * kLog2E);
             total += x[j];
         }
         total = group_sum<L>(total);
-        if (part == 0)
-            factor[sub] = on ? __fdiv_rn(a.weight_scale, a.renormalise ? picked : total) : 0.f;
-        if (sums && on) {
-            const float inv = __fdiv_rn(1.f, total);
+        float ex[kItems], picked = 0.f;
+#pragma unroll
+        for (int s = 0; s < kItems; ++s) {
+            ex[s] = 0.f;
+            if (s * L + part < k && on) {
+                const auto *p = static_cast<const typename Elem<DT>::T *>(a.logits.p);
+                ex[s] = exp2_fast((Elem<DT>::widen(p[t * a.logits.ld + item[s]]) - top) * kLog2E);
+                picked += ex[s];
+                if (sums) atomicAdd(count + item[s], 1);
+            }
+        }
+        picked = group_sum<L>(picked);
+        const float factor = __fdividef(a.weight_scale, a.renormalise ? picked : total);
+#pragma unroll
+        for (int s = 0; s < kItems; ++s) {
+            const int i = s * L + part;
+            if (i < k && t < tokens) {
+                a.chosen[t * k + i] = on ? item[s] : -1;
+                a.weights[t * k + i] = on ? ex[s] * factor : 0.f;
+            }
+        }
+        if (!sums) continue;
+        if (on) {
+            const float inv = __fdividef(1.f, total);
 #pragma unroll
             for (int j = 0; j < N; ++j) prob[j] = fmaf(x[j], inv, prob[j]);
             if (part == 0) {
@@ -212,17 +275,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a, bool 
                 ++counted;
             }
         }
-        if (sums && part == 0 && t < tokens)
+        if (part == 0 && t < tokens)
             reinterpret_cast<float2 *>(a.lse)[t] = on ? make_float2(top, total)
                                                       : make_float2(0.f, 1.f);
-        __syncwarp();
-        const int n = static_cast<int>(min(static_cast<int64_t>(kTokens), tokens - t0)) * k;
-        for (int i = lane; i < n; i += 32) {
-            const float f = factor[a.by_k.quotient(i)];
-            a.chosen[t0 * k + i] = expert[i];
-            a.weights[t0 * k + i] = f == 0.f ? 0.f : weight[i] * f;
-        }
-        __syncwarp();
     }
     if (!sums) return;
     fa_allow_dependents();
@@ -240,7 +295,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a, bool 
     int32_t *const seen = reinterpret_cast<int32_t *>(sum + kRouteWarps * (L * N + 1));
     if (lane < L)
 #pragma unroll
-        for (int j = 0; j < N; ++j) sum[warp * (L * N + 1) + lane * N + j] = prob[j];
+        for (int j = 0; j < N; ++j) sum[warp * (L * N + 1) + expert_of<L>(part, j)] = prob[j];
     if (lane == 0) {
         sum[warp * (L * N + 1) + L * N] = z;
         seen[warp] = counted;
@@ -263,93 +318,110 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a, bool 
     }
 }
 
-template <int L, int N>
+template <int L, int R>
 size_t route_shared(const RouteArgs &a) {
-    const size_t words = kRouteWarps * (32 / L) * (2 * static_cast<size_t>(a.top_k) + 1);
-    return 4 * (words + (a.summary ? a.logits.cols + kRouteWarps * (L * N + 1) + kRouteWarps : 0));
+    return a.summary ? 4 * (a.logits.cols + kRouteWarps * (L * R * kRun + 1) + kRouteWarps) : 0;
 }
 
-// Joins the CTAs' sums in order and takes the losses: one CTA, a warp for 32 experts at a time
-// and the CTAs' parts in turn.
-__global__ void __launch_bounds__(1024) route_sums_kernel(RouteArgs a) {
-    __shared__ float part[32][33];
-    __shared__ int32_t parti[32][33];
-    __shared__ float fp[32];
-    __shared__ float z_sum;
-    __shared__ int32_t n_sum;
+// Joins the CTAs' sums in order, eight experts a CTA and 128 CTAs' parts side by side; the CTA that
+// comes last takes the losses.
+constexpr int kSumThreads = 1024, kSumExperts = 8;
+template <typename T>
+__device__ __forceinline__ T warp_total(T x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+__global__ void __launch_bounds__(kSumThreads) route_sums_kernel(RouteArgs a) {
+    constexpr int kWarps = kSumThreads / 32, kSlices = kSumThreads / kSumExperts;
+    __shared__ float prob[kWarps][kSumExperts], z_part[kWarps];
+    __shared__ int32_t count[kWarps][kSumExperts], n_part[kWarps];
     fa_grid_dependency_wait();
     const int experts = static_cast<int>(a.logits.cols);
     const int ctas = static_cast<int>(a.plan.ctas);
     const RouteSums in = route_sums(a.scratch, ctas, experts);
-    const int x = threadIdx.x % 32, y = threadIdx.x / 32;
-    if (y == 0) {
-        float z = 0.f;
-        int32_t n = 0;
-        for (int c = x; c < ctas; c += 32) {
-            z += in.z[c];
-            n += in.tokens[c];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int e = blockIdx.x * kSumExperts + threadIdx.x % kSumExperts;
+    float s = 0.f, z = 0.f;
+    int32_t k = 0, n = 0;
+    if (e < experts) {
+#pragma unroll 4
+        for (int c = threadIdx.x / kSumExperts; c < ctas; c += kSlices) {
+            s += in.prob[static_cast<int64_t>(c) * experts + e];
+            k += in.count[static_cast<int64_t>(c) * experts + e];
         }
+    }
+    for (int c = threadIdx.x; c < ctas; c += kSumThreads) {
+        z += in.z[c];
+        n += in.tokens[c];
+    }
+    z = warp_total(z);
+    n = warp_total(n);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            z += __shfl_xor_sync(0xffffffffu, z, o);
-            n += __shfl_xor_sync(0xffffffffu, n, o);
-        }
-        if (x == 0) {
-            z_sum = z;
-            n_sum = n;
-        }
+    for (int o = 16; o >= kSumExperts; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        k += __shfl_xor_sync(0xffffffffu, k, o);
+    }
+    if (lane < kSumExperts) {
+        prob[warp][lane] = s;
+        count[warp][lane] = k;
+    }
+    if (lane == 0) {
+        z_part[warp] = z;
+        n_part[warp] = n;
     }
     __syncthreads();
-    const float n = static_cast<float>(n_sum);
-    const float inv = n_sum ? __fdiv_rn(1.f, n) : 0.f;
-    float dot = 0.f;  // of counts and mean probabilities, in the first warp
-    for (int e0 = 0; e0 < experts; e0 += 32) {
-        const int e = e0 + x;
-        float s = 0.f;
-        int32_t k = 0;
-        if (e < experts)
-            for (int c = y; c < ctas; c += 32) {
-                s += in.prob[static_cast<int64_t>(c) * experts + e];
-                k += in.count[static_cast<int64_t>(c) * experts + e];
-            }
-        part[y][x] = s;
-        parti[y][x] = k;
-        __syncthreads();
-        if (y == 0 && e < experts) {
-            s = 0.f;
-            k = 0;
+    if (warp) return;
+    z = warp_total(z_part[lane]);
+    n = warp_total(n_part[lane]);
+    s = 0.f;
+    k = 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                s += part[i][x];
-                k += parti[i][x];
-            }
-            s *= inv;
-            a.mean_prob[e] = s;
-            a.counts[e] = k;
-            dot = fmaf(static_cast<float>(k), s, dot);
-        }
-        __syncthreads();
+    for (int w = 0; w < kWarps; w += 32 / kSumExperts) {
+        s += prob[w + lane / kSumExperts][lane % kSumExperts];
+        k += count[w + lane / kSumExperts][lane % kSumExperts];
     }
-    if (y == 0) fp[x] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        dot = 0.f;
-        for (int i = 0; i < 32; ++i) dot += fp[i];
-        const float balance =
-            dot * __fdiv_rn(static_cast<float>(experts), static_cast<float>(a.top_k)) * inv;
-        const float z = z_sum * inv;
-        a.summary[0] = a.balance_coef * balance + a.z_coef * z;
-        a.summary[1] = balance;
-        a.summary[2] = z;
-        a.summary[3] = n;
+#pragma unroll
+    for (int o = 16; o >= kSumExperts; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        k += __shfl_xor_sync(0xffffffffu, k, o);
     }
+    const float counted = static_cast<float>(n);
+    const float inv = n ? __fdiv_rn(1.f, counted) : 0.f;
+    s *= inv;
+    const bool mine = lane < kSumExperts && e < experts;
+    if (mine) {
+        a.mean_prob[e] = s;
+        a.counts[e] = k;
+    }
+    float dot = warp_total(mine ? static_cast<float>(k) * s : 0.f);
+    int32_t before = 0;
+    if (lane == 0) {
+        __stcg(in.dot + blockIdx.x, dot);
+        __threadfence();
+        before = atomicAdd(in.joined, 1);
+        __threadfence();
+    }
+    if (__shfl_sync(0xffffffffu, before, 0) != static_cast<int32_t>(gridDim.x) - 1) return;
+    dot = 0.f;
+    for (unsigned i = lane; i < gridDim.x; i += 32) dot += __ldcg(in.dot + i);
+    dot = warp_total(dot);
+    if (lane) return;
+    const float balance =
+        dot * __fdiv_rn(static_cast<float>(experts), static_cast<float>(a.top_k)) * inv;
+    a.summary[0] = a.balance_coef * balance + a.z_coef * (z * inv);
+    a.summary[1] = balance;
+    a.summary[2] = z * inv;
+    a.summary[3] = counted;
 }
 
-template <int DT, int L, int N>
-__global__ void __launch_bounds__(kRouteThreads) route_gradient_kernel(RouteGradArgs a, bool vec) {
-    constexpr int kTokens = 32 / L;
-    __shared__ long long counted_part[kRouteWarps];
-    __shared__ float row[kRouteWarps][32 * N];  // the chosen experts' part, by expert
+// LISTED: as the forward pass (at most kListed were chosen).
+template <int DT, int L, int R, bool LISTED>
+__global__ void __launch_bounds__(kGradThreads) route_gradient_kernel(RouteGradArgs a, bool vec) {
+    constexpr int kTokens = 32 / L, N = R * kRun, kWarps = kGradThreads / 32;
+    constexpr int kItems = ((LISTED ? kListed : FA_ROUTE_MAX_CHOSEN) + L - 1) / L;  // of a lane
+    __shared__ long long counted_part[kWarps];
+    __shared__ __align__(16) float row[kWarps][32 * N];  // the chosen experts' part, by expert
     const RouteArgs &r = a.r;
     const int k = r.top_k, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int sub = lane / L, part = lane % L;
@@ -357,38 +429,53 @@ __global__ void __launch_bounds__(kRouteThreads) route_gradient_kernel(RouteGrad
     const int experts = static_cast<int>(r.logits.cols);
     // the counted tokens are the counts' sum over top_k
     long long n = 0;
-    for (int e = threadIdx.x; e < experts; e += kRouteThreads) n += r.counts[e];
+    for (int e = threadIdx.x; e < experts; e += kGradThreads) n += r.counts[e];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     if (lane == 0) counted_part[warp] = n;
     __syncthreads();
     n = 0;
-    for (int w = 0; w < kRouteWarps; ++w) n += counted_part[w];
-    const float total = static_cast<float>(n / k);
+    for (int w = 0; w < kWarps; ++w) n += counted_part[w];
     const float gl = a.grad_loss && n ? *a.grad_loss : 0.f;
-    const float inv = n ? __fdiv_rn(1.f, total) : 0.f;
-    const float bal = gl * r.balance_coef * static_cast<float>(experts) * inv;
+    const float inv = n ? __fdiv_rn(static_cast<float>(k), static_cast<float>(n)) : 0.f;
+    // balance_coef * experts / n * f_e = bal * counts_e, with f_e = counts_e / (n k)
+    const float bal = gl * r.balance_coef * static_cast<float>(experts) * inv *
+                      (n ? __fdiv_rn(1.f, static_cast<float>(n)) : 0.f);
     const float zc = 2.f * gl * r.z_coef * inv;
-    float load[N];  // balance_coef * experts / n * f of this lane's experts
+    float load[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        const int e = part * N + j;
-        load[j] = e < experts && n
-                      ? bal * __fdiv_rn(static_cast<float>(r.counts[e]), static_cast<float>(n))
-                      : 0.f;
+        const int e = expert_of<L>(part, j);
+        load[j] = e < experts ? bal * static_cast<float>(r.counts[e]) : 0.f;
     }
     const float inv_scale = __fdiv_rn(1.f, r.weight_scale);
     float *const mine = row[warp] + sub * L * N;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps * kTokens;
-    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp) * kTokens;
-         t0 < tokens; t0 += step) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kTokens;
+    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTokens; t0 < tokens;
+         t0 += step) {
         const int64_t t = t0 + sub;
         const bool in = t < tokens, on = in && (!r.counted || r.counted[t]);
-        float x[N];
+        float x[N], w[kItems], d[kItems];
+        int e[kItems];
         float2 lse = make_float2(0.f, 1.f);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            w[i] = d[i] = 0.f;
+            e[i] = -1;
+        }
         if (on) {
-            load_logits<DT, N>(r.logits, t, part * N, vec, x);
+            load_logits<DT, L, R>(r.logits, t, part, vec, x);
             lse = reinterpret_cast<const float2 *>(r.lse)[t];
+            if (a.dweights) {
+#pragma unroll
+                for (int i = 0; i < kItems; ++i)
+                    if (i * L + part < k) {
+                        const int64_t at = t * k + i * L + part;
+                        w[i] = r.weights[at];
+                        d[i] = a.dweights[at];
+                        e[i] = r.chosen[at];
+                    }
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) x[j] = -INFINITY;
@@ -397,25 +484,24 @@ __global__ void __launch_bounds__(kRouteThreads) route_gradient_kernel(RouteGrad
         float back = 0.f;
         if (a.dweights) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) mine[part * N + j] = 0.f;
-            for (int i = part; i < k; i += L)
-                if (on) back = fmaf(a.dweights[t * k + i], r.weights[t * k + i], back);
+            for (int i = 0; i < kItems; ++i) back = fmaf(d[i], w[i], back);
             back = group_sum<L>(back) * inv_scale;
+#pragma unroll
+            for (int j = 0; j < N; j += 4)
+                *reinterpret_cast<float4 *>(mine + expert_of<L>(part, j)) =
+                    make_float4(0.f, 0.f, 0.f, 0.f);
             __syncwarp();
-            for (int i = part; i < k; i += L)
-                if (on) {
-                    const float w = r.weights[t * k + i], d = a.dweights[t * k + i];
-                    const int e = r.chosen[t * k + i];
-                    if (static_cast<unsigned>(e) < static_cast<unsigned>(L * N))
-                        mine[e] = r.renormalise ? w * (d - back) : w * d;
-                }
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+                if (static_cast<unsigned>(e[i]) < static_cast<unsigned>(L * N))
+                    mine[e[i]] = r.renormalise ? w[i] * (d[i] - back) : w[i] * d[i];
             __syncwarp();
         }
-        const float s = __fdiv_rn(1.f, lse.y);
+        const float s = __fdividef(1.f, lse.y);
         float mean = 0.f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            x[j] = expf(x[j] - lse.x) * s;
+            x[j] = exp2_fast((x[j] - lse.x) * kLog2E) * s;
             mean = fmaf(x[j], load[j], mean);
         }
         mean = group_sum<L>(mean);
@@ -425,48 +511,57 @@ __global__ void __launch_bounds__(kRouteThreads) route_gradient_kernel(RouteGrad
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             x[j] *= load[j] + same;
-            if (a.dweights) x[j] += mine[part * N + j];
-            if (!on) x[j] = 0.f;
+            if (r.counted && !on) x[j] = 0.f;
+        }
+        if (a.dweights) {
+#pragma unroll
+            for (int j = 0; j < N; j += 4) {
+                const float4 m = *reinterpret_cast<const float4 *>(mine + expert_of<L>(part, j));
+                x[j] += m.x;
+                x[j + 1] += m.y;
+                x[j + 2] += m.z;
+                x[j + 3] += m.w;
+            }
         }
         __syncwarp();
-        using T = typename Elem<DT>::T;
-        T *p = static_cast<T *>(a.dlogits.p) + t * a.dlogits.ld + part * N;
-        const int left = experts - part * N;
-        int valid = !in || left < 0 ? 0 : left < N ? left : N;
-        if (valid && !fa_in_bounds(part * N, valid, experts)) valid = 0;
-        if (vec) {
-            if (valid == N) {
-                store_n<DT, N>(p, x);
-            } else {
+        // a token past the last one has no run to write
+        MatrixArgs to = a.dlogits;
+        if (!in) to.cols = 0;
 #pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (j < valid) p[j] = Elem<DT>::round(x[j]);
-            }
-        } else {
-            store_any<DT, N>(p, x, valid, 0xffffffffu, L);
+        for (int q = 0; q < R; ++q) {
+            const int c = (q * L + part) * kRun;
+            if (vec)
+                store_run<DT, true>(to, t, c, x + q * kRun, 0xffffffffu, L);
+            else
+                store_run<DT, false>(to, t, c, x + q * kRun, 0xffffffffu, L);
         }
     }
 }
 
-// Calls f with the lanes of a token and the experts of a lane.
+// Calls f with the lanes of a token and the runs of a lane.
 template <typename F>
 cudaError_t for_lanes(int64_t experts, F f) {
     using std::integral_constant;
-    const integral_constant<int, 8> n8{};
-    if (experts <= 8) return f(integral_constant<int, 1>{}, n8);
-    if (experts <= 16) return f(integral_constant<int, 2>{}, n8);
-    if (experts <= 32) return f(integral_constant<int, 4>{}, n8);
-    if (experts <= 64) return f(integral_constant<int, 8>{}, n8);
-    if (experts <= 128) return f(integral_constant<int, 16>{}, n8);
-    if (experts <= 256) return f(integral_constant<int, 32>{}, n8);
-    if (experts <= 512) return f(integral_constant<int, 32>{}, integral_constant<int, 16>{});
-    return f(integral_constant<int, 32>{}, integral_constant<int, 32>{});
+    const integral_constant<int, 1> r1{};
+    const integral_constant<int, 2> r2{};
+    if (experts <= 8) return f(integral_constant<int, 1>{}, r1);
+    if (experts <= 16) return f(integral_constant<int, 2>{}, r1);
+    if (experts <= 32) return f(integral_constant<int, 4>{}, r1);
+    if (experts <= 64) return f(integral_constant<int, 8>{}, r1);
+    if (experts <= 128) return f(integral_constant<int, 8>{}, r2);
+    if (experts <= 256) return f(integral_constant<int, 16>{}, r2);
+    if (experts <= 512) return f(integral_constant<int, 32>{}, r2);
+    return f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
 }
 
-int lanes_of(int64_t experts) {
-    int lanes = 1;
-    while (lanes < 32 && lanes * 8 < experts) lanes *= 2;
-    return lanes;
+// Tokens of a warp's turn.
+int tokens_of(int64_t experts) {
+    int tokens = 1;
+    for_lanes(experts, [&](auto l, auto) {
+        tokens = 32 / l();
+        return cudaSuccess;
+    });
+    return tokens;
 }
 
 }  // namespace
@@ -476,36 +571,53 @@ FA_BOUNDS_VIOLATIONS(route_bounds_violations, g_route_oob)
 // CTAs of a pass: every warp with one turn of tokens until the SMs are full.
 RoutePlan route_plan(int64_t tokens, int64_t experts) {
     RoutePlan p{0, 0};
-    const int64_t turn = kRouteWarps * (32 / lanes_of(experts));
+    const int64_t turn = kRouteWarps * tokens_of(experts);
     p.ctas = (tokens + turn - 1) / turn;
-    if (p.ctas > 2 * kSms) p.ctas = 2 * kSms;
-    p.bytes = p.ctas * (experts + 1) * 8;
+    if (p.ctas > kRouteCtas * kSms) p.ctas = kRouteCtas * kSms;
+    p.bytes = p.ctas * (experts + 1) * 8 + 4 * (FA_ROUTE_MAX_EXPERTS / 8 + 1);
     return p;
 }
 
 cudaError_t launch_route(const RouteArgs &a, fa_dtype dt, cudaStream_t stream) {
     const bool vec = aligned_rows(a.logits, dt);
     const cudaError_t err = for_dtype(dt, [&](auto d) {
-        return for_lanes(a.logits.cols, [&](auto l, auto n) {
+        return for_lanes(a.logits.cols, [&](auto l, auto r) {
+            auto *kernel = a.top_k <= kListed ? route_kernel<d(), l(), r(), true>
+                                              : route_kernel<d(), l(), r(), false>;
+            const size_t smem = route_shared<l(), r()>(a);
+            if (smem > 48 * 1024) {
+                const cudaError_t e =
+                    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+                if (e != cudaSuccess) return e;
+            }
             if (a.plan.ctas)
-                route_kernel<d(), l(), n()><<<static_cast<unsigned>(a.plan.ctas), kRouteThreads,
-                                             route_shared<l(), n()>(a), stream>>>(a, vec);
+                kernel<<<static_cast<unsigned>(a.plan.ctas), kRouteThreads, smem, stream>>>(a, vec);
             return cudaGetLastError();
         });
     });
     if (err != cudaSuccess || !a.summary) return err;
-    return launch_dependent(route_sums_kernel, dim3(1), dim3(1024), 0, stream, a);
+    if (!a.plan.ctas) {  // no token: nothing was summed
+        const size_t row = 4 * a.logits.cols;
+        cudaError_t e = cudaMemsetAsync(a.counts, 0, row, stream);
+        if (e == cudaSuccess) e = cudaMemsetAsync(a.mean_prob, 0, row, stream);
+        return e == cudaSuccess ? cudaMemsetAsync(a.summary, 0, 16, stream) : e;
+    }
+    return launch_dependent(route_sums_kernel, 
+                            dim3((a.logits.cols + kSumExperts - 1) / kSumExperts),
+                            dim3(kSumThreads), 0, stream, a);
 }
 
 cudaError_t launch_route_gradient(const RouteGradArgs &a, fa_dtype dt, cudaStream_t stream) {
     const bool vec = aligned_rows(a.r.logits, dt) && aligned_rows(a.dlogits, dt);
-    const int64_t turn = kRouteWarps * (32 / lanes_of(a.r.logits.cols));
+    const int64_t turn = kGradThreads / 32 * tokens_of(a.r.logits.cols);
     int64_t ctas = (a.r.logits.rows + turn - 1) / turn;
-    if (ctas > 8 * kSms) ctas = 8 * kSms;
+    if (ctas > 3 * kSms) ctas = 3 * kSms;
     return for_dtype(dt, [&](auto d) {
-        return for_lanes(a.r.logits.cols, [&](auto l, auto n) {
-            route_gradient_kernel<d(), l(), n()>
-                <<<static_cast<unsigned>(ctas), kRouteThreads, 0, stream>>>(a, vec);
+        return for_lanes(a.r.logits.cols, [&](auto l, auto r) {
+            auto *kernel = a.r.top_k <= kListed ? route_gradient_kernel<d(), l(), r(), true>
+                                                : route_gradient_kernel<d(), l(), r(), false>;
+            kernel<<<static_cast<unsigned>(ctas), kGradThreads, 0, stream>>>(a, vec);
             return cudaGetLastError();
         });
     });

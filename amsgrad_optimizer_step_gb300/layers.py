@@ -4,6 +4,9 @@
 the tail of a gated MLP that keeps its two inputs in 8 bits until the backward pass, and
 nothing else; ``token_logprobs``, ``preference_loss`` and ``policy_loss`` go from the logits
 to a loss, and ``policy_step`` takes the policy loss and the logits' gradient in one pass.
+``block_join`` adds a block's output to the residual stream with the norms behind and before it,
+its gate and its dropout; ``norm`` is the first of these norms and ``dropout`` stands alone;
+``route`` chooses the experts of a routed block, with the loss that balances them.
 Gradients come in the operands' types, so that they go into an optimizer bucket as they are;
 a non-finite one is found by the optimizer's statistics and skips its step.  All arithmetic
 but the plain matrix products runs in the library's kernels.
@@ -16,10 +19,11 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
+from . import block_ops as blocks
 from . import model_ops as ops
 
 __all__ = ["embedding", "gated_activation", "gated_down", "token_logprobs", "preference_loss",
-           "policy_loss", "policy_step"]
+           "policy_loss", "policy_step", "dropout", "norm", "block_join", "route"]
 
 
 def _flat(x: torch.Tensor) -> torch.Tensor:
@@ -262,3 +266,184 @@ def policy_step(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tens
                        _tokens(ref_logp), _tokens(weights), dlogits, clip_low, clip_high, kl_coef,
                        denominator, logit_scale, loss_scale)
     return out.summary, dlogits.view(logits.shape)
+
+
+# ---- residual blocks -------------------------------------------------------------------
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, seed, offset, counter):
+        flat = _flat(x)
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        blocks.fa_dropout(flat, out.view(flat.shape), blocks.Dropout(p, seed, offset, counter))
+        ctx.save_for_backward(counter)  # one that is moved on before the backward pass is refused
+        ctx.key = p, seed, offset
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        (counter,) = ctx.saved_tensors
+        flat = _flat(dout)
+        dx = torch.empty(flat.shape, dtype=dout.dtype, device=dout.device)
+        blocks.fa_dropout(flat, dx, blocks.Dropout(*ctx.key, counter))
+        return dx.view(dout.shape), None, None, None, None
+
+
+def _matrix_like(x: torch.Tensor) -> torch.Tensor:
+    if x.dim() == 0:
+        raise ValueError("a tensor of one dimension at least is needed")
+    return x
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
+            counter: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x with each element dropped with probability p (a multiple of 2^-16) and the others
+    multiplied by 1 / (1 - p).  Which ones follows from the arguments and the element's place
+    alone, and nothing is kept for the backward pass: every call of a step takes another
+    ``offset`` (below 2^32, say), and every step another ``seed`` or ``counter`` (int64 [1] on
+    the device, added to offset, for captured steps; moved on after the backward pass)."""
+    return _Dropout.apply(_matrix_like(x), p, seed, offset, counter)
+
+
+class _Join(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, residual, branch, post_weight, gate, pre_weight, join, pre_norm, dtype,
+                grad_enabled):
+        flat = _flat(residual)
+        rows, cols = flat.shape
+        y = None if branch is None else _flat(branch)
+        gates = None if gate is None else _flat(gate)
+        keep = grad_enabled and any(ctx.needs_input_grad[:5])
+
+        def rstd(on):
+            if not (on and keep):
+                return None
+            return torch.empty(rows, dtype=torch.float32, device=flat.device)
+
+        post_rstd, pre_rstd = rstd(branch is not None and join.post_norm), rstd(pre_norm)
+        # a norm alone leaves the stream as it is
+        out = normed = None
+        if branch is not None:
+            out = torch.empty(residual.shape, dtype=flat.dtype, device=flat.device)
+        if pre_norm:
+            normed = torch.empty(residual.shape, dtype=dtype, device=flat.device)
+        blocks.fa_block_join(join, flat, y, None if out is None else out.view(flat.shape),
+                             None if normed is None else normed.view(flat.shape), post_rstd,
+                             pre_rstd, post_weight, pre_weight, gates)
+        if keep:
+            counter = None if join.dropout is None else join.dropout.counter
+            ctx.save_for_backward(flat if out is None else out, y, post_rstd, pre_rstd, post_weight, gates, pre_weight,
+                                  counter)
+        ctx.join, ctx.pre_norm, ctx.gate_shape = join, pre_norm, None if gate is None else gate.shape
+        ctx.set_materialize_grads(False)
+        if out is None:
+            return normed
+        return (out, normed) if pre_norm else out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        out, y, post_rstd, pre_rstd, post_weight, gate, pre_weight, _ = ctx.saved_tensors
+        if y is None:
+            dout, dnormed = None, grads[0]
+        else:
+            dout, dnormed = grads if ctx.pre_norm else (grads[0], None)
+        if dout is None and dnormed is None:
+            return (None,) * 9
+        shape = (dnormed if dout is None else dout).shape
+        out = _flat(out)
+        dout, dnormed = (None if g is None else _flat(g) for g in (dout, dnormed))
+        pre = dnormed is not None
+        need = ctx.needs_input_grad
+
+        def like(t, on):
+            if t is None or not on:
+                return None
+            return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+        dresidual, dbranch = like(out, need[0]), like(y, need[1])
+        dpost, dgate = like(post_weight, need[2]), like(gate, need[3])
+        dpre = like(pre_weight, need[4] and pre)
+        scratch = None
+        if dpost is not None or dgate is not None or dpre is not None:
+            scratch = blocks.join_scratch(*out.shape, 0 if gate is None else gate.shape[0],
+                                          out.device)
+        blocks.fa_block_join_gradient(
+            ctx.join, out if pre else None, y, dout, dnormed, dresidual, dbranch, scratch,
+            post_rstd, pre_rstd if pre else None, post_weight, pre_weight if pre else None, gate,
+            dpost, dpre, dgate)
+        return (None if dresidual is None else dresidual.view(shape),
+                None if dbranch is None else dbranch.view(shape), dpost,
+                None if dgate is None else dgate.view(ctx.gate_shape), dpre) + (None,) * 4
+
+
+def norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+         weight_offset: float = 0.0, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """(weight + weight_offset) * x / sqrt(mean(x^2) + eps) over the last dimension: the norm
+    before the first block, where there is nothing to join yet.  ``dtype``: the result's, where
+    an FP32 stream goes into 16-bit products."""
+    join = blocks.Join(False, 1.0, 1.0, eps, weight_offset)
+    return _Join.apply(_matrix_like(x), None, None, None, weight, join, True, dtype or x.dtype,
+                       torch.is_grad_enabled())
+
+
+def block_join(residual: torch.Tensor, branch: torch.Tensor,
+               post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+               pre_weight: Optional[torch.Tensor] = None, post_norm: bool = True,
+               pre_norm: bool = True, residual_scale: float = 1.0, branch_scale: float = 1.0,
+               eps: float = 1e-6, weight_offset: float = 0.0, p: float = 0.0, seed: int = 0,
+               offset: int = 0, counter: Optional[torch.Tensor] = None):
+    """The residual stream behind a block, and the next block's normed input: (out, normed), or
+    out alone without ``pre_norm``, with
+      out = residual_scale * residual + branch_scale * gate * dropout(norm(branch))
+      normed = norm(out as it is stored)
+    (see fa_join; ``p``, ``seed``, ``offset`` and ``counter`` as for dropout).  The gate is
+    [columns], or [groups, columns] with groups equal runs of the flattened rows.  The stream may
+    be FP32 over a 16-bit branch, and so may the weights."""
+    if branch.shape != residual.shape:
+        raise ValueError(f"branch: shape {tuple(branch.shape)}, expected {tuple(residual.shape)}")
+    drop = blocks.Dropout(p, seed, offset, counter) if p else None
+    join = blocks.Join(post_norm, residual_scale, branch_scale, eps, weight_offset, drop)
+    return _Join.apply(_matrix_like(residual), branch, post_weight, gate, pre_weight, join,
+                       pre_norm, branch.dtype, torch.is_grad_enabled())
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, counted, settings):
+        flat = _flat(logits)
+        counted = None if counted is None else counted.reshape(-1).contiguous()
+        out = blocks.route_buffers(flat.shape[0], flat.shape[1], k, flat.device)
+        blocks.fa_route(flat, out, counted, *settings)
+        ctx.save_for_backward(flat, counted, out.chosen, out.weights, out.lse, out.counts)
+        ctx.settings = settings
+        ctx.mark_non_differentiable(out.chosen, out.counts)
+        ctx.set_materialize_grads(False)
+        return out.chosen, out.weights, out.loss.view(()), out.counts
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _, dweights, dloss, __):
+        flat, counted, chosen, weights, lse, counts = ctx.saved_tensors
+        if dweights is None and dloss is None:
+            return None, None, None, None
+        out = blocks.RouteBuffers(chosen, weights, lse, counts, *[None] * 6)
+        dlogits = torch.empty(flat.shape, dtype=flat.dtype, device=flat.device)
+        blocks.fa_route_gradient(flat, out, dlogits,
+                                 None if dweights is None else dweights.float().contiguous(),
+                                 None if dloss is None else dloss.reshape(1).float(), counted,
+                                 *ctx.settings)
+        return dlogits, None, None, None
+
+
+def route(logits: torch.Tensor, k: int, counted: Optional[torch.Tensor] = None,
+          renormalise: bool = True, weight_scale: float = 1.0, balance_coef: float = 0.0,
+          z_coef: float = 0.0) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(chosen [tokens, k], weights [tokens, k], loss, counts [experts]) of tokens' logits
+    [tokens, experts] (see fa_router).  The weights' gradient and the loss's go into the logits
+    in one pass."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits: shape {tuple(logits.shape)}, expected a matrix")
+    return _Route.apply(logits, k, counted,
+                        (renormalise, weight_scale, balance_coef, z_coef))

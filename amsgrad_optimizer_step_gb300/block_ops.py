@@ -17,7 +17,7 @@ import torch
 
 from . import _lib
 from ._lib import FaDropoutKey, FaJoin, FaJoinGradient, FaRouter, FaRouting, check
-from .model_ops import _FLOATS, _code, _matrix, _rows, _same, _stream, _vector
+from .model_ops import _FLOATS, _code, _matrix, _rows, _stream, _vector
 
 __all__ = [
     "fa_dropout", "fa_block_join", "fa_block_join_scratch", "fa_block_join_gradient", "fa_route",
@@ -26,6 +26,34 @@ __all__ = [
 ]
 
 _U64 = (1 << 64) - 1
+_F32, _I32, _I64, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
+
+
+# A generation step's call is bound by the host: what a tensor is asked is asked once, and in the
+# order in which it is usually right; a refusal's message is built on the way out.
+
+def _mat(name: str, t: torch.Tensor, shape, dtype) -> tuple[int, int]:
+    """Pointer and row distance of a matrix of this shape and type, with adjacent elements in a
+    row."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape == shape:
+        row, col = t.stride()
+        if col == 1 and row >= shape[1]:
+            return t.data_ptr(), row
+    return t.data_ptr(), _rows(name, t, shape)
+
+
+def _mat_or_none(name: str, t: Optional[torch.Tensor], shape, dtype) -> tuple[Optional[int], int]:
+    return (None, shape[1]) if t is None else _mat(name, t, shape, dtype)
+
+
+def _vec_or_none(name: str, t: Optional[torch.Tensor], n: int, dtype) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype is dtype and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    return _vector(name, t, n, dtype)
 
 
 # ---- dropout -----------------------------------------------------------------------
@@ -40,19 +68,20 @@ class Dropout(NamedTuple):
 
 
 def _key(drop: Dropout) -> FaDropoutKey:
-    counter = drop.counter
-    return FaDropoutKey(drop.p, drop.seed & _U64, drop.offset & _U64,
-                        None if counter is None else _vector("counter", counter, 1, torch.int64))
+    p, seed, offset, counter = drop
+    return FaDropoutKey(p, seed & _U64, offset & _U64, _vec_or_none("counter", counter, 1, _I64))
 
 
 def fa_dropout(x: torch.Tensor, out: torch.Tensor, drop: Dropout, stream=None) -> None:
     """out = x with elements dropped and the others multiplied by 1 / (1 - p); its gradient is
     the same call on the output's.  out may be x itself."""
     rows, cols = shape = _matrix("x", x)
-    key = _key(drop)
+    dtype = x.dtype
+    ptr, ld = _mat("x", x, shape, dtype)
+    to, to_ld = _mat("out", out, shape, dtype)
     check("fa_dropout", _lib.load().fa_dropout(
-        rows, cols, x.data_ptr(), _rows("x", x, shape), _code("x", x, _FLOATS),
-        ctypes.byref(key), _same(x.dtype, "out", out), _rows("out", out, shape), _stream(stream)))
+        rows, cols, ptr, ld, _code("x", x, _FLOATS), ctypes.byref(_key(drop)), to, to_ld,
+        _stream(stream)))
 
 
 # ---- the join of a block to the residual stream ------------------------------------------
@@ -70,45 +99,27 @@ class Join(NamedTuple):
 _JOIN = Join()
 
 
-def _weight(name: str, t: Optional[torch.Tensor], shape, dtype) -> tuple[Optional[int], int]:
-    """Pointer and row distance of a weight ([cols]) or gate ([groups, cols])."""
-    if t is None:
-        return None, shape[-1]
-    ptr = _same(dtype, name, t)
-    if len(shape) == 1:
-        return _vector(name, t, shape[0], dtype), shape[0]
-    return ptr, _rows(name, t, shape)
-
-
-def _join_record(j: Join, like: torch.Tensor, stream_dtype, branch, post_weight, pre_weight, gate):
-    """The C record, the weights' type and the key that it points to."""
-    rows, cols = shape = like.shape
-    dtype = branch.dtype if branch is not None else like.dtype
-    weights = [w for w in (post_weight, pre_weight, gate) if w is not None]
-    wdtype = weights[0].dtype if weights else dtype
-    groups = 1
+def _join_record(j: Join, shape, dtype, stream_dtype, branch, post_weight, pre_weight, gate):
+    """The C record (which keeps the key it points to), and the weights' type."""
+    rows, cols = shape
+    some = post_weight if post_weight is not None else pre_weight if pre_weight is not None else gate
+    wdtype = dtype if some is None else some.dtype
+    post_norm, residual_scale, branch_scale, eps, weight_offset, drop = j
+    y, y_ld = _mat_or_none("branch", branch, shape, dtype)
+    w1 = _vec_or_none("post_weight", post_weight, cols, wdtype)
+    w2 = _vec_or_none("pre_weight", pre_weight, cols, wdtype)
+    g, g_ld, groups = None, cols, 1
     if gate is not None:
         groups = _matrix("gate", gate)[0]
-    key = None if j.dropout is None else _key(j.dropout)
-    gate_ptr, gate_ld = _weight("gate", gate, (groups, cols), wdtype)
-    record = FaJoin(
-        rows, cols, _FLOATS.get(dtype, -1), _FLOATS.get(stream_dtype, -1),
-        _FLOATS.get(wdtype, -1), int(bool(j.post_norm)),
-        None if branch is None else branch.data_ptr(),
-        cols if branch is None else _rows("branch", branch, shape),
-        _weight("post_weight", post_weight, (cols,), wdtype)[0],
-        _weight("pre_weight", pre_weight, (cols,), wdtype)[0], gate_ptr, gate_ld, groups,
-        j.residual_scale, j.branch_scale, j.eps, j.weight_offset,
-        None if key is None else ctypes.addressof(key))
-    return record, dtype, wdtype, key
-
-
-def _optional(name: str, t: Optional[torch.Tensor], shape, dtype) -> tuple[Optional[int], int]:
-    return (None, shape[1]) if t is None else (_same(dtype, name, t), _rows(name, t, shape))
-
-
-def _per_row(name: str, t: Optional[torch.Tensor], rows: int) -> Optional[int]:
-    return None if t is None else _vector(name, t, rows, torch.float32)
+        g, g_ld = _mat("gate", gate, (groups, cols), wdtype)
+    codes = _FLOATS.get
+    record = FaJoin(rows, cols, codes(dtype, -1), codes(stream_dtype, -1), codes(wdtype, -1),
+                    bool(post_norm), y, y_ld, w1, w2, g, g_ld, groups, residual_scale,
+                    branch_scale, eps, weight_offset)
+    if drop is not None:
+        record.key = _key(drop)
+        record.dropout = ctypes.addressof(record.key)
+    return record, wdtype
 
 
 def fa_block_join(join: Optional[Join], residual: torch.Tensor, branch: Optional[torch.Tensor],
@@ -121,20 +132,18 @@ def fa_block_join(join: Optional[Join], residual: torch.Tensor, branch: Optional
     """out = residual_scale * residual + branch_scale * gate * dropout(norm(branch)), and normed
     = the norm of out as it is stored.  The rstd vectors keep what the gradient takes.  out may
     be the residual itself.  The branch's type is normed's too (without a branch normed's own)."""
-    rows, cols = shape = _matrix("residual", residual)
-    j = join or _JOIN
-    like = branch if branch is not None else normed if normed is not None else residual
-    if like.shape != shape:
-        raise ValueError(f"shape {tuple(like.shape)}, expected {tuple(shape)}")
-    record, dtype, _, key = _join_record(
-        j, residual if branch is None and normed is None else like, residual.dtype, branch,
-        post_weight, pre_weight, gate)
-    out_ptr, out_ld = _optional("out", out, shape, residual.dtype)
-    normed_ptr, normed_ld = _optional("normed", normed, shape, dtype)
+    shape = _matrix("residual", residual)
+    typed = branch if branch is not None else normed if normed is not None else residual
+    dtype, stream_dtype = typed.dtype, residual.dtype
+    record, _ = _join_record(join or _JOIN, shape, dtype, stream_dtype, branch, post_weight,
+                             pre_weight, gate)
+    r, r_ld = _mat("residual", residual, shape, stream_dtype)
+    o, o_ld = _mat_or_none("out", out, shape, stream_dtype)
+    n, n_ld = _mat_or_none("normed", normed, shape, dtype)
     check("fa_block_join", _lib.load().fa_block_join(
-        ctypes.byref(record), residual.data_ptr(), _rows("residual", residual, shape), out_ptr,
-        out_ld, normed_ptr, normed_ld, _per_row("post_rstd", post_rstd, rows),
-        _per_row("pre_rstd", pre_rstd, rows), _stream(stream)))
+        ctypes.byref(record), r, r_ld, o, o_ld, n, n_ld,
+        _vec_or_none("post_rstd", post_rstd, shape[0], _F32),
+        _vec_or_none("pre_rstd", pre_rstd, shape[0], _F32), _stream(stream)))
 
 
 def fa_block_join_scratch(rows: int, cols: int, groups: int) -> int:
@@ -166,27 +175,32 @@ def fa_block_join_gradient(join: Optional[Join], out: Optional[torch.Tensor],
     """Gradients of fa_block_join, from the stream as it stored it (``out``), the branch and the
     rstd vectors.  dout or dnormed may be None (no gradient; no second norm); a result that is
     None is not taken."""
-    j = join or _JOIN
-    like = next((t for t in (branch, dnormed, dout, out) if t is not None), None)
-    if like is None:
+    typed = branch if branch is not None else dnormed
+    streamed = dout if dout is not None else out
+    if typed is None and streamed is None:
         raise ValueError("neither a branch nor a gradient is given")
-    rows, cols = shape = _matrix("branch", like)
-    streams = [t for t in (dout, out, dresidual) if t is not None]
-    stream_dtype = streams[0].dtype if streams else like.dtype
-    typed = branch if branch is not None else dnormed if dnormed is not None else like
-    record, dtype, wdtype, key = _join_record(j, typed, stream_dtype, branch, post_weight,
-                                              pre_weight, gate)
+    if typed is None:
+        typed = streamed
+    elif streamed is None:
+        streamed = dresidual if dresidual is not None else typed
+    rows, cols = shape = _matrix("branch", typed)
+    dtype, stream_dtype = typed.dtype, streamed.dtype
+    record, wdtype = _join_record(join or _JOIN, shape, dtype, stream_dtype, branch, post_weight,
+                                  pre_weight, gate)
     g = FaJoinGradient(
-        *_optional("out", out, shape, stream_dtype), _per_row("post_rstd", post_rstd, rows),
-        _per_row("pre_rstd", pre_rstd, rows), *_optional("dout", dout, shape, stream_dtype),
-        *_optional("dnormed", dnormed, shape, dtype),
-        *_optional("dresidual", dresidual, shape, stream_dtype),
-        *_optional("dbranch", dbranch, shape, dtype),
-        _weight("dpost_weight", dpost_weight, (cols,), wdtype)[0],
-        _weight("dpre_weight", dpre_weight, (cols,), wdtype)[0],
-        *_weight("dgate", dgate, (record.groups, cols), wdtype),
-        None if scratch is None else _vector("scratch", scratch, scratch.numel(), torch.uint8),
-        0 if scratch is None else scratch.numel())
+        *_mat_or_none("out", out, shape, stream_dtype),
+        _vec_or_none("post_rstd", post_rstd, rows, _F32),
+        _vec_or_none("pre_rstd", pre_rstd, rows, _F32),
+        *_mat_or_none("dout", dout, shape, stream_dtype),
+        *_mat_or_none("dnormed", dnormed, shape, dtype),
+        *_mat_or_none("dresidual", dresidual, shape, stream_dtype),
+        *_mat_or_none("dbranch", dbranch, shape, dtype),
+        _vec_or_none("dpost_weight", dpost_weight, cols, wdtype),
+        _vec_or_none("dpre_weight", dpre_weight, cols, wdtype),
+        *_mat_or_none("dgate", dgate, (record.groups, cols), wdtype))
+    if scratch is not None:
+        size = scratch.numel()
+        g.scratch, g.scratch_bytes = _vec_or_none("scratch", scratch, size, _U8), size
     check("fa_block_join_gradient", _lib.load().fa_block_join_gradient(
         ctypes.byref(record), ctypes.byref(g), _stream(stream)))
 
@@ -231,29 +245,31 @@ def route_buffers(tokens: int, experts: int, k: int, device, loss: bool = True) 
 
 def _router(logits: torch.Tensor, k: int, counted: Optional[torch.Tensor], renormalise: bool,
             weight_scale: float, balance_coef: float, z_coef: float) -> FaRouter:
-    tokens, experts = _matrix("logits", logits)
-    if counted is not None and counted.dtype is torch.bool:
-        counted = counted.view(torch.uint8)
-    return FaRouter(tokens, experts, logits.data_ptr(), _code("logits", logits, _FLOATS),
-                    _rows("logits", logits, logits.shape),
-                    None if counted is None else _vector("counted", counted, tokens, torch.uint8),
-                    k, int(bool(renormalise)), weight_scale, balance_coef, z_coef)
+    tokens, experts = shape = logits.shape
+    ptr, ld = _mat("logits", logits, shape, logits.dtype)
+    mask = None
+    if counted is not None:  # a bool is a byte
+        mask = _vec_or_none("counted", counted, tokens,
+                            torch.bool if counted.dtype is torch.bool else _U8)
+    return FaRouter(tokens, experts, ptr, _code("logits", logits, _FLOATS), ld, mask, k,
+                    bool(renormalise), weight_scale, balance_coef, z_coef)
 
 
 def _routing(out: RouteBuffers, tokens: int, experts: int) -> tuple[FaRouting, int]:
-    k = _matrix("chosen", out.chosen)[1]
-    f32, i32 = torch.float32, torch.int32
-    pairs = _vector("chosen", out.chosen, tokens * k, i32), _vector("weights", out.weights,
-                                                                    tokens * k, f32)
-    if out.lse is None:
+    chosen, weights, lse, counts, mean_prob, summary, _, _, _, scratch = out
+    k = _matrix("chosen", chosen)[1]
+    pairs = (_vec_or_none("chosen", chosen, tokens * k, _I32),
+             _vec_or_none("weights", weights, tokens * k, _F32))
+    if lse is None:
         return FaRouting(*pairs), k
-    kept = _vector("lse", out.lse, 2 * tokens, f32), _vector("counts", out.counts, experts, i32)
-    if out.summary is None:  # what a gradient reads
+    kept = (_vec_or_none("lse", lse, 2 * tokens, _F32),
+            _vec_or_none("counts", counts, experts, _I32))
+    if summary is None:  # what a gradient reads
         return FaRouting(*pairs, *kept), k
-    return FaRouting(*pairs, *kept, _vector("mean_prob", out.mean_prob, experts, f32),
-                     _vector("summary", out.summary, 4, f32),
-                     _vector("scratch", out.scratch, out.scratch.numel(), torch.uint8),
-                     out.scratch.numel()), k
+    size = scratch.numel()
+    return FaRouting(*pairs, *kept, _vec_or_none("mean_prob", mean_prob, experts, _F32),
+                     _vec_or_none("summary", summary, 4, _F32),
+                     _vec_or_none("scratch", scratch, size, _U8), size), k
 
 
 def fa_route(logits: torch.Tensor, out: RouteBuffers, counted: Optional[torch.Tensor] = None,
@@ -281,10 +297,7 @@ def fa_route_gradient(logits: torch.Tensor, out: RouteBuffers, dlogits: torch.Te
         raise ValueError("the buffers are those of a pass without a loss: nothing was kept")
     r, k = _routing(out, tokens, experts)
     x = _router(logits, k, counted, renormalise, weight_scale, balance_coef, z_coef)
-    f32 = torch.float32
+    to, to_ld = _mat("dlogits", dlogits, logits.shape, logits.dtype)
     check("fa_route_gradient", _lib.load().fa_route_gradient(
-        ctypes.byref(x), ctypes.byref(r),
-        None if dweights is None else _vector("dweights", dweights, tokens * k, f32),
-        None if grad_loss is None else _vector("grad_loss", grad_loss, 1, f32),
-        _same(logits.dtype, "dlogits", dlogits), _rows("dlogits", dlogits, logits.shape),
-        _stream(stream)))
+        ctypes.byref(x), ctypes.byref(r), _vec_or_none("dweights", dweights, tokens * k, _F32),
+        _vec_or_none("grad_loss", grad_loss, 1, _F32), to, to_ld, _stream(stream)))

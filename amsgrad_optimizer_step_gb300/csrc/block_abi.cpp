@@ -16,8 +16,6 @@ namespace {
 
 using namespace fa;
 
-constexpr int64_t kDropColumns = 64;  // of a block of fa_dropout's grid
-
 // A dropout record on the host, and its device scalar.
 fa_status check_key(const fa_dropout_key *k) {
     return k->p >= 0.0 && k->p <= 1.0 ? FA_OK : FA_ERR_OPTION;
@@ -169,11 +167,9 @@ fa_status fa_dropout(int64_t rows, int64_t cols, const void *x, int64_t x_ld, fa
     const Matrix ins[] = {key_vec(key), mat(x, rows, cols, x_ld, e)};
     FA_TRY(check_outputs(outs, 1, ins, x == out && x_ld == out_ld ? 1 : 2));
     TraceRange trace("fa_dropout");
-    DropoutArgs a;
+    DropoutArgs a{};
     a.x = matrix_args(x, rows, cols, x_ld);
     a.out = matrix_args(out, rows, cols, out_ld);
-    a.blocks = blocks;
-    a.by_blocks = Divider(static_cast<uint32_t>(blocks));
     a.drop = drop_args(key);
     return cuda_status(launch_dropout(a, dtype, static_cast<cudaStream_t>(stream)));
 }

@@ -22,9 +22,10 @@ struct DropArgs {
     const uint64_t *counter;  // or nullptr
     float scale;              // of what is kept
 };
+constexpr int kDropColumns = 128;  // whose blocks over all rows the grid's limit counts
 struct DropoutArgs {
     MatrixArgs x, out;
-    int64_t blocks;  // of 64 columns
+    int64_t blocks;  // of a row, and the division by them (set by the launch)
     Divider by_blocks;
     DropArgs drop;
 };
@@ -136,6 +137,17 @@ inline cudaError_t for_stream_dtype(fa_dtype dt, fa_dtype st, F f) {
         return st == FA_F32 ? f(d, std::integral_constant<int, FA_F32>{}) : f(d, d);
     });
 }
+
+#if defined(__CUDACC__)
+// Allows ``kernel`` that much dynamic shared memory, where it is more than every kernel may have.
+template <typename Kernel>
+inline cudaError_t allow_shared(Kernel kernel, size_t bytes) {
+    constexpr size_t kAlways = 40 * 1024;  // of 48 KB, with what the kernels declare
+    if (bytes <= kAlways) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(bytes));
+}
+#endif
 
 // Defines a file's ``name``_bounds_violations over its counter.
 #if FA_BOUNDS_CHECK

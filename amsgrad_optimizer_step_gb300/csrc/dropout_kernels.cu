@@ -1,9 +1,14 @@
 // Dropout whose mask is drawn again wherever it is needed and never stored.
 //
 // One Philox block of 128 bits serves a run of eight columns, so a thread that takes one
-// 16-byte vector of 16-bit elements (two of FP32) draws once.  Rows that lie densely are one
-// long row of runs; others go in blocks of 64 columns, eight lanes each, as whole 16-byte
-// vectors where they are aligned and as the 16-byte lines around them where not.
+// 16-byte vector of 16-bit elements (two of FP32) draws once.  Rows that lie densely and aligned are
+// one long row of runs.  Rows at other addresses are taken in the vectors that memory has, and it is
+// the random bits that are moved to where their columns lie in them, from the lane before; where
+// input and output lie differently in their vectors, the data are moved too, by eight lanes with
+// two runs each.
+//
+// Reads and writes bound the first (16384 x 5632 BF16: 56 us, 6.6 TB/s); moving data bound odd rows
+// (4099 x 5633 FP16: 37 us with a run a lane, 33 with two, of which the bytes need 14).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -20,7 +25,9 @@ namespace {
 
 constexpr int kDropThreads = 256;
 constexpr int kDropLanes = 8;  // per block of columns
-constexpr int kDropBlock = kDropLanes * kRun;
+constexpr int kPair = 2 * kRun;  // consecutive columns of a lane
+constexpr int kDropBlock = kDropLanes * kPair;
+static_assert(kDropBlock == kDropColumns, "the host limits the blocks");
 
 __device__ __forceinline__ void drop(const DropArgs &d, const Kept &kept, float *x) {
 #pragma unroll
@@ -54,43 +61,122 @@ __global__ void __launch_bounds__(kDropThreads) dropout_dense_kernel(DropoutArgs
     }
 }
 
-template <int DT, bool ALIGNED>
+// Rows whose vectors hold the same columns of input and output.  A warp takes 31 vectors (pairs of
+// them for FP32) of eight elements of a row; its first lane draws the bits that the second needs of
+// the run before.
+constexpr int kShiftedVectors = 31;
+template <int DT>
+__global__ void __launch_bounds__(kDropThreads) dropout_shifted_kernel(DropoutArgs a) {
+    using T = typename Elem<DT>::T;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * (kDropThreads / 32) + threadIdx.x / 32;
+    if (w >= a.x.rows * a.blocks) return;  // a whole warp
+    const int lane = threadIdx.x % 32;
+    const int64_t row = a.by_blocks.quotient(static_cast<uint32_t>(w));
+    const int64_t u = (w - row * a.blocks) * kShiftedVectors + lane - 1;
+    const T *from = static_cast<const T *>(a.x.p) + row * a.x.ld;
+    T *to = static_cast<T *>(a.out.p) + row * a.out.ld;
+    // columns of the row's first vector that are before it
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15) / sizeof(T);
+    const int64_t c = u * kRun - shift, end = c + kRun < a.x.cols ? c + kRun : a.x.cols;
+    const int64_t begin = c < 0 ? 0 : c;
+    const bool any = lane > 0 && begin < end && fa_in_bounds(begin, end - begin, a.x.cols);
+    const bool whole = any && end - begin == kRun;
+    float x[kRun];
+    if (whole) {
+        Raw<DT, kRun> raw;
+        raw.load(from + c);
+        raw.widen(x);
+    } else if (any) {
+#pragma unroll
+        for (int j = 0; j < kRun; ++j)
+            x[j] = c + j >= begin && c + j < end ? Elem<DT>::widen(from[c + j]) : 0.f;
+    }
+    Kept kept;
+    kept.draw(a.drop, row * ((a.x.cols + kRun - 1) / kRun) + u, drop_call(a.drop));
+    if (shift) {  // the same for all lanes
+        uint32_t cat[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            cat[k] = __shfl_up_sync(0xffffffffu, kept.w[k], 1);
+            cat[4 + k] = kept.w[k];
+        }
+        move_down<4>(cat, 2 * (kRun - shift), kept.w);
+    }
+    if (!any) return;
+    drop(a.drop, kept, x);
+    if (whole) {
+        store_n<DT, kRun>(to + c, x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kRun; ++j)
+            if (c + j >= begin && c + j < end) to[c + j] = Elem<DT>::round(x[j]);
+    }
+}
+
+template <int DT>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(DropoutArgs a) {
+    using T = typename Elem<DT>::T;
     const int64_t b = static_cast<int64_t>(blockIdx.x) * (kDropThreads / kDropLanes) +
                       threadIdx.x / kDropLanes;
     if (b >= a.x.rows * a.blocks) return;  // all eight lanes of a block
     const int64_t row = a.by_blocks.quotient(static_cast<uint32_t>(b));
-    const int64_t c = (b - row * a.blocks) * kDropBlock + threadIdx.x % kDropLanes * kRun;
-    const Raw<DT, kRun> raw = load_run<DT, ALIGNED>(a.x, row, c);
-    Kept kept;
-    kept.draw(a.drop, row * ((a.x.cols + kRun - 1) / kRun) + c / kRun, drop_call(a.drop));
-    float x[kRun];
+    const int64_t c = (b - row * a.blocks) * kDropBlock + threadIdx.x % kDropLanes * kPair;
+    const int64_t left = a.x.cols - c;
+    int valid = left < 0 ? 0 : left < kPair ? static_cast<int>(left) : kPair;
+    if (valid && !fa_in_bounds(c, valid, a.x.cols)) valid = 0;
+    RawAny<DT, kPair> raw;
+    raw.load(static_cast<const T *>(a.x.p) + row * a.x.ld + c, valid,
+             Span(a.x.p, ((a.x.rows - 1) * a.x.ld + a.x.cols) * sizeof(T)));
+    float x[kPair];
     raw.widen(x);
-    drop(a.drop, kept, x);
-    store_run<DT, ALIGNED>(a.out, row, c, x, 0xffu << (threadIdx.x & 24), kDropLanes);
+    const uint64_t call = drop_call(a.drop);
+    const int64_t block = row * ((a.x.cols + kRun - 1) / kRun) + c / kRun;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        Kept kept;
+        kept.draw(a.drop, block + r, call);
+        drop(a.drop, kept, x + r * kRun);
+    }
+    store_any<DT, kPair>(static_cast<T *>(a.out.p) + row * a.out.ld + c, x, valid,
+                         0xffu << (threadIdx.x & 24), kDropLanes);
+}
+
+// Whether every row of the two starts at the same place of a vector.
+bool alike(const MatrixArgs &x, const MatrixArgs &y, int64_t size) {
+    const auto at = [](const MatrixArgs &m) { return reinterpret_cast<uintptr_t>(m.p) % 16; };
+    return at(x) == at(y) && (x.rows == 1 || (x.ld - y.ld) * size % 16 == 0);
 }
 
 }  // namespace
 
 FA_BOUNDS_VIOLATIONS(dropout_bounds_violations, g_dropout_oob)
 
-cudaError_t launch_dropout(const DropoutArgs &a, fa_dtype dt, cudaStream_t stream) {
-    const bool vec = aligned_rows(a.x, dt) && aligned_rows(a.out, dt);
+cudaError_t launch_dropout(const DropoutArgs &args, fa_dtype dt, cudaStream_t stream) {
+    DropoutArgs a = args;
+    const int64_t runs = (a.x.cols + kRun - 1) / kRun;
     const bool dense = a.x.cols % kRun == 0 &&
-                       (a.x.rows == 1 || (a.x.ld == a.x.cols && a.out.ld == a.out.cols));
+                       (a.x.rows == 1 || (a.x.ld == a.x.cols && a.out.ld == a.out.cols)) &&
+                       aligned_rows(a.x, dt) && aligned_rows(a.out, dt);
     return for_dtype(dt, [&](auto d) {
-        if (vec && dense) {
+        const auto grid = [](int64_t units, int64_t each) {
+            return static_cast<unsigned>((units + each - 1) / each);
+        };
+        if (dense) {
             constexpr int R = 2;
-            const int64_t runs = a.x.rows * (a.x.cols / kRun);
-            const int64_t ctas = (runs + R * kDropThreads - 1) / (R * kDropThreads);
             dropout_dense_kernel<d(), R>
-                <<<static_cast<unsigned>(ctas), kDropThreads, 0, stream>>>(a);
-        } else {
-            constexpr int kBlocks = kDropThreads / kDropLanes;
-            const int64_t ctas = (a.x.rows * a.blocks + kBlocks - 1) / kBlocks;
-            auto *kernel = vec ? dropout_kernel<d(), true> : dropout_kernel<d(), false>;
-            kernel<<<static_cast<unsigned>(ctas), kDropThreads, 0, stream>>>(a);
+                <<<grid(a.x.rows * runs, R * kDropThreads), kDropThreads, 0, stream>>>(a);
+            return cudaGetLastError();
         }
+        const bool shifted = alike(a.x, a.out, sizeof(typename Elem<d()>::T));
+        // (a row that begins inside a vector may have one more than its runs)
+        a.blocks = shifted ? runs / kShiftedVectors + 1 : (a.x.cols + kDropBlock - 1) / kDropBlock;
+        a.by_blocks = Divider(static_cast<uint32_t>(a.blocks));
+        if (shifted)
+            dropout_shifted_kernel<d()>
+                <<<grid(a.x.rows * a.blocks, kDropThreads / 32), kDropThreads, 0, stream>>>(a);
+        else
+            dropout_kernel<d()><<<grid(a.x.rows * a.blocks, kDropThreads / kDropLanes),
+                                  kDropThreads, 0, stream>>>(a);
         return cudaGetLastError();
     });
 }

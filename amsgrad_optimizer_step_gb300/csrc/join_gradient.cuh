@@ -634,8 +634,7 @@ __global__ void __launch_bounds__(32 * kJoinSlices) join_sums_kernel(JoinGradArg
 template <typename Kernel>
 cudaError_t launch_rows(Kernel kernel, const JoinGradArgs &a, int threads, size_t smem,
                         cudaStream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_shared(kernel, smem);
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(a.plan.ctas), threads, smem, stream>>>(a);
     return cudaGetLastError();

@@ -353,8 +353,7 @@ template <int DT, int ST, int R, bool VEC, bool RING, bool DROP>
 cudaError_t launch_as(const JoinArgs &a, dim3 block, size_t smem, bool stage,
                       cudaStream_t stream) {
     auto *kernel = join_kernel<DT, ST, R, VEC, RING, DROP>;
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_shared(kernel, smem);
     if (e != cudaSuccess) return e;
     int64_t grid = (a.rows + block.y - 1) / block.y;
     if (grid > kSms) grid = kSms;  // the SMs are full, and the weights are staged once

@@ -585,12 +585,8 @@ cudaError_t launch_route(const RouteArgs &a, fa_dtype dt, cudaStream_t stream) {
             auto *kernel = a.top_k <= kListed ? route_kernel<d(), l(), r(), true>
                                               : route_kernel<d(), l(), r(), false>;
             const size_t smem = route_shared<l(), r()>(a);
-            if (smem > 48 * 1024) {
-                const cudaError_t e =
-                    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-                if (e != cudaSuccess) return e;
-            }
+            const cudaError_t e = allow_shared(kernel, smem);
+            if (e != cudaSuccess) return e;
             if (a.plan.ctas)
                 kernel<<<static_cast<unsigned>(a.plan.ctas), kRouteThreads, smem, stream>>>(a, vec);
             return cudaGetLastError();

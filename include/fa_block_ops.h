@@ -49,7 +49,7 @@ typedef struct fa_dropout_key {
  * (the pages have no counterpart).  The gradient is the same call on the
  * output's gradient.  out may be x itself (same pointer and ld).  rows == 0 or
  * cols == 0: nothing is launched or checked.  FA_ERR_SIZE for more than 2^31 - 1 blocks
- * of 64 columns (rows * ceil(cols / 64)).
+ * of 128 columns (rows * ceil(cols / 128)).
  */
 fa_status fa_dropout(int64_t rows, int64_t cols, const void *x, int64_t x_ld, fa_dtype dtype,
                      const fa_dropout_key *key, void *out, int64_t out_ld, void *stream);

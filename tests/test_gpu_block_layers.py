@@ -2,11 +2,14 @@
 routed block that uses them together."""
 
 import math
+import os
+import sys
 
 import pytest
 import torch
 
 import block_reference as B
+from conftest import ROOT
 from model_reference import DTYPES, U32, UNIT, assert_close
 from test_gpu_model_ops import gen, randn
 
@@ -266,3 +269,48 @@ def test_a_routed_block(layers):
     for name, a, b in zip(p, grads, torch.autograd.grad(want, list(q.values()))):
         # products of up to 64 terms on both sides of every operator, of the order of the largest
         assert bool(((a.double() - b).abs() <= 2000 * U32 * b.abs().max()).all()), name
+
+
+@pytest.fixture(scope="module")
+def example():
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    try:
+        import preference_training
+    finally:
+        sys.path.pop(0)
+    return preference_training
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_the_example_trains_with_joined_blocks(example, dt):
+    out = example.train(steps=6, dtype=dt, joins=True, log=lambda *_: None)
+    assert all(math.isfinite(x) for x in out["losses"]) and out["skipped"] <= 2
+
+
+def test_the_examples_gradients(layers, example):
+    """Along its own gradient a loss changes by the gradient's square: central differences in FP32,
+    dropout on.  The MLPs' gradients come from inputs kept in 8 bits, each off by 1/254 of its
+    block's largest at most; a hundredth of the whole is a generous bound on their sum."""
+    model = example.SmallModel(97, 48, 64, 2, torch.float32, DEV, joins=True, dropout=0.2)
+    ids = torch.randint(0, 97, (200,), device=DEV, generator=gen(15))
+
+    def loss():
+        model.calls = 0  # the same elements are dropped
+        return layers.token_logprobs(model(ids), ids).double().mean()
+
+    params = list(model.parameters())
+    grads = torch.autograd.grad(loss(), params)
+    assert all(bool(g.any()) for g in grads)
+    square = sum(g.double().square().sum() for g in grads).item()
+    step = 1e-2 / math.sqrt(square)
+    ends = []
+    for sign in (1, -1):
+        with torch.no_grad():
+            for w, g in zip(params, grads):
+                w.add_(g, alpha=sign * step)
+        ends.append(loss().item())
+        with torch.no_grad():
+            for w, g in zip(params, grads):
+                w.sub_(g, alpha=sign * step)
+    change = (ends[0] - ends[1]) / (2 * step)
+    assert abs(change - square) < 0.01 * square

@@ -132,6 +132,13 @@ __device__ __forceinline__ float sum_of_pair(uint64_t p) {
 }
 
 template <int DT>
+__device__ __forceinline__ float one_weight(const JoinArgs &a, const void *p, int64_t at,
+                                            float offset) {
+    if (!p) return 1.f;
+    return offset + (a.wide_weights ? static_cast<const float *>(p)[at]
+                                    : Elem<DT>::widen(static_cast<const typename Elem<DT>::T *>(p)[at]));
+}
+template <int DT>
 __device__ __forceinline__ void store_weight(void *p, bool wide, int64_t at, float x) {
     if (wide)
         static_cast<float *>(p)[at] = x;
@@ -211,11 +218,10 @@ join_gradient_kernel(JoinGradArgs a) {
         keep(0, r, w);
     }
     float *const sums = a.sums + blockIdx.x * a.plan.parts * a.plan.pitch;
-    // the gate's group of the row, and the turns that its rows begin and end with (where a group is
-    // all rows, the first CTA counts as the one that begins it)
+    // the gate's group of the row, and the turns that its rows begin and end with
     int64_t group = own_gate ? a.j.by_group.quotient(static_cast<uint32_t>(first)) : 0;
-    int64_t group_begin = own_gate ? group * a.j.group_rows - first : -static_cast<int64_t>(blockIdx.x);
-    int64_t group_end = own_gate ? group_begin + a.j.group_rows : gridDim.x == 1 ? count : count + 1;
+    int64_t group_begin = own_gate ? group * a.j.group_rows - first : 0;
+    int64_t group_end = own_gate ? group_begin + a.j.group_rows : count + 1;
     bool flushed = false;
 
     const auto new_group = [&] {
@@ -231,6 +237,19 @@ join_gradient_kernel(JoinGradArgs a) {
     };
     // The group's sums: whole where all its rows are this CTA's, else a part of them.
     const auto flush = [&] {
+        if (!own_gate) {  // K itself: what it is times is the same for all CTAs
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int c = (r * blockDim.x + threadIdx.x) * kRun, valid = valid_cols(c, cols);
+                float k[kRun];
+                from_pairs(sum_k[r], k);
+                float *const at = sums + kPost * a.plan.pitch + c;
+#pragma unroll
+                for (int j = 0; j < kRun; ++j)
+                    if (j < valid) at[j] = scale * k[j];
+            }
+            return;
+        }
         const bool begun_here = group_begin >= 0, whole = begun_here && group_end <= count;
         float *const gate_part = sums + (begun_here ? kTail : kHead) * a.plan.pitch;
 #pragma unroll
@@ -445,9 +464,10 @@ __global__ void __launch_bounds__(kMaxThreads) join_gradient_wide_kernel(JoinGra
     // lanes of one warp hold consecutive runs, and all of them take every turn
     const int64_t turns = (blocks + blockDim.x - 1) / blockDim.x;
     float *const sums = a.sums + blockIdx.x * a.plan.parts * a.plan.pitch;
-    int64_t group = a.j.gate ? a.j.by_group.quotient(static_cast<uint32_t>(first)) : 0;
-    int64_t group_first = a.j.gate ? group * a.j.group_rows : first;
-    int64_t group_last = a.j.gate ? group_first + a.j.group_rows : last;
+    const bool own_gate = a.j.gate && a.j.group_rows < a.j.rows;
+    int64_t group = own_gate ? a.j.by_group.quotient(static_cast<uint32_t>(first)) : 0;
+    int64_t group_first = own_gate ? group * a.j.group_rows : first;
+    int64_t group_last = own_gate ? group_first + a.j.group_rows : last;
     bool flushed = false;
     fa_allow_dependents();
 
@@ -491,6 +511,12 @@ __global__ void __launch_bounds__(kMaxThreads) join_gradient_wide_kernel(JoinGra
         }
     };
     const auto flush = [&] {
+        if (!own_gate) {  // K itself
+            for (int64_t q = threadIdx.x; q < blocks; q += blockDim.x)
+                for (int j = 0; j < valid_cols(q * kRun, a.j.cols); ++j)
+                    sums[kPost * a.plan.pitch + q * kRun + j] = scale * sum_k[q * kRun + j];
+            return;
+        }
         const bool begun_here = group_first >= first, whole = begun_here && group_last <= last;
         float *const gate_part = sums + (begun_here ? kTail : kHead) * a.plan.pitch;
         for (int64_t q = threadIdx.x; q < blocks; q += blockDim.x) {
@@ -584,51 +610,72 @@ __global__ void __launch_bounds__(kMaxThreads) join_gradient_wide_kernel(JoinGra
                 sums[kPre * a.plan.pitch + q * kRun + j] = sum_p[q * kRun + j];
 }
 
-// Joins the CTAs' sums in order.  A block takes 32 columns of one result, 16 runs of CTAs
-// side by side.  blockIdx.y: the first weight, the second, then the gate's groups, or (where
-// there are more groups than CTAs) the border before each CTA, whose group it joins if it is
-// the group's first border.
-constexpr int kJoinSlices = 16;
+// Joins the CTAs' sums in order: K for the first weight and a gate that all rows share, the second
+// weight's, then the gate's groups, or (where there are more groups than CTAs) the border before each
+// CTA, whose group it joins if it is the group's first border.  A block takes 32 columns and 16 runs
+// of CTAs side by side, or 128 and four of a group, whose rows few CTAs share.
+constexpr int kSumThreads = 512;
 template <int DT>
-__global__ void __launch_bounds__(32 * kJoinSlices) join_sums_kernel(JoinGradArgs a) {
-    __shared__ float part[kJoinSlices][32];
+__global__ void __launch_bounds__(kSumThreads) join_sums_kernel(JoinGradArgs a) {
+    __shared__ float part[kSumThreads];
     fa_grid_dependency_wait();
-    const int64_t col = blockIdx.x * 32 + threadIdx.x;
     const JoinPlan &p = a.plan;
+    const int cols = static_cast<int>(a.j.cols), blocks = (cols + 31) / 32;
+    const int wide_blocks = (cols + 127) / 128;
+    const int b = blockIdx.x;
+    const int what = b < blocks ? kPost : b < 2 * blocks ? kPre : kHead;
+    const int width = what == kHead ? 128 : 32, slices = kSumThreads / width;
+    const int x = threadIdx.x % width, y = threadIdx.x / width;
     int64_t c0 = 0, c1 = p.ctas - 1, group = 0;
-    const int what = blockIdx.y < 2 ? static_cast<int>(blockIdx.y) : kHead;
-    if (what == kPost && !a.dpost_weight) return;
+    int col = b % blocks * 32 + x;
+    // a gate of several groups is in the first weight's sum already, and has sums of its own
+    const bool own_gate = a.j.gate && a.j.group_rows < a.j.rows;
     if (what == kPre && !a.dpre_weight) return;
+    if (what == kPost && !a.dpost_weight && (own_gate || !a.dgate)) return;
     if (what == kHead) {
-        group = blockIdx.y - 2;
+        const int64_t at = (b - 2 * blocks) / wide_blocks;
+        col = (b - 2 * blocks) % wide_blocks * 128 + x;
+        group = at;
         if (a.groups > p.ctas) {
-            const int64_t row = (group + 1) * p.chunk;
+            const int64_t row = (at + 1) * p.chunk;
             if (row >= a.j.rows || row % a.j.group_rows == 0) return;
             group = row / a.j.group_rows;
         }
         c0 = group * a.j.group_rows / p.chunk;
         c1 = ((group + 1) * a.j.group_rows - 1) / p.chunk;
         if (c0 == c1) return;  // written by its CTA
-        if (a.groups > p.ctas && c0 != static_cast<int64_t>(blockIdx.y) - 2) return;
+        if (a.groups > p.ctas && c0 != at) return;
     }
     float s = 0.f;
-    if (col < a.j.cols) {
+    if (col < cols) {
         // a group's first CTA began it: its part is the tail
 #pragma unroll 8
-        for (int64_t c = c0 + threadIdx.y; c <= c1; c += kJoinSlices) {
+        for (int64_t c = c0 + y; c <= c1; c += slices) {
             const int row = what == kHead && c == c0 ? kTail : what;
             const int64_t at = (c * p.parts + row) * p.pitch + col;
             if (fa_in_bounds(at, 1, p.ctas * p.parts * p.pitch)) s += a.sums[at];
         }
     }
-    part[threadIdx.y][threadIdx.x] = s;
+    part[threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y || col >= a.j.cols) return;
+    if (y || col >= cols) return;
     s = 0.f;
-#pragma unroll
-    for (int k = 0; k < kJoinSlices; ++k) s += part[k][threadIdx.x];
-    void *out = what == kPost ? a.dpost_weight : what == kPre ? a.dpre_weight : a.dgate;
-    store_weight<DT>(out, a.j.wide_weights, (what == kHead ? group * a.dgate_ld : 0) + col, s);
+    for (int k = 0; k < slices; ++k) s += part[k * width + x];
+    const bool wide = a.j.wide_weights;
+    if (what == kHead) {
+        store_weight<DT>(a.dgate, wide, group * a.dgate_ld + col, s);
+    } else if (what == kPre) {
+        store_weight<DT>(a.dpre_weight, wide, col, s);
+    } else if (own_gate) {
+        store_weight<DT>(a.dpost_weight, wide, col, s);
+    } else {
+        if (a.dpost_weight)
+            store_weight<DT>(a.dpost_weight, wide, col, s * one_weight<DT>(a.j, a.j.gate, col, 0.f));
+        if (a.dgate)
+            store_weight<DT>(a.dgate, wide, col,
+                             s * one_weight<DT>(a.j, a.j.post_norm ? a.j.post_weight : nullptr, col,
+                                                a.j.weight_offset));
+    }
 }
 
 template <typename Kernel>
@@ -676,10 +723,11 @@ cudaError_t launch_gradient(const JoinGradArgs &a, cudaStream_t stream) {
         err = launch_rows(join_gradient_wide_kernel<DT, ST>, a, shape.threads,
                           2 * a.plan.pitch * sizeof(float), stream);
     if (err != cudaSuccess || (!a.dpost_weight && !a.dpre_weight && !a.dgate)) return err;
-    const int64_t groups = !a.dgate ? 0 : a.groups > a.plan.ctas ? a.plan.ctas - 1 : a.groups;
-    const dim3 grid(static_cast<unsigned>((a.j.cols + 31) / 32),
-                    static_cast<unsigned>(2 + groups));
-    return launch_dependent(join_sums_kernel<DT>, grid, dim3(32, kJoinSlices), 0, stream, a);
+    const bool own_gate = a.dgate && a.j.group_rows < a.j.rows;
+    const int64_t groups = !own_gate ? 0 : a.groups > a.plan.ctas ? a.plan.ctas - 1 : a.groups;
+    const int64_t blocks = 2 * ((a.j.cols + 31) / 32) + groups * ((a.j.cols + 127) / 128);
+    return launch_dependent(join_sums_kernel<DT>, dim3(static_cast<unsigned>(blocks)),
+                            dim3(kSumThreads), 0, stream, a);
 }
 
 cudaError_t read_row_error(int *flag, bool clear) {

@@ -101,9 +101,10 @@ __device__ __forceinline__ void join_pairs(uint64_t alpha, uint64_t *p, const ui
 
 // Many rows.  blockDim: the lanes of a team, the teams; R runs a lane.  VEC: rows of whole, aligned
 // runs (else they are read from any address).  RING: the runs of the team's next row are asked for
-// while it works on this one.  DROP: false where nothing is dropped.
-template <int DT, int ST, int R, bool VEC, bool RING, bool DROP>
-__global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool stage) {
+// while it works on this one.  ALL: a branch that is normed, a gate that all rows share or none, and
+// both results (asked once, not in every row).  DROP: false where nothing is dropped.
+template <int DT, int ST, int R, bool VEC, bool RING, bool ALL, bool DROP>
+__global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool staged_weights) {
     constexpr int kD = Raw<DT, kRun>::kWords, kS = Raw<ST, kRun>::kWords;
     extern __shared__ float4 staged[];
     __shared__ Parts parts;
@@ -111,8 +112,9 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
     const float inv_cols = 1.f / static_cast<float>(cols);
     const int q0 = threadIdx.x, lanes = blockDim.x;  // this lane's runs: q0, q0 + lanes, ...
     const int threads = blockDim.x * blockDim.y, thread = threadIdx.y * lanes + q0;
-    const bool branch = a.branch.p, dropped = DROP && a.dropped;
-    const bool own_gate = a.gate && (!stage || a.group_rows < a.rows);  // read row by row
+    const bool stage = ALL || staged_weights;
+    const bool branch = ALL || a.branch.p, dropped = DROP && (ALL || a.dropped);
+    const bool own_gate = !ALL && a.gate && (!stage || a.group_rows < a.rows);  // row by row
     // the weights, as two planes of four columns of each run: the scale of the branch with its
     // norm's weight and a gate that all rows share, and the second norm's weight
     float4 *const plane_post = staged, *const plane_pre = staged + 2 * runs;
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
             }
         }
         float rstd = 1.f;
-        if (a.post_norm) {
+        if (ALL || a.post_norm) {
             rstd = team_rstd<DT, R>(y, inv_cols, a.eps, parts.at[turn] + team_part);
             turn ^= 1;
             if (a.post_rstd && q0 == 0) a.post_rstd[row] = rstd;
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
             from_pairs(p, v);
             x[r].from(v);  // as it is stored
             if (VEC) {
-                if (a.out.p && q < runs) store_raw<ST>(a.out, row, q * kRun, x[r]);
+                if ((ALL || a.out.p) && q < runs) store_raw<ST>(a.out, row, q * kRun, x[r]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kRun; ++j)  // what is not there adds nothing to the sum
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
             }
             if (VEC && q >= runs) zero(x[r]);
         }
-        if (!a.normed.p) continue;
+        if (!ALL && !a.normed.p) continue;
         // the norm is that of the stored values
         rstd = team_rstd<ST, R>(x, inv_cols, a.eps, parts.at[turn] + team_part);
         turn ^= 1;
@@ -349,16 +351,25 @@ __global__ void __launch_bounds__(32 * kMaxWarps) join_few_kernel(JoinArgs a, bo
     store(a.normed, std::integral_constant<int, DT>{});
 }
 
-template <int DT, int ST, int R, bool VEC, bool RING, bool DROP>
+template <int DT, int ST, int R, bool VEC, bool RING, bool ALL, bool DROP>
 cudaError_t launch_as(const JoinArgs &a, dim3 block, size_t smem, bool stage,
                       cudaStream_t stream) {
-    auto *kernel = join_kernel<DT, ST, R, VEC, RING, DROP>;
+    auto *kernel = join_kernel<DT, ST, R, VEC, RING, ALL, DROP>;
     const cudaError_t e = allow_shared(kernel, smem);
     if (e != cudaSuccess) return e;
     int64_t grid = (a.rows + block.y - 1) / block.y;
     if (grid > kSms) grid = kSms;  // the SMs are full, and the weights are staged once
     kernel<<<static_cast<unsigned>(grid), block, smem, stream>>>(a, stage);
     return cudaGetLastError();
+}
+
+template <int DT, int ST, int R, bool RING>
+cudaError_t launch_parts(const JoinArgs &a, dim3 block, size_t smem, cudaStream_t stream) {
+    const bool all = a.branch.p && a.post_norm && a.out.p && a.normed.p &&
+                     (!a.gate || a.group_rows >= a.rows);
+    return !all ? launch_as<DT, ST, R, true, RING, false, true>(a, block, smem, true, stream)
+           : a.dropped ? launch_as<DT, ST, R, true, RING, true, true>(a, block, smem, true, stream)
+                       : launch_as<DT, ST, R, true, RING, true, false>(a, block, smem, true, stream);
 }
 
 template <int DT, int ST, int R, bool VEC>
@@ -379,12 +390,12 @@ cudaError_t launch_many(const JoinArgs &a, cudaStream_t stream) {
         if (4 * room >= 3 * static_cast<int>(block.y)) {
             const dim3 fewer(block.x, room);
             const size_t smem = weights + static_cast<size_t>(team) * room;
-            return a.dropped
-                       ? launch_as<DT, ST, R, true, true, true>(a, fewer, smem, true, stream)
-                       : launch_as<DT, ST, R, true, true, false>(a, fewer, smem, true, stream);
+            return launch_parts<DT, ST, R, true>(a, fewer, smem, stream);
         }
     }
-    return launch_as<DT, ST, R, VEC, false, true>(a, block, stage ? weights : 0, stage, stream);
+    if constexpr (VEC && ST == FA_F32)
+        if (stage) return launch_parts<DT, ST, R, false>(a, block, weights, stream);
+    return launch_as<DT, ST, R, VEC, false, false, true>(a, block, stage ? weights : 0, stage, stream);
 }
 
 }  // namespace

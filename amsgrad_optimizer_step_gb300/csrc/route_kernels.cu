@@ -230,12 +230,17 @@ route_kernel(RouteArgs a, bool vec) {
             if (DT == FA_F32) again = __any_sync(0xffffffffu, same && on);
         }
         if (again) choose_whole<L, N>(x, part, experts, k, take);
-        float top = x[0];
+        // the first choice is the row's largest logit
+        float ex[kItems], picked = 0.f;
 #pragma unroll
-        for (int j = 1; j < N; ++j) top = fmaxf(top, x[j]);
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int s = 0; s < kItems; ++s) {
+            ex[s] = 0.f;
+            if (s * L + part < k && on) {
+                const auto *p = static_cast<const typename Elem<DT>::T *>(a.logits.p);
+                ex[s] = Elem<DT>::widen(p[t * a.logits.ld + item[s]]);
+            }
+        }
+        const float top = __shfl_sync(0xffffffffu, ex[0], 0, L);
         float total = 0.f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -243,17 +248,13 @@ route_kernel(RouteArgs a, bool vec) {
             total += x[j];
         }
         total = group_sum<L>(total);
-        float ex[kItems], picked = 0.f;
 #pragma unroll
-        for (int s = 0; s < kItems; ++s) {
-            ex[s] = 0.f;
+        for (int s = 0; s < kItems; ++s)
             if (s * L + part < k && on) {
-                const auto *p = static_cast<const typename Elem<DT>::T *>(a.logits.p);
-                ex[s] = exp2_fast((Elem<DT>::widen(p[t * a.logits.ld + item[s]]) - top) * kLog2E);
+                ex[s] = exp2_fast((ex[s] - top) * kLog2E);
                 picked += ex[s];
                 if (sums) atomicAdd(count + item[s], 1);
             }
-        }
         picked = group_sum<L>(picked);
         const float factor = __fdividef(a.weight_scale, a.renormalise ? picked : total);
 #pragma unroll
@@ -270,7 +271,7 @@ route_kernel(RouteArgs a, bool vec) {
 #pragma unroll
             for (int j = 0; j < N; ++j) prob[j] = fmaf(x[j], inv, prob[j]);
             if (part == 0) {
-                const float lse = top + logf(total);
+                const float lse = top + __logf(total);
                 z = fmaf(lse, lse, z);
                 ++counted;
             }
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(kGradThreads) route_gradient_kernel(RouteGradA
             mean = fmaf(x[j], load[j], mean);
         }
         mean = group_sum<L>(mean);
-        float same = fmaf(zc, lse.x + logf(lse.y), -mean);
+        float same = fmaf(zc, lse.x + __logf(lse.y), -mean);
         // without renormalising, every expert takes from the chosen ones' weights
         if (a.dweights && !r.renormalise) same -= back * r.weight_scale;
 #pragma unroll

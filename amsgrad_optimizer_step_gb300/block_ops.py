@@ -35,17 +35,19 @@ _F32, _I32, _I64, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
 def _mat(name: str, t: torch.Tensor, shape, dtype) -> tuple[int, int]:
     """Pointer and row distance of a matrix of this shape and type, with adjacent elements in a
     row."""
+    if t.dtype is dtype and t.is_contiguous() and t.shape == shape:
+        return t.data_ptr(), shape[1]
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.shape == shape:
-        row, col = t.stride()
-        if col == 1 and row >= shape[1]:
-            return t.data_ptr(), row
     return t.data_ptr(), _rows(name, t, shape)
 
 
 def _mat_or_none(name: str, t: Optional[torch.Tensor], shape, dtype) -> tuple[Optional[int], int]:
-    return (None, shape[1]) if t is None else _mat(name, t, shape, dtype)
+    if t is None:
+        return None, shape[1]
+    if t.dtype is dtype and t.is_contiguous() and t.shape == shape:
+        return t.data_ptr(), shape[1]
+    return _mat(name, t, shape, dtype)
 
 
 def _vec_or_none(name: str, t: Optional[torch.Tensor], n: int, dtype) -> Optional[int]:

@@ -101,8 +101,8 @@ __device__ __forceinline__ void join_pairs(uint64_t alpha, uint64_t *p, const ui
 
 // Many rows.  blockDim: the lanes of a team, the teams; R runs a lane.  VEC: rows of whole, aligned
 // runs (else they are read from any address).  RING: the runs of the team's next row are asked for
-// while it works on this one.  ALL: a branch that is normed, a gate that all rows share or none, and
-// both results (asked once, not in every row).  DROP: false where nothing is dropped.
+// while it works on this one.  ALL: a branch, a gate that all rows share or none, and both results
+// (asked once, not in every row).  DROP: false where nothing is dropped.
 template <int DT, int ST, int R, bool VEC, bool RING, bool ALL, bool DROP>
 __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool staged_weights) {
     constexpr int kD = Raw<DT, kRun>::kWords, kS = Raw<ST, kRun>::kWords;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
             }
         }
         float rstd = 1.f;
-        if (ALL || a.post_norm) {
+        if (a.post_norm) {
             rstd = team_rstd<DT, R>(y, inv_cols, a.eps, parts.at[turn] + team_part);
             turn ^= 1;
             if (a.post_rstd && q0 == 0) a.post_rstd[row] = rstd;
@@ -365,7 +365,7 @@ cudaError_t launch_as(const JoinArgs &a, dim3 block, size_t smem, bool stage,
 
 template <int DT, int ST, int R, bool RING>
 cudaError_t launch_parts(const JoinArgs &a, dim3 block, size_t smem, cudaStream_t stream) {
-    const bool all = a.branch.p && a.post_norm && a.out.p && a.normed.p &&
+    const bool all = a.branch.p && a.out.p && a.normed.p &&
                      (!a.gate || a.group_rows >= a.rows);
     return !all ? launch_as<DT, ST, R, true, RING, false, true>(a, block, smem, true, stream)
            : a.dropped ? launch_as<DT, ST, R, true, RING, true, true>(a, block, smem, true, stream)

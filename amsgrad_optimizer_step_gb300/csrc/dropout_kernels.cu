@@ -61,10 +61,11 @@ __global__ void __launch_bounds__(kDropThreads) dropout_dense_kernel(DropoutArgs
     }
 }
 
-// Rows whose vectors hold the same columns of input and output.  A warp takes 31 vectors (pairs of
-// them for FP32) of eight elements of a row; its first lane draws the bits that the second needs of
-// the run before.
-constexpr int kShiftedVectors = 31;
+// Rows whose vectors hold the same columns of input and output.  A warp takes twice 31 vectors
+// (pairs of them for FP32) of eight elements of a row; its first lane draws the bits that the second
+// needs of the run before.
+constexpr int kShiftedLanes = 31, kShiftedTurns = 2;
+constexpr int kShiftedVectors = kShiftedTurns * kShiftedLanes;
 template <int DT>
 __global__ void __launch_bounds__(kDropThreads) dropout_shifted_kernel(DropoutArgs a) {
     using T = typename Elem<DT>::T;
@@ -72,44 +73,56 @@ __global__ void __launch_bounds__(kDropThreads) dropout_shifted_kernel(DropoutAr
     if (w >= a.x.rows * a.blocks) return;  // a whole warp
     const int lane = threadIdx.x % 32;
     const int64_t row = a.by_blocks.quotient(static_cast<uint32_t>(w));
-    const int64_t u = (w - row * a.blocks) * kShiftedVectors + lane - 1;
-    const T *from = static_cast<const T *>(a.x.p) + row * a.x.ld;
-    T *to = static_cast<T *>(a.out.p) + row * a.out.ld;
+    const int64_t part = w - row * a.blocks, run0 = part * kShiftedVectors, col0 = run0 * kRun;
+    const T *row_from = static_cast<const T *>(a.x.p) + row * a.x.ld;
     // columns of the row's first vector that are before it
-    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15) / sizeof(T);
-    const int64_t c = u * kRun - shift, end = c + kRun < a.x.cols ? c + kRun : a.x.cols;
-    const int64_t begin = c < 0 ? 0 : c;
-    const bool any = lane > 0 && begin < end && fa_in_bounds(begin, end - begin, a.x.cols);
-    const bool whole = any && end - begin == kRun;
-    float x[kRun];
-    if (whole) {
-        Raw<DT, kRun> raw;
-        raw.load(from + c);
-        raw.widen(x);
-    } else if (any) {
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(row_from) & 15) / sizeof(T);
+    // a lane's elements, counted from col0: c to c + 8 (a turn further on in the second turn), as
+    // far as the row has them
+    const int c0 = (lane - 1) * kRun - shift, low = part ? -kRun : 0;
+    const int left = static_cast<int>(min(a.x.cols - col0, static_cast<int64_t>(1) << 20));
+    const T *from = row_from + col0 + c0;
+    T *to = static_cast<T *>(a.out.p) + row * a.out.ld + col0 + c0;
+    Raw<DT, kRun> raw[kShiftedTurns];
+    bool any[kShiftedTurns], whole[kShiftedTurns];
 #pragma unroll
-        for (int j = 0; j < kRun; ++j)
-            x[j] = c + j >= begin && c + j < end ? Elem<DT>::widen(from[c + j]) : 0.f;
+    for (int r = 0; r < kShiftedTurns; ++r) {
+        const int c = c0 + r * kShiftedLanes * kRun, begin = max(c, low), end = min(c + kRun, left);
+        any[r] = lane > 0 && begin < end && fa_in_bounds(col0 + begin, end - begin, a.x.cols);
+        whole[r] = any[r] && end - begin == kRun;
+        if (whole[r]) raw[r].load(from + r * kShiftedLanes * kRun);
     }
-    Kept kept;
-    kept.draw(a.drop, row * ((a.x.cols + kRun - 1) / kRun) + u, drop_call(a.drop));
-    if (shift) {  // the same for all lanes
-        uint32_t cat[8];
+    const uint64_t call = drop_call(a.drop);
+    const int64_t block = row * ((a.x.cols + kRun - 1) / kRun) + run0 + (lane - 1);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            cat[k] = __shfl_up_sync(0xffffffffu, kept.w[k], 1);
-            cat[4 + k] = kept.w[k];
+    for (int r = 0; r < kShiftedTurns; ++r) {
+        const int c = c0 + r * kShiftedLanes * kRun;
+        if (c - c0 >= left + kRun) return;  // all lanes: nothing of the row is left
+        Kept kept;
+        kept.draw(a.drop, block + r * kShiftedLanes, call);
+        if (shift) {  // the same for all lanes
+            uint32_t cat[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                cat[k] = __shfl_up_sync(0xffffffffu, kept.w[k], 1);
+                cat[4 + k] = kept.w[k];
+            }
+            move_down<4>(cat, 2 * (kRun - shift), kept.w);
         }
-        move_down<4>(cat, 2 * (kRun - shift), kept.w);
-    }
-    if (!any) return;
-    drop(a.drop, kept, x);
-    if (whole) {
-        store_n<DT, kRun>(to + c, x);
-    } else {
+        const T *p = from + r * kShiftedLanes * kRun;
+        T *q = to + r * kShiftedLanes * kRun;
+        if (whole[r]) {
+            float x[kRun];
+            raw[r].widen(x);
+            drop(a.drop, kept, x);
+            store_n<DT, kRun>(q, x);
+        } else if (any[r]) {
 #pragma unroll
-        for (int j = 0; j < kRun; ++j)
-            if (c + j >= begin && c + j < end) to[c + j] = Elem<DT>::round(x[j]);
+            for (int j = 0; j < kRun; ++j)
+                if (c + j >= max(c, low) && c + j < min(c + kRun, left))
+                    q[j] = Elem<DT>::round(kept(j, a.drop.threshold)
+                                               ? Elem<DT>::widen(p[j]) * a.drop.scale : 0.f);
+        }
     }
 }
 

@@ -583,8 +583,9 @@ cudaError_t launch_route(const RouteArgs &a, fa_dtype dt, cudaStream_t stream) {
     const bool vec = aligned_rows(a.logits, dt);
     const cudaError_t err = for_dtype(dt, [&](auto d) {
         return for_lanes(a.logits.cols, [&](auto l, auto r) {
-            auto *kernel = a.top_k <= kListed ? route_kernel<d(), l(), r(), true>
-                                              : route_kernel<d(), l(), r(), false>;
+            auto *kernel = route_kernel<d(), l(), r(), true>;
+            if constexpr (l() > 1)  // (one lane: there are no more experts than a list has)
+                if (a.top_k > kListed) kernel = route_kernel<d(), l(), r(), false>;
             const size_t smem = route_shared<l(), r()>(a);
             const cudaError_t e = allow_shared(kernel, smem);
             if (e != cudaSuccess) return e;
@@ -612,8 +613,9 @@ cudaError_t launch_route_gradient(const RouteGradArgs &a, fa_dtype dt, cudaStrea
     if (ctas > 3 * kSms) ctas = 3 * kSms;
     return for_dtype(dt, [&](auto d) {
         return for_lanes(a.r.logits.cols, [&](auto l, auto r) {
-            auto *kernel = a.r.top_k <= kListed ? route_gradient_kernel<d(), l(), r(), true>
-                                                : route_gradient_kernel<d(), l(), r(), false>;
+            auto *kernel = route_gradient_kernel<d(), l(), r(), true>;
+            if constexpr (l() > 1)
+                if (a.r.top_k > kListed) kernel = route_gradient_kernel<d(), l(), r(), false>;
             kernel<<<static_cast<unsigned>(ctas), kGradThreads, 0, stream>>>(a, vec);
             return cudaGetLastError();
         });

@@ -7,8 +7,9 @@
 // input and output lie differently in their vectors, the data are moved too, by eight lanes with
 // two runs each.
 //
-// Reads and writes bound the first (16384 x 5632 BF16: 56 us, 6.6 TB/s); moving data bound odd rows
-// (4099 x 5633 FP16: 37 us with a run a lane, 33 with two, of which the bytes need 14).
+// Reads and writes bound the first (16384 x 5632 BF16: 56 us, 6.6 TB/s); issue slots bound
+// odd rows, most of them the generator's (4099 x 5633 FP16: 25 us, of which the bytes need 14; moving
+// all data with a run a lane took 37, with two 33).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -8,6 +8,12 @@
 // the first norm's mean, which needs the second's gradient G = t - rstd_pre * mean(s1) * xh, is
 // s2 - rstd_pre * mean(s1) * s3.  The gradients of the first weight and of the gate are both
 // multiples, column by column, of K = sum over rows of v G: one sum serves both.
+//
+// 16384 x 2048 BF16, everything on, takes 74 us of which the bytes need 59 (66 without dropout): a
+// row's reduction, whose wait the other CTAs of an SM hide, and issue slots bound it.  Copies of 16
+// bytes by every thread took 89; two CTAs an SM instead of three, two runs a thread, or the next
+// row's first half before a row's second where only one CTA fits (8192 x 4096: 89 against 78): no
+// faster.  The CTAs' sums are joined in 6 to 11 us.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -11,8 +11,9 @@
 // than eight are chosen.  Sums over tokens stay with the lane that holds the expert, then go by
 // CTA and in order.
 //
-// Instructions bound it, not memory: 65536 tokens, 8 of 128 experts, BF16, took 51 us with a
-// maximum over all keys for every choice, of which the bytes need 3.
+// Instructions bound it, not memory: 65536 tokens, 8 of 128 experts, BF16, take 21 us, of which
+// the bytes need 3 (51 with a maximum over all keys for every choice), the join of the CTAs' sums 7.5
+// and the gradient 16.5; 8 of 256, FP32, 46, 7.6 and 30.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -45,6 +45,7 @@ struct JoinArgs {
     float residual_scale, branch_scale, eps, weight_offset;
     float *post_rstd, *pre_rstd;  // or nullptr
     DropArgs drop;
+    int32_t ld8;  // the matrices' common_ld8 where rows are taken that begin anywhere, else -1
 };
 cudaError_t launch_block_join(const JoinArgs &a, fa_dtype dt, fa_dtype st, cudaStream_t stream);
 

@@ -2,6 +2,8 @@
 // FA_BOUNDS_COUNTER first.
 #pragma once
 
+#include <initializer_list>
+
 #include "block_internal.h"
 #include "model_runs.cuh"
 #include "philox.cuh"
@@ -37,6 +39,70 @@ __device__ __forceinline__ void load_weights(const JoinArgs &a, const void *p, i
     }
 #pragma unroll
     for (int j = 0; j < kRun; ++j) w[j] += offset;
+}
+
+template <int DT>
+__device__ __forceinline__ float one_weight(const JoinArgs &a, const void *p, int64_t at,
+                                            float offset) {
+    if (!p) return 1.f;
+    return offset + (a.wide_weights ? static_cast<const float *>(p)[at]
+                                    : Elem<DT>::widen(static_cast<const typename Elem<DT>::T *>(p)[at]));
+}
+// Of a run that begins at column ``c``, which may be negative: its weights, zeros in place of what is
+// no column, and the stores of what is one.
+__device__ __forceinline__ bool is_column(int c, int cols) {
+    return static_cast<unsigned>(c) < static_cast<unsigned>(cols);
+}
+template <int DT>
+__device__ __forceinline__ void load_columns(const JoinArgs &a, const void *p, int64_t row0, int c,
+                                             int cols, float offset, float *w) {
+#pragma unroll
+    for (int j = 0; j < kRun; ++j)
+        w[j] = is_column(c + j, cols) ? one_weight<DT>(a, p, row0 + c + j, offset) : 0.f;
+}
+template <int DT>
+__device__ __forceinline__ void keep_columns(Raw<DT, kRun> &x, int c, int cols) {
+    float v[kRun];
+    x.widen(v);
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) v[j] = is_column(c + j, cols) ? v[j] : 0.f;
+    x.from(v);  // exact: they came from this type
+}
+template <int DT>
+__device__ __forceinline__ void store_columns(typename Elem<DT>::T *p, const float *v, int c, int cols) {
+#pragma unroll
+    for (int j = 0; j < kRun; ++j)
+        if (is_column(c + j, cols)) p[j] = Elem<DT>::round(v[j]);
+}
+template <int DT>
+__device__ __forceinline__ void store_columns(const MatrixArgs &m, int64_t row, const float *v, int c) {
+    store_columns<DT>(static_cast<typename Elem<DT>::T *>(m.p) + row * m.ld + c, v, c,
+                      static_cast<int>(m.cols));
+}
+// (c: where a line begins in memory)
+template <int DT>
+__device__ __forceinline__ Raw<DT, kRun> read_columns(const MatrixArgs &m, int64_t row, int c) {
+    const auto *p = static_cast<const typename Elem<DT>::T *>(m.p) + row * m.ld + c;
+    const int cols = static_cast<int>(m.cols);
+    Raw<DT, kRun> x;
+    if (c >= 0 && c + kRun <= cols) {
+        x.load(p);
+    } else {
+        float v[kRun];
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) v[j] = is_column(c + j, cols) ? Elem<DT>::widen(p[j]) : 0.f;
+        x.from(v);  // exact: they came from this type
+    }
+    return x;
+}
+// Asks a vector of 16-bit columns into a slot: zeros behind the last one, the end of the row before in
+// front of the first.
+template <int DT>
+__device__ __forceinline__ void ask_columns(const MatrixArgs &m, int64_t row, int c, uint4 *slot) {
+    static_assert(Raw<DT, kRun>::kWords == 1, "a vector");
+    const int left = static_cast<int>(m.cols) - c, n = left < kRun ? left : kRun;
+    if (n <= 0 || !fa_in_bounds(row * m.ld + c, n, (m.rows - 1) * m.ld + m.cols)) return;
+    copy_async16(slot, static_cast<const typename Elem<DT>::T *>(m.p) + row * m.ld + c, 2 * n);
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -118,6 +184,19 @@ template <int DT>
 __device__ __forceinline__ void take_run(const uint4 *slot, int stride, Raw<DT, kRun> &x) {
 #pragma unroll
     for (int k = 0; k < Raw<DT, kRun>::kWords; ++k) x.r[k] = slot[k * stride];
+}
+
+// The row distance modulo eight that all of the matrices have that are there, where they begin on a
+// 16-byte boundary; else -1.  Their 16-byte lines then begin at the same columns in a row of all of
+// them, and at the same ones again eight rows on.
+inline int common_ld8(std::initializer_list<const MatrixArgs *> matrices) {
+    int64_t ld8 = -1;
+    for (const MatrixArgs *m : matrices) {
+        if (!m->p) continue;
+        if (reinterpret_cast<uintptr_t>(m->p) % 16 || (ld8 >= 0 && m->ld % kRun != ld8)) return -1;
+        ld8 = m->ld % kRun;
+    }
+    return static_cast<int>(ld8);
 }
 
 }  // namespace fa

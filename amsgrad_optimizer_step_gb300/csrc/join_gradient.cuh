@@ -55,23 +55,46 @@ struct Ring {
         const int n = (kSmShared / ctas - 2048 - weights) / bytes(threads);
         return n < kMost ? n : kMost;
     }
+    // Bytes to copy of a row whose first run begins ``shift`` columns before it: its 16-byte lines, of
+    // the last row without one that ends behind the matrix.
+    static __device__ __forceinline__ uint32_t lines(const JoinGradArgs &a, int64_t row, int shift,
+                                                     int size) {
+        const int bytes = (static_cast<int>(a.j.cols) + shift) * size;
+        return (row + 1 < a.j.rows ? bytes + 15 : bytes) & ~15;
+    }
     // By one thread: asks for a row.
-    static __device__ __forceinline__ void issue(const JoinGradArgs &a, int64_t row, uint4 *slot,
-                                                 uint64_t *bar) {
+    static __device__ __forceinline__ void issue(const JoinGradArgs &a, int64_t row, int shift,
+                                                 uint4 *slot, uint64_t *bar) {
         if (!fa_in_bounds(row, 1, a.j.rows)) return;
-        const int runs = static_cast<int>(a.j.cols) / kRun, reach = R * blockDim.x;
-        const uint32_t s = 16 * kS * runs, d = 16 * kD * runs;
+        const int reach = R * blockDim.x;
+        const uint32_t s = lines(a, row, shift, 2 * kS), d = lines(a, row, shift, 2 * kD);
         row_expect(bar, (a.dout.p ? s : 0) + (a.out.p ? s : 0) + (a.dnormed.p ? d : 0) +
                             (a.j.branch.p ? d : 0));
         const auto copy = [&](const MatrixArgs &m, int size, uint32_t bytes, int at) {
             if (m.p)
-                row_copy(slot + at * reach, static_cast<const char *>(m.p) + row * m.ld * size,
+                row_copy(slot + at * reach, static_cast<const char *>(m.p) + (row * m.ld - shift) * size,
                          bytes, bar);
         };
         copy(a.dout, 2 * kS, s, 0);
         copy(a.out, 2 * kS, s, kS);
         copy(a.dnormed, 2 * kD, d, 2 * kS);
         copy(a.j.branch, 2 * kD, d, 2 * kS + kD);
+    }
+    // By the thread of the last row's last run: what ``lines`` left out.
+    static __device__ void complete(const JoinGradArgs &a, int64_t row, int shift, uint4 *slot) {
+        const int cols = static_cast<int>(a.j.cols), reach = R * blockDim.x;
+        const auto copy = [&](const MatrixArgs &m, auto type, int at) {
+            using T = typename Elem<decltype(type)::value>::T;
+            T *const to = reinterpret_cast<T *>(slot + at * reach) + shift;
+            const T *const from = static_cast<const T *>(m.p) + row * m.ld;
+            const int there = static_cast<int>(lines(a, row, shift, sizeof(T)) / sizeof(T)) - shift;
+            for (int c = there; m.p && c < cols; ++c)
+                if (fa_in_bounds(c, 1, cols)) to[c] = from[c];
+        };
+        copy(a.dout, std::integral_constant<int, ST>{}, 0);
+        copy(a.out, std::integral_constant<int, ST>{}, kS);
+        copy(a.dnormed, std::integral_constant<int, DT>{}, 2 * kS);
+        copy(a.j.branch, std::integral_constant<int, DT>{}, 2 * kS + kD);
     }
     template <int W, typename T>
     static __device__ __forceinline__ void take(const uint4 *at, T &x) {
@@ -138,13 +161,6 @@ __device__ __forceinline__ float sum_of_pair(uint64_t p) {
 }
 
 template <int DT>
-__device__ __forceinline__ float one_weight(const JoinArgs &a, const void *p, int64_t at,
-                                            float offset) {
-    if (!p) return 1.f;
-    return offset + (a.wide_weights ? static_cast<const float *>(p)[at]
-                                    : Elem<DT>::widen(static_cast<const typename Elem<DT>::T *>(p)[at]));
-}
-template <int DT>
 __device__ __forceinline__ void store_weight(void *p, bool wide, int64_t at, float x) {
     if (wide)
         static_cast<float *>(p)[at] = x;
@@ -158,9 +174,14 @@ enum { kPost = 0, kPre = 1, kHead = 2, kTail = 3 };
 // RING: rows of whole, aligned runs that go through the ring; else each row is read when its turn
 // comes, from any address.  ALL: both norms, the branch and every matrix's gradient are there
 // (what a training step asks for, without a question a row).  DROP: false where nothing is dropped.
-template <int DT, int ST, int R, bool RING, bool ALL, bool DROP>
+// SHIFT: rows of the ring that begin anywhere.  The 16-byte lines of matrices of one row distance begin at
+// the same columns, and at the same ones again eight rows on.  A CTA's rows are a multiple of eight
+// apart, so its run q is columns [8 q - shift, 8 q - shift + 8) in all of them: whole lines but
+// for the row's two ends, and the columns' sums stay where they are.
+template <int DT, int ST, int R, bool RING, bool ALL, bool DROP, bool SHIFT>
 __global__ void __launch_bounds__(R == 1 ? kJoinThreads : kMaxThreads)
 join_gradient_kernel(JoinGradArgs a) {
+    static_assert(!SHIFT || (RING && R == 1), "a run a thread");
     extern __shared__ uint4 ring[];
     __shared__ __align__(16) float part[2][4 * kPartWarps];
     using Rows = Ring<DT, ST, R>;
@@ -173,13 +194,19 @@ join_gradient_kernel(JoinGradArgs a) {
     const int count = static_cast<int>((end - first + stride - 1) / stride);
     const bool pre = ALL || a.dnormed.p, branch = ALL || a.j.branch.p;
     const bool post = ALL || (a.j.post_norm && branch), dropped = DROP && (ALL || a.j.dropped);
-    const int cols = static_cast<int>(a.j.cols), runs = (cols + kRun - 1) / kRun;
+    const int cols = static_cast<int>(a.j.cols), row_blocks = (cols + kRun - 1) / kRun;
+    const int shift = SHIFT ? static_cast<int>(first) * a.j.ld8 % kRun : 0;
+    const int runs = SHIFT ? (cols + shift + kRun - 1) / kRun : row_blocks;
+    const auto column = [&](int r) {  // the first of run r
+        return static_cast<int>(r * blockDim.x + threadIdx.x) * kRun - shift;
+    };
+    const bool whole = !SHIFT || (column(0) >= 0 && column(0) + kRun <= cols);  // R == 1
     const float inv_cols = 1.f / static_cast<float>(cols);
     const int lane = threadIdx.x % 32;
     for (int i = threadIdx.x; i < 2 * 4 * kPartWarps; i += blockDim.x) part[0][i] = 0.f;
     const int row_vectors = RING ? Rows::kVectors * blockDim.x : 0;
     if (RING) {
-        if (runs < R * static_cast<int>(blockDim.x) || !a.dout.p || !pre || !branch) {
+        if (SHIFT || runs < R * static_cast<int>(blockDim.x) || !a.dout.p || !pre || !branch) {
             for (int i = threadIdx.x; i < a.stages * row_vectors; i += blockDim.x)
                 ring[i] = make_uint4(0u, 0u, 0u, 0u);
             shared_writes_before_copies();
@@ -189,7 +216,7 @@ join_gradient_kernel(JoinGradArgs a) {
             for (int i = 0; i < a.stages; ++i) row_barrier_init(bars + i);
             row_barriers_ready();
             for (int i = 0; i < a.stages && i < count; ++i)
-                Rows::issue(a, first + i * stride, ring + i * row_vectors, bars + i);
+                Rows::issue(a, first + i * stride, shift, ring + i * row_vectors, bars + i);
         }
     }
     __syncthreads();
@@ -214,8 +241,11 @@ join_gradient_kernel(JoinGradArgs a) {
     uint64_t sum_k[R][kPairs] = {}, sum_p[R][kPairs] = {};
     // the weights of run r: what: a weight or the gate's row, ``offset`` added
     const auto weights = [&](const void *p, int64_t row0, int r, float offset, float *w) {
-        const int c = (r * blockDim.x + threadIdx.x) * kRun;
-        load_weights<DT>(a.j, p, row0 + c, valid_cols(c, cols), offset, w);
+        const int c = column(r);
+        if constexpr (SHIFT)
+            load_columns<DT>(a.j, p, row0, c, cols, offset, w);
+        else
+            load_weights<DT>(a.j, p, row0 + c, valid_cols(c, cols), offset, w);
     };
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -246,13 +276,13 @@ join_gradient_kernel(JoinGradArgs a) {
         if (!own_gate) {  // K itself: what it is times is the same for all CTAs
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int c = (r * blockDim.x + threadIdx.x) * kRun, valid = valid_cols(c, cols);
+                const int c = column(r);
                 float k[kRun];
                 from_pairs(sum_k[r], k);
                 float *const at = sums + kPost * a.plan.pitch + c;
 #pragma unroll
                 for (int j = 0; j < kRun; ++j)
-                    if (j < valid) at[j] = scale * k[j];
+                    if (is_column(c + j, cols)) at[j] = scale * k[j];
             }
             return;
         }
@@ -260,7 +290,7 @@ join_gradient_kernel(JoinGradArgs a) {
         float *const gate_part = sums + (begun_here ? kTail : kHead) * a.plan.pitch;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int c = (r * blockDim.x + threadIdx.x) * kRun, valid = valid_cols(c, cols);
+            const int c = column(r);
             float w[kRun], k[kRun];
             from_pairs(sum_k[r], k);
             if (a.dpost_weight) {
@@ -268,7 +298,7 @@ join_gradient_kernel(JoinGradArgs a) {
                 float *const at = sums + kPost * a.plan.pitch + c;
 #pragma unroll
                 for (int j = 0; j < kRun; ++j)
-                    if (j < valid) {
+                    if (is_column(c + j, cols)) {
                         const float x = scale * w[j] * k[j];
                         at[j] = flushed ? at[j] + x : x;
                     }
@@ -277,7 +307,7 @@ join_gradient_kernel(JoinGradArgs a) {
                 weights(post ? a.j.post_weight : nullptr, 0, r, a.j.weight_offset, w);
 #pragma unroll
                 for (int j = 0; j < kRun; ++j)
-                    if (j < valid) {
+                    if (is_column(c + j, cols)) {
                         const float x = scale * w[j] * k[j];
                         if (whole)
                             store_weight<DT>(a.dgate, a.j.wide_weights,
@@ -301,8 +331,8 @@ join_gradient_kernel(JoinGradArgs a) {
     int64_t row = first;
     using S = typename Elem<ST>::T;
     using D = typename Elem<DT>::T;
-    S *to_residual = static_cast<S *>(a.dresidual.p) + first * a.dresidual.ld + threadIdx.x * kRun;
-    D *to_branch = static_cast<D *>(a.dbranch.p) + first * a.dbranch.ld + threadIdx.x * kRun;
+    S *to_residual = static_cast<S *>(a.dresidual.p) + first * a.dresidual.ld + column(0);
+    D *to_branch = static_cast<D *>(a.dbranch.p) + first * a.dbranch.ld + column(0);
     const int64_t residual_step = stride * a.dresidual.ld, branch_step = stride * a.dbranch.ld;
     for (int n = 0; n < count;
          ++n, row += stride, to_residual += residual_step, to_branch += branch_step) {
@@ -323,7 +353,15 @@ join_gradient_kernel(JoinGradArgs a) {
         GradRow<DT, ST, R> g;
         if (RING) {
             failed = !row_wait(bars + stage, parity);
+            if (SHIFT && row == a.j.rows - 1 && static_cast<int>(threadIdx.x) == runs - 1)
+                Rows::complete(a, row, shift, ring + stage * row_vectors);
             Rows::read(ring + stage * row_vectors, g);
+            if (SHIFT && !whole) {  // a neighbour's elements
+                keep_columns<ST>(g.dout[0], column(0), cols);
+                keep_columns<ST>(g.x[0], column(0), cols);
+                keep_columns<DT>(g.dn[0], column(0), cols);
+                keep_columns<DT>(g.y[0], column(0), cols);
+            }
         } else {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -366,8 +404,10 @@ join_gradient_kernel(JoinGradArgs a) {
             for (int j = 0; j < kPairs; ++j) ym[r][j] = mul2(ym[r][j], both(rq));
             if (dropped) {
                 Kept kept;
-                kept.draw(a.j.drop, static_cast<uint64_t>(row) * runs + (r * blockDim.x + threadIdx.x),
-                          call);
+                const uint64_t block =
+                    static_cast<uint64_t>(row) * row_blocks + (r * blockDim.x + threadIdx.x);
+                kept.draw(a.j.drop, block, call);
+                if (SHIFT && shift) kept.begin_before(a.j.drop, block, call, shift);
                 kept.mask(ym[r], a.j.drop.threshold);
                 kept.mask(am[r], a.j.drop.threshold);
             }
@@ -388,7 +428,8 @@ join_gradient_kernel(JoinGradArgs a) {
             if (failed) break;
             // every thread has read its part of the slot
             if (threadIdx.x == 0 && n + a.stages < count)
-                Rows::issue(a, row + a.stages * stride, ring + stage * row_vectors, bars + stage);
+                Rows::issue(a, row + a.stages * stride, shift, ring + stage * row_vectors,
+                            bars + stage);
             if (++stage == a.stages) {
                 stage = 0;
                 parity ^= 1;
@@ -419,14 +460,18 @@ join_gradient_kernel(JoinGradArgs a) {
                 from_pairs(dr, v);
                 if (!RING)
                     store_run<ST, false>(a.dresidual, row, q * kRun, v, 0xffffffffu, 32);
-                else if (q < runs && fa_in_bounds(q * kRun, kRun, cols))
+                else if (SHIFT && !whole)
+                    store_columns<ST>(to_residual, v, column(0), cols);
+                else if (q < runs && fa_in_bounds(column(r), kRun, cols))
                     store_n<ST, kRun>(to_residual + r * blockDim.x * kRun, v);
             }
             if (ALL || a.dbranch.p) {
                 from_pairs(db, v);
                 if (!RING)
                     store_run<DT, false>(a.dbranch, row, q * kRun, v, 0xffffffffu, 32);
-                else if (q < runs && fa_in_bounds(q * kRun, kRun, cols))
+                else if (SHIFT && !whole)
+                    store_columns<DT>(to_branch, v, column(0), cols);
+                else if (q < runs && fa_in_bounds(column(r), kRun, cols))
                     store_n<DT, kRun>(to_branch + r * blockDim.x * kRun, v);
             }
         }
@@ -443,12 +488,12 @@ join_gradient_kernel(JoinGradArgs a) {
     if (a.dpre_weight) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int c = (r * blockDim.x + threadIdx.x) * kRun, valid = valid_cols(c, cols);
+            const int c = column(r);
             float v[kRun];
             from_pairs(sum_p[r], v);
 #pragma unroll
             for (int j = 0; j < kRun; ++j)
-                if (j < valid) sums[kPre * a.plan.pitch + c + j] = v[j];
+                if (is_column(c + j, cols)) sums[kPre * a.plan.pitch + c + j] = v[j];
         }
     }
 }
@@ -697,32 +742,52 @@ template <int DT, int ST, int R>
 cudaError_t launch_gradient_rows(const JoinGradArgs &a, bool vec, int threads,
                                  cudaStream_t stream) {
     JoinGradArgs args = a;
+    const bool shifted = a.j.ld8 >= 0;
     const int weights = 4 * R * threads * static_cast<int>(sizeof(float4));
     const int row_bytes = Ring<DT, ST, R>::bytes(threads);
     args.stages = Ring<DT, ST, R>::stages(threads, join_ctas_per_sm({threads, R}, row_bytes), weights);
     if (vec && args.stages >= 2) {
         const size_t smem = weights + args.stages * row_bytes;
         const bool all = a.j.post_norm && a.dnormed.p && a.dout.p && a.dresidual.p && a.dbranch.p;
-        auto *kernel = !all         ? join_gradient_kernel<DT, ST, R, true, false, true>
-                       : a.j.dropped ? join_gradient_kernel<DT, ST, R, true, true, true>
-                                     : join_gradient_kernel<DT, ST, R, true, true, false>;
+        auto *kernel = !all          ? join_gradient_kernel<DT, ST, R, true, false, true, false>
+                       : a.j.dropped ? join_gradient_kernel<DT, ST, R, true, true, true, false>
+                                     : join_gradient_kernel<DT, ST, R, true, true, false, false>;
+        if constexpr (R == 1)
+            if (shifted) kernel = join_gradient_kernel<DT, ST, R, true, false, true, true>;
         return launch_rows(kernel, args, threads, smem, stream);
     }
     args.stages = 0;
-    return launch_rows(join_gradient_kernel<DT, ST, R, false, false, true>, args, threads, weights,
+    return launch_rows(join_gradient_kernel<DT, ST, R, false, false, true, false>, args, threads, weights,
                        stream);
 }
 
 template <int DT, int ST>
-cudaError_t launch_gradient(const JoinGradArgs &a, cudaStream_t stream) {
+cudaError_t launch_gradient(const JoinGradArgs &given, cudaStream_t stream) {
+    JoinGradArgs a = given;
+    a.j.ld8 = -1;
     const fa_dtype dt = static_cast<fa_dtype>(DT), st = static_cast<fa_dtype>(ST);
-    const JoinShape shape = join_shape(a.j.cols);
+    JoinShape shape = join_shape(a.j.cols);
     const bool vec = a.j.cols % kRun == 0 && aligned_rows(a.j.branch, dt) && aligned_rows(a.out, st) &&
                      aligned_rows(a.dout, st) && aligned_rows(a.dnormed, dt) &&
                      aligned_rows(a.dresidual, st) && aligned_rows(a.dbranch, dt);
+    // Rows that begin anywhere, at least one a CTA, go through the ring too, if all matrices' do alike
+    // (16384 x 2047 BF16: 119 us, 188 with every run put together from two lines).  A gate's
+    // groups need a CTA's rows one after another.
+    const JoinShape wider = join_shape(a.j.cols + kRun - 1);
+    if (!vec && wider.runs == 1 && a.j.cols >= 2 * kRun && !(a.j.gate && a.j.group_rows < a.j.rows)) {
+        static_assert(kSms % kRun == 0, "a CTA's rows are a multiple of eight apart");
+        const int64_t ctas =
+            kSms * join_ctas_per_sm(wider, Ring<DT, ST, 1>::bytes(wider.threads));
+        if (a.j.rows >= ctas && ctas * a.plan.parts * a.plan.pitch * 4 <= a.plan.bytes)
+            a.j.ld8 = common_ld8({&a.j.branch, &a.out, &a.dout, &a.dnormed, &a.dresidual, &a.dbranch});
+        if (a.j.ld8 >= 0) {
+            shape = wider;
+            a.plan.ctas = ctas;
+        }
+    }
     cudaError_t err;
     if (shape.runs == 1)
-        err = launch_gradient_rows<DT, ST, 1>(a, vec, shape.threads, stream);
+        err = launch_gradient_rows<DT, ST, 1>(a, vec || a.j.ld8 >= 0, shape.threads, stream);
     else if (shape.runs == 2)
         err = launch_gradient_rows<DT, ST, 2>(a, vec, shape.threads, stream);
     else

@@ -102,34 +102,46 @@ __device__ __forceinline__ void join_pairs(uint64_t alpha, uint64_t *p, const ui
 // Many rows.  blockDim: the lanes of a team, the teams; R runs a lane.  VEC: rows of whole, aligned
 // runs (else they are read from any address).  RING: the runs of the team's next row are asked for
 // while it works on this one.  ALL: a branch, a gate that all rows share or none, and both results
-// (asked once, not in every row).  DROP: false where nothing is dropped.
-template <int DT, int ST, int R, bool VEC, bool RING, bool ALL, bool DROP>
+// (asked once, not in every row).  DROP: false where nothing is dropped.  SHIFT: rows of VEC that begin
+// anywhere, in matrices of one common_ld8.  The rows of a CTA are a multiple of eight apart, so its
+// run q is columns [8 q - shift, 8 q - shift + 8) in all of them, whole lines but for the row's
+// two ends.
+template <int DT, int ST, int R, bool VEC, bool RING, bool ALL, bool DROP, bool SHIFT>
 __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool staged_weights) {
     constexpr int kD = Raw<DT, kRun>::kWords, kS = Raw<ST, kRun>::kWords;
     extern __shared__ float4 staged[];
     __shared__ Parts parts;
-    const int cols = static_cast<int>(a.cols), runs = (cols + kRun - 1) / kRun;
+    const int cols = static_cast<int>(a.cols), row_blocks = (cols + kRun - 1) / kRun;
+    const int shift = SHIFT ? static_cast<int>(blockIdx.x) % kRun * a.ld8 % kRun : 0;
+    const int runs = SHIFT ? (cols + shift + kRun - 1) / kRun : row_blocks;
+    const auto whole = [&](int q) {  // a run of columns alone
+        return !SHIFT || (q * kRun >= shift && q * kRun - shift + kRun <= cols);
+    };
     const float inv_cols = 1.f / static_cast<float>(cols);
     const int q0 = threadIdx.x, lanes = blockDim.x;  // this lane's runs: q0, q0 + lanes, ...
     const int threads = blockDim.x * blockDim.y, thread = threadIdx.y * lanes + q0;
     const bool stage = ALL || staged_weights;
     const bool branch = ALL || a.branch.p, dropped = DROP && (ALL || a.dropped);
-    const bool own_gate = !ALL && a.gate && (!stage || a.group_rows < a.rows);  // row by row
+    const bool own_gate = !ALL && !SHIFT && a.gate && (!stage || a.group_rows < a.rows);  // row by row
     // the weights, as two planes of four columns of each run: the scale of the branch with its
     // norm's weight and a gate that all rows share, and the second norm's weight
     float4 *const plane_post = staged, *const plane_pre = staged + 2 * runs;
     const float scale = dropped ? a.drop.scale * a.branch_scale : a.branch_scale;
     for (int q = thread; stage && q < runs; q += threads) {
-        const int valid = valid_cols(q * kRun, cols);
         float w[kRun], g[kRun];
-        load_weights<DT>(a, a.post_norm ? a.post_weight : nullptr, q * kRun, valid,
-                         a.weight_offset, w);
-        load_weights<DT>(a, own_gate ? nullptr : a.gate, q * kRun, valid, 0.f, g);
+        const auto load = [&](const void *p, float offset, float *to) {
+            if constexpr (SHIFT)
+                load_columns<DT>(a, p, 0, q * kRun - shift, cols, offset, to);
+            else
+                load_weights<DT>(a, p, q * kRun, valid_cols(q * kRun, cols), offset, to);
+        };
+        load(a.post_norm ? a.post_weight : nullptr, a.weight_offset, w);
+        load(own_gate ? nullptr : a.gate, 0.f, g);
 #pragma unroll
         for (int j = 0; j < kRun; ++j) w[j] *= scale * g[j];
         plane_post[q] = make_float4(w[0], w[1], w[2], w[3]);
         plane_post[q + runs] = make_float4(w[4], w[5], w[6], w[7]);
-        load_weights<DT>(a, a.pre_weight, q * kRun, valid, a.weight_offset, w);
+        load(a.pre_weight, a.weight_offset, w);
         plane_pre[q] = make_float4(w[0], w[1], w[2], w[3]);
         plane_pre[q + runs] = make_float4(w[4], w[5], w[6], w[7]);
     }
@@ -166,9 +178,14 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
 #pragma unroll
             for (int r = 0; r < R; ++r, at += run_stride) {
                 const int q = q0 + r * lanes;
-                if (q >= runs || !fa_in_bounds(q * kRun, kRun, cols)) continue;
-                if (branch) ask_run<DT>(a.branch, row, q, at, threads);
-                ask_run<ST>(a.residual, row, q, at + kD * threads, threads);
+                if constexpr (SHIFT && RING) {
+                    if (branch) ask_columns<DT>(a.branch, row, q * kRun - shift, at);
+                    ask_columns<ST>(a.residual, row, q * kRun - shift, at + kD * threads);
+                } else {
+                    if (q >= runs || !fa_in_bounds(q * kRun, kRun, cols)) continue;
+                    if (branch) ask_run<DT>(a.branch, row, q, at, threads);
+                    ask_run<ST>(a.residual, row, q, at + kD * threads, threads);
+                }
             }
         }
         copy_async_commit();
@@ -177,6 +194,8 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
     const uint64_t alpha = both(a.residual_scale);
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
     int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (SHIFT)
+        row = blockIdx.x % kRun + static_cast<int64_t>(blockIdx.x / kRun * blockDim.y + threadIdx.y) * kRun;
     const int team_part = threadIdx.y * ((lanes / 32 + 3) / 4 * 4);
     int turn = 0, slot = 0;  // of the sums' places; of this row
     if (RING) ask(row, slot);
@@ -192,13 +211,23 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
             for (int r = 0; r < R; ++r, at += run_stride) {
                 take_run(at, threads, y[r]);
                 take_run(at + kD * threads, threads, x[r]);
+                if (SHIFT && q0 + r * lanes == 0 && shift) {  // the end of the row before
+                    keep_columns<DT>(y[r], -shift, cols);
+                    keep_columns<ST>(x[r], -shift, cols);
+                }
             }
         } else {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 zero(y[r]);
-                if (branch) y[r] = read_run<DT, VEC>(a.branch, row, q0 + r * lanes, runs);
-                x[r] = read_run<ST, VEC>(a.residual, row, q0 + r * lanes, runs);
+                if constexpr (SHIFT) {
+                    const int c = (q0 + r * lanes) * kRun - shift;
+                    if (branch) y[r] = read_columns<DT>(a.branch, row, c);
+                    x[r] = read_columns<ST>(a.residual, row, c);
+                } else {
+                    if (branch) y[r] = read_run<DT, VEC>(a.branch, row, q0 + r * lanes, runs);
+                    x[r] = read_run<ST, VEC>(a.residual, row, q0 + r * lanes, runs);
+                }
             }
         }
         float rstd = 1.f;
@@ -209,7 +238,7 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
         }
         const uint64_t root = both(rstd);
         const int64_t group = own_gate ? a.by_group.quotient(static_cast<uint32_t>(row)) : 0;
-        uint64_t block = static_cast<uint64_t>(row) * runs + q0;
+        uint64_t block = static_cast<uint64_t>(row) * row_blocks + q0;
 #pragma unroll
         for (int r = 0; r < R; ++r, block += lanes) {
             const int q = q0 + r * lanes;
@@ -232,6 +261,7 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
                 if (dropped) {
                     Kept kept;
                     kept.draw(a.drop, block, call);
+                    if (SHIFT && shift) kept.begin_before(a.drop, block, call, shift);
                     kept.mask(f, a.drop.threshold);
                 }
                 join_pairs(alpha, p, f);
@@ -242,8 +272,11 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
             float v[kRun];
             from_pairs(p, v);
             x[r].from(v);  // as it is stored
-            if (VEC) {
-                if ((ALL || a.out.p) && q < runs) store_raw<ST>(a.out, row, q * kRun, x[r]);
+            if (SHIFT && !whole(q)) {
+                if (a.out.p) store_columns<ST>(a.out, row, v, q * kRun - shift);
+                keep_columns<ST>(x[r], q * kRun - shift, cols);
+            } else if (VEC) {
+                if ((ALL || a.out.p) && q < runs) store_raw<ST>(a.out, row, q * kRun - shift, x[r]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kRun; ++j)  // what is not there adds nothing to the sum
@@ -251,7 +284,7 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
                 x[r].from(v);
                 if (a.out.p) store_run<ST, false>(a.out, row, q * kRun, v, 0xffffffffu, 32);
             }
-            if (VEC && q >= runs) zero(x[r]);
+            if (VEC && !SHIFT && q >= runs) zero(x[r]);
         }
         if (!ALL && !a.normed.p) continue;
         // the norm is that of the stored values
@@ -269,10 +302,12 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
             for (int j = 0; j < kPairs; ++j) p[j] = mul2(mul2(p[j], root_pre), w[j]);
             float v[kRun];
             from_pairs(p, v);
-            if (VEC) {
+            if (SHIFT && !whole(q)) {
+                store_columns<DT>(a.normed, row, v, q * kRun - shift);
+            } else if (VEC) {
                 Raw<DT, kRun> n;
                 n.from(v);
-                if (q < runs) store_raw<DT>(a.normed, row, q * kRun, n);
+                if (q < runs) store_raw<DT>(a.normed, row, q * kRun - shift, n);
             } else {
                 store_run<DT, false>(a.normed, row, q * kRun, v, 0xffffffffu, 32);
             }
@@ -351,14 +386,15 @@ __global__ void __launch_bounds__(32 * kMaxWarps) join_few_kernel(JoinArgs a, bo
     store(a.normed, std::integral_constant<int, DT>{});
 }
 
-template <int DT, int ST, int R, bool VEC, bool RING, bool ALL, bool DROP>
+template <int DT, int ST, int R, bool VEC, bool RING, bool ALL, bool DROP, bool SHIFT = false>
 cudaError_t launch_as(const JoinArgs &a, dim3 block, size_t smem, bool stage,
                       cudaStream_t stream) {
-    auto *kernel = join_kernel<DT, ST, R, VEC, RING, ALL, DROP>;
+    auto *kernel = join_kernel<DT, ST, R, VEC, RING, ALL, DROP, SHIFT>;
     const cudaError_t e = allow_shared(kernel, smem);
     if (e != cudaSuccess) return e;
     int64_t grid = (a.rows + block.y - 1) / block.y;
-    if (grid > kSms) grid = kSms;  // the SMs are full, and the weights are staged once
+    // the SMs are full, and the weights are staged once (SHIFT: every eighth CTA has rows of one kind)
+    if (SHIFT || grid > kSms) grid = kSms;
     kernel<<<static_cast<unsigned>(grid), block, smem, stream>>>(a, stage);
     return cudaGetLastError();
 }
@@ -372,9 +408,11 @@ cudaError_t launch_parts(const JoinArgs &a, dim3 block, size_t smem, cudaStream_
                        : launch_as<DT, ST, R, true, RING, true, false>(a, block, smem, true, stream);
 }
 
-template <int DT, int ST, int R, bool VEC>
+// VEC, SHIFT: as the kernel has them.
+template <int DT, int ST, int R, bool VEC, bool SHIFT>
 cudaError_t launch_many(const JoinArgs &a, cudaStream_t stream) {
-    const int runs = static_cast<int>((a.cols + kRun - 1) / kRun);
+    // (SHIFT: the most that a row can have)
+    const int runs = static_cast<int>((a.cols + (SHIFT ? 2 : 1) * (kRun - 1)) / kRun);
     const int warps = (runs + 32 * R - 1) / (32 * R), teams = kTeamThreads / 32 / warps;
     const int weights = 4 * static_cast<int>(sizeof(float4)) * runs;
     const bool stage = weights <= kMostShared;
@@ -390,12 +428,23 @@ cudaError_t launch_many(const JoinArgs &a, cudaStream_t stream) {
         if (4 * room >= 3 * static_cast<int>(block.y)) {
             const dim3 fewer(block.x, room);
             const size_t smem = weights + static_cast<size_t>(team) * room;
-            return launch_parts<DT, ST, R, true>(a, fewer, smem, stream);
+            if constexpr (SHIFT)
+                return launch_as<DT, ST, R, true, true, false, true, true>(a, fewer, smem, true, stream);
+            else
+                return launch_parts<DT, ST, R, true>(a, fewer, smem, stream);
         }
     }
-    if constexpr (VEC && ST == FA_F32)
-        if (stage) return launch_parts<DT, ST, R, false>(a, block, weights, stream);
-    return launch_as<DT, ST, R, VEC, false, false, true>(a, block, stage ? weights : 0, stage, stream);
+    if constexpr (SHIFT) {
+        if constexpr (ST == FA_F32)
+            return launch_as<DT, ST, R, true, false, false, true, true>(a, block, weights, true, stream);
+        else
+            return launch_many<DT, ST, R, false, false>(a, stream);
+    } else {
+        if constexpr (VEC && ST == FA_F32)
+            if (stage) return launch_parts<DT, ST, R, false>(a, block, weights, stream);
+        return launch_as<DT, ST, R, VEC, false, false, true>(a, block, stage ? weights : 0, stage,
+                                                             stream);
+    }
 }
 
 }  // namespace
@@ -406,6 +455,14 @@ cudaError_t launch_block_join(const JoinArgs &a, fa_dtype dt, fa_dtype st, cudaS
     const bool vec = a.cols % kRun == 0 && aligned_rows(a.branch, dt) &&
                      aligned_rows(a.residual, st) && aligned_rows(a.out, st) &&
                      aligned_rows(a.normed, dt);
+    // Rows that begin anywhere, in all matrices alike (16384 x 2047 BF16: 62 us, 110 with every run
+    // put together from two lines).  A gate's groups are not dealt out by eights.
+    static_assert(kSms % kRun == 0, "a CTA's rows are a multiple of eight apart");
+    JoinArgs shifted = a;
+    const bool fits = a.cols >= 2 * kRun && a.cols + 2 * (kRun - 1) <= 2 * kRun * kTeamThreads;
+    shifted.ld8 = vec || !fits || (a.gate && a.group_rows < a.rows)
+                      ? -1
+                      : common_ld8({&a.branch, &a.residual, &a.out, &a.normed});
     // few rows: fewer than four warps an SM with a run a lane
     const int64_t warps = ((a.cols + kRun - 1) / kRun + 31) / 32;
     return for_stream_dtype(dt, st, [&](auto d, auto s) {
@@ -415,11 +472,13 @@ cudaError_t launch_block_join(const JoinArgs &a, fa_dtype dt, fa_dtype st, cudaS
             return cudaGetLastError();
         }
         // two runs a lane are what 64 registers hold of the work on them
-        if (warps == 1)
-            return vec ? launch_many<d(), s(), 1, true>(a, stream)
-                       : launch_many<d(), s(), 1, false>(a, stream);
-        return vec ? launch_many<d(), s(), 2, true>(a, stream)
-                   : launch_many<d(), s(), 2, false>(a, stream);
+        const auto many = [&](auto r) {
+            return vec ? launch_many<d(), s(), r(), true, false>(a, stream)
+                   : shifted.ld8 >= 0 ? launch_many<d(), s(), r(), true, true>(shifted, stream)
+                                      : launch_many<d(), s(), r(), false, false>(a, stream);
+        };
+        return warps == 1 ? many(std::integral_constant<int, 1>{})
+                          : many(std::integral_constant<int, 2>{});
     });
 }
 

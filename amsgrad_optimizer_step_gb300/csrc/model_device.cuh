@@ -351,6 +351,13 @@ __device__ __forceinline__ void copy_async16(void *shared, const void *global) {
                  "l"(global)
                  : "memory");
 }
+// The first ``bytes`` of the 16, and zeros.
+__device__ __forceinline__ void copy_async16(void *shared, const void *global, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(shared))),
+                 "l"(global), "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void copy_async_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
 }

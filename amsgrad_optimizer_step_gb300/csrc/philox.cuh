@@ -44,6 +44,13 @@ struct Kept {
         w[2] = r.z;
         w[3] = r.w;
     }
+    // Those of a run that begins ``shift`` columns (1 to 7) before the block's, whose own are here.
+    __device__ __forceinline__ void begin_before(const DropArgs &d, uint64_t block, uint64_t call,
+                                                 int shift) {
+        const uint4 r = philox(block - 1, call, d.key);
+        const uint32_t cat[8] = {r.x, r.y, r.z, r.w, w[0], w[1], w[2], w[3]};
+        move_down<4>(cat, 16 - 2 * shift, w);
+    }
     __device__ __forceinline__ void all() { w[0] = w[1] = w[2] = w[3] = 0xffffffffu; }
     // Zeros in place of the dropped ones of four pairs.
     __device__ __forceinline__ void mask(uint64_t *p, uint32_t threshold) const {

@@ -753,7 +753,10 @@ cudaError_t launch_gradient_rows(const JoinGradArgs &a, bool vec, int threads,
                        : a.j.dropped ? join_gradient_kernel<DT, ST, R, true, true, true, false>
                                      : join_gradient_kernel<DT, ST, R, true, true, false, false>;
         if constexpr (R == 1)
-            if (shifted) kernel = join_gradient_kernel<DT, ST, R, true, false, true, true>;
+            if (shifted)
+                kernel = !all          ? join_gradient_kernel<DT, ST, R, true, false, true, true>
+                         : a.j.dropped ? join_gradient_kernel<DT, ST, R, true, true, true, true>
+                                       : join_gradient_kernel<DT, ST, R, true, true, false, true>;
         return launch_rows(kernel, args, threads, smem, stream);
     }
     args.stages = 0;
@@ -771,7 +774,7 @@ cudaError_t launch_gradient(const JoinGradArgs &given, cudaStream_t stream) {
                      aligned_rows(a.dout, st) && aligned_rows(a.dnormed, dt) &&
                      aligned_rows(a.dresidual, st) && aligned_rows(a.dbranch, dt);
     // Rows that begin anywhere, at least one a CTA, go through the ring too, if all matrices' do alike
-    // (16384 x 2047 BF16: 119 us, 188 with every run put together from two lines).  A gate's
+    // (16384 x 2047 BF16: 99 us, 188 with every run put together from two lines).  A gate's
     // groups need a CTA's rows one after another.
     const JoinShape wider = join_shape(a.j.cols + kRun - 1);
     if (!vec && wider.runs == 1 && a.j.cols >= 2 * kRun && !(a.j.gate && a.j.group_rows < a.j.rows)) {

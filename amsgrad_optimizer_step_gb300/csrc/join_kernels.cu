@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
     const int threads = blockDim.x * blockDim.y, thread = threadIdx.y * lanes + q0;
     const bool stage = ALL || staged_weights;
     const bool branch = ALL || a.branch.p, dropped = DROP && (ALL || a.dropped);
-    const bool own_gate = !ALL && !SHIFT && a.gate && (!stage || a.group_rows < a.rows);  // row by row
+    const bool own_gate = !ALL && a.gate && (!stage || a.group_rows < a.rows);  // row by row
     // the weights, as two planes of four columns of each run: the scale of the branch with its
     // norm's weight and a gate that all rows share, and the second norm's weight
     float4 *const plane_post = staged, *const plane_pre = staged + 2 * runs;
@@ -252,8 +252,11 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
                 for (int j = 0; j < kPairs; ++j) f[j] = mul2(mul2(f[j], root), w[j]);
                 if (own_gate) {
                     float g[kRun];
-                    load_weights<DT>(a, a.gate, group * a.gate_ld + q * kRun,
-                                     valid_cols(q * kRun, cols), 0.f, g);
+                    if constexpr (SHIFT)
+                        load_columns<DT>(a, a.gate, group * a.gate_ld, q * kRun - shift, cols, 0.f, g);
+                    else
+                        load_weights<DT>(a, a.gate, group * a.gate_ld + q * kRun,
+                                         valid_cols(q * kRun, cols), 0.f, g);
                     to_pairs(g, w);
 #pragma unroll
                     for (int j = 0; j < kPairs; ++j) f[j] = mul2(f[j], w[j]);
@@ -455,14 +458,13 @@ cudaError_t launch_block_join(const JoinArgs &a, fa_dtype dt, fa_dtype st, cudaS
     const bool vec = a.cols % kRun == 0 && aligned_rows(a.branch, dt) &&
                      aligned_rows(a.residual, st) && aligned_rows(a.out, st) &&
                      aligned_rows(a.normed, dt);
-    // Rows that begin anywhere, in all matrices alike (16384 x 2047 BF16: 62 us, 110 with every run
-    // put together from two lines).  A gate's groups are not dealt out by eights.
+    // Rows that begin anywhere, in all matrices alike (16384 x 2047 BF16: 64 us, and 90 with eight
+    // gates; 110 and 123 with every run put together from two lines).
     static_assert(kSms % kRun == 0, "a CTA's rows are a multiple of eight apart");
     JoinArgs shifted = a;
     const bool fits = a.cols >= 2 * kRun && a.cols + 2 * (kRun - 1) <= 2 * kRun * kTeamThreads;
-    shifted.ld8 = vec || !fits || (a.gate && a.group_rows < a.rows)
-                      ? -1
-                      : common_ld8({&a.branch, &a.residual, &a.out, &a.normed});
+    shifted.ld8 =
+        vec || !fits ? -1 : common_ld8({&a.branch, &a.residual, &a.out, &a.normed});
     // few rows: fewer than four warps an SM with a run a lane
     const int64_t warps = ((a.cols + kRun - 1) / kRun + 31) / 32;
     return for_stream_dtype(dt, st, [&](auto d, auto s) {
@@ -477,8 +479,11 @@ cudaError_t launch_block_join(const JoinArgs &a, fa_dtype dt, fa_dtype st, cudaS
                    : shifted.ld8 >= 0 ? launch_many<d(), s(), r(), true, true>(shifted, stream)
                                       : launch_many<d(), s(), r(), false, false>(a, stream);
         };
-        return warps == 1 ? many(std::integral_constant<int, 1>{})
-                          : many(std::integral_constant<int, 2>{});
+        // three warps' runs fill four warps by twos: 65153 x 515 BF16 took 98 us with one a lane and 114
+        // with two; whole runs, which wait for memory, 63 and 62 (64528 x 520)
+        return warps == 1 || (warps == 3 && shifted.ld8 >= 0)
+                   ? many(std::integral_constant<int, 1>{})
+                   : many(std::integral_constant<int, 2>{});
     });
 }
 

@@ -110,3 +110,12 @@ def test_no_access_out_of_range(checked):  # noqa: F811
                 torch.cuda.synchronize()
                 assert fa.fa_bounds_check_report() == (True, 0)
             assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("rows,groups", [(1400, 700), (1400, 7), (1400, 1400), (1401, 3), (4000, 2)])
+@pytest.mark.parametrize("kind", [KINDS[2], KINDS[3], KINDS[0]])
+def test_gates_of_several_groups(rows, groups, kind):
+    for cols in (515, 1003):
+        c = Case(rows, cols, *kind, groups=groups, p=0.1)
+        c.forward()
+        c.backward()

@@ -61,7 +61,8 @@ struct JoinPlan {
 JoinPlan join_plan(int64_t rows, int64_t cols, int64_t groups, int element_bytes);
 
 // Threads of a row of the gradient and runs of a thread: one up to 6144 columns, two up to 8192
-// (the columns' sums are two registers a column); 0: more, with the sums in shared memory.
+// (the columns' sums are two registers a column); 0: more, in clusters, or from any address with the
+// sums in shared memory.
 struct JoinShape {
     int threads, runs;
 };
@@ -83,7 +84,9 @@ struct JoinGradArgs {
     int64_t dgate_ld, groups;
     float *sums;
     JoinPlan plan;
-    int32_t stages;  // of the kernel's ring (set by the launch)
+    // set by the launch: of the kernel's ring; where a cluster has the row, its CTAs, the row's columns
+    // and the first run of the part of them that this is
+    int32_t stages, split, all_cols, first_run;
 };
 cudaError_t launch_block_join_gradient(const JoinGradArgs &a, fa_dtype dt, fa_dtype st,
                                        cudaStream_t stream);

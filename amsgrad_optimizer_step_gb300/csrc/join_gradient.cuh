@@ -16,6 +16,7 @@
 // faster.  The CTAs' sums are joined in 6 to 11 us.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -29,6 +30,8 @@ FA_BOUNDS_COUNTER(g_join_gradient_oob)
 
 namespace fa {
 namespace {
+
+namespace cg = cooperative_groups;
 
 // One row's four matrices as a thread holds them.
 template <int DT, int ST, int R>
@@ -154,6 +157,32 @@ __device__ __forceinline__ bool row_sum3(float &s1, float &s2, float &s3, float 
     return failed;
 }
 
+// The same over a row that a cluster of ``ctas`` holds: every warp writes its part into all of them.
+constexpr int kMostSplit = 4;
+constexpr int kSplitPlaces = 2 * kMostSplit * 4 * kPartWarps * static_cast<int>(sizeof(float));
+__device__ __forceinline__ bool cluster_sum3(float &s1, float &s2, float &s3,
+                                             float (*part)[4 * kPartWarps], int ctas, bool failed) {
+    cg::cluster_group cluster = cg::this_cluster();
+    float c = warp_sum3(s1, s2, s3);
+    const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
+    failed = __any_sync(0xffffffffu, failed);
+    if (lane / 8 == 3) c = failed ? 1.f : 0.f;  // in place of the sum of nothing
+    if (lane % 8 == 0) {
+        float *const mine = part[cluster.block_rank()] + lane / 8 * kPartWarps + threadIdx.x / 32;
+        for (int r = 0; r < ctas; ++r) *cluster.map_shared_rank(mine, r) = c;
+    }
+    cluster.sync();
+    c = 0.f;
+    for (int r = 0; r < ctas; ++r)
+        for (int w = lane % 8; w < warps; w += 8) c += part[r][lane / 8 * kPartWarps + w];
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    s1 = __shfl_sync(0xffffffffu, c, 0);
+    s2 = __shfl_sync(0xffffffffu, c, 8);
+    s3 = __shfl_sync(0xffffffffu, c, 16);
+    return __shfl_sync(0xffffffffu, c, 24) != 0.f;
+}
+
 __device__ __forceinline__ float sum_of_pair(uint64_t p) {
     float lo, hi;
     unpair(p, lo, hi);
@@ -177,33 +206,36 @@ enum { kPost = 0, kPre = 1, kHead = 2, kTail = 3 };
 // SHIFT: rows of the ring that begin anywhere.  The 16-byte lines of matrices of one row distance begin at
 // the same columns, and at the same ones again eight rows on.  A CTA's rows are a multiple of eight
 // apart, so its run q is columns [8 q - shift, 8 q - shift + 8) in all of them: whole lines but
-// for the row's two ends, and the columns' sums stay where they are.
-template <int DT, int ST, int R, bool RING, bool ALL, bool DROP, bool SHIFT>
-__global__ void __launch_bounds__(R == 1 ? kJoinThreads : kMaxThreads)
-join_gradient_kernel(JoinGradArgs a) {
+// for the row's two ends, and the columns' sums stay where they are.  SPLIT: ``a`` has the columns of
+// one CTA, and a cluster has the row.
+template <int DT, int ST, int R, bool RING, bool ALL, bool DROP, bool SHIFT, bool SPLIT>
+__device__ __forceinline__ void join_gradient_rows(const JoinGradArgs &a) {
     static_assert(!SHIFT || (RING && R == 1), "a run a thread");
     extern __shared__ uint4 ring[];
-    __shared__ __align__(16) float part[2][4 * kPartWarps];
+    constexpr int kParts = SPLIT ? kMostSplit : 1;  // of the row's sums
+    __shared__ __align__(16) float part[2][kParts][4 * kPartWarps];
     using Rows = Ring<DT, ST, R>;
     __shared__ uint64_t bars[Rows::kMost];
     // the CTA's rows: first, first + stride, ...
     const bool own_gate = a.j.gate && a.j.group_rows < a.j.rows;
-    const int64_t stride = own_gate ? 1 : gridDim.x;
-    const int64_t first = own_gate ? blockIdx.x * a.plan.chunk : blockIdx.x;
+    const int64_t cta = SPLIT ? blockIdx.x / a.split : blockIdx.x;  // or the cluster
+    const int64_t stride = own_gate ? 1 : a.plan.ctas;
+    const int64_t first = own_gate ? cta * a.plan.chunk : cta;
     const int64_t end = own_gate && first + a.plan.chunk < a.j.rows ? first + a.plan.chunk : a.j.rows;
     const int count = static_cast<int>((end - first + stride - 1) / stride);
     const bool pre = ALL || a.dnormed.p, branch = ALL || a.j.branch.p;
     const bool post = ALL || (a.j.post_norm && branch), dropped = DROP && (ALL || a.j.dropped);
-    const int cols = static_cast<int>(a.j.cols), row_blocks = (cols + kRun - 1) / kRun;
+    const int cols = static_cast<int>(a.j.cols), all_cols = SPLIT ? a.all_cols : cols;
+    const int row_blocks = (all_cols + kRun - 1) / kRun, first_run = SPLIT ? a.first_run : 0;
     const int shift = SHIFT ? static_cast<int>(first) * a.j.ld8 % kRun : 0;
-    const int runs = SHIFT ? (cols + shift + kRun - 1) / kRun : row_blocks;
+    const int runs = (cols + shift + kRun - 1) / kRun;
     const auto column = [&](int r) {  // the first of run r
         return static_cast<int>(r * blockDim.x + threadIdx.x) * kRun - shift;
     };
     const bool whole = !SHIFT || (column(0) >= 0 && column(0) + kRun <= cols);  // R == 1
-    const float inv_cols = 1.f / static_cast<float>(cols);
+    const float inv_cols = 1.f / static_cast<float>(all_cols);
     const int lane = threadIdx.x % 32;
-    for (int i = threadIdx.x; i < 2 * 4 * kPartWarps; i += blockDim.x) part[0][i] = 0.f;
+    for (int i = threadIdx.x; i < 2 * kParts * 4 * kPartWarps; i += blockDim.x) part[0][0][i] = 0.f;
     const int row_vectors = RING ? Rows::kVectors * blockDim.x : 0;
     if (RING) {
         if (SHIFT || runs < R * static_cast<int>(blockDim.x) || !a.dout.p || !pre || !branch) {
@@ -219,7 +251,10 @@ join_gradient_kernel(JoinGradArgs a) {
                 Rows::issue(a, first + i * stride, shift, ring + i * row_vectors, bars + i);
         }
     }
-    __syncthreads();
+    if constexpr (SPLIT)
+        cg::this_cluster().sync();
+    else
+        __syncthreads();
     const float scale = dropped ? a.j.branch_scale * a.j.drop.scale : a.j.branch_scale;
     const uint64_t call = dropped ? drop_call(a.j.drop) : 0;
     // the thread's weights, in slots of its own: w_pre, then scale * gate * w_post, of each run
@@ -253,7 +288,7 @@ join_gradient_kernel(JoinGradArgs a) {
         weights(pre ? a.j.pre_weight : nullptr, 0, r, a.j.weight_offset, w);
         keep(0, r, w);
     }
-    float *const sums = a.sums + blockIdx.x * a.plan.parts * a.plan.pitch;
+    float *const sums = a.sums + cta * a.plan.parts * a.plan.pitch;
     // the gate's group of the row, and the turns that its rows begin and end with
     int64_t group = own_gate ? a.j.by_group.quotient(static_cast<uint32_t>(first)) : 0;
     int64_t group_begin = own_gate ? group * a.j.group_rows - first : 0;
@@ -405,7 +440,7 @@ join_gradient_kernel(JoinGradArgs a) {
             if (dropped) {
                 Kept kept;
                 const uint64_t block =
-                    static_cast<uint64_t>(row) * row_blocks + (r * blockDim.x + threadIdx.x);
+                    static_cast<uint64_t>(row) * row_blocks + first_run + (r * blockDim.x + threadIdx.x);
                 kept.draw(a.j.drop, block, call);
                 if (SHIFT && shift) kept.begin_before(a.j.drop, block, call, shift);
                 kept.mask(ym[r], a.j.drop.threshold);
@@ -423,7 +458,10 @@ join_gradient_kernel(JoinGradArgs a) {
         float back = 0.f, mean = 0.f;  // times xh: taken off t; times yh: taken off dbranch
         float f1 = sum_of_pair(s1), f2 = sum_of_pair(s2), f3 = sum_of_pair(s3);
         // (the other part is still being read)
-        failed = row_sum3(f1, f2, f3, part[n % 2], failed);
+        if constexpr (SPLIT)
+            failed = cluster_sum3(f1, f2, f3, part[n % 2], a.split, failed);
+        else
+            failed = row_sum3(f1, f2, f3, part[n % 2][0], failed);
         if (RING) {
             if (failed) break;
             // every thread has read its part of the slot
@@ -498,8 +536,27 @@ join_gradient_kernel(JoinGradArgs a) {
     }
 }
 
-// Rows of more than two runs a thread: their columns' sums lie in shared memory, and a row is
-// read again from L2 once its three sums are there.
+template <int DT, int ST, int R, bool RING, bool ALL, bool DROP, bool SHIFT>
+__global__ void __launch_bounds__(R == 1 ? kJoinThreads : kMaxThreads)
+join_gradient_kernel(const __grid_constant__ JoinGradArgs a) {
+    join_gradient_rows<DT, ST, R, RING, ALL, DROP, SHIFT, false>(a);
+}
+
+// Rows wider than a CTA holds: a cluster's CTAs have a part of the columns each, and what a row's sums
+// are is exchanged.  2048 x 16384 BF16 by fours: 159 us, 2730 x 12288 by twos 121; in one CTA that reads
+// the row twice 451 and more.
+struct SplitArgs {
+    JoinGradArgs of[kMostSplit];
+};
+template <int DT, int ST>
+__global__ void __launch_bounds__(kJoinThreads)
+join_gradient_split_kernel(const __grid_constant__ SplitArgs a) {
+    join_gradient_rows<DT, ST, 1, true, false, true, false, true>(
+        a.of[cg::this_cluster().block_rank()]);
+}
+
+// Rows of more than two runs a thread, at any addresses: their columns' sums lie in shared memory, and a
+// row is read again from L2 once its three sums are there.
 template <int DT, int ST>
 __global__ void __launch_bounds__(kMaxThreads) join_gradient_wide_kernel(JoinGradArgs a) {
     extern __shared__ float wide_sums[];
@@ -764,6 +821,74 @@ cudaError_t launch_gradient_rows(const JoinGradArgs &a, bool vec, int threads,
                        stream);
 }
 
+template <typename Kernel>
+cudaError_t clusters_at_once(int *n, Kernel kernel, int threads, size_t smem, int cluster) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(kSms / cluster * cluster));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+}
+
+// Whole runs of rows that no CTA holds.  ``a.plan`` becomes the clusters'.
+template <int DT, int ST>
+cudaError_t launch_split(JoinGradArgs &a, cudaStream_t stream) {
+    const int runs = static_cast<int>(a.j.cols) / kRun;
+    SplitArgs args;
+    int threads = 0, mine = 0, weights = 0, stages = 0;
+    for (a.split = 2; a.split <= kMostSplit; a.split *= 2) {
+        mine = (runs + a.split - 1) / a.split;
+        threads = (mine + 31) / 32 * 32;
+        weights = 4 * threads * static_cast<int>(sizeof(float4));
+        stages = Ring<DT, ST, 1>::stages(threads, 1, weights + kSplitPlaces);
+        if (threads <= kJoinThreads && stages >= 2) break;
+    }
+    if (a.split > kMostSplit) return cudaErrorInvalidConfiguration;
+    const size_t smem = weights + stages * Ring<DT, ST, 1>::bytes(threads);
+    const auto kernel = join_gradient_split_kernel<DT, ST>;
+    cudaError_t e = allow_shared(kernel, smem);
+    if (e != cudaSuccess) return e;
+    int clusters = 0;  // that run side by side: 76 of two, 36 of four (38 are two rounds: 277 us for 159)
+    e = clusters_at_once(&clusters, kernel, threads, smem, a.split);
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    if (clusters > kSms / a.split) clusters = kSms / a.split;
+    a.plan.chunk = (a.j.rows + clusters - 1) / clusters;
+    a.plan.ctas = (a.j.rows + a.plan.chunk - 1) / a.plan.chunk;
+    a.stages = stages;
+    a.all_cols = static_cast<int32_t>(a.j.cols);
+    const int weight_bytes = a.j.wide_weights ? 4 : sizeof(typename Elem<DT>::T);
+    for (int i = 0; i < a.split; ++i) {
+        JoinGradArgs &p = args.of[i];
+        p = a;
+        const int64_t first = static_cast<int64_t>(i) * mine * kRun;
+        p.first_run = i * mine;
+        p.j.cols = first + mine * kRun < a.j.cols ? mine * kRun : a.j.cols - first;
+        for (MatrixArgs *m : {&p.j.branch, &p.out, &p.dout, &p.dnormed, &p.dresidual, &p.dbranch}) {
+            const bool of_branch = m == &p.j.branch || m == &p.dnormed || m == &p.dbranch;
+            const int size = of_branch ? sizeof(typename Elem<DT>::T) : sizeof(typename Elem<ST>::T);
+            if (m->p) m->p = static_cast<char *>(m->p) + first * size;
+            m->cols = p.j.cols;
+        }
+        const auto along = [&](auto &w) {
+            if (w) w = static_cast<char *>(const_cast<void *>(w)) + first * weight_bytes;
+        };
+        along(p.j.post_weight);
+        along(p.j.pre_weight);
+        along(p.j.gate);
+        along(p.dgate);
+        p.sums = a.sums + first;
+    }
+    return launch_clusters(kernel, dim3(static_cast<unsigned>(a.plan.ctas * a.split)), dim3(threads), smem,
+                           a.split, false, stream, args);
+}
+
 template <int DT, int ST>
 cudaError_t launch_gradient(const JoinGradArgs &given, cudaStream_t stream) {
     JoinGradArgs a = given;
@@ -793,6 +918,8 @@ cudaError_t launch_gradient(const JoinGradArgs &given, cudaStream_t stream) {
         err = launch_gradient_rows<DT, ST, 1>(a, vec || a.j.ld8 >= 0, shape.threads, stream);
     else if (shape.runs == 2)
         err = launch_gradient_rows<DT, ST, 2>(a, vec, shape.threads, stream);
+    else if (vec)
+        err = launch_split<DT, ST>(a, stream);
     else
         err = launch_rows(join_gradient_wide_kernel<DT, ST>, a, shape.threads,
                           2 * a.plan.pitch * sizeof(float), stream);

@@ -1,6 +1,7 @@
 """Joins of rows that begin anywhere in their 16-byte lines, as contiguous matrices of odd widths
 have them: enough rows for the paths that take them in the lines that memory has, against the
-formulas in 64 bits, in themselves and beside rows that are not finite."""
+formulas in 64 bits, in themselves and beside rows that are not finite; and rows that are wider
+than one CTA holds."""
 
 import pytest
 import torch
@@ -119,3 +120,64 @@ def test_gates_of_several_groups(rows, groups, kind):
         c = Case(rows, cols, *kind, groups=groups, p=0.1)
         c.forward()
         c.backward()
+
+
+# rows that a cluster of two or four CTAs holds, at their first and last widths, and those (6160 FP32)
+# whose row a CTA holds but no two
+@pytest.mark.parametrize("cols", [6160, 8200, 12288, 12296, 16376, 16384])
+@pytest.mark.parametrize("kind", KINDS)
+def test_wide_rows(cols, kind):
+    for rows, groups, p in ((1, 1, 0.0), (3, 3, 0.1), (77, 1, 0.1), (160, 4, 0.0)):
+        c = Case(rows, cols, *kind, groups=groups, p=p)
+        c.forward(check=False)
+        c.backward()
+
+
+@pytest.mark.parametrize("flags", FLAGS)
+def test_wide_rows_of_all_parts(flags):
+    for cols in (8200, 16384):
+        c = Case(90, cols, "bf16", "f32", "f32", **flags)
+        c.forward(check=False)
+        c.backward()
+
+
+def test_wide_rows_through_the_checked_build(checked):  # noqa: F811
+    for dt, cols in (("bf16", 8200), ("f32", 16384)):
+        c = Case(100, cols, dt, p=0.1, groups=2)
+        c.forward(check=False)
+        want = list(c.backward(check=False).values())
+        with _lib.using(checked):
+            fa.fa_bounds_check_report(clear=True)
+            got = list(c.backward(check=False, draw=False).values())
+            torch.cuda.synchronize()
+            assert fa.fa_bounds_check_report() == (True, 0)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_a_captured_gradient_that_is_replayed():
+    """Both new kinds of rows in a graph, on inputs that change between the replays."""
+    cases = [Case(1300, 515, "bf16", p=0.1), Case(20, 16384, "bf16", p=0.1), Case(20, 8200, "f32")]
+    for c in cases:
+        c.forward(check=False)
+        c.draw()
+        scratch = fa.join_scratch(c.rows, c.cols, c.groups, c.out.device)
+        outs = [torch.empty_like(t) for t in (c.residual, c.branch, c.post_weight, c.pre_weight,
+                                              c.gate)]
+
+        def run():
+            fa.fa_block_join_gradient(c.record, c.out, c.branch, c.dout, c.dnormed, outs[0],
+                                      outs[1], scratch, c.post_rstd, c.pre_rstd, c.post_weight,
+                                      c.pre_weight, c.gate, *outs[2:])
+
+        graph = torch.cuda.CUDAGraph()
+        run()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            run()
+        c.dout.mul_(-2)
+        for t in outs:
+            t.fill_(NAN)
+        graph.replay()
+        replayed = [t.clone() for t in outs]
+        run()
+        assert all(torch.equal(a, b) for a, b in zip(replayed, outs))

@@ -795,26 +795,35 @@ cudaError_t launch_rows(Kernel kernel, const JoinGradArgs &a, int threads, size_
     return cudaGetLastError();
 }
 
+// Rows that the ring of a CTA of this many threads has room for.
+template <int DT, int ST, int R>
+int ring_stages(int threads) {
+    const int row_bytes = Ring<DT, ST, R>::bytes(threads);
+    return Ring<DT, ST, R>::stages(threads, join_ctas_per_sm({threads, R}, row_bytes),
+                                   4 * R * threads * static_cast<int>(sizeof(float4)));
+}
+
 template <int DT, int ST, int R>
 cudaError_t launch_gradient_rows(const JoinGradArgs &a, bool vec, int threads,
                                  cudaStream_t stream) {
     JoinGradArgs args = a;
-    const bool shifted = a.j.ld8 >= 0;
-    const int weights = 4 * R * threads * static_cast<int>(sizeof(float4));
-    const int row_bytes = Ring<DT, ST, R>::bytes(threads);
-    args.stages = Ring<DT, ST, R>::stages(threads, join_ctas_per_sm({threads, R}, row_bytes), weights);
-    if (vec && args.stages >= 2) {
-        const size_t smem = weights + args.stages * row_bytes;
-        const bool all = a.j.post_norm && a.dnormed.p && a.dout.p && a.dresidual.p && a.dbranch.p;
-        auto *kernel = !all          ? join_gradient_kernel<DT, ST, R, true, false, true, false>
-                       : a.j.dropped ? join_gradient_kernel<DT, ST, R, true, true, true, false>
-                                     : join_gradient_kernel<DT, ST, R, true, true, false, false>;
-        if constexpr (R == 1)
-            if (shifted)
-                kernel = !all          ? join_gradient_kernel<DT, ST, R, true, false, true, true>
-                         : a.j.dropped ? join_gradient_kernel<DT, ST, R, true, true, true, true>
-                                       : join_gradient_kernel<DT, ST, R, true, true, false, true>;
-        return launch_rows(kernel, args, threads, smem, stream);
+    const size_t weights = 4 * R * threads * sizeof(float4);
+    args.stages = ring_stages<DT, ST, R>(threads);
+    if constexpr (R == 1 || DT != FA_F32) {  // (no ring has two rows of FP32 that wide)
+        if (vec && args.stages >= 2) {
+            const size_t smem = weights + args.stages * Ring<DT, ST, R>::bytes(threads);
+            const bool all =
+                a.j.post_norm && a.dnormed.p && a.dout.p && a.dresidual.p && a.dbranch.p;
+            auto *kernel = !all          ? join_gradient_kernel<DT, ST, R, true, false, true, false>
+                           : a.j.dropped ? join_gradient_kernel<DT, ST, R, true, true, true, false>
+                                         : join_gradient_kernel<DT, ST, R, true, true, false, false>;
+            if constexpr (R == 1)
+                if (a.j.ld8 >= 0)
+                    kernel = !all          ? join_gradient_kernel<DT, ST, R, true, false, true, true>
+                             : a.j.dropped ? join_gradient_kernel<DT, ST, R, true, true, true, true>
+                                           : join_gradient_kernel<DT, ST, R, true, true, false, true>;
+            return launch_rows(kernel, args, threads, smem, stream);
+        }
     }
     args.stages = 0;
     return launch_rows(join_gradient_kernel<DT, ST, R, false, false, true, false>, args, threads, weights,
@@ -913,13 +922,18 @@ cudaError_t launch_gradient(const JoinGradArgs &given, cudaStream_t stream) {
             a.plan.ctas = ctas;
         }
     }
+    // Whole rows of which no two fit beside each other are a cluster's (2048 x 8192 FP32: 107 us, 158 in
+    // one CTA without a ring; 2730 x 6144: 115 and 125).
+    const int stages = shape.runs == 1   ? ring_stages<DT, ST, 1>(shape.threads)
+                       : shape.runs == 2 ? ring_stages<DT, ST, 2>(shape.threads)
+                                         : 0;
     cudaError_t err;
-    if (shape.runs == 1)
+    if (vec && stages < 2)
+        err = launch_split<DT, ST>(a, stream);
+    else if (shape.runs == 1)
         err = launch_gradient_rows<DT, ST, 1>(a, vec || a.j.ld8 >= 0, shape.threads, stream);
     else if (shape.runs == 2)
         err = launch_gradient_rows<DT, ST, 2>(a, vec, shape.threads, stream);
-    else if (vec)
-        err = launch_split<DT, ST>(a, stream);
     else
         err = launch_rows(join_gradient_wide_kernel<DT, ST>, a, shape.threads,
                           2 * a.plan.pitch * sizeof(float), stream);

@@ -181,3 +181,12 @@ def test_a_captured_gradient_that_is_replayed():
         replayed = [t.clone() for t in outs]
         run()
         assert all(torch.equal(a, b) for a, b in zip(replayed, outs))
+
+
+@pytest.mark.parametrize("cols", [4096, 5120, 5632, 6144, 8192])
+def test_rows_of_which_a_cta_holds_one(cols):
+    for rows, groups in ((5, 1), (400, 4)):
+        for kind in (KINDS[0], KINDS[3]):
+            c = Case(rows, cols, *kind, groups=groups, p=0.1)
+            c.forward(check=False)
+            c.backward()

@@ -67,7 +67,8 @@ fa_status fa_dropout(int64_t rows, int64_t cols, const void *x, int64_t x_ld, fa
  *   xh   = out / sqrt(mean(out^2) + eps)
  *   normed = (pre_weight + weight_offset) * xh
  * D drops elements (see fa_dropout_key; NULL: none).  The second norm is that of ``out``
- * as it is stored, so it can be taken again from it bit for bit (a join without a branch).
+ * as it is stored, so it can be taken again from it bit for bit (a join without a branch, of the same
+ * rows in matrices that lie alike: of one row distance, from 16-byte boundaries).
  * Weights that are NULL are 1 (and have no offset added).
  */
 typedef struct fa_join {

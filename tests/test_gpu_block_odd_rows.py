@@ -190,3 +190,13 @@ def test_rows_of_which_a_cta_holds_one(cols):
             c = Case(rows, cols, *kind, groups=groups, p=0.1)
             c.forward(check=False)
             c.backward()
+
+
+def test_the_norm_can_be_taken_again():
+    for cols, dt, st in ((515, "bf16", "bf16"), (1003, "f32", "f32"), (2042, "f16", "f32")):
+        c = Case(1300, cols, dt, st, p=0.1)
+        c.forward(check=False)
+        again = torch.empty_like(c.normed)
+        fa.fa_block_join(fa.Join(False, eps=c.eps), c.out, None, None, again,
+                         pre_weight=c.pre_weight)
+        assert torch.equal(again, c.normed)

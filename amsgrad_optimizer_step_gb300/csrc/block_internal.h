@@ -77,6 +77,16 @@ inline int join_ctas_per_sm(const JoinShape &shape, int row_bytes) {
     return n;
 }
 
+// CTAs of the gradient of ``rows``: as many as an SM has room for, but 16 rows each at least once there
+// are 256 threads on an SM, since every CTA's sums are written and read again (5000 x 256 BF16: 23 us,
+// 31 with two rows each; 4000 x 2048 35 and 41).
+inline int64_t join_ctas(int64_t rows, const JoinShape &shape, int row_bytes) {
+    const int64_t most = kSms * join_ctas_per_sm(shape, row_bytes);
+    const int64_t filled = kSms * ((255 + shape.threads) / shape.threads);
+    const int64_t n = rows / 16 > filled ? rows / 16 : filled;
+    return n < most ? n : most;
+}
+
 struct JoinGradArgs {
     JoinArgs j;  // branch, weights, gate, scales; post_rstd and pre_rstd are read
     MatrixArgs out, dout, dnormed, dresidual, dbranch;  // p nullptr where there is none

@@ -914,7 +914,7 @@ cudaError_t launch_gradient(const JoinGradArgs &given, cudaStream_t stream) {
     if (!vec && wider.runs == 1 && a.j.cols >= 2 * kRun && !(a.j.gate && a.j.group_rows < a.j.rows)) {
         static_assert(kSms % kRun == 0, "a CTA's rows are a multiple of eight apart");
         const int64_t ctas =
-            kSms * join_ctas_per_sm(wider, Ring<DT, ST, 1>::bytes(wider.threads));
+            join_ctas(a.j.rows, wider, Ring<DT, ST, 1>::bytes(wider.threads)) / kRun * kRun;
         if (a.j.rows >= ctas && ctas * a.plan.parts * a.plan.pitch * 4 <= a.plan.bytes)
             a.j.ld8 = common_ld8({&a.j.branch, &a.out, &a.dout, &a.dnormed, &a.dresidual, &a.dbranch});
         if (a.j.ld8 >= 0) {

@@ -19,7 +19,7 @@ JoinPlan join_plan(int64_t rows, int64_t cols, int64_t groups, int element_bytes
     if (rows == 0 || cols == 0) return p;
     const JoinShape shape = join_shape(cols);
     const int reach = kRun * shape.threads * (shape.runs ? shape.runs : 1);
-    const int64_t ctas = kSms * join_ctas_per_sm(shape, reach * element_bytes);
+    const int64_t ctas = join_ctas(rows, shape, reach * element_bytes);
     p.chunk = (rows + ctas - 1) / ctas;
     p.ctas = (rows + p.chunk - 1) / p.chunk;
     p.pitch = (cols + kRun - 1) / kRun * kRun;

@@ -1,7 +1,8 @@
 // The gradient of a join: the kernels, as the files of the two kinds of stream include them
 // (the branch's type, or FP32).
 //
-// A CTA takes a run of consecutive rows and keeps the columns' sums in registers.
+// A CTA takes rows that lie a grid apart (one after another under a gate of several groups) and keeps
+// the columns' sums in registers.
 // Per row it needs three sums over the columns, in one reduction: with d = dnormed * w_pre,
 // t = dout + rstd_pre * d, a = branch_scale * gate * w_post and v = yh where it is kept,
 //   s1 = sum d xh,  s2 = sum a v t,  s3 = sum a v xh

@@ -7,9 +7,9 @@
 // integers in the logits' order with the expert's number in their low bits, so that one maximum
 // gives the expert, ties to the lower number: those of 16-bit logits hold the whole logit, those
 // of FP32 its upper bits, and where two of the keys that matter agree in these (one token in some
-// hundred) the warp chooses again by whole logits, an expert at a time, which is also how more
-// than eight are chosen.  Sums over tokens stay with the lane that holds the expert, then go by
-// CTA and in order.
+// hundred), or one lane's list gave all eight and holds no ninth to compare, the warp chooses again
+// by whole logits, an expert at a time, which is also how more than eight are chosen.  Sums over
+// tokens stay with the lane that holds the expert, then go by CTA and in order.
 //
 // Instructions bound it, not memory: 65536 tokens, 8 of 128 experts, BF16, take 21 us, of which
 // the bytes need 3 (51 with a maximum over all keys for every choice), the join of the CTAs' sums 7.5
@@ -219,6 +219,8 @@ route_kernel(RouteArgs a, bool vec) {
                 if (i > k || (i == k && (DT != FA_F32 || k == experts))) break;
                 const uint32_t best = group_max<L>(key[0]);
                 if (DT == FA_F32) same |= i > 0 && (best | kNumber) == (before | kNumber);
+                // a lane that gave all eight has no ninth in its list, which may be short of it
+                if (DT == FA_F32 && R > 1 && i == kListed) same |= key[0] == 0u;
                 before = best;
                 if (i == k) break;
                 take(i, static_cast<int>(kNumber - (best & kNumber)));

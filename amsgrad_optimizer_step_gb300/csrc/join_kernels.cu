@@ -24,7 +24,9 @@ namespace {
 constexpr int kTeamThreads = 1024;  // of a CTA and an SM at most, in 64 registers each
 constexpr int kMaxWarps = 32;
 constexpr int kMostShared = 220 * 1024;
-constexpr float kHuge = 0x1p-70f;  // rows whose squares pass FP32 are summed at this scale
+// Rows whose squares pass FP32 are summed at this scale: 2^14 squares of up to 2^96 do not, and the root
+// of such a row is 2^57 at least, so that what is lost below adds nothing to it.
+constexpr float kHuge = 0x1p-80f;
 
 // The sum over a team's lanes, in every one.  ``part``: four floats for each four warps, not in
 // use by the call before.

@@ -1,10 +1,12 @@
 """The residual blocks' operators where their numbers or their callers come to an end: choices that
-one list of the router holds alone."""
+one list of the router holds alone, and squares next to FP32's largest."""
 
 import pytest
 import torch
 
-from test_gpu_block_ops import DEV, _built, check_route  # noqa: F401
+import block_reference as B
+from model_reference import assert_close
+from test_gpu_block_ops import DEV, Case, _built, check_route  # noqa: F401
 from test_gpu_model_ops import gen
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +42,38 @@ def test_the_largest_logits_with_one_lane(experts, spread):
             logits[t, mine[7 + t // 4 % 2]] += step
     check_route(logits, 8)
     check_route(logits, 7)
+
+
+# ---- squares next to FP32's largest -----------------------------------------------------
+
+@pytest.mark.parametrize("kind", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("cols,least", [(4104, 1e38), (8192, 1e38), (8192, 2.8e38), (16383, 1e38),
+                                        (16384, 1e38)])
+def test_norms_of_the_largest_rows(kind, cols, least):
+    """Elements of 1e38 to 3e38: their roots' inverses are FP32's subnormals, which are off by half
+    of 2^-149, and the norms are of order one."""
+    half = 2.0 ** -150
+    for rows in (3, 40):
+        c = Case(rows, cols, *kind, alpha=1.0, p=0.1 if rows == 40 else 0.0, seed=cols)
+        for t, most in ((c.residual, 2.9e38), (c.branch, 3.3e38)):
+            t.copy_((least + (most - least) * torch.rand(rows, cols, device=DEV, generator=c.g)) *
+                    torch.sign(t.float()))
+        c.forward(check=False)
+        want, err, rstd = B.join(c.residual, c.branch, c.post_weight, c.gate, True, c.alpha, c.beta,
+                                 c.eps, 0.0, c.mask, c.scale)
+        share = (want - c.residual.double()).abs()
+        assert_close(c.out, want, err + share * (half / rstd), "out")
+        normed, err, pre_rstd = B.norm(c.out, c.pre_weight, c.eps, 0.0)
+        assert_close(c.normed, normed, err + normed.abs() * (half / pre_rstd), "normed")
+        for got, root in ((c.post_rstd, rstd), (c.pre_rstd, pre_rstd)):
+            assert bool(((got.double()[:, None] - root).abs() <= B.ROOT * root + 2 * half).all())
+        got = c.backward(check=False)
+        want = B.join_gradient(c.out, c.branch, c.dout, c.dnormed, c.post_rstd, c.pre_rstd,
+                               c.post_weight, c.pre_weight, c.gate, True, c.alpha, c.beta, 0.0,
+                               c.mask, c.scale)
+        yh = c.branch.double() * c.post_rstd.double()[:, None]
+        for name, x in got.items():
+            value, err = want[name]
+            if name == "dbranch":  # a difference of two subnormal products
+                err = err + 4 * half * (1 + yh.abs())
+            assert_close(x, value, err, name)

@@ -3,6 +3,7 @@
 // route_kernels.cu).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -153,13 +154,17 @@ inline cudaError_t for_stream_dtype(fa_dtype dt, fa_dtype st, F f) {
 }
 
 #if defined(__CUDACC__)
-// Allows ``kernel`` that much dynamic shared memory, where it is more than every kernel may have.
-template <typename Kernel>
-inline cudaError_t allow_shared(Kernel kernel, size_t bytes) {
-    constexpr size_t kAlways = 40 * 1024;  // of 48 KB, with what the kernels declare
-    if (bytes <= kAlways) return cudaSuccess;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(bytes));
+// Allows a kernel kMost bytes of dynamic shared memory, once on each device: what any of its calls
+// needs, since the attribute is the kernel's and other threads launch it too.
+template <auto kKernel, int kMost>
+inline cudaError_t allow_shared() {
+    static std::atomic<bool> allowed[64] = {};  // set twice by racing threads, it is the same
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && allowed[dev].load(std::memory_order_acquire))) return e;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e == cudaSuccess && dev < 64) allowed[dev].store(true, std::memory_order_release);
+    return e;
 }
 #endif
 

@@ -787,12 +787,14 @@ __global__ void __launch_bounds__(kSumThreads) join_sums_kernel(JoinGradArgs a) 
     }
 }
 
-template <typename Kernel>
-cudaError_t launch_rows(Kernel kernel, const JoinGradArgs &a, int threads, size_t smem,
-                        cudaStream_t stream) {
-    const cudaError_t e = allow_shared(kernel, smem);
+// What a CTA alone on its SM has beside a kernel's own arrays (see Ring::stages).
+constexpr int kMostShared = kSmShared - 2048;
+
+template <auto kKernel>
+cudaError_t launch_rows(const JoinGradArgs &a, int threads, size_t smem, cudaStream_t stream) {
+    const cudaError_t e = allow_shared<kKernel, kMostShared>();
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(a.plan.ctas), threads, smem, stream>>>(a);
+    kKernel<<<static_cast<unsigned>(a.plan.ctas), threads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -815,20 +817,23 @@ cudaError_t launch_gradient_rows(const JoinGradArgs &a, bool vec, int threads,
             const size_t smem = weights + args.stages * Ring<DT, ST, R>::bytes(threads);
             const bool all =
                 a.j.post_norm && a.dnormed.p && a.dout.p && a.dresidual.p && a.dbranch.p;
-            auto *kernel = !all          ? join_gradient_kernel<DT, ST, R, true, false, true, false>
-                           : a.j.dropped ? join_gradient_kernel<DT, ST, R, true, true, true, false>
-                                         : join_gradient_kernel<DT, ST, R, true, true, false, false>;
+            const auto launch = [&](auto shift) {
+                const auto as = [&](auto every, auto drop) {
+                    return launch_rows<join_gradient_kernel<DT, ST, R, true, every(), drop(), shift()>>(
+                        args, threads, smem, stream);
+                };
+                const std::true_type yes{};
+                const std::false_type no{};
+                return !all ? as(no, yes) : a.j.dropped ? as(yes, yes) : as(yes, no);
+            };
             if constexpr (R == 1)
-                if (a.j.ld8 >= 0)
-                    kernel = !all          ? join_gradient_kernel<DT, ST, R, true, false, true, true>
-                             : a.j.dropped ? join_gradient_kernel<DT, ST, R, true, true, true, true>
-                                           : join_gradient_kernel<DT, ST, R, true, true, false, true>;
-            return launch_rows(kernel, args, threads, smem, stream);
+                if (a.j.ld8 >= 0) return launch(std::true_type{});
+            return launch(std::false_type{});
         }
     }
     args.stages = 0;
-    return launch_rows(join_gradient_kernel<DT, ST, R, false, false, true, false>, args, threads, weights,
-                       stream);
+    return launch_rows<join_gradient_kernel<DT, ST, R, false, false, true, false>>(args, threads, weights,
+                                                                                  stream);
 }
 
 template <typename Kernel>
@@ -861,8 +866,8 @@ cudaError_t launch_split(JoinGradArgs &a, cudaStream_t stream) {
     }
     if (a.split > kMostSplit) return cudaErrorInvalidConfiguration;
     const size_t smem = weights + stages * Ring<DT, ST, 1>::bytes(threads);
-    const auto kernel = join_gradient_split_kernel<DT, ST>;
-    cudaError_t e = allow_shared(kernel, smem);
+    constexpr auto kernel = join_gradient_split_kernel<DT, ST>;
+    cudaError_t e = allow_shared<kernel, kMostShared - kSplitPlaces>();
     if (e != cudaSuccess) return e;
     int clusters = 0;  // that run side by side: 76 of two, 36 of four (38 are two rounds: 277 us for 159)
     e = clusters_at_once(&clusters, kernel, threads, smem, a.split);
@@ -936,8 +941,8 @@ cudaError_t launch_gradient(const JoinGradArgs &given, cudaStream_t stream) {
     else if (shape.runs == 2)
         err = launch_gradient_rows<DT, ST, 2>(a, vec, shape.threads, stream);
     else
-        err = launch_rows(join_gradient_wide_kernel<DT, ST>, a, shape.threads,
-                          2 * a.plan.pitch * sizeof(float), stream);
+        err = launch_rows<join_gradient_wide_kernel<DT, ST>>(a, shape.threads,
+                                                             2 * a.plan.pitch * sizeof(float), stream);
     if (err != cudaSuccess || (!a.dpost_weight && !a.dpre_weight && !a.dgate)) return err;
     const bool own_gate = a.dgate && a.j.group_rows < a.j.rows;
     const int64_t groups = !own_gate ? 0 : a.groups > a.plan.ctas ? a.plan.ctas - 1 : a.groups;

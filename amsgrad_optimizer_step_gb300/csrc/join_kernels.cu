@@ -394,8 +394,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps) join_few_kernel(JoinArgs a, bo
 template <int DT, int ST, int R, bool VEC, bool RING, bool ALL, bool DROP, bool SHIFT = false>
 cudaError_t launch_as(const JoinArgs &a, dim3 block, size_t smem, bool stage,
                       cudaStream_t stream) {
-    auto *kernel = join_kernel<DT, ST, R, VEC, RING, ALL, DROP, SHIFT>;
-    const cudaError_t e = allow_shared(kernel, smem);
+    constexpr auto kernel = join_kernel<DT, ST, R, VEC, RING, ALL, DROP, SHIFT>;
+    const cudaError_t e = allow_shared<kernel, kMostShared>();
     if (e != cudaSuccess) return e;
     int64_t grid = (a.rows + block.y - 1) / block.y;
     // the SMs are full, and the weights are staged once (SHIFT: every eighth CTA has rows of one kind)

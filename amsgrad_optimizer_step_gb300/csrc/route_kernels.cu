@@ -324,6 +324,8 @@ route_kernel(RouteArgs a, bool vec) {
 
 template <int L, int R>
 size_t route_shared(const RouteArgs &a) {
+    constexpr int kMost = L * R * kRun;  // experts
+    static_assert(4 * (kMost + kRouteWarps * (kMost + 2)) <= 48 * 1024, "what every kernel may have");
     return a.summary ? 4 * (a.logits.cols + kRouteWarps * (L * R * kRun + 1) + kRouteWarps) : 0;
 }
 
@@ -590,8 +592,6 @@ cudaError_t launch_route(const RouteArgs &a, fa_dtype dt, cudaStream_t stream) {
             if constexpr (l() > 1)  // (one lane: there are no more experts than a list has)
                 if (a.top_k > kListed) kernel = route_kernel<d(), l(), r(), false>;
             const size_t smem = route_shared<l(), r()>(a);
-            const cudaError_t e = allow_shared(kernel, smem);
-            if (e != cudaSuccess) return e;
             if (a.plan.ctas)
                 kernel<<<static_cast<unsigned>(a.plan.ctas), kRouteThreads, smem, stream>>>(a, vec);
             return cudaGetLastError();

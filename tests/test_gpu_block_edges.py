@@ -1,10 +1,15 @@
 """The residual blocks' operators where their numbers or their callers come to an end: choices that
-one list of the router holds alone, and squares next to FP32's largest."""
+one list of the router holds alone, squares next to FP32's largest, and calls of several threads at
+once."""
+
+import threading
+
 
 import pytest
 import torch
 
 import block_reference as B
+from amsgrad_optimizer_step_gb300 import _lib
 from model_reference import assert_close
 from test_gpu_block_ops import DEV, Case, _built, check_route  # noqa: F401
 from test_gpu_model_ops import gen
@@ -77,3 +82,60 @@ def test_norms_of_the_largest_rows(kind, cols, least):
             if name == "dbranch":  # a difference of two subnormal products
                 err = err + 4 * half * (1 + yh.abs())
             assert_close(x, value, err, name)
+
+
+# ---- several threads ---------------------------------------------------------------------
+
+class Recorded:
+    """The library, with the arguments of the joins' calls kept."""
+
+    def __init__(self):
+        self.lib, self.calls = _lib.load(), []
+
+    def __getattr__(self, name):
+        call = getattr(self.lib, name)
+        if name not in ("fa_block_join", "fa_block_join_gradient"):
+            return call
+
+        def keep(*args):
+            self.calls.append((call, args))
+            return call(*args)
+
+        return keep
+
+
+@pytest.mark.parametrize("shapes,which", [
+    (((304, 264, "bf16"), (31, 5120, "bf16")), 0), (((1, 2048, "bf16"), (1, 5120, "bf16")), 1),
+    (((1, 6160, "f32"), (1, 16384, "f32")), 1), (((1, 515, "bf16"), (1, 16383, "bf16")), 1)])
+def test_joins_of_two_widths_by_several_threads(shapes, which):
+    """One kernel with two amounts of shared memory, called as fast as threads can: no launch is
+    refused, and the results are those of a call alone."""
+    work = []
+    for i in range(6):
+        c, lib, stream = Case(*shapes[i // 3], p=0.1), Recorded(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream), _lib.using(lib):
+            c.forward(check=False)
+            made = c.backward(check=False)
+        stream.synchronize()
+        made = [c.out, c.normed, *made.values()]
+        work.append((made, [t.clone() for t in made], lib.calls[which], c))
+    torch.cuda.synchronize()
+    start, refused = threading.Event(), [0] * len(work)
+
+    def run(i):
+        call, args = work[i][2]
+        start.wait()
+        for _ in range(3000):
+            refused[i] += call(*args) != 0
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    start.set()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not any(refused), refused
+    for made, want, _, _ in work:
+        assert all(torch.equal(a, b) for a, b in zip(made, want))

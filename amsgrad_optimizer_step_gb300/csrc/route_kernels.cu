@@ -415,7 +415,9 @@ __global__ void __launch_bounds__(kSumThreads) route_sums_kernel(RouteArgs a) {
     if (lane) return;
     const float balance =
         dot * __fdiv_rn(static_cast<float>(experts), static_cast<float>(a.top_k)) * inv;
-    a.summary[0] = a.balance_coef * balance + a.z_coef * (z * inv);
+    // without a coefficient z adds nothing, its overflow (but not a NaN) included
+    const float z_loss = a.z_coef == 0.f && isinf(z) ? 0.f : a.z_coef * (z * inv);
+    a.summary[0] = a.balance_coef * balance + z_loss;
     a.summary[1] = balance;
     a.summary[2] = z * inv;
     a.summary[3] = counted;

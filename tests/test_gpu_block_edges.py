@@ -1,6 +1,6 @@
 """The residual blocks' operators where their numbers or their callers come to an end: choices that
-one list of the router holds alone, squares next to FP32's largest, and calls of several threads at
-once."""
+one list of the router holds alone, squares next to FP32's largest, losses that nobody asked
+for, and calls of several threads at once."""
 
 import threading
 
@@ -8,11 +8,12 @@ import threading
 import pytest
 import torch
 
+import amsgrad_optimizer_step_gb300 as fa
 import block_reference as B
 from amsgrad_optimizer_step_gb300 import _lib
 from model_reference import assert_close
 from test_gpu_block_ops import DEV, Case, _built, check_route  # noqa: F401
-from test_gpu_model_ops import gen
+from test_gpu_model_ops import gen, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -82,6 +83,22 @@ def test_norms_of_the_largest_rows(kind, cols, least):
             if name == "dbranch":  # a difference of two subnormal products
                 err = err + 4 * half * (1 + yh.abs())
             assert_close(x, value, err, name)
+
+
+# ---- losses ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_a_loss_that_has_no_weight_adds_nothing(dt):
+    """Logits whose squared log-sum-exp passes FP32: without a z coefficient the loss is the balance's."""
+    logits = (randn(gen(3), 70, 40) + 5e19).to(dt)
+    b = fa.route_buffers(70, 40, 4, DEV)
+    for balance in (0.5, 0.0):
+        fa.fa_route(logits, b, balance_coef=balance)
+        assert b.z.item() == float("inf") and bool(torch.isfinite(b.balance).all())
+        assert b.loss.item() == balance * b.balance.item()
+    logits[3, 5] = float("nan")  # what is not a number stays so
+    fa.fa_route(logits, b)
+    assert bool(torch.isnan(b.loss).all())
 
 
 # ---- several threads ---------------------------------------------------------------------

@@ -11,7 +11,7 @@ import torch
 import amsgrad_optimizer_step_gb300 as fa
 import block_reference as B
 from amsgrad_optimizer_step_gb300 import _lib
-from model_reference import assert_close
+from model_reference import U32, assert_close
 from test_gpu_block_ops import DEV, Case, _built, check_route  # noqa: F401
 from test_gpu_model_ops import gen, randn
 
@@ -99,6 +99,23 @@ def test_a_loss_that_has_no_weight_adds_nothing(dt):
     logits[3, 5] = float("nan")  # what is not a number stays so
     fa.fa_route(logits, b)
     assert bool(torch.isnan(b.loss).all())
+
+
+def test_the_log_of_sums_next_to_one():
+    """p * lse of the larger of two logits, 0 and -d, which the z loss's gradient is."""
+    n = 20000
+    d = torch.linspace(0, 9, n, device=DEV)
+    logits = torch.stack([torch.zeros_like(d), -d], 1)
+    b, dlogits = fa.route_buffers(n, 2, 1, DEV), torch.empty_like(logits)
+    fa.fa_route(logits, b, z_coef=n / 2)
+    fa.fa_route_gradient(logits, b, dlogits, grad_loss=torch.ones(1, device=DEV), z_coef=n / 2)
+    d, x = d.double(), logits.double()
+    lse, p = torch.logsumexp(x, 1), torch.softmax(x, 1)[:, 0]
+    # the exponential: its argument's two roundings and two units; of the sum 1 + e its share; the
+    # sum's own rounding is one of 1; the logarithm's unit; then the coefficient, p and the product
+    share = torch.exp(-d) * (2 * d + 4) / (1 + torch.exp(-d))
+    err = p * (share + 1 + 2 * lse) * U32 + p * lse * (share + 5) * U32
+    assert bool(((dlogits[:, 0].double() - p * lse).abs() <= err).all())
 
 
 # ---- several threads ---------------------------------------------------------------------

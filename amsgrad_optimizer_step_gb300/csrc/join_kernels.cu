@@ -109,7 +109,7 @@ __device__ __forceinline__ void join_pairs(uint64_t alpha, uint64_t *p, const ui
 // run q is columns [8 q - shift, 8 q - shift + 8) in all of them, whole lines but for the row's
 // two ends.
 template <int DT, int ST, int R, bool VEC, bool RING, bool ALL, bool DROP, bool SHIFT>
-__global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool staged_weights) {
+__global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a) {
     constexpr int kD = Raw<DT, kRun>::kWords, kS = Raw<ST, kRun>::kWords;
     extern __shared__ float4 staged[];
     __shared__ Parts parts;
@@ -122,14 +122,13 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
     const float inv_cols = 1.f / static_cast<float>(cols);
     const int q0 = threadIdx.x, lanes = blockDim.x;  // this lane's runs: q0, q0 + lanes, ...
     const int threads = blockDim.x * blockDim.y, thread = threadIdx.y * lanes + q0;
-    const bool stage = ALL || staged_weights;
     const bool branch = ALL || a.branch.p, dropped = DROP && (ALL || a.dropped);
-    const bool own_gate = !ALL && a.gate && (!stage || a.group_rows < a.rows);  // row by row
+    const bool own_gate = !ALL && a.gate && a.group_rows < a.rows;  // row by row
     // the weights, as two planes of four columns of each run: the scale of the branch with its
     // norm's weight and a gate that all rows share, and the second norm's weight
     float4 *const plane_post = staged, *const plane_pre = staged + 2 * runs;
     const float scale = dropped ? a.drop.scale * a.branch_scale : a.branch_scale;
-    for (int q = thread; stage && q < runs; q += threads) {
+    for (int q = thread; q < runs; q += threads) {
         float w[kRun], g[kRun];
         const auto load = [&](const void *p, float offset, float *to) {
             if constexpr (SHIFT)
@@ -149,30 +148,28 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a, bool sta
     }
     clear_parts(parts, thread, threads);
     // a lane's slots: the branch's and the stream's runs, of two rows; those of no run stay 0
-    uint4 *const ring = reinterpret_cast<uint4 *>(staged + (stage ? 4 * runs : 0)) + thread;
+    uint4 *const ring = reinterpret_cast<uint4 *>(staged + 4 * runs) + thread;
     const int run_stride = (kD + kS) * threads;
     if (RING)
         for (int k = 0; k < 2 * R * (kD + kS); ++k)
             ring[k * threads] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     const auto weights = [&](const float4 *plane, int q, uint64_t *w) {
-        if (stage) {
-            if (q >= runs) q = 0;  // not used
-            const float4 lo = plane[q], hi = plane[q + runs];
-            w[0] = pair(lo.x, lo.y);
-            w[1] = pair(lo.z, lo.w);
-            w[2] = pair(hi.x, hi.y);
-            w[3] = pair(hi.z, hi.w);
-        } else {
-            const bool post = plane == plane_post;
-            float x[kRun];
-            load_weights<DT>(a, !post ? a.pre_weight : a.post_norm ? a.post_weight : nullptr,
-                             q * kRun, valid_cols(q * kRun, cols), a.weight_offset, x);
-            to_pairs(x, w);
+        // (what is not there is not read: read all the same, a join without its second norm spilled
+        // registers, 39 us for 33 at 16384 x 2048 BF16)
+        const bool post = plane == plane_post;
+        if (!ALL && !SHIFT &&
+            !(post ? a.gate || (a.post_norm && a.post_weight) : a.pre_weight != nullptr)) {
 #pragma unroll
-            for (int j = 0; j < kPairs; ++j)
-                if (post) w[j] = mul2(w[j], both(scale));
+            for (int j = 0; j < kPairs; ++j) w[j] = both(post ? scale : 1.f);
+            return;
         }
+        if (q >= runs) q = 0;  // not used
+        const float4 lo = plane[q], hi = plane[q + runs];
+        w[0] = pair(lo.x, lo.y);
+        w[1] = pair(lo.z, lo.w);
+        w[2] = pair(hi.x, hi.y);
+        w[3] = pair(hi.z, hi.w);
     };
     const auto ask = [&](int64_t row, int slot) {
         if (row < a.rows) {
@@ -392,25 +389,24 @@ __global__ void __launch_bounds__(32 * kMaxWarps) join_few_kernel(JoinArgs a, bo
 }
 
 template <int DT, int ST, int R, bool VEC, bool RING, bool ALL, bool DROP, bool SHIFT = false>
-cudaError_t launch_as(const JoinArgs &a, dim3 block, size_t smem, bool stage,
-                      cudaStream_t stream) {
+cudaError_t launch_as(const JoinArgs &a, dim3 block, size_t smem, cudaStream_t stream) {
     constexpr auto kernel = join_kernel<DT, ST, R, VEC, RING, ALL, DROP, SHIFT>;
     const cudaError_t e = allow_shared<kernel, kMostShared>();
     if (e != cudaSuccess) return e;
     int64_t grid = (a.rows + block.y - 1) / block.y;
     // the SMs are full, and the weights are staged once (SHIFT: every eighth CTA has rows of one kind)
     if (SHIFT || grid > kSms) grid = kSms;
-    kernel<<<static_cast<unsigned>(grid), block, smem, stream>>>(a, stage);
+    kernel<<<static_cast<unsigned>(grid), block, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
-template <int DT, int ST, int R, bool RING>
+template <int DT, int ST, int R, bool RING, bool SHIFT>
 cudaError_t launch_parts(const JoinArgs &a, dim3 block, size_t smem, cudaStream_t stream) {
     const bool all = a.branch.p && a.out.p && a.normed.p &&
                      (!a.gate || a.group_rows >= a.rows);
-    return !all ? launch_as<DT, ST, R, true, RING, false, true>(a, block, smem, true, stream)
-           : a.dropped ? launch_as<DT, ST, R, true, RING, true, true>(a, block, smem, true, stream)
-                       : launch_as<DT, ST, R, true, RING, true, false>(a, block, smem, true, stream);
+    return !all ? launch_as<DT, ST, R, true, RING, false, true, SHIFT>(a, block, smem, stream)
+           : a.dropped ? launch_as<DT, ST, R, true, RING, true, true, SHIFT>(a, block, smem, stream)
+                       : launch_as<DT, ST, R, true, RING, true, false, SHIFT>(a, block, smem, stream);
 }
 
 // VEC, SHIFT: as the kernel has them.
@@ -419,8 +415,9 @@ cudaError_t launch_many(const JoinArgs &a, cudaStream_t stream) {
     // (SHIFT: the most that a row can have)
     const int runs = static_cast<int>((a.cols + (SHIFT ? 2 : 1) * (kRun - 1)) / kRun);
     const int warps = (runs + 32 * R - 1) / (32 * R), teams = kTeamThreads / 32 / warps;
-    const int weights = 4 * static_cast<int>(sizeof(float4)) * runs;
-    const bool stage = weights <= kMostShared;
+    constexpr int kRunWeights = 4 * static_cast<int>(sizeof(float4));
+    static_assert(FA_JOIN_MAX_COLS / kRun * kRunWeights <= kMostShared, "the weights of any row fit");
+    const int weights = kRunWeights * runs;
     const dim3 block(32 * warps, warps > 1 && teams > 16 ? 16 : teams);  // 16: a barrier each
     if constexpr (VEC && ST != FA_F32) {
         // The ring, where it has room for three quarters of the teams.  16384 x 2048 BF16 took 57 us
@@ -433,22 +430,23 @@ cudaError_t launch_many(const JoinArgs &a, cudaStream_t stream) {
         if (4 * room >= 3 * static_cast<int>(block.y)) {
             const dim3 fewer(block.x, room);
             const size_t smem = weights + static_cast<size_t>(team) * room;
-            if constexpr (SHIFT)
-                return launch_as<DT, ST, R, true, true, false, true, true>(a, fewer, smem, true, stream);
+            // (ALL, for rows that begin anywhere: 65153 x 515 BF16, a run a lane, 94 us and 104 without; with
+            // two it is as fast without)
+            if constexpr (SHIFT && R > 1)
+                return launch_as<DT, ST, R, true, true, false, true, true>(a, fewer, smem, stream);
             else
-                return launch_parts<DT, ST, R, true>(a, fewer, smem, stream);
+                return launch_parts<DT, ST, R, true, SHIFT>(a, fewer, smem, stream);
         }
     }
     if constexpr (SHIFT) {
         if constexpr (ST == FA_F32)
-            return launch_as<DT, ST, R, true, false, false, true, true>(a, block, weights, true, stream);
+            return launch_as<DT, ST, R, true, false, false, true, true>(a, block, weights, stream);
         else
             return launch_many<DT, ST, R, false, false>(a, stream);
+    } else if constexpr (VEC && ST == FA_F32) {
+        return launch_parts<DT, ST, R, false, false>(a, block, weights, stream);
     } else {
-        if constexpr (VEC && ST == FA_F32)
-            if (stage) return launch_parts<DT, ST, R, false>(a, block, weights, stream);
-        return launch_as<DT, ST, R, VEC, false, false, true>(a, block, stage ? weights : 0, stage,
-                                                             stream);
+        return launch_as<DT, ST, R, VEC, false, false, true>(a, block, weights, stream);
     }
 }
 
@@ -481,7 +479,7 @@ cudaError_t launch_block_join(const JoinArgs &a, fa_dtype dt, fa_dtype st, cudaS
                    : shifted.ld8 >= 0 ? launch_many<d(), s(), r(), true, true>(shifted, stream)
                                       : launch_many<d(), s(), r(), false, false>(a, stream);
         };
-        // three warps' runs fill four warps by twos: 65153 x 515 BF16 took 98 us with one a lane and 114
+        // three warps' runs fill four warps by twos: 65153 x 515 BF16 took 94 us with one a lane and 114
         // with two; whole runs, which wait for memory, 63 and 62 (64528 x 520)
         return warps == 1 || (warps == 3 && shifted.ld8 >= 0)
                    ? many(std::integral_constant<int, 1>{})

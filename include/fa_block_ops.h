@@ -139,8 +139,8 @@ typedef struct fa_join_gradient {
  *   dgate = sum over the group's rows of branch_scale * D(b) * G
  *   dpre_weight = sum of dnormed * xh,  dpost_weight = sum of db * yh
  *   dbranch = post_rstd * (e - yh * mean(e * yh)),  e = db * (post_weight + weight_offset)
- * (dbranch = db without the first norm).  A dropped element has no gradient, whatever the
- * branch holds there.  Sums over rows are FP32, in groups whose sums are joined in order:
+ * (dbranch = db without the first norm: a dropped element then has no gradient, whatever the
+ * branch holds there; with the norm it is part of its row's mean, forward and back).  Sums over rows are FP32, in groups whose sums are joined in order:
  * reproducible bit for bit.  Weights' gradients are written, not added to.  rows == 0:
  * they are set to 0; cols == 0: nothing is launched or checked.
  */

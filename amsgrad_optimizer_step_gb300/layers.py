@@ -411,15 +411,19 @@ def block_join(residual: torch.Tensor, branch: torch.Tensor,
 
 class _Route(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, k, counted, settings):
+    def forward(ctx, logits, k, counted, settings, loss, grad_enabled):
         flat = _flat(logits)
         counted = None if counted is None else counted.reshape(-1).contiguous()
-        out = blocks.route_buffers(flat.shape[0], flat.shape[1], k, flat.device)
+        keep = grad_enabled and ctx.needs_input_grad[0]
+        out = blocks.route_buffers(flat.shape[0], flat.shape[1], k, flat.device, loss or keep)
         blocks.fa_route(flat, out, counted, *settings)
-        ctx.save_for_backward(flat, counted, out.chosen, out.weights, out.lse, out.counts)
+        if keep:
+            ctx.save_for_backward(flat, counted, out.chosen, out.weights, out.lse, out.counts)
         ctx.settings = settings
-        ctx.mark_non_differentiable(out.chosen, out.counts)
+        ctx.mark_non_differentiable(out.chosen, *([out.counts] if loss else []))
         ctx.set_materialize_grads(False)
+        if not loss:
+            return out.chosen, out.weights, None, None
         return out.chosen, out.weights, out.loss.view(()), out.counts
 
     @staticmethod
@@ -427,23 +431,27 @@ class _Route(torch.autograd.Function):
     def backward(ctx, _, dweights, dloss, __):
         flat, counted, chosen, weights, lse, counts = ctx.saved_tensors
         if dweights is None and dloss is None:
-            return None, None, None, None
+            return (None,) * 6
         out = blocks.RouteBuffers(chosen, weights, lse, counts, *[None] * 6)
         dlogits = torch.empty(flat.shape, dtype=flat.dtype, device=flat.device)
         blocks.fa_route_gradient(flat, out, dlogits,
                                  None if dweights is None else dweights.float().contiguous(),
                                  None if dloss is None else dloss.reshape(1).float(), counted,
                                  *ctx.settings)
-        return dlogits, None, None, None
+        return (dlogits,) + (None,) * 5
 
 
 def route(logits: torch.Tensor, k: int, counted: Optional[torch.Tensor] = None,
           renormalise: bool = True, weight_scale: float = 1.0, balance_coef: float = 0.0,
-          z_coef: float = 0.0) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+          z_coef: float = 0.0, loss: bool = True
+          ) -> tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
     """(chosen [tokens, k], weights [tokens, k], loss, counts [experts]) of tokens' logits
     [tokens, experts] (see fa_router).  The weights' gradient and the loss's go into the logits
-    in one pass."""
+    in one pass.  ``loss`` False: no loss and no counts (None), and where no gradient will be taken
+    either, as in a generation step, one kernel that sums nothing over the tokens."""
     if logits.dim() != 2:
         raise ValueError(f"logits: shape {tuple(logits.shape)}, expected a matrix")
-    return _Route.apply(logits, k, counted,
-                        (renormalise, weight_scale, balance_coef, z_coef))
+    if not loss and (balance_coef or z_coef):
+        raise ValueError("a coefficient of a loss that is not taken")
+    return _Route.apply(logits, k, counted, (renormalise, weight_scale, balance_coef, z_coef),
+                        bool(loss), torch.is_grad_enabled())

@@ -118,6 +118,33 @@ def test_the_log_of_sums_next_to_one():
     assert bool(((dlogits[:, 0].double() - p * lse).abs() <= err).all())
 
 
+def test_a_route_without_a_loss(monkeypatch):
+    """layers.route of a generation step: the same choice and weights, and no sums over the tokens."""
+    from amsgrad_optimizer_step_gb300 import layers
+    summed = []
+    plain = layers.blocks.fa_route
+    monkeypatch.setattr(layers.blocks, "fa_route", lambda x, out, *args: (
+        summed.append(out.summary is not None), plain(x, out, *args))[1])
+    logits = randn(gen(4), 50, 72).requires_grad_()
+    want = layers.route(logits, 3, None, False, 2.0)
+    assert summed.pop()
+    with torch.no_grad():
+        got = layers.route(logits, 3, None, False, 2.0, loss=False)
+        assert not summed.pop() and got[2:] == (None, None) and not got[1].requires_grad
+        layers.route(logits, 3)
+        assert summed.pop()  # who does not say so has the loss and the counts as ever
+    for a, b in zip(got[:2], want):
+        assert torch.equal(a, b)
+    got = layers.route(logits.detach(), 3, loss=False)
+    assert not summed.pop() and got[2:] == (None, None)
+    got = layers.route(logits, 3, None, False, 2.0, loss=False)  # with a gradient, which needs them
+    assert summed.pop() and got[2:] == (None, None) and not got[0].requires_grad
+    assert torch.equal(got[1], want[1])
+    dw = randn(gen(5), 50, 3)
+    (a,), (b,) = (torch.autograd.grad(x, logits, dw) for x in (got[1], want[1]))
+    assert torch.equal(a, b)
+
+
 # ---- several threads ---------------------------------------------------------------------
 
 class Recorded:

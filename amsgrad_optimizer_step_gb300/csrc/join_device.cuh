@@ -76,7 +76,8 @@ __device__ __forceinline__ void store_columns(typename Elem<DT>::T *p, const flo
 }
 template <int DT>
 __device__ __forceinline__ void store_columns(const MatrixArgs &m, int64_t row, const float *v, int c) {
-    store_columns<DT>(static_cast<typename Elem<DT>::T *>(m.p) + row * m.ld + c, v, c,
+    if (fa_in_bounds(row, 1, m.rows))
+        store_columns<DT>(static_cast<typename Elem<DT>::T *>(m.p) + row * m.ld + c, v, c,
                       static_cast<int>(m.cols));
 }
 // (c: where a line begins in memory)
@@ -85,12 +86,14 @@ __device__ __forceinline__ Raw<DT, kRun> read_columns(const MatrixArgs &m, int64
     const auto *p = static_cast<const typename Elem<DT>::T *>(m.p) + row * m.ld + c;
     const int cols = static_cast<int>(m.cols);
     Raw<DT, kRun> x;
-    if (c >= 0 && c + kRun <= cols) {
+    const bool there = fa_in_bounds(row, 1, m.rows);
+    if (there && c >= 0 && c + kRun <= cols) {
         x.load(p);
     } else {
         float v[kRun];
 #pragma unroll
-        for (int j = 0; j < kRun; ++j) v[j] = is_column(c + j, cols) ? Elem<DT>::widen(p[j]) : 0.f;
+        for (int j = 0; j < kRun; ++j)
+            v[j] = there && is_column(c + j, cols) ? Elem<DT>::widen(p[j]) : 0.f;
         x.from(v);  // exact: they came from this type
     }
     return x;
@@ -139,7 +142,7 @@ __device__ __forceinline__ void zero(Raw<DT, kRun> &x) {
 template <int DT>
 __device__ __forceinline__ void store_raw(const MatrixArgs &m, int64_t row, int64_t c,
                                           const Raw<DT, kRun> &x) {
-    if (!fa_in_bounds(c, kRun, m.cols)) return;
+    if (!fa_in_bounds(c, kRun, m.cols) || !fa_in_bounds(row, 1, m.rows)) return;
     auto *p = static_cast<typename Elem<DT>::T *>(m.p) + row * m.ld + c;
 #pragma unroll
     for (int k = 0; k < Raw<DT, kRun>::kWords; ++k) __stcs(reinterpret_cast<uint4 *>(p) + k, x.r[k]);
@@ -153,7 +156,7 @@ __device__ __forceinline__ Raw<DT, kRun> read_run(const MatrixArgs &m, int64_t r
     if constexpr (VEC) {
         Raw<DT, kRun> x;
         zero(x);
-        if (q < runs && fa_in_bounds(q * kRun, kRun, m.cols))
+        if (q < runs && fa_in_bounds(q * kRun, kRun, m.cols) && fa_in_bounds(row, 1, m.rows))
             x.load(static_cast<const typename Elem<DT>::T *>(m.p) + row * m.ld + q * kRun);
         return x;
     } else {

@@ -72,17 +72,23 @@ struct Ring {
         if (!fa_in_bounds(row, 1, a.j.rows)) return;
         const int reach = R * blockDim.x;
         const uint32_t s = lines(a, row, shift, 2 * kS), d = lines(a, row, shift, 2 * kD);
-        row_expect(bar, (a.dout.p ? s : 0) + (a.out.p ? s : 0) + (a.dnormed.p ? d : 0) +
-                            (a.j.branch.p ? d : 0));
-        const auto copy = [&](const MatrixArgs &m, int size, uint32_t bytes, int at) {
-            if (m.p)
+        // (the lines lie in the matrix, in front of and behind the row too, and in the matrix's slots)
+        const auto inside = [&](const MatrixArgs &m, int size, uint32_t bytes) {
+            return m.p && fa_in_bounds(row * m.ld - shift, bytes / size, (m.rows - 1) * m.ld + m.cols) &&
+                   fa_in_bounds(0, bytes, 8 * size * reach);
+        };
+        const bool dout = inside(a.dout, 2 * kS, s), out = inside(a.out, 2 * kS, s);
+        const bool dnormed = inside(a.dnormed, 2 * kD, d), branch = inside(a.j.branch, 2 * kD, d);
+        row_expect(bar, (dout ? s : 0) + (out ? s : 0) + (dnormed ? d : 0) + (branch ? d : 0));
+        const auto copy = [&](bool it, const MatrixArgs &m, int size, uint32_t bytes, int at) {
+            if (it)
                 row_copy(slot + at * reach, static_cast<const char *>(m.p) + (row * m.ld - shift) * size,
                          bytes, bar);
         };
-        copy(a.dout, 2 * kS, s, 0);
-        copy(a.out, 2 * kS, s, kS);
-        copy(a.dnormed, 2 * kD, d, 2 * kS);
-        copy(a.j.branch, 2 * kD, d, 2 * kS + kD);
+        copy(dout, a.dout, 2 * kS, s, 0);
+        copy(out, a.out, 2 * kS, s, kS);
+        copy(dnormed, a.dnormed, 2 * kD, d, 2 * kS);
+        copy(branch, a.j.branch, 2 * kD, d, 2 * kS + kD);
     }
     // By the thread of the last row's last run: what ``lines`` left out.
     static __device__ void complete(const JoinGradArgs &a, int64_t row, int shift, uint4 *slot) {
@@ -93,7 +99,7 @@ struct Ring {
             const T *const from = static_cast<const T *>(m.p) + row * m.ld;
             const int there = static_cast<int>(lines(a, row, shift, sizeof(T)) / sizeof(T)) - shift;
             for (int c = there; m.p && c < cols; ++c)
-                if (fa_in_bounds(c, 1, cols)) to[c] = from[c];
+                if (fa_in_bounds(c, 1, cols) && fa_in_bounds(shift + c, 1, kRun * reach)) to[c] = from[c];
         };
         copy(a.dout, std::integral_constant<int, ST>{}, 0);
         copy(a.out, std::integral_constant<int, ST>{}, kS);
@@ -290,6 +296,10 @@ __device__ __forceinline__ void join_gradient_rows(const JoinGradArgs &a) {
         keep(0, r, w);
     }
     float *const sums = a.sums + cta * a.plan.parts * a.plan.pitch;
+    const auto in_sums = [&](int which, int c) {  // of the CTA's sums, in what they have room for
+        const int64_t at = (cta * a.plan.parts + which) * a.plan.pitch + first_run * kRun + c;
+        return is_column(c, cols) && fa_in_bounds(at, 1, a.plan.bytes / 4);
+    };
     // the gate's group of the row, and the turns that its rows begin and end with
     int64_t group = own_gate ? a.j.by_group.quotient(static_cast<uint32_t>(first)) : 0;
     int64_t group_begin = own_gate ? group * a.j.group_rows - first : 0;
@@ -318,7 +328,7 @@ __device__ __forceinline__ void join_gradient_rows(const JoinGradArgs &a) {
                 float *const at = sums + kPost * a.plan.pitch + c;
 #pragma unroll
                 for (int j = 0; j < kRun; ++j)
-                    if (is_column(c + j, cols)) at[j] = scale * k[j];
+                    if (in_sums(kPost, c + j)) at[j] = scale * k[j];
             }
             return;
         }
@@ -334,7 +344,7 @@ __device__ __forceinline__ void join_gradient_rows(const JoinGradArgs &a) {
                 float *const at = sums + kPost * a.plan.pitch + c;
 #pragma unroll
                 for (int j = 0; j < kRun; ++j)
-                    if (is_column(c + j, cols)) {
+                    if (in_sums(kPost, c + j)) {
                         const float x = scale * w[j] * k[j];
                         at[j] = flushed ? at[j] + x : x;
                     }
@@ -348,7 +358,7 @@ __device__ __forceinline__ void join_gradient_rows(const JoinGradArgs &a) {
                         if (whole)
                             store_weight<DT>(a.dgate, a.j.wide_weights,
                                              group * a.dgate_ld + c + j, x);
-                        else
+                        else if (in_sums(begun_here ? kTail : kHead, c + j))
                             gate_part[c + j] = x;
                     }
             }
@@ -494,14 +504,15 @@ __device__ __forceinline__ void join_gradient_rows(const JoinGradArgs &a) {
                     db[j] = fma2(mul2(y[j], both(rq)), both(-mean), mul2(db[j], both(rq)));
             }
             const int q = r * blockDim.x + threadIdx.x;
+            const bool there = fa_in_bounds(row, 1, a.j.rows);
             float v[kRun];
             if (ALL || a.dresidual.p) {
                 from_pairs(dr, v);
                 if (!RING)
                     store_run<ST, false>(a.dresidual, row, q * kRun, v, 0xffffffffu, 32);
                 else if (SHIFT && !whole)
-                    store_columns<ST>(to_residual, v, column(0), cols);
-                else if (q < runs && fa_in_bounds(column(r), kRun, cols))
+                    store_columns<ST>(to_residual, v, column(0), there ? cols : 0);
+                else if (q < runs && there && fa_in_bounds(column(r), kRun, cols))
                     store_n<ST, kRun>(to_residual + r * blockDim.x * kRun, v);
             }
             if (ALL || a.dbranch.p) {
@@ -509,8 +520,8 @@ __device__ __forceinline__ void join_gradient_rows(const JoinGradArgs &a) {
                 if (!RING)
                     store_run<DT, false>(a.dbranch, row, q * kRun, v, 0xffffffffu, 32);
                 else if (SHIFT && !whole)
-                    store_columns<DT>(to_branch, v, column(0), cols);
-                else if (q < runs && fa_in_bounds(column(r), kRun, cols))
+                    store_columns<DT>(to_branch, v, column(0), there ? cols : 0);
+                else if (q < runs && there && fa_in_bounds(column(r), kRun, cols))
                     store_n<DT, kRun>(to_branch + r * blockDim.x * kRun, v);
             }
         }
@@ -532,7 +543,7 @@ __device__ __forceinline__ void join_gradient_rows(const JoinGradArgs &a) {
             from_pairs(sum_p[r], v);
 #pragma unroll
             for (int j = 0; j < kRun; ++j)
-                if (is_column(c + j, cols)) sums[kPre * a.plan.pitch + c + j] = v[j];
+                if (in_sums(kPre, c + j)) sums[kPre * a.plan.pitch + c + j] = v[j];
         }
     }
 }
@@ -573,6 +584,9 @@ __global__ void __launch_bounds__(kMaxThreads) join_gradient_wide_kernel(JoinGra
     // lanes of one warp hold consecutive runs, and all of them take every turn
     const int64_t turns = (blocks + blockDim.x - 1) / blockDim.x;
     float *const sums = a.sums + blockIdx.x * a.plan.parts * a.plan.pitch;
+    const auto in_sums = [&](int which, int64_t c) {
+        return fa_in_bounds((blockIdx.x * a.plan.parts + which) * a.plan.pitch + c, 1, a.plan.bytes / 4);
+    };
     const bool own_gate = a.j.gate && a.j.group_rows < a.j.rows;
     int64_t group = own_gate ? a.j.by_group.quotient(static_cast<uint32_t>(first)) : 0;
     int64_t group_first = own_gate ? group * a.j.group_rows : first;
@@ -623,7 +637,8 @@ __global__ void __launch_bounds__(kMaxThreads) join_gradient_wide_kernel(JoinGra
         if (!own_gate) {  // K itself
             for (int64_t q = threadIdx.x; q < blocks; q += blockDim.x)
                 for (int j = 0; j < valid_cols(q * kRun, a.j.cols); ++j)
-                    sums[kPost * a.plan.pitch + q * kRun + j] = scale * sum_k[q * kRun + j];
+                    if (in_sums(kPost, q * kRun + j))
+                        sums[kPost * a.plan.pitch + q * kRun + j] = scale * sum_k[q * kRun + j];
             return;
         }
         const bool begun_here = group_first >= first, whole = begun_here && group_last <= last;
@@ -640,11 +655,11 @@ __global__ void __launch_bounds__(kMaxThreads) join_gradient_wide_kernel(JoinGra
                 const float k = scale * sum_k[c + j];
                 sum_k[c + j] = 0.f;
                 float *at = sums + kPost * a.plan.pitch + c + j;
-                if (a.dpost_weight) *at = flushed ? *at + g[j] * k : g[j] * k;
+                if (a.dpost_weight && in_sums(kPost, c + j)) *at = flushed ? *at + g[j] * k : g[j] * k;
                 if (a.dgate && whole)
                     store_weight<DT>(a.dgate, a.j.wide_weights, group * a.dgate_ld + c + j,
                                      w[j] * k);
-                else if (a.dgate)
+                else if (a.dgate && in_sums(begun_here ? kTail : kHead, c + j))
                     gate_part[c + j] = w[j] * k;
             }
         }
@@ -716,7 +731,8 @@ __global__ void __launch_bounds__(kMaxThreads) join_gradient_wide_kernel(JoinGra
     if (a.dpre_weight)
         for (int64_t q = threadIdx.x; q < blocks; q += blockDim.x)
             for (int j = 0; j < valid_cols(q * kRun, a.j.cols); ++j)
-                sums[kPre * a.plan.pitch + q * kRun + j] = sum_p[q * kRun + j];
+                if (in_sums(kPre, q * kRun + j))
+                    sums[kPre * a.plan.pitch + q * kRun + j] = sum_p[q * kRun + j];
 }
 
 // Joins the CTAs' sums in order: K for the first weight and a gate that all rows share, the second

@@ -20,7 +20,7 @@ __device__ __forceinline__ Raw<DT, kRun> load_run(const MatrixArgs &m, int64_t r
     using E = Elem<DT>;
     const typename E::T *p = static_cast<const typename E::T *>(m.p) + row * m.ld + c;
     const int valid = valid_cols(c, m.cols);
-    if (valid && !fa_in_bounds(c, valid, m.cols)) return {};
+    if (valid && !(fa_in_bounds(c, valid, m.cols) && fa_in_bounds(row, 1, m.rows))) return {};
     if constexpr (ALIGNED) {
         Raw<DT, kRun> x;
         if (c + kRun <= m.cols) {
@@ -45,7 +45,7 @@ __device__ __forceinline__ void store_run(const MatrixArgs &m, int64_t row, int6
     using E = Elem<DT>;
     typename E::T *p = static_cast<typename E::T *>(m.p) + row * m.ld + c;
     int valid = valid_cols(c, m.cols);
-    if (valid && !fa_in_bounds(c, valid, m.cols)) valid = 0;
+    if (valid && !(fa_in_bounds(c, valid, m.cols) && fa_in_bounds(row, 1, m.rows))) valid = 0;
     if constexpr (ALIGNED) {
         if (c + kRun <= m.cols) {
             store_n<DT, kRun>(p, x);

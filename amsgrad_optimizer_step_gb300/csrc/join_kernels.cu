@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kTeamThreads) join_kernel(JoinArgs a) {
         // (what is not there is not read: read all the same, a join without its second norm spilled
         // registers, 39 us for 33 at 16384 x 2048 BF16)
         const bool post = plane == plane_post;
-        if (!ALL && !SHIFT &&
+        if (VEC && !ALL && !SHIFT &&
             !(post ? a.gate || (a.post_norm && a.post_weight) : a.pre_weight != nullptr)) {
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) w[j] = both(post ? scale : 1.f);

@@ -7,9 +7,9 @@
 // integers in the logits' order with the expert's number in their low bits, so that one maximum
 // gives the expert, ties to the lower number: those of 16-bit logits hold the whole logit, those
 // of FP32 its upper bits, and where two of the keys that matter agree in these (one token in some
-// hundred), or one lane's list gave all eight and holds no ninth to compare, the warp chooses again
-// by whole logits, an expert at a time, which is also how more than eight are chosen.  Sums over
-// tokens stay with the lane that holds the expert, then go by CTA and in order.
+// hundred) the warp chooses again by whole logits, an expert at a time, which is also how more
+// than eight are chosen.  Sums over tokens stay with the lane that holds the expert, then go by
+// CTA and in order.
 //
 // Exponentials and quotients are the hardware's, two units each in the last place beside the rounding of
 // an exponential's argument, as the weights' and probabilities' bounds in the tests have it; the
@@ -207,24 +207,30 @@ route_kernel(RouteArgs a, bool vec) {
         bool again = !LISTED;
         if (LISTED) {
             constexpr uint32_t kNumber = (1u << kBits) - 1;
-            uint32_t key[N];
+            uint32_t key[N], cut = 0;
             // (what is past the last expert is -infinity, and its number is behind all that there are)
 #pragma unroll
             for (int j = 0; j < N; ++j) key[j] = numbered_key<kBits>(x[j], expert_of<L>(part, j));
 #pragma unroll
             for (int r = 0; r < R; ++r) sort8(key + r * kRun);
 #pragma unroll
-            for (int r = 1; r < R; ++r) merge8(key, key + r * kRun);
+            for (int r = 1; r < R; ++r) {
+                if (DT == FA_F32 && k == kListed)  // the largest key that a list of eight leaves out
+#pragma unroll
+                    for (int j = 0; j < kRun; ++j) cut = max(cut, min(key[j], key[r * kRun + 7 - j]));
+                merge8(key, key + r * kRun);
+            }
             uint32_t before = 0xffffffffu;
             bool same = false;
 #pragma unroll
             for (int i = 0; i <= kListed; ++i) {
                 // (FP32 asks for one more, which the last choice has to be above)
                 if (i > k || (i == k && (DT != FA_F32 || k == experts))) break;
+                // a lane that gave all eight has its ninth outside its list (65536 tokens whose largest lie in
+                // one of 32 runs: 43 us, 111 where such lanes were all chosen again; 3 % of any other)
+                if (DT == FA_F32 && R > 1 && i == kListed) key[0] = max(key[0], cut);
                 const uint32_t best = group_max<L>(key[0]);
                 if (DT == FA_F32) same |= i > 0 && (best | kNumber) == (before | kNumber);
-                // a lane that gave all eight has no ninth in its list, which may be short of it
-                if (DT == FA_F32 && R > 1 && i == kListed) same |= key[0] == 0u;
                 before = best;
                 if (i == k) break;
                 take(i, static_cast<int>(kNumber - (best & kNumber)));
@@ -470,6 +476,7 @@ __global__ void __launch_bounds__(kGradThreads) route_gradient_kernel(RouteGradA
         float x[N], w[kItems], d[kItems];
         int e[kItems];
         float2 lse = make_float2(0.f, 1.f);
+        float z_part = 0.f;
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
             w[i] = d[i] = 0.f;
@@ -478,6 +485,7 @@ __global__ void __launch_bounds__(kGradThreads) route_gradient_kernel(RouteGradA
         if (on) {
             load_logits<DT, L, R>(r.logits, t, part, vec, x);
             lse = reinterpret_cast<const float2 *>(r.lse)[t];
+            z_part = lse.x + logf(lse.y);
             if (a.dweights) {
 #pragma unroll
                 for (int i = 0; i < kItems; ++i)
@@ -517,7 +525,7 @@ __global__ void __launch_bounds__(kGradThreads) route_gradient_kernel(RouteGradA
             mean = fmaf(x[j], load[j], mean);
         }
         mean = group_sum<L>(mean);
-        float same = fmaf(zc, lse.x + logf(lse.y), -mean);
+        float same = fmaf(zc, z_part, -mean);
         // without renormalising, every expert takes from the chosen ones' weights
         if (a.dweights && !r.renormalise) same -= back * r.weight_scale;
 #pragma unroll

@@ -125,7 +125,6 @@ RouteArgs route_args(const fa_router *x, const fa_routing *r) {
     a.logits = matrix_args(x->logits, x->tokens, x->experts, x->ld);
     a.counted = x->counted;
     a.top_k = x->top_k;
-    a.by_k = Divider(static_cast<uint32_t>(x->top_k));
     a.renormalise = x->renormalise != 0;
     a.weight_scale = static_cast<float>(x->weight_scale);
     a.balance_coef = static_cast<float>(x->balance_coef);

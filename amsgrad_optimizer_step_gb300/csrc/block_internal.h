@@ -115,7 +115,6 @@ struct RouteArgs {
     MatrixArgs logits;
     const uint8_t *counted;
     int32_t top_k;
-    Divider by_k;
     bool renormalise;
     float weight_scale, balance_coef, z_coef;
     int32_t *chosen;

@@ -15,9 +15,12 @@
 // an exponential's argument, as the weights' and probabilities' bounds in the tests have it; the
 // logarithm is the library's, since the hardware's error is absolute and the sum is often next to 1.
 //
-// Instructions bound it, not memory: 65536 tokens, 8 of 128 experts, BF16, take 21 us, of which
-// the bytes need 3 (51 with a maximum over all keys for every choice), the join of the CTAs' sums 7.5
-// and the gradient 16.5; 8 of 256, FP32, 46, 7.6 and 30.
+// 65536 tokens, 8 of 128 experts, BF16, take 21 us, of which the bytes need 3 (51 with a maximum over
+// all keys for every choice), the join of the CTAs' sums 8 and the gradient 16.5; 8 of 256, FP32, 49, 8
+// and 30.5.  Neither memory (10 to 34 % of its rate) nor issue slots (59 and 53 %, the gradient 53 and
+// 47) bound it: with 80 registers a thread a third of the warps fit an SM, and a warp spends 26 % of its
+// time waiting for memory (the gradient 42 to 53): for its logits and the chosen ones' second reading;
+// 13 to 16 % for shuffles and shared memory, 15 to 18 % for the arithmetic before it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
